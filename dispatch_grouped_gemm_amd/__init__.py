@@ -15,6 +15,11 @@ Entry points (same names as the C ABI):
     moe_forward_static_need, moe_set_tile_table, moe_get_tile_config,
     moe_pack_weights, moe_unpack_weights, moe_packed_codes_bytes, moe_packed_scales_bytes,
     moe_gemm1_swiglu_packed, moe_gemm2_packed, moe_check_shape, moe_strerror
+around the layer (the router, token rows to their experts and back, and a shared
+projection with low-rank adapters; gradients where a training step needs them):
+    moe_route, moe_route_backward, moe_permute, moe_permute_backward,
+    moe_unpermute, moe_unpermute_backward, moe_adapter_check,
+    moe_adapter_workspace_size, moe_adapter_project
 """
 
 from __future__ import annotations
@@ -38,6 +43,9 @@ __all__ = [
     "moe_packed_scales_bytes", "PackedWeights",
     "moe_gemm1_swiglu_packed", "moe_gemm2_packed",
     "pack_layer_weights", "DispatchBuffers",
+    "moe_route", "moe_route_backward", "moe_permute", "moe_permute_backward",
+    "moe_unpermute", "moe_unpermute_backward", "AdapterShape", "moe_adapter_check",
+    "moe_adapter_workspace_size", "moe_adapter_project", "alloc_adapter_workspace",
     "alloc_dispatch", "alloc_workspace", "COMPACT", "FIXED_SLOT", "Y_BF16", "Y_FP8", "Y_AUTO",
 ]
 
@@ -62,7 +70,9 @@ EXPORTED = ["moe_check_shape", "moe_row_capacity", "moe_dispatch_workspace_size"
             "moe_get_tile_config", "moe_pack_weights", "moe_unpack_weights",
             "moe_packed_codes_bytes",
             "moe_packed_scales_bytes", "moe_gemm1_swiglu_packed", "moe_gemm2_packed",
-            "moe_strerror"]
+            "moe_route", "moe_route_backward", "moe_permute", "moe_permute_backward",
+            "moe_unpermute", "moe_unpermute_backward", "moe_adapter_check",
+            "moe_adapter_workspace_size", "moe_adapter_project", "moe_strerror"]
 
 
 class MoeError(RuntimeError):
@@ -89,6 +99,10 @@ class _CForwardArgs(ctypes.Structure):
                 ("y_format", ctypes.c_int32), ("w13_packed", ctypes.c_void_p),
                 ("w13_packed_scale", ctypes.c_void_p), ("w2_packed", ctypes.c_void_p),
                 ("w2_packed_scale", ctypes.c_void_p)]
+
+
+class _CAdapterShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "H", "N", "L", "rank")]
 
 
 class TileEntry(ctypes.Structure):
@@ -125,6 +139,19 @@ class MoeShape:
         return _CShape(self.T, self.H, self.I, self.K, self.E_total, self.expert_begin,
                        self.E_local, self.dispatch_mode, self.capacity, self.gate_limit,
                        self.up_limit)
+
+
+@dataclass(frozen=True)
+class AdapterShape:
+    """Sizes of moe_adapter_project: T rows of H values to N, L adapters of `rank`."""
+    T: int
+    H: int
+    N: int
+    L: int
+    rank: int
+
+    def c(self) -> _CAdapterShape:
+        return _CAdapterShape(self.T, self.H, self.N, self.L, self.rank)
 
 
 _lib = None
@@ -201,6 +228,22 @@ def lib() -> ctypes.CDLL:
         h.moe_gemm1_swiglu_packed.restype = ctypes.c_int
         h.moe_gemm2_packed.argtypes = [S, P, P, P, P, P, P, P, P, P, P]
         h.moe_gemm2_packed.restype = ctypes.c_int
+        i32 = ctypes.c_int32
+        A = ctypes.POINTER(_CAdapterShape)
+        h.moe_route.argtypes = [S, i32, P, i32, P, P, P]
+        h.moe_route_backward.argtypes = [S, i32, P, i32, P, P, P, P, P]
+        h.moe_permute.argtypes = [S, i32, P, P, P, P]
+        h.moe_permute_backward.argtypes = h.moe_permute.argtypes
+        h.moe_unpermute.argtypes = [S, i32, P, P, P, P, P]
+        h.moe_unpermute_backward.argtypes = [S, i32, P, P, P, P, P, P, P]
+        h.moe_adapter_check.argtypes = [A]
+        h.moe_adapter_project.argtypes = [A, i32, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
+        for n in ("moe_route", "moe_route_backward", "moe_permute", "moe_permute_backward",
+                  "moe_unpermute", "moe_unpermute_backward", "moe_adapter_check",
+                  "moe_adapter_project"):
+            getattr(h, n).restype = ctypes.c_int
+        h.moe_adapter_workspace_size.argtypes = [A]
+        h.moe_adapter_workspace_size.restype = ctypes.c_size_t
         h.moe_strerror.argtypes = [ctypes.c_int]
         h.moe_strerror.restype = ctypes.c_char_p
         _lib = h
@@ -745,3 +788,157 @@ def moe_forward_persistent(shape: MoeShape, x_fp8, x_scale, topk_ids, topk_w, w1
                            w2, w2_scale, out_bf16, workspace, stream=None):
     moe_forward(shape, x_fp8, x_scale, topk_ids, topk_w, w13, w13_scale, w2, w2_scale,
                 out_bf16, workspace, stream=stream, persistent=True)
+
+
+# ---- the router, the rows to their experts and back, the adapters -----------------
+
+_ELEM = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_I32 = {torch.int32}
+_F32 = {torch.float32}
+
+
+def _elem(t: torch.Tensor, name: str, allowed=(0, 1, 2)):
+    """The element code, dtype set and device that a call's other tensors share."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a tensor" % name)
+    code = _ELEM.get(t.dtype)
+    if code not in allowed:
+        raise TypeError("%s has dtype %s" % (name, t.dtype))
+    if t.device.type != "cuda":
+        raise ValueError("%s is on %s, expected a GPU" % (name, t.device))
+    return code, {t.dtype}, t.device
+
+
+def _launch(fn, where: str, device, *args):
+    """Call fn(*args) with the tensors' device current."""
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args), where)
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args), where)
+
+
+def moe_route(shape: MoeShape, logits, topk_ids, topk_w, renormalize: bool = True, stream=None):
+    """The router: logits [T, E_total] (bf16, fp16 or float32) to topk_ids and topk_w
+    [T, K], the K largest in falling order (equal ones by the lower id), weights the
+    softmax over them (renormalize) or over all experts.  -inf and NaN are never
+    chosen; slots left over get -1 and 0."""
+    code, dts, dev = _elem(logits, "logits")
+    T, K = shape.T, shape.K
+    args = [_ptr(logits, "logits", (T, shape.E_total), dts, dev), 1 if renormalize else 0,
+            _ptr(topk_ids, "topk_ids", (T, K), _I32, dev),
+            _ptr(topk_w, "topk_w", (T, K), _F32, dev)]
+    _launch(lib().moe_route, "moe_route", dev, ctypes.byref(shape.c()), code, *args,
+            _stream(stream, dev))
+
+
+def moe_route_backward(shape: MoeShape, logits, topk_ids, topk_w, dtopk_w, dlogits,
+                       renormalize: bool = True, stream=None):
+    """dlogits [T, E_total] from dtopk_w [T, K] and moe_route's ids and weights; logits
+    may be None when the weights were renormalised."""
+    code, dts, dev = _elem(dlogits, "dlogits")
+    T, K, E = shape.T, shape.K, shape.E_total
+    lp = None
+    if logits is not None or not renormalize:
+        lp = _ptr(logits, "logits", (T, E), dts, dev)
+    args = [lp, 1 if renormalize else 0, _ptr(topk_ids, "topk_ids", (T, K), _I32, dev),
+            _ptr(topk_w, "topk_w", (T, K), _F32, dev),
+            _ptr(dtopk_w, "dtopk_w", (T, K), _F32, dev),
+            _ptr(dlogits, "dlogits", (T, E), dts, dev)]
+    _launch(lib().moe_route_backward, "moe_route_backward", dev, ctypes.byref(shape.c()), code,
+            *args, _stream(stream, dev))
+
+
+def _row_sizes(shape: MoeShape):
+    """(T, H), (row capacity, H) and (T*K,), as alloc_dispatch sizes them."""
+    return ((shape.T, shape.H), (max(moe_row_capacity(shape), 1), shape.H),
+            (max(shape.T * shape.K, 1),))
+
+
+def moe_permute(shape: MoeShape, x, route_row, rows, stream=None):
+    """rows[route_row[t, k]] = x[t]: token rows [T, H] to the rows [R, H] of their
+    experts (route_row of moe_dispatch); rows without a route are left as they are."""
+    code, dts, dev = _elem(x, "x")
+    tok, row, slots = _row_sizes(shape)
+    args = [_ptr(x, "x", tok, dts, dev), _ptr(route_row, "route_row", slots, _I32, dev),
+            _ptr(rows, "rows", row, dts, dev)]
+    _launch(lib().moe_permute, "moe_permute", dev, ctypes.byref(shape.c()), code, *args,
+            _stream(stream, dev))
+
+
+def moe_permute_backward(shape: MoeShape, drows, route_row, dx, stream=None):
+    """dx[t] = sum over k of drows[route_row[t, k]]: moe_permute's gradient."""
+    code, dts, dev = _elem(drows, "drows")
+    tok, row, slots = _row_sizes(shape)
+    args = [_ptr(drows, "drows", row, dts, dev), _ptr(route_row, "route_row", slots, _I32, dev),
+            _ptr(dx, "dx", tok, dts, dev)]
+    _launch(lib().moe_permute_backward, "moe_permute_backward", dev, ctypes.byref(shape.c()),
+            code, *args, _stream(stream, dev))
+
+
+def moe_unpermute(shape: MoeShape, rows, topk_w, route_row, out, stream=None):
+    """out[t] = sum over k of topk_w[t, k] rows[route_row[t, k]] (topk_w None: weights
+    of 1), in float32, k ascending, rounded once."""
+    code, dts, dev = _elem(rows, "rows")
+    tok, row, slots = _row_sizes(shape)
+    wp = None if topk_w is None else _ptr(topk_w, "topk_w", (shape.T, shape.K), _F32, dev)
+    args = [_ptr(rows, "rows", row, dts, dev), wp,
+            _ptr(route_row, "route_row", slots, _I32, dev), _ptr(out, "out", tok, dts, dev)]
+    _launch(lib().moe_unpermute, "moe_unpermute", dev, ctypes.byref(shape.c()), code, *args,
+            _stream(stream, dev))
+
+
+def moe_unpermute_backward(shape: MoeShape, dout, rows, topk_w, route_row, drows, dtopk_w,
+                           stream=None):
+    """moe_unpermute's gradients: drows[route_row[t, k]] = topk_w[t, k] dout[t] and
+    dtopk_w[t, k] = <dout[t], rows[route_row[t, k]]> (0 for skipped slots).  drows or
+    dtopk_w may be None; rows may be None without dtopk_w."""
+    code, dts, dev = _elem(dout, "dout")
+    tok, row, slots = _row_sizes(shape)
+    tk = (shape.T, shape.K)
+    if drows is None and dtopk_w is None:
+        raise ValueError("moe_unpermute_backward: give drows, dtopk_w or both")
+    args = [_ptr(dout, "dout", tok, dts, dev),
+            None if rows is None and dtopk_w is None else _ptr(rows, "rows", row, dts, dev),
+            None if topk_w is None else _ptr(topk_w, "topk_w", tk, _F32, dev),
+            _ptr(route_row, "route_row", slots, _I32, dev),
+            None if drows is None else _ptr(drows, "drows", row, dts, dev),
+            None if dtopk_w is None else _ptr(dtopk_w, "dtopk_w", tk, _F32, dev)]
+    _launch(lib().moe_unpermute_backward, "moe_unpermute_backward", dev,
+            ctypes.byref(shape.c()), code, *args, _stream(stream, dev))
+
+
+def moe_adapter_check(shape: AdapterShape) -> int:
+    return lib().moe_adapter_check(ctypes.byref(shape.c()))
+
+
+def moe_adapter_workspace_size(shape: AdapterShape) -> int:
+    return int(lib().moe_adapter_workspace_size(ctypes.byref(shape.c())))
+
+
+def alloc_adapter_workspace(shape: AdapterShape, device) -> torch.Tensor:
+    """A moe_adapter_project workspace for `shape`."""
+    return torch.empty(max(moe_adapter_workspace_size(shape), 256), dtype=torch.uint8,
+                       device=device)
+
+
+def moe_adapter_project(shape: AdapterShape, x, w, adapter_ids, a, b, scale, out, workspace,
+                        base=None, stream=None):
+    """out[t] = base[t] + scale[l] (x[t] A_l^T) B_l^T with l = adapter_ids[t] (-1: no
+    adapter), base = x W^T for a shared weight w [N, H], or the given base [T, N] (w
+    None; base may be out).  x [T, H], a [L, rank, H], b [L, N, rank], scale float32
+    [L] or None, out [T, N], bf16 or fp16; workspace of alloc_adapter_workspace."""
+    code, dts, dev = _elem(x, "x", (0, 1))
+    T, H, N, L, r = shape.T, shape.H, shape.N, shape.L, shape.rank
+    if (w is None) == (base is None):
+        raise ValueError("moe_adapter_project: give w or base")
+    args = [_ptr(x, "x", (T, H), dts, dev),
+            None if w is None else _ptr(w, "w", (N, H), dts, dev),
+            None if base is None else _ptr(base, "base", (T, N), dts, dev),
+            _ptr(adapter_ids, "adapter_ids", (T,), _I32, dev),
+            _ptr(a, "a", (L, r, H), dts, dev), _ptr(b, "b", (L, N, r), dts, dev),
+            None if scale is None else _ptr(scale, "scale", (L,), _F32, dev),
+            _ptr(out, "out", (T, N), dts, dev)]
+    ws = _ptr(workspace, "workspace", None, {torch.uint8}, dev)
+    _launch(lib().moe_adapter_project, "moe_adapter_project", dev, ctypes.byref(shape.c()), code,
+            *args, ws, workspace.numel(), _stream(stream, dev))

@@ -616,6 +616,148 @@ int moe_get_tile_config(const moe_shape *s, int32_t gemm, moe_tile_entry *out)
     return MOE_OK;
 }
 
+// ---- the router, the rows to their experts and back, the adapters ----------
+
+static bool elem_type(int32_t dtype)
+{
+    return dtype == MOE_DT_BF16 || dtype == MOE_DT_F16 || dtype == MOE_DT_F32;
+}
+
+int moe_route(const moe_shape *s, int32_t dtype, const void *logits, int32_t renormalize,
+              int32_t *topk_ids, float *topk_w, void *stream)
+{
+    int rc = moe_check_shape(s);
+    if (rc != MOE_OK)
+        return rc;
+    if (!elem_type(dtype))
+        return MOE_EINVAL;
+    if (!moe::route_supported(*s))
+        return MOE_ENOTSUP;
+    if (s->T == 0)
+        return MOE_OK;
+    if (!logits || !topk_ids || !topk_w)
+        return MOE_EINVAL;
+    return hip_status(moe::launch_route(*s, dtype, renormalize != 0, logits, topk_ids, topk_w,
+                                        as_stream(stream)));
+}
+
+int moe_route_backward(const moe_shape *s, int32_t dtype, const void *logits,
+                       int32_t renormalize, const int32_t *topk_ids, const float *topk_w,
+                       const float *dtopk_w, void *dlogits, void *stream)
+{
+    int rc = moe_check_shape(s);
+    if (rc != MOE_OK)
+        return rc;
+    if (!elem_type(dtype))
+        return MOE_EINVAL;
+    if (!moe::route_supported(*s))
+        return MOE_ENOTSUP;
+    if (s->T == 0)
+        return MOE_OK;
+    if ((!logits && !renormalize) || !topk_ids || !topk_w || !dtopk_w || !dlogits)
+        return MOE_EINVAL;
+    return hip_status(moe::launch_route_backward(*s, dtype, renormalize != 0, logits, topk_ids,
+                                                 topk_w, dtopk_w, dlogits, as_stream(stream)));
+}
+
+// Checks shared by the four row entry points; *go is false for T = 0.
+static int rows_check(const moe_shape *s, int32_t dtype, bool *go)
+{
+    *go = false;
+    int rc = moe_check_shape(s);
+    if (rc != MOE_OK)
+        return rc;
+    if (!elem_type(dtype))
+        return MOE_EINVAL;
+    *go = s->T > 0;
+    return MOE_OK;
+}
+
+int moe_permute(const moe_shape *s, int32_t dtype, const void *x, const int32_t *route_row,
+                void *rows, void *stream)
+{
+    bool go;
+    int rc = rows_check(s, dtype, &go);
+    if (!go)
+        return rc;
+    if (!x || !route_row || !rows || !all_aligned16(x, rows))
+        return MOE_EINVAL;
+    return hip_status(moe::launch_permute(*s, dtype, x, route_row, rows, as_stream(stream)));
+}
+
+int moe_permute_backward(const moe_shape *s, int32_t dtype, const void *drows,
+                         const int32_t *route_row, void *dx, void *stream)
+{
+    return moe_unpermute(s, dtype, drows, nullptr, route_row, dx, stream);
+}
+
+int moe_unpermute(const moe_shape *s, int32_t dtype, const void *rows, const float *topk_w,
+                  const int32_t *route_row, void *out, void *stream)
+{
+    bool go;
+    int rc = rows_check(s, dtype, &go);
+    if (!go)
+        return rc;
+    if (!rows || !route_row || !out || !all_aligned16(rows, out))
+        return MOE_EINVAL;
+    return hip_status(
+        moe::launch_unpermute(*s, dtype, rows, topk_w, route_row, out, as_stream(stream)));
+}
+
+int moe_unpermute_backward(const moe_shape *s, int32_t dtype, const void *dout,
+                           const void *rows, const float *topk_w, const int32_t *route_row,
+                           void *drows, float *dtopk_w, void *stream)
+{
+    bool go;
+    int rc = rows_check(s, dtype, &go);
+    if (!go)
+        return rc;
+    if (!dout || !route_row || (!drows && !dtopk_w) || (dtopk_w && !rows) ||
+        !all_aligned16(dout, rows, drows))
+        return MOE_EINVAL;
+    return hip_status(moe::launch_unpermute_backward(*s, dtype, dout, rows, topk_w, route_row,
+                                                     drows, dtopk_w, as_stream(stream)));
+}
+
+int moe_adapter_check(const moe_adapter_shape *s)
+{
+    if (!s || s->T < 0 || s->H <= 0 || s->N <= 0 || s->L < 1 || s->rank < 1)
+        return MOE_EINVAL;
+    if (s->H % 128 != 0 || s->H > (1 << 17) || s->N % 8 != 0 || s->N > (1 << 20) ||
+        s->rank % 8 != 0 || s->rank > 256 || (long long)s->T * s->H >= (1ll << 32) ||
+        (long long)s->T * s->N >= (1ll << 32))
+        return MOE_ENOTSUP;
+    return MOE_OK;
+}
+
+size_t moe_adapter_workspace_size(const moe_adapter_shape *s)
+{
+    if (moe_adapter_check(s) != MOE_OK)
+        return 0;
+    return moe::adapter_workspace_bytes(*s);
+}
+
+int moe_adapter_project(const moe_adapter_shape *s, int32_t dtype, const void *x, const void *w,
+                        const void *base, const int32_t *adapter_ids, const void *a,
+                        const void *b, const float *scale, void *out, void *ws, size_t ws_bytes,
+                        void *stream)
+{
+    int rc = moe_adapter_check(s);
+    if (rc != MOE_OK)
+        return rc;
+    if (dtype != MOE_DT_BF16 && dtype != MOE_DT_F16)
+        return MOE_EINVAL;
+    if (s->T == 0)
+        return MOE_OK;
+    if (!x || !adapter_ids || !a || !b || !out || (w != nullptr) == (base != nullptr) ||
+        !all_aligned16(x, w, base, a, b, out))
+        return MOE_EINVAL;
+    if (!ws || ws_bytes < moe::adapter_workspace_bytes(*s) || ((uintptr_t)ws % kAlign) != 0)
+        return MOE_EWORKSPACE;
+    return hip_status(moe::launch_adapter_project(*s, dtype, x, w, base, adapter_ids, a, b, scale,
+                                                  out, ws, as_stream(stream)));
+}
+
 const char *moe_strerror(int code)
 {
     switch (code) {
@@ -625,7 +767,8 @@ const char *moe_strerror(int code)
         return "invalid argument";
     case MOE_ENOTSUP:
         return "shape not supported (H and I multiples of 128, K <= 8, E_local <= 512, "
-               "T*H and I*H below 2^32)";
+               "T*H and I*H below 2^32; router: E_total <= 1024; adapters: H a multiple of "
+               "128 up to 2^17, N of 8 up to 2^20, rank of 8 up to 256)";
     case MOE_EWORKSPACE:
         return "workspace missing, too small or not 256-byte aligned";
     case MOE_EHIP:

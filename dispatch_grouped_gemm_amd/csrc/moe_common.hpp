@@ -542,6 +542,27 @@ hipError_t launch_gemm2_stream(const moe_shape &s, const uint8_t *h, const uint8
                                const uint8_t *w2p, const uint8_t *w2ps, const YRows &y,
                                hipStream_t st);
 
+// The router, the rows to their experts and back, and the adapters
+// (arguments as the C ABI's; w null in the sums means weights of 1).
+bool route_supported(const moe_shape &s);
+hipError_t launch_route(const moe_shape &s, int dtype, bool renorm, const void *logits,
+                        int32_t *ids, float *w, hipStream_t st);
+hipError_t launch_route_backward(const moe_shape &s, int dtype, bool renorm, const void *logits,
+                                 const int32_t *ids, const float *w, const float *dw,
+                                 void *dlogits, hipStream_t st);
+hipError_t launch_permute(const moe_shape &s, int dtype, const void *x, const int32_t *route_row,
+                          void *rows, hipStream_t st);
+hipError_t launch_unpermute(const moe_shape &s, int dtype, const void *rows, const float *w,
+                            const int32_t *route_row, void *out, hipStream_t st);
+hipError_t launch_unpermute_backward(const moe_shape &s, int dtype, const void *dout,
+                                     const void *rows, const float *w, const int32_t *route_row,
+                                     void *drows, float *dw, hipStream_t st);
+size_t adapter_workspace_bytes(const moe_adapter_shape &s);
+hipError_t launch_adapter_project(const moe_adapter_shape &s, int dtype, const void *x,
+                                  const void *w, const void *base, const int32_t *ids,
+                                  const void *a, const void *b, const float *scale, void *out,
+                                  void *ws, hipStream_t st);
+
 int device_cu_count();
 
 } // namespace moe

@@ -1,0 +1,217 @@
+// Rows to their experts and back, with gradients, on the dispatch's route
+// table route_row[T*K] (the row of slot (t, k), or -1):
+//   permute             rows[route_row[t,k]] = x[t]
+//   permute_backward    dx[t] = sum_k drows[route_row[t,k]]
+//   unpermute           out[t] = sum_k w[t,k] rows[route_row[t,k]]
+//   unpermute_backward  drows[route_row[t,k]] = w[t,k] dout[t],
+//                       dw[t,k] = <dout[t], rows[route_row[t,k]]>
+// All four walk the tokens: a token's row is read or written once however
+// many experts it goes to, each of its expert rows once, and no two slots
+// share a row, so there are no atomics and every sum has a fixed order.
+// Sums are float32, k ascending, rounded once.  Bound by memory.
+#include "elem.hpp"
+
+namespace moe {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxK = 8;
+
+// A thread takes one 16-byte piece of a token's row and stores it K times.
+template <int DT>
+__global__ void __launch_bounds__(kThreads)
+permute_kernel(int T, int H, int K, long R, const void *__restrict__ x,
+               const int32_t *__restrict__ route_row, void *__restrict__ rows)
+{
+    const int pieces = H / Elem<DT>::kVec;
+    const long i = (long)blockIdx.x * kThreads + threadIdx.x;
+    if (i >= (long)T * pieces)
+        return;
+    const int t = (int)(i / pieces);
+    const int p = (int)(i - (long)t * pieces);
+    const uint4 v = static_cast<const uint4 *>(x)[i];
+    for (int k = 0; k < K; ++k) {
+        const int row = checked_row(route_row[(size_t)t * K + k], R);
+        if (row >= 0)
+            static_cast<uint4 *>(rows)[(size_t)row * pieces + p] = v;
+    }
+}
+
+// A thread takes one 16-byte piece of a token's row: its slots' pieces all
+// loaded, then summed in ascending k.
+template <int DT, bool kWeights>
+__global__ void __launch_bounds__(kThreads)
+unpermute_kernel(int T, int H, int K, long R, const void *__restrict__ rows,
+                 const float *__restrict__ w, const int32_t *__restrict__ route_row,
+                 void *__restrict__ out)
+{
+#pragma clang fp contract(off)
+    constexpr int V = Elem<DT>::kVec;
+    const int pieces = H / V;
+    const long i = (long)blockIdx.x * kThreads + threadIdx.x;
+    if (i >= (long)T * pieces)
+        return;
+    const int t = (int)(i / pieces);
+    const int p = (int)(i - (long)t * pieces);
+    int row[kMaxK];
+    uint4 q[kMaxK];
+#pragma unroll
+    for (int k = 0; k < kMaxK; ++k)
+        row[k] = k < K ? checked_row(route_row[(size_t)t * K + k], R) : -1;
+#pragma unroll
+    for (int k = 0; k < kMaxK; ++k)
+        if (row[k] >= 0)
+            q[k] = static_cast<const uint4 *>(rows)[(size_t)row[k] * pieces + p];
+    float acc[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+        acc[j] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kMaxK; ++k) {
+        if (row[k] < 0)
+            continue;
+        const float wk = kWeights ? w[(size_t)t * K + k] : 1.0f;
+        float f[V];
+        Elem<DT>::unpack(q[k], f);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float pr = kWeights ? wk * f[j] : f[j];
+            acc[j] = acc[j] + pr;
+        }
+    }
+    static_cast<uint4 *>(out)[i] = Elem<DT>::pack(acc);
+}
+
+// A workgroup takes one token: its dout row read once, its expert rows read
+// for the weights' gradients (kDots) and their gradients written (kRows).
+template <int DT, bool kRows, bool kDots, bool kWeights>
+__global__ void __launch_bounds__(kThreads)
+unpermute_backward_kernel(int T, int H, int K, long R, const void *__restrict__ dout,
+                          const void *__restrict__ rows, const float *__restrict__ w,
+                          const int32_t *__restrict__ route_row, void *__restrict__ drows,
+                          float *__restrict__ dw)
+{
+    constexpr int V = Elem<DT>::kVec;
+    __shared__ float part[kThreads / 64][kMaxK];
+    const int pieces = H / V;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    for (int t = blockIdx.x; t < T; t += gridDim.x) {
+        int row[kMaxK];
+        float wk[kMaxK], dot[kMaxK];
+#pragma unroll
+        for (int k = 0; k < kMaxK; ++k) {
+            row[k] = k < K ? checked_row(route_row[(size_t)t * K + k], R) : -1;
+            wk[k] = kWeights && row[k] >= 0 ? w[(size_t)t * K + k] : 1.0f;
+            dot[k] = 0.0f;
+        }
+        for (int p = threadIdx.x; p < pieces; p += kThreads) {
+            float g[V];
+            Elem<DT>::unpack(static_cast<const uint4 *>(dout)[(size_t)t * pieces + p], g);
+#pragma unroll
+            for (int k = 0; k < kMaxK; ++k) {
+                if (row[k] < 0)
+                    continue;
+                const size_t at = (size_t)row[k] * pieces + p;
+                if (kDots) {
+                    float f[V];
+                    Elem<DT>::unpack(static_cast<const uint4 *>(rows)[at], f);
+#pragma unroll
+                    for (int j = 0; j < V; ++j)
+                        dot[k] += g[j] * f[j];
+                }
+                if (kRows) {
+                    float d[V];
+#pragma unroll
+                    for (int j = 0; j < V; ++j)
+                        d[j] = kWeights ? wk[k] * g[j] : g[j];
+                    static_cast<uint4 *>(drows)[at] = Elem<DT>::pack(d);
+                }
+            }
+        }
+        if (!kDots)
+            continue;
+#pragma unroll
+        for (int k = 0; k < kMaxK; ++k) {
+            float v = dot[k];
+#pragma unroll
+            for (int d = 32; d; d >>= 1)
+                v += __shfl_xor(v, d);
+            if (lane == 0)
+                part[wave][k] = v;
+        }
+        __syncthreads();
+        if ((int)threadIdx.x < K) {
+            float v = 0.0f;
+#pragma unroll
+            for (int u = 0; u < kThreads / 64; ++u)
+                v += part[u][threadIdx.x];
+            dw[(size_t)t * K + threadIdx.x] = v;
+        }
+        __syncthreads();
+    }
+}
+
+unsigned piece_grid(const moe_shape &s, int dtype)
+{
+    const long n = (long)s.T * (s.H * (long)elem_bytes(dtype) / 16);
+    return (unsigned)((n + kThreads - 1) / kThreads);
+}
+
+} // namespace
+
+hipError_t launch_permute(const moe_shape &s, int dtype, const void *x, const int32_t *route_row,
+                          void *rows, hipStream_t st)
+{
+    const long R = moe_row_capacity(&s);
+    const unsigned grid = piece_grid(s, dtype);
+    if (dtype == MOE_DT_F32)
+        permute_kernel<MOE_DT_F32><<<grid, kThreads, 0, st>>>(s.T, s.H, s.K, R, x, route_row,
+                                                              rows);
+    else // a copy: 16-bit types alike
+        permute_kernel<MOE_DT_BF16><<<grid, kThreads, 0, st>>>(s.T, s.H, s.K, R, x, route_row,
+                                                               rows);
+    return hipGetLastError();
+}
+
+hipError_t launch_unpermute(const moe_shape &s, int dtype, const void *rows, const float *w,
+                            const int32_t *route_row, void *out, hipStream_t st)
+{
+    const long R = moe_row_capacity(&s);
+    const unsigned grid = piece_grid(s, dtype);
+    with_elem(dtype, [&](auto dt) {
+        constexpr int DT = decltype(dt)::value;
+        if (w)
+            unpermute_kernel<DT, true>
+                <<<grid, kThreads, 0, st>>>(s.T, s.H, s.K, R, rows, w, route_row, out);
+        else
+            unpermute_kernel<DT, false>
+                <<<grid, kThreads, 0, st>>>(s.T, s.H, s.K, R, rows, w, route_row, out);
+    });
+    return hipGetLastError();
+}
+
+hipError_t launch_unpermute_backward(const moe_shape &s, int dtype, const void *dout,
+                                     const void *rows, const float *w, const int32_t *route_row,
+                                     void *drows, float *dw, hipStream_t st)
+{
+    const long R = moe_row_capacity(&s);
+    with_elem(dtype, [&](auto dt) {
+        constexpr int DT = decltype(dt)::value;
+        const auto go = [&](auto kernel) {
+            kernel<<<min(s.T, 1 << 20), kThreads, 0, st>>>(s.T, s.H, s.K, R, dout, rows, w,
+                                                           route_row, drows, dw);
+        };
+        if (drows && dw)
+            go(w ? unpermute_backward_kernel<DT, true, true, true>
+                 : unpermute_backward_kernel<DT, true, true, false>);
+        else if (drows)
+            go(w ? unpermute_backward_kernel<DT, true, false, true>
+                 : unpermute_backward_kernel<DT, true, false, false>);
+        else
+            go(unpermute_backward_kernel<DT, false, true, false>);
+    });
+    return hipGetLastError();
+}
+
+} // namespace moe

@@ -467,6 +467,105 @@ int moe_set_tile_table(const moe_tile_entry *entries, int32_t n);
  * the register-streaming kernels serve the shape. */
 int moe_get_tile_config(const moe_shape *shape, int32_t gemm, moe_tile_entry *out);
 
+/*
+ * Around the layer: the router before the dispatch, the token rows sorted to
+ * their experts' rows and back with gradients, and a shared projection with
+ * low-rank adapters.  Element types of these entry points:
+ */
+#define MOE_DT_BF16 0
+#define MOE_DT_F16 1
+#define MOE_DT_F32 2
+
+/*
+ * The router: logits[T, E_total] (dtype any of the three) to topk_ids[T, K]
+ * and topk_w[T, K] as the dispatch and the combine take them.  Per token the
+ * eligible logits are those above -inf (a NaN is not); the K largest are
+ * chosen, equal ones by the lower id, and written in falling order with
+ *   w_k = exp(l_k - m) / sum_j exp(l_j - m),  m the largest logit,
+ * summed in float32 over the chosen (renormalize != 0) or over every
+ * eligible expert.  Logits equal to m count 1, also at m = +inf.  Where fewer
+ * than K are eligible the remaining slots get id -1 and weight 0.
+ * MOE_ENOTSUP for E_total above 1024.  H, I, the expert range and the
+ * dispatch mode of the shape are checked and not used.  T = 0 is a no-op.
+ */
+int moe_route(const moe_shape *shape, int32_t dtype, const void *logits, int32_t renormalize,
+              int32_t *topk_ids, float *topk_w, void *stream);
+
+/*
+ * Its gradient: dlogits[T, E_total] (every element written) from dtopk_w[T, K],
+ * with the ids and weights moe_route wrote,
+ *   dlogits_e = p_e (g_e - sum_k w_k g_k),
+ * g_e the dtopk_w of the slot that chose e (0 for the rest), p_e the weight of
+ * a chosen expert and 0 elsewhere (renormalize != 0; logits may then be NULL),
+ * or the softmax over the eligible logits.  Slots whose id is outside
+ * [0, E_total) are left out, whatever their weight and gradient hold.
+ */
+int moe_route_backward(const moe_shape *shape, int32_t dtype, const void *logits,
+                       int32_t renormalize, const int32_t *topk_ids, const float *topk_w,
+                       const float *dtopk_w, void *dlogits, void *stream);
+
+/*
+ * Token rows to their experts' rows and back, on the route_row table of
+ * moe_dispatch (either mode); R = moe_row_capacity(shape), x, out and their
+ * gradients [T, H], rows and their gradient [R, H], all of one dtype:
+ *   moe_permute            rows[route_row[t,k]] = x[t]
+ *   moe_permute_backward   dx[t] = sum_k drows[route_row[t,k]]
+ *   moe_unpermute          out[t] = sum_k topk_w[t,k] rows[route_row[t,k]]
+ *   moe_unpermute_backward drows[route_row[t,k]] = topk_w[t,k] dout[t],
+ *                          dtopk_w[t,k] = <dout[t], rows[route_row[t,k]]>
+ * Slots outside [0, R) (the dispatch's -1) are skipped, and their dtopk_w is
+ * 0; a token without any gets a +0 row.  Sums are float32 in ascending k,
+ * rounded once (with bf16 rows moe_unpermute gives moe_combine's bits).
+ * topk_w NULL means weights of 1.  moe_unpermute_backward writes drows or
+ * dtopk_w or both (one may be NULL; rows is read only for dtopk_w).  Rows
+ * that hold no route are neither read nor written.  Buffers do not overlap.
+ * x, rows, out and their gradients start on 16-byte boundaries.  T = 0 is a
+ * no-op.
+ */
+int moe_permute(const moe_shape *shape, int32_t dtype, const void *x, const int32_t *route_row,
+                void *rows, void *stream);
+int moe_permute_backward(const moe_shape *shape, int32_t dtype, const void *drows,
+                         const int32_t *route_row, void *dx, void *stream);
+int moe_unpermute(const moe_shape *shape, int32_t dtype, const void *rows, const float *topk_w,
+                  const int32_t *route_row, void *out, void *stream);
+int moe_unpermute_backward(const moe_shape *shape, int32_t dtype, const void *dout,
+                           const void *rows, const float *topk_w, const int32_t *route_row,
+                           void *drows, float *dtopk_w, void *stream);
+
+/*
+ * A shared projection with low-rank adapters of many requests:
+ *   out[t] = base[t] + scale[l] (x[t] A_l^T) B_l^T,  l = adapter_ids[t],
+ * x [T, H], A [L, rank, H], B [L, N, rank], scale float [L] (NULL: 1), out
+ * [T, N]; base[t] is x[t] W^T with the shared weight W [N, H], or the rows
+ * base [T, N] of a projection computed elsewhere (exactly one of w and base;
+ * base may be out itself, otherwise buffers do not overlap).  A row whose id
+ * is outside [0, L) (-1) has no adapter: its out is base[t].  Rows of one
+ * adapter need not be neighbours, though they are faster so.  An adapter of
+ * lower rank is padded with zeros.  dtype MOE_DT_BF16 or MOE_DT_F16; every
+ * sum in float32, x A^T kept to float32 precision, out rounded once.
+ * workspace: moe_adapter_workspace_size bytes of scratch, 256-byte aligned;
+ * calls that overlap on one workspace race.  The other buffers are 16-byte
+ * aligned (adapter_ids and scale 4-byte).
+ */
+typedef struct moe_adapter_shape {
+    int32_t T;    /* rows (0 is a valid no-op); T*H and T*N below 2^32 */
+    int32_t H;    /* input size, a multiple of 128, at most 2^17 */
+    int32_t N;    /* output size, a multiple of 8, at most 2^20 */
+    int32_t L;    /* adapters, at least 1 */
+    int32_t rank; /* a multiple of 8, at most 256 */
+} moe_adapter_shape;
+
+/* Check a shape; MOE_OK or the code a call with it would return. */
+int moe_adapter_check(const moe_adapter_shape *shape);
+
+/* Scratch bytes of moe_adapter_project; 0 for a refused shape or T = 0. */
+size_t moe_adapter_workspace_size(const moe_adapter_shape *shape);
+
+int moe_adapter_project(const moe_adapter_shape *shape, int32_t dtype, const void *x,
+                        const void *w, const void *base, const int32_t *adapter_ids,
+                        const void *a, const void *b, const float *scale, void *out,
+                        void *workspace, size_t workspace_bytes, void *stream);
+
 /* Static description of a return code. */
 const char *moe_strerror(int code);
 

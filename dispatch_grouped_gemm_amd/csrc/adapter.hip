@@ -3,15 +3,16 @@
 // base = x W^T computed here, or given; a row of id -1 (or past the
 // adapters) has no second term.
 //
-// Two launches.  The first ("shrink") makes v[t] = x[t] A_l^T in float32.
-// The second computes x W^T in 16x16x32 MFMA tiles and, once a tile's sums
-// are complete, adds the adapters' term to them in registers ("expand"), so
-// out is written once and rounded once.
+// "Shrink" makes v[t] = x[t] A_l^T in float32.  "Project" computes x W^T in
+// MFMA tiles and, once a tile's sums are complete, adds the adapters' term
+// to them in registers ("expand"), so out is written once and rounded once.
 //
 // Rows come in any order.  Whoever owns a set of rows walks the different
-// ids among them: an adapter's product is formed for all the rows of the
-// set (the matrix instruction costs the same) and taken only where the id
+// ids among them: an adapter's product is formed for 16 rows at a time (the
+// matrix instruction costs the same for one) and taken only where the id
 // matches, so no row ever sees another adapter's values, infinite or NaN.
+// Past kFewRows rows, a first launch orders the rows by adapter, so that a
+// tile holds few of them; results do not depend on that order.
 //
 // v keeps float32's precision through the matrix instruction: it enters as
 // the sum of two 16-bit values, hi = round(v) and lo = round(v - hi).  fp16
@@ -23,14 +24,15 @@ namespace moe {
 
 namespace {
 
-constexpr int kThreads = 256;
-
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 
 struct AShape {
     int T, H, N, L, r;
 };
+
+constexpr int kFewRows = 256;       // rows shrunk without an order
+constexpr int kOrderKeys = 1 << 13; // adapters the ordering launch counts in LDS
 
 // D(16x16) += A(16x32) B(32x16): lane l holds A's row / B's column l mod 16
 // at k = 8 (l div 16) .. + 7, and D's column l mod 16 at rows
@@ -46,6 +48,19 @@ __device__ __forceinline__ v4f mfma(const uint4 &a, const uint4 &b, v4f c)
                                                       __builtin_bit_cast(v8h, b), c, 0, 0, 0);
 }
 
+// This thread's wavefront in the workgroup, in a scalar register: the matrix
+// instruction does not look at which lanes are active, so every branch
+// around one has to be a scalar branch.
+__device__ __forceinline__ int wave_of()
+{
+    return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+}
+
+__device__ __forceinline__ const uint4 &piece(const uint16_t *p)
+{
+    return *reinterpret_cast<const uint4 *>(p);
+}
+
 // v as hi + lo, both 16-bit.
 template <int DT>
 __device__ __forceinline__ void split8(const float *v, uint4 &hi, uint4 &lo)
@@ -59,173 +74,742 @@ __device__ __forceinline__ void split8(const float *v, uint4 &hi, uint4 &lo)
     lo = Elem<DT>::pack(d);
 }
 
-// ids of the 16 rows that lanes 0..15 (and their copies) hold; -1 where a
-// row has no adapter.
-__device__ __forceinline__ int adapter_of(const AShape &s, const int32_t *ids, long t)
+// The row at place i (order: the rows sorted by adapter, or null), clamped
+// to the last place, and its adapter; -1 where there is none.
+struct Row {
+    int t, id;
+};
+__device__ __forceinline__ Row row_at(const AShape &s, const int32_t *__restrict__ order,
+                                      const int32_t *__restrict__ ids, long i)
 {
-    const int id = t < s.T ? ids[t] : -1;
-    return (unsigned)id < (unsigned)s.L ? id : -1;
+    const long c = i < s.T ? i : s.T - 1;
+    const int t = order ? order[c] : (int)c;
+    const int id = ids[t];
+    return Row{t, i < s.T && (unsigned)id < (unsigned)s.L ? id : -1};
 }
 
-// One wavefront: 16 rows x 16 of the rank over one part of H.
-template <int DT>
-__global__ void __launch_bounds__(64)
-shrink_kernel(AShape s, const uint16_t *__restrict__ x, const int32_t *__restrict__ ids,
-              const uint16_t *__restrict__ a, float *__restrict__ v)
+// Column of the output that row i (0..15) of block f (of NF) of 16 weight
+// rows stands for, within the 16 NF columns of a wavefront: a lane then
+// holds 4 NF neighbouring columns of its token.
+template <int NF>
+__device__ __forceinline__ int column_of(int f, int i)
 {
-    const int lane = threadIdx.x;
-    const long t = (long)blockIdx.x * 16 + (lane & 15);
-    const int j = blockIdx.y * 16 + (lane & 15);
-    const int id = adapter_of(s, ids, t);
-    const uint16_t *xr = x + (size_t)(t < s.T ? t : s.T - 1) * s.H + 8 * (lane >> 4);
-    uint64_t todo = __ballot(id >= 0 && lane < 16);
-    while (todo) {
-        const int g = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
-        todo &= ~__ballot(id == g);
-        const uint16_t *ar =
-            a + ((size_t)g * s.r + (j < s.r ? j : s.r - 1)) * s.H + 8 * (lane >> 4);
-        v4f c = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int h = 0; h < s.H; h += 32)
-            c = mfma<DT>(*reinterpret_cast<const uint4 *>(ar + h),
-                         *reinterpret_cast<const uint4 *>(xr + h), c);
-        const int j0 = blockIdx.y * 16 + 4 * (lane >> 4);
-        if (id == g && j0 < s.r)
-            *reinterpret_cast<v4f *>(v + (size_t)t * s.r + j0) = c;
+    return 4 * NF * (i >> 2) + 4 * f + (i & 3);
+}
+
+// ---------------------------------------------------------------------------
+// Order: the rows by adapter, those without one last, as a list of rows.
+// One workgroup: a histogram in LDS, its scan, and a claim of a place per
+// row (places inside an adapter in whatever order the claims land).  A
+// wavefront whose rows share an adapter claims with one atomic.
+// ---------------------------------------------------------------------------
+constexpr int kOrderThreads = 1024;
+
+__global__ void __launch_bounds__(kOrderThreads)
+order_kernel(AShape s, const int32_t *__restrict__ ids, int32_t *__restrict__ order)
+{
+    extern __shared__ int count[]; // L + 1
+    __shared__ int wsum[kOrderThreads / 64];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int keys = s.L + 1;
+    for (int i = tid; i < keys; i += kOrderThreads)
+        count[i] = 0;
+    __syncthreads();
+    // claims one place of key k for every lane with in set
+    const auto claim = [&](int k, bool in) -> int {
+        const uint64_t act = __ballot(in);
+        if (!act)
+            return 0;
+        const int first = __builtin_ctzll(act);
+        const int k0 = __builtin_amdgcn_readlane(k, first);
+        if (__ballot(in && k != k0) == 0) {
+            int at = 0;
+            if (lane == first)
+                at = atomicAdd(&count[k0], __builtin_popcountll(act));
+            at = __builtin_amdgcn_readlane(at, first);
+            return at + __builtin_popcountll(act & ((1ull << lane) - 1));
+        }
+        return in ? atomicAdd(&count[k], 1) : 0;
+    };
+    const auto key = [&](long t) {
+        const int id = ids[t];
+        return (unsigned)id < (unsigned)s.L ? id : s.L;
+    };
+    const long rounds = ((long)s.T + kOrderThreads - 1) / kOrderThreads;
+    for (long q = 0; q < rounds; ++q) {
+        const long t = q * kOrderThreads + tid;
+        const bool in = t < s.T;
+        claim(in ? key(t) : 0, in);
+    }
+    __syncthreads();
+    // exclusive scan of the counts, per keys of each thread
+    const int per = (keys + kOrderThreads - 1) / kOrderThreads;
+    const int b = min(keys, tid * per), e = min(keys, b + per);
+    int sum = 0;
+    for (int i = b; i < e; ++i)
+        sum += count[i];
+    int inc = sum;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(inc, d);
+        if (lane >= d)
+            inc += o;
+    }
+    if (lane == 63)
+        wsum[wave] = inc;
+    __syncthreads();
+    int run = inc - sum;
+    for (int w = 0; w < wave; ++w)
+        run += wsum[w];
+    for (int i = b; i < e; ++i) {
+        const int c = count[i];
+        count[i] = run;
+        run += c;
+    }
+    __syncthreads();
+    for (long q = 0; q < rounds; ++q) {
+        const long t = q * kOrderThreads + tid;
+        const bool in = t < s.T;
+        const int at = claim(in ? key(t) : 0, in);
+        if (in)
+            order[at] = (int)t;
     }
 }
 
-// Adds the adapters' term of 16 rows (lane's row: l mod 16, its id) to the
-// sums of NF blocks of 16 columns from n0.
+// ---------------------------------------------------------------------------
+// Shrink.  Both forms: a workgroup's wavefronts split H, each summing its
+// part for all of the workgroup's rows and rank values straight from global
+// memory, and the parts meet in LDS in a fixed order.
+// ---------------------------------------------------------------------------
+
+// The sums over one wavefront's part of H: row pieces xr (per 16 rows) with
+// rows of A, J blocks of 16.  Steps of 64 values: 128 bytes of every row.
+template <int DT, int F, int J, int NW>
+__device__ __forceinline__ void shrink_part(int H, int wave, const uint16_t *const *xr,
+                                            const uint16_t *const *ar, const bool *live,
+                                            v4f (*acc)[J])
+{
+    constexpr int D = F * J > 2 ? 2 : 4; // steps in flight
+    const int steps = H / 64;
+    for (int i0 = wave; i0 < steps; i0 += NW * D) {
+        uint4 xq[D][F][2], aq[D][J][2];
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            const int h = 64 * min(i0 + d * NW, steps - 1);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+                    aq[d][j][k] = piece(ar[j] + h + 32 * k);
+#pragma unroll
+                for (int f = 0; f < F; ++f)
+                    if (live[f])
+                        xq[d][f][k] = piece(xr[f] + h + 32 * k);
+            }
+        }
+#pragma unroll
+        for (int d = 0; d < D; ++d)
+            if (i0 + d * NW < steps)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int f = 0; f < F; ++f)
+                        if (live[f])
+#pragma unroll
+                            for (int j = 0; j < J; ++j)
+                                acc[f][j] = mfma<DT>(aq[d][j][k], xq[d][f][k], acc[f][j]);
+    }
+}
+
+// Few rows: workgroup (t, block of 16 of the rank).  Row t works for the
+// next 16 rows of its adapter if the rows before it of the same adapter
+// fill whole sixteens, else it has nothing to do: every adapter's A is read
+// by as few workgroups as its rows allow, in whatever order they come.
+constexpr int kFewWaves = 16;
+
+template <int DT>
+__global__ void __launch_bounds__(64 * kFewWaves)
+shrink_few_kernel(AShape s, const uint16_t *__restrict__ x, const int32_t *__restrict__ ids,
+                  const uint16_t *__restrict__ a, float *__restrict__ v)
+{
+    __shared__ uint64_t mask[kFewRows / 64];
+    __shared__ int member[16];
+    __shared__ v4f part[kFewWaves][64];
+    const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = wave_of();
+    const int id = ids[t];
+    if ((unsigned)id >= (unsigned)s.L)
+        return;
+    bool same = false;
+    if (tid < kFewRows) {
+        same = tid < s.T && ids[tid] == id;
+        const uint64_t m = __ballot(same);
+        if (lane == 0)
+            mask[wave] = m;
+    }
+    if (tid < 16)
+        member[tid] = -1;
+    __syncthreads();
+    // rows of this adapter before row i
+    const auto before = [&](int i) {
+        int n = 0;
+        for (int w = 0; w < kFewRows / 64; ++w) {
+            const int b = i - 64 * w;
+            if (b > 0)
+                n += __builtin_popcountll(b >= 64 ? mask[w] : mask[w] & ((1ull << b) - 1));
+        }
+        return n;
+    };
+    const int first = before(t);
+    if (first % 16)
+        return;
+    if (same) {
+        const int at = before(tid) - first;
+        if (at >= 0 && at < 16)
+            member[at] = tid;
+    }
+    __syncthreads();
+    const int row = member[lane & 15];
+    const int j = blockIdx.y * 16 + (lane & 15);
+    const uint16_t *xr[1] = {x + (size_t)(row < 0 ? t : row) * s.H + 8 * (lane >> 4)};
+    const uint16_t *ar[1] = {a + ((size_t)id * s.r + min(j, s.r - 1)) * s.H + 8 * (lane >> 4)};
+    const bool live[1] = {true};
+    v4f acc[1][1] = {{v4f{0.0f, 0.0f, 0.0f, 0.0f}}};
+    shrink_part<DT, 1, 1, kFewWaves>(s.H, wave, xr, ar, live, acc);
+    part[wave][lane] = acc[0][0];
+    __syncthreads();
+    const int j0 = blockIdx.y * 16 + 4 * (lane >> 4);
+    if (wave == 0 && row >= 0 && j0 < s.r) {
+        v4f sum = part[0][lane];
+        for (int w = 1; w < kFewWaves; ++w)
+            sum += part[w][lane];
+        *reinterpret_cast<v4f *>(v + (size_t)row * s.r + j0) = sum;
+    }
+}
+
+// Many rows, ordered: workgroup (16 F places, 16 J of the rank).
+constexpr int kManyWaves = 8;
+
+template <int DT, int F, int J>
+__global__ void __launch_bounds__(64 * kManyWaves)
+shrink_many_kernel(AShape s, const uint16_t *__restrict__ x, const int32_t *__restrict__ ids,
+                   const int32_t *__restrict__ order, const uint16_t *__restrict__ a,
+                   float *__restrict__ v)
+{
+    __shared__ v4f part[kManyWaves][F * J][64];
+    const int lane = threadIdx.x & 63, wave = wave_of();
+    Row row[F];
+    const uint16_t *xr[F];
+    uint32_t todo[F];
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+        row[f] = row_at(s, order, ids, (long)blockIdx.x * 16 * F + 16 * f + (lane & 15));
+        xr[f] = x + (size_t)row[f].t * s.H + 8 * (lane >> 4);
+        todo[f] = (uint32_t)__ballot(row[f].id >= 0) & 0xffffu;
+    }
+    while (true) {
+        int g = -1;
+#pragma unroll
+        for (int f = F - 1; f >= 0; --f)
+            if (todo[f])
+                g = __builtin_amdgcn_readlane(row[f].id, __builtin_ctz(todo[f]));
+        if (g < 0)
+            return;
+        bool live[F];
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+            const uint32_t m = (uint32_t)__ballot(row[f].id == g) & 0xffffu;
+            live[f] = m != 0;
+            todo[f] &= ~m;
+        }
+        const uint16_t *ar[J];
+        v4f acc[F][J];
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int at = (blockIdx.y * J + j) * 16 + (lane & 15);
+            ar[j] = a + ((size_t)g * s.r + min(at, s.r - 1)) * s.H + 8 * (lane >> 4);
+#pragma unroll
+            for (int f = 0; f < F; ++f)
+                acc[f][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+        shrink_part<DT, F, J, kManyWaves>(s.H, wave, xr, ar, live, acc);
+#pragma unroll
+        for (int f = 0; f < F; ++f)
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                part[wave][f * J + j][lane] = acc[f][j];
+        __syncthreads();
+#pragma unroll
+        for (int f = 0; f < F; ++f)
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                if ((f * J + j) % kManyWaves != wave)
+                    continue;
+                const int j0 = (blockIdx.y * J + j) * 16 + 4 * (lane >> 4);
+                if (row[f].id == g && j0 < s.r) {
+                    v4f sum = part[0][f * J + j][lane];
+                    for (int w = 1; w < kManyWaves; ++w)
+                        sum += part[w][f * J + j][lane];
+                    *reinterpret_cast<v4f *>(v + (size_t)row[f].t * s.r + j0) = sum;
+                }
+            }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Expand: adds the adapters' term of 16 rows (the lane's: row) to the sums of
+// 16 NF columns from n0 (in column_of's order).
+// ---------------------------------------------------------------------------
 template <int DT, int NF>
 __device__ __forceinline__ void expand(const AShape &s, const float *__restrict__ v,
                                        const uint16_t *__restrict__ b,
-                                       const float *__restrict__ scale, long t, int id, int n0,
+                                       const float *__restrict__ scale, const Row &row, int n0,
                                        v4f *acc)
 {
     const int lane = threadIdx.x & 63;
     const int k0 = 8 * (lane >> 4);
-    const float *vr = v + (size_t)t * s.r;
+    uint32_t todo = (uint32_t)__ballot(row.id >= 0) & 0xffffu;
+    if (!todo)
+        return;
+    const float *vr = v + (size_t)row.t * s.r + k0;
     int ex = 0;
     if constexpr (DT == MOE_DT_F16) {
-        float m = 0.0f;
-        if (id >= 0)
-            for (int k = k0; k < s.r; k += 32)
+        float top = 0.0f;
+        if (row.id >= 0)
+            for (int k = 0; k + k0 < s.r; k += 32)
                 for (int i = 0; i < 8; ++i)
-                    m = fmaxf(m, fabsf(vr[k + i]));
-        m = fmaxf(m, __shfl_xor(m, 16));
-        m = fmaxf(m, __shfl_xor(m, 32));
-        if (m > 0.0f && m < INFINITY)
-            (void)frexpf(m, &ex);
+                    top = fmaxf(top, fabsf(vr[k + i]));
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        if (top > 0.0f && top < INFINITY)
+            (void)frexpf(top, &ex);
     }
-    const float sc = id < 0 ? 0.0f : scale ? scale[id] : 1.0f;
-    uint64_t todo = __ballot(id >= 0 && lane < 16);
-    while (todo) {
-        const int g = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
-        todo &= ~__ballot(id == g);
+    size_t col[NF];
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+        col[f] = (size_t)min(n0 + column_of<NF>(f, lane & 15), s.N - 1) * s.r + k0;
+    do {
+        const int g = __builtin_amdgcn_readlane(row.id, __builtin_ctz(todo));
+        const bool mine = row.id == g;
+        todo &= ~(uint32_t)__ballot(mine);
+        const uint16_t *bg = b + (size_t)g * s.N * s.r;
+        const float sc = scale ? scale[g] : 1.0f;
         v4f d[NF];
 #pragma unroll
         for (int f = 0; f < NF; ++f)
             d[f] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
         for (int k = 0; k < s.r; k += 32) {
-            const bool in = k + k0 < s.r;
+            const bool there = k + k0 < s.r;
             float f8[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                f8[i] = in && id == g ? vr[k + k0 + i] : 0.0f;
-                if constexpr (DT == MOE_DT_F16)
-                    f8[i] = ldexpf(f8[i], -ex);
+            for (int i = 0; i < 8; ++i)
+                f8[i] = 0.0f;
+            if (there && mine) {
+                const v4f v0 = *reinterpret_cast<const v4f *>(vr + k);
+                const v4f v1 = *reinterpret_cast<const v4f *>(vr + k + 4);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    f8[i] = DT == MOE_DT_F16 ? ldexpf(v0[i], -ex) : v0[i];
+                    f8[i + 4] = DT == MOE_DT_F16 ? ldexpf(v1[i], -ex) : v1[i];
+                }
             }
             uint4 hi, lo;
             split8<DT>(f8, hi, lo);
 #pragma unroll
             for (int f = 0; f < NF; ++f) {
-                const int n = min(n0 + 16 * f + (lane & 15), s.N - 1);
-                uint4 bq = {0, 0, 0, 0};
-                if (in)
-                    bq = *reinterpret_cast<const uint4 *>(b + ((size_t)g * s.N + n) * s.r + k +
-                                                          k0);
+                const uint4 bq = there ? piece(bg + col[f] + k) : uint4{0, 0, 0, 0};
                 d[f] = mfma<DT>(bq, hi, d[f]);
                 d[f] = mfma<DT>(bq, lo, d[f]);
             }
         }
-        if (id == g)
+        if (mine)
 #pragma unroll
             for (int f = 0; f < NF; ++f)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    acc[f][i] += sc * ldexpf(d[f][i], ex);
-    }
+                    acc[f][i] += sc * (DT == MOE_DT_F16 ? ldexpf(d[f][i], ex) : d[f][i]);
+    } while (todo);
 }
 
-// Four wavefronts: 64 rows x 64 columns, each wavefront 16 rows.
-template <int DT>
-__global__ void __launch_bounds__(kThreads)
-project_kernel(AShape s, const uint16_t *__restrict__ x, const uint16_t *__restrict__ w,
-               const uint16_t *base, const int32_t *__restrict__ ids,
-               const uint16_t *__restrict__ b, const float *__restrict__ scale,
-               const float *__restrict__ v, uint16_t *out)
+// The 4 NF neighbouring columns of one row that a lane holds, rounded and
+// stored (or the base's values loaded): columns from n, in pieces of 8 (N is
+// a multiple of 8; NF = 1 has pieces of 4).
+template <int DT, int NF>
+__device__ __forceinline__ void store_cols(const AShape &s, uint16_t *out, int t, int n,
+                                           const v4f *acc)
 {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const long t0 = (long)blockIdx.x * 64 + wave * 16;
-    if (t0 >= s.T)
-        return;
-    const long t = t0 + (lane & 15);
-    const int n0 = blockIdx.y * 64;
-    const int id = adapter_of(s, ids, t);
-    v4f acc[4];
-#pragma unroll
-    for (int f = 0; f < 4; ++f)
-        acc[f] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    if (w) {
-        const uint16_t *xr = x + (size_t)(t < s.T ? t : s.T - 1) * s.H + 8 * (lane >> 4);
-        const uint16_t *wr[4];
-#pragma unroll
-        for (int f = 0; f < 4; ++f)
-            wr[f] = w + (size_t)min(n0 + 16 * f + (lane & 15), s.N - 1) * s.H + 8 * (lane >> 4);
-        for (int h = 0; h < s.H; h += 32) {
-            const uint4 xq = *reinterpret_cast<const uint4 *>(xr + h);
-#pragma unroll
-            for (int f = 0; f < 4; ++f)
-                acc[f] = mfma<DT>(*reinterpret_cast<const uint4 *>(wr[f] + h), xq, acc[f]);
-        }
-    }
-    if (!w && t < s.T)
-#pragma unroll
-        for (int f = 0; f < 4; ++f) {
-            const int n = n0 + 16 * f + 4 * (lane >> 4);
-            if (n < s.N)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    acc[f][i] = Elem<DT>::load(base + (size_t)t * s.N + n + i);
-        }
-    expand<DT, 4>(s, v, b, scale, t < s.T ? t : s.T - 1, id, n0, acc);
-    if (t >= s.T)
-        return;
-#pragma unroll
-    for (int f = 0; f < 4; ++f) {
-        const int n = n0 + 16 * f + 4 * (lane >> 4);
+    uint16_t *o = out + (size_t)t * s.N + n;
+    if constexpr (NF == 1) {
+        const float f[8] = {acc[0][0], acc[0][1], acc[0][2], acc[0][3], 0.0f, 0.0f, 0.0f, 0.0f};
+        const uint4 q = Elem<DT>::pack(f);
         if (n < s.N)
+            *reinterpret_cast<uint2 *>(o) = uint2{q.x, q.y};
+    } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                Elem<DT>::store(out + (size_t)t * s.N + n + i, acc[f][i]);
+        for (int p = 0; p < NF / 2; ++p) {
+            const v4f a = acc[2 * p], b = acc[2 * p + 1];
+            const float f[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+            if (n + 8 * p < s.N)
+                *reinterpret_cast<uint4 *>(o + 8 * p) = Elem<DT>::pack(f);
+        }
     }
 }
 
+// ---------------------------------------------------------------------------
+// Project, few rows: bound by reading W once.  A workgroup holds 16 MF rows
+// and 16 NF columns; its wavefronts split H (interleaved 128-byte pieces of
+// each row) and read W and x straight into registers, D steps in flight;
+// their sums meet in LDS in a fixed order, wavefront m finishing rows 16 m.
+// ---------------------------------------------------------------------------
+constexpr int kSkinnyWaves = 8;
+
+template <int DT, int MF, int NF>
+__global__ void __launch_bounds__(64 * kSkinnyWaves)
+project_skinny_kernel(AShape s, const uint16_t *__restrict__ x, const uint16_t *__restrict__ w,
+                      const int32_t *__restrict__ ids, const uint16_t *__restrict__ b,
+                      const float *__restrict__ scale, const float *__restrict__ v,
+                      uint16_t *__restrict__ out)
+{
+    constexpr int D = MF >= 8 ? 2 : MF >= 4 ? 3 : MF >= 2 ? 4 : 6;
+    __shared__ v4f part[kSkinnyWaves][MF][NF][64];
+    const int lane = threadIdx.x & 63, wave = wave_of();
+    const long m0 = (long)blockIdx.y * 16 * MF;
+    const int n0 = blockIdx.x * 16 * NF;
+    const uint16_t *xr[MF], *wr[NF];
+#pragma unroll
+    for (int m = 0; m < MF; ++m)
+        xr[m] = x + (size_t)min(m0 + 16 * m + (lane & 15), (long)s.T - 1) * s.H + 8 * (lane >> 4);
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+        wr[f] = w + (size_t)min(n0 + column_of<NF>(f, lane & 15), s.N - 1) * s.H +
+                8 * (lane >> 4);
+    v4f acc[MF][NF];
+#pragma unroll
+    for (int m = 0; m < MF; ++m)
+#pragma unroll
+        for (int f = 0; f < NF; ++f)
+            acc[m][f] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    const int steps = s.H / 64;
+    uint4 wq[D][NF][2], xq[D][MF][2];
+    const auto load = [&](int d, int i) {
+        const int h = 64 * min(i, steps - 1);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+            for (int f = 0; f < NF; ++f)
+                wq[d][f][k] = piece(wr[f] + h + 32 * k);
+#pragma unroll
+            for (int m = 0; m < MF; ++m)
+                xq[d][m][k] = piece(xr[m] + h + 32 * k);
+        }
+    };
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+        load(d, wave + d * kSkinnyWaves);
+    for (int i0 = wave; i0 < steps; i0 += D * kSkinnyWaves) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            const int i = i0 + d * kSkinnyWaves;
+            if (i < steps)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int m = 0; m < MF; ++m)
+#pragma unroll
+                        for (int f = 0; f < NF; ++f)
+                            acc[m][f] = mfma<DT>(wq[d][f][k], xq[d][m][k], acc[m][f]);
+            load(d, i + D * kSkinnyWaves);
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < MF; ++m)
+#pragma unroll
+        for (int f = 0; f < NF; ++f)
+            part[wave][m][f][lane] = acc[m][f];
+    __syncthreads();
+    if (wave >= MF)
+        return;
+    const long i = m0 + 16 * wave + (lane & 15);
+    const Row row = row_at(s, nullptr, ids, i);
+    v4f sum[NF];
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+        sum[f] = part[0][wave][f][lane];
+#pragma unroll
+        for (int q = 1; q < kSkinnyWaves; ++q)
+            sum[f] += part[q][wave][f][lane];
+    }
+    expand<DT, NF>(s, v, b, scale, row, n0, sum);
+    if (i < s.T)
+        store_cols<DT, NF>(s, out, row.t, n0 + 4 * NF * (lane >> 4), sum);
+}
+
+// ---------------------------------------------------------------------------
+// Project, many rows: BM places x BN columns per workgroup, WM x WN
+// wavefronts of 16 MF rows x 64 columns.  K steps of 64 values (128 bytes a
+// row) go from global memory to LDS without registers, two stages; the
+// loads of step k + 1 are in flight while step k multiplies.  A row's eight
+// 16-byte pieces are stored at piece ^ (row / 2 mod 8): the 16 rows that one
+// operand read touches then lie in different banks.
+// ---------------------------------------------------------------------------
+template <int BM, int BN>
+struct Tile {
+    static constexpr int kRow = 128;                       // bytes of a row's step
+    static constexpr int kStage = (BM + BN) * kRow;
+};
+
+// Tile index of a workgroup: neighbouring workgroups run on different XCDs,
+// so each XCD gets a contiguous run of tiles; inside it, tiles go down 8 row
+// tiles before the next column tile, so the tiles that run together on an
+// XCD share rows and columns in its L2.
+__device__ __forceinline__ void tile_of(int b, int tm, int tn, int *im, int *in)
+{
+    const int total = tm * tn, xcd = b & 7, idx = b >> 3;
+    const int base = total >> 3, rem = total & 7;
+    const int q = xcd * base + min(xcd, rem) + idx;
+    const int group = q / (8 * tn), first = group * 8;
+    const int rows = min(8, tm - first), in_group = q - group * 8 * tn;
+    *im = first + in_group % rows;
+    *in = in_group / rows;
+}
+
+template <int DT, int BM, int BN, int WM, int WN>
+__global__ void __launch_bounds__(64 * WM * WN)
+project_tiled_kernel(AShape s, int tm, int tn, const uint16_t *__restrict__ x,
+                     const uint16_t *__restrict__ w, const int32_t *__restrict__ ids,
+                     const int32_t *__restrict__ order, const uint16_t *__restrict__ b,
+                     const float *__restrict__ scale, const float *__restrict__ v,
+                     uint16_t *__restrict__ out)
+{
+    constexpr int NW = WM * WN, MF = BM / WM / 16, NF = 4;
+    static_assert(BN == 64 * WN && (BM + BN) % (8 * NW) == 0, "wavefronts cover the tile");
+    constexpr int U = (BM + BN) / 8 / NW; // 1 KiB loads per wavefront and step
+    using Tl = Tile<BM, BN>;
+    __shared__ __align__(1024) uint8_t lds[2 * Tl::kStage];
+    const int lane = threadIdx.x & 63, wave = wave_of();
+    int im, in;
+    tile_of(blockIdx.x, tm, tn, &im, &in);
+    const long m0 = (long)im * BM;
+    const int n0 = in * BN;
+
+    // this lane's byte offsets: load u covers 8 LDS rows, x's first
+    uint32_t voff[U];
+    const uint8_t *base[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int row = (wave * U + u) * 8 + (lane >> 3);
+        const int at = ((lane & 7) ^ ((row >> 1) & 7)) * 16;
+        if ((wave * U + u) * 8 < BM) {
+            const long i = min(m0 + row, (long)s.T - 1);
+            const int t = order ? order[i] : (int)i;
+            voff[u] = (uint32_t)t * (uint32_t)(2 * s.H) + at;
+            base[u] = reinterpret_cast<const uint8_t *>(x);
+        } else {
+            const int rw = row - BM;
+            const int n = (rw & ~63) + column_of<NF>((rw >> 4) & 3, rw & 15);
+            const int nc = min(n, s.N - 1 - n0);
+            voff[u] = (uint32_t)nc * (uint32_t)(2 * s.H) + at;
+            base[u] = reinterpret_cast<const uint8_t *>(w + (size_t)n0 * s.H);
+        }
+    }
+    const uint32_t l0 = lds_addr(lds);
+    const auto load = [&](int step, int buf) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            g2lds<16>(base[u] + (size_t)step * Tl::kRow, voff[u],
+                      l0 + buf * Tl::kStage + (wave * U + u) * 1024);
+    };
+
+    const int wm = wave / WN, wn = wave % WN;
+    const int swz = (lane & 15) >> 1;
+    const int off0 = (lane & 15) * Tl::kRow + (((lane >> 4) ^ swz) * 16);
+    const int xoff = wm * MF * 16 * Tl::kRow, woff = (BM + wn * 64) * Tl::kRow;
+    v4f acc[MF][NF];
+#pragma unroll
+    for (int m = 0; m < MF; ++m)
+#pragma unroll
+        for (int f = 0; f < NF; ++f)
+            acc[m][f] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    const int steps = s.H / 64; // even: H is a multiple of 128
+    const auto multiply = [&](int buf) {
+        const uint8_t *st = lds + buf * Tl::kStage;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int o = off0 ^ (64 * k);
+            uint4 wq[NF];
+#pragma unroll
+            for (int f = 0; f < NF; ++f)
+                wq[f] = *reinterpret_cast<const uint4 *>(st + woff + f * 16 * Tl::kRow + o);
+#pragma unroll
+            for (int m = 0; m < MF; ++m) {
+                const uint4 xq =
+                    *reinterpret_cast<const uint4 *>(st + xoff + m * 16 * Tl::kRow + o);
+#pragma unroll
+                for (int f = 0; f < NF; ++f)
+                    acc[m][f] = mfma<DT>(wq[f], xq, acc[m][f]);
+            }
+        }
+    };
+    load(0, 0);
+    for (int k = 0; k < steps; k += 2) {
+        wait_vmcnt<0>();
+        raw_barrier();
+        load(k + 1, 1);
+        multiply(0);
+        wait_vmcnt<0>();
+        raw_barrier();
+        if (k + 2 < steps)
+            load(k + 2, 0);
+        multiply(1);
+    }
+
+    // 16 rows at a time, in order (their loads would not fit in registers
+    // beside the sums all at once)
+#pragma unroll
+    for (int m = 0; m < MF; ++m) {
+        const long i = m0 + (wm * MF + m) * 16 + (lane & 15);
+        const Row row = row_at(s, order, ids, i);
+        expand<DT, NF>(s, v, b, scale, row, n0 + wn * 64, acc[m]);
+        if (i < s.T)
+            store_cols<DT, NF>(s, out, row.t, n0 + wn * 64 + 16 * (lane >> 4), acc[m]);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// A given base: bound by reading it and writing out.  A wavefront takes 16
+// places x 64 columns.
+// ---------------------------------------------------------------------------
+constexpr int kAddWaves = 4;
+
 template <int DT>
-hipError_t adapter_of_type(const moe_adapter_shape &sh, const void *x, const void *w,
-                           const void *base, const int32_t *ids, const void *a, const void *b,
-                           const float *scale, void *out, float *v, hipStream_t st)
+__global__ void __launch_bounds__(64 * kAddWaves)
+add_kernel(AShape s, const uint16_t *base, const int32_t *__restrict__ ids,
+           const int32_t *__restrict__ order, const uint16_t *__restrict__ b,
+           const float *__restrict__ scale, const float *__restrict__ v, uint16_t *out)
+{
+    constexpr int NF = 4;
+    const int lane = threadIdx.x & 63, wave = wave_of();
+    const int n0 = (blockIdx.y * kAddWaves + wave) * 16 * NF;
+    const long i = (long)blockIdx.x * 16 + (lane & 15);
+    if (n0 >= s.N)
+        return;
+    const Row row = row_at(s, order, ids, i);
+    const int n = n0 + 4 * NF * (lane >> 4);
+    v4f acc[NF];
+#pragma unroll
+    for (int p = 0; p < NF / 2; ++p) {
+        float f[8] = {};
+        if (n + 8 * p < s.N)
+            Elem<DT>::unpack(piece(base + (size_t)row.t * s.N + n + 8 * p), f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            acc[2 * p][e] = f[e];
+            acc[2 * p + 1][e] = f[4 + e];
+        }
+    }
+    expand<DT, NF>(s, v, b, scale, row, n0, acc);
+    if (i < s.T)
+        store_cols<DT, NF>(s, out, row.t, n, acc);
+}
+
+size_t order_bytes(const moe_adapter_shape &s)
+{
+    return s.T > kFewRows && s.L < kOrderKeys ? ((size_t)s.T * sizeof(int32_t) + 255) / 256 * 256
+                                              : 0;
+}
+
+int up(long n, int by) { return (int)((n + by - 1) / by); }
+
+template <int DT>
+hipError_t shrink_many(const AShape &s, const uint16_t *x, const int32_t *ids,
+                       const int32_t *order, const uint16_t *a, float *v, hipStream_t st)
+{
+    const int cus = device_cu_count();
+    const int rb = up(s.r, 16);
+    const auto go = [&](auto f, auto j) {
+        constexpr int F = decltype(f)::value, J = decltype(j)::value;
+        shrink_many_kernel<DT, F, J><<<dim3(up(s.T, 16 * F), up(rb, J)), 64 * kManyWaves, 0, st>>>(
+            s, x, ids, order, a, v);
+    };
+    std::integral_constant<int, 1> c1;
+    std::integral_constant<int, 2> c2;
+    std::integral_constant<int, 4> c4;
+    // blocks as large as leave every CU a workgroup: x is read once per
+    // block of the rank, A once per block of rows
+    const int t1 = up(s.T, 16), t2 = up(s.T, 32);
+    if (rb >= 3 && t2 >= cus)
+        go(c2, c4);
+    else if (rb >= 3 && t1 >= cus)
+        go(c1, c4);
+    else if (rb >= 2 && t2 >= cus)
+        go(c2, c2);
+    else if (rb >= 2 && t1 * up(rb, 2) >= cus)
+        go(c1, c2);
+    else if (rb == 1 && t2 >= cus)
+        go(c2, c1);
+    else
+        go(c1, c1);
+    return hipGetLastError();
+}
+
+template <int DT>
+hipError_t adapter_of_type(const moe_adapter_shape &sh, const void *x_, const void *w_,
+                           const void *base, const int32_t *ids, const void *a_, const void *b_,
+                           const float *scale, void *out_, uint8_t *ws, hipStream_t st)
 {
     const AShape s{sh.T, sh.H, sh.N, sh.L, sh.rank};
-    const auto *xe = static_cast<const uint16_t *>(x);
-    shrink_kernel<DT><<<dim3((s.T + 15u) / 16u, (s.r + 15) / 16), 64, 0, st>>>(
-        s, xe, ids, static_cast<const uint16_t *>(a), v);
-    hipError_t e = hipGetLastError();
+    const auto *x = static_cast<const uint16_t *>(x_), *w = static_cast<const uint16_t *>(w_);
+    const auto *a = static_cast<const uint16_t *>(a_), *b = static_cast<const uint16_t *>(b_);
+    auto *out = static_cast<uint16_t *>(out_);
+    int32_t *order = order_bytes(sh) ? reinterpret_cast<int32_t *>(ws) : nullptr;
+    float *v = reinterpret_cast<float *>(ws + order_bytes(sh));
+    hipError_t e;
+    if (order) {
+        order_kernel<<<1, kOrderThreads, (s.L + 1) * sizeof(int), st>>>(s, ids, order);
+        if ((e = hipGetLastError()) != hipSuccess)
+            return e;
+    }
+    if (s.T <= kFewRows) {
+        shrink_few_kernel<DT><<<dim3(s.T, up(s.r, 16)), 64 * kFewWaves, 0, st>>>(s, x, ids, a, v);
+        e = hipGetLastError();
+    } else {
+        e = shrink_many<DT>(s, x, ids, order, a, v, st);
+    }
     if (e != hipSuccess)
         return e;
-    project_kernel<DT><<<dim3((s.T + 63u) / 64u, (s.N + 63) / 64), kThreads, 0, st>>>(
-        s, xe, static_cast<const uint16_t *>(w), static_cast<const uint16_t *>(base), ids,
-        static_cast<const uint16_t *>(b), scale, v, static_cast<uint16_t *>(out));
+    if (!w) {
+        add_kernel<DT><<<dim3(up(s.T, 16), up(s.N, 64 * kAddWaves)), 64 * kAddWaves, 0, st>>>(
+            s, static_cast<const uint16_t *>(base), ids, order, b, scale, v, out);
+        return hipGetLastError();
+    }
+    const auto skinny = [&](auto m, auto n) {
+        constexpr int MF = decltype(m)::value, NF = decltype(n)::value;
+        project_skinny_kernel<DT, MF, NF>
+            <<<dim3(up(s.N, 16 * NF), up(s.T, 16 * MF)), 64 * kSkinnyWaves, 0, st>>>(
+                s, x, w, ids, b, scale, v, out);
+    };
+    std::integral_constant<int, 1> c1;
+    std::integral_constant<int, 2> c2;
+    std::integral_constant<int, 4> c4;
+    std::integral_constant<int, 8> c8;
+    if (s.T <= 16)
+        skinny(c1, c1);
+    else if (s.T <= 32)
+        skinny(c2, c2);
+    else if (s.T <= 64)
+        skinny(c4, c2);
+    else if (s.T <= kFewRows)
+        skinny(c8, c2);
+    else if ((long)up(s.T, 256) * up(s.N, 256) >= device_cu_count()) {
+        const int tm = up(s.T, 256), tn = up(s.N, 256);
+        project_tiled_kernel<DT, 256, 256, 2, 4><<<tm * tn, 512, 0, st>>>(
+            s, tm, tn, x, w, ids, order, b, scale, v, out);
+    } else {
+        const int tm = up(s.T, 128), tn = up(s.N, 128);
+        project_tiled_kernel<DT, 128, 128, 2, 2><<<tm * tn, 256, 0, st>>>(
+            s, tm, tn, x, w, ids, order, b, scale, v, out);
+    }
     return hipGetLastError();
 }
 
@@ -233,7 +817,7 @@ hipError_t adapter_of_type(const moe_adapter_shape &sh, const void *x, const voi
 
 size_t adapter_workspace_bytes(const moe_adapter_shape &s)
 {
-    return (size_t)s.T * s.rank * sizeof(float);
+    return order_bytes(s) + (size_t)s.T * s.rank * sizeof(float);
 }
 
 hipError_t launch_adapter_project(const moe_adapter_shape &s, int dtype, const void *x,
@@ -241,10 +825,10 @@ hipError_t launch_adapter_project(const moe_adapter_shape &s, int dtype, const v
                                   const void *a, const void *b, const float *scale, void *out,
                                   void *ws, hipStream_t st)
 {
-    float *v = static_cast<float *>(ws);
+    uint8_t *p = static_cast<uint8_t *>(ws);
     if (dtype == MOE_DT_BF16)
-        return adapter_of_type<MOE_DT_BF16>(s, x, w, base, ids, a, b, scale, out, v, st);
-    return adapter_of_type<MOE_DT_F16>(s, x, w, base, ids, a, b, scale, out, v, st);
+        return adapter_of_type<MOE_DT_BF16>(s, x, w, base, ids, a, b, scale, out, p, st);
+    return adapter_of_type<MOE_DT_F16>(s, x, w, base, ids, a, b, scale, out, p, st);
 }
 
 } // namespace moe

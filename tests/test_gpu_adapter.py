@@ -59,6 +59,8 @@ SIZES = [
     (511, 768, 768, 6, 64),
     (700, 256, 2304, 3, 16),
     (1025, 384, 392, 12, 48),
+    (300, 128, 64, 9000, 8),                       # more adapters than the order counts
+    (4111, 128, 4104, 9, 16),                      # the largest tiles
 ]
 
 

@@ -176,6 +176,36 @@ order_kernel(AShape s, const int32_t *__restrict__ ids, int32_t *__restrict__ or
     }
 }
 
+// Steps wave, wave + NW, ... of `steps` for one wavefront, D of them in
+// flight: mul(d) multiplies the operands that load(d, step) sent for.  The
+// barriers keep the loads where they stand (left alone, the compiler moves
+// each next to its use and waits for it there); loads past the last step
+// repeat it, so that the count of loads in flight is always known.
+template <int NW, int D, typename Load, typename Mul>
+__device__ __forceinline__ void stream_steps(int steps, int wave, Load load, Mul mul)
+{
+    const int n = wave < steps ? (steps - wave + NW - 1) / NW : 0;
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+        load(d, min(wave + d * NW, steps - 1));
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    int i = 0;
+    for (; i + D <= n; i += D) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            mul(d);
+            __builtin_amdgcn_sched_barrier(0);
+            load(d, min(wave + (i + d + D) * NW, steps - 1));
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+#pragma unroll
+    for (int d = 0; d + 1 < D; ++d)
+        if (i + d < n)
+            mul(d);
+}
+
 // ---------------------------------------------------------------------------
 // Shrink.  Both forms: a workgroup's wavefronts split H, each summing its
 // part for all of the workgroup's rows and rank values straight from global
@@ -183,42 +213,35 @@ order_kernel(AShape s, const int32_t *__restrict__ ids, int32_t *__restrict__ or
 // ---------------------------------------------------------------------------
 
 // The sums over one wavefront's part of H: row pieces xr (per 16 rows) with
-// rows of A, J blocks of 16.  Steps of 64 values: 128 bytes of every row.
+// rows of A, J blocks of 16.
 template <int DT, int F, int J, int NW>
 __device__ __forceinline__ void shrink_part(int H, int wave, const uint16_t *const *xr,
-                                            const uint16_t *const *ar, const bool *live,
-                                            v4f (*acc)[J])
+                                            const uint16_t *const *ar, v4f (*acc)[J])
 {
-    constexpr int D = F * J > 2 ? 2 : 4; // steps in flight
-    const int steps = H / 64;
-    for (int i0 = wave; i0 < steps; i0 += NW * D) {
-        uint4 xq[D][F][2], aq[D][J][2];
-#pragma unroll
-        for (int d = 0; d < D; ++d) {
-            const int h = 64 * min(i0 + d * NW, steps - 1);
+    constexpr int D = F + J > 4 ? 3 : 4;
+    uint4 xq[D][F][2], aq[D][J][2];
+    stream_steps<NW, D>(
+        H / 64, wave,
+        [&](int d, int step) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
 #pragma unroll
+                for (int f = 0; f < F; ++f)
+                    xq[d][f][k] = piece(xr[f] + 64 * step + 32 * k);
+#pragma unroll
                 for (int j = 0; j < J; ++j)
-                    aq[d][j][k] = piece(ar[j] + h + 32 * k);
+                    aq[d][j][k] = piece(ar[j] + 64 * step + 32 * k);
+            }
+        },
+        [&](int d) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
 #pragma unroll
                 for (int f = 0; f < F; ++f)
-                    if (live[f])
-                        xq[d][f][k] = piece(xr[f] + h + 32 * k);
-            }
-        }
 #pragma unroll
-        for (int d = 0; d < D; ++d)
-            if (i0 + d * NW < steps)
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-#pragma unroll
-                    for (int f = 0; f < F; ++f)
-                        if (live[f])
-#pragma unroll
-                            for (int j = 0; j < J; ++j)
-                                acc[f][j] = mfma<DT>(aq[d][j][k], xq[d][f][k], acc[f][j]);
-    }
+                    for (int j = 0; j < J; ++j)
+                        acc[f][j] = mfma<DT>(aq[d][j][k], xq[d][f][k], acc[f][j]);
+        });
 }
 
 // Few rows: workgroup (t, block of 16 of the rank).  Row t works for the
@@ -272,9 +295,8 @@ shrink_few_kernel(AShape s, const uint16_t *__restrict__ x, const int32_t *__res
     const int j = blockIdx.y * 16 + (lane & 15);
     const uint16_t *xr[1] = {x + (size_t)(row < 0 ? t : row) * s.H + 8 * (lane >> 4)};
     const uint16_t *ar[1] = {a + ((size_t)id * s.r + min(j, s.r - 1)) * s.H + 8 * (lane >> 4)};
-    const bool live[1] = {true};
     v4f acc[1][1] = {{v4f{0.0f, 0.0f, 0.0f, 0.0f}}};
-    shrink_part<DT, 1, 1, kFewWaves>(s.H, wave, xr, ar, live, acc);
+    shrink_part<DT, 1, 1, kFewWaves>(s.H, wave, xr, ar, acc);
     part[wave][lane] = acc[0][0];
     __syncthreads();
     const int j0 = blockIdx.y * 16 + 4 * (lane >> 4);
@@ -314,13 +336,9 @@ shrink_many_kernel(AShape s, const uint16_t *__restrict__ x, const int32_t *__re
                 g = __builtin_amdgcn_readlane(row[f].id, __builtin_ctz(todo[f]));
         if (g < 0)
             return;
-        bool live[F];
 #pragma unroll
-        for (int f = 0; f < F; ++f) {
-            const uint32_t m = (uint32_t)__ballot(row[f].id == g) & 0xffffu;
-            live[f] = m != 0;
-            todo[f] &= ~m;
-        }
+        for (int f = 0; f < F; ++f)
+            todo[f] &= ~(uint32_t)__ballot(row[f].id == g);
         const uint16_t *ar[J];
         v4f acc[F][J];
 #pragma unroll
@@ -331,7 +349,7 @@ shrink_many_kernel(AShape s, const uint16_t *__restrict__ x, const int32_t *__re
             for (int f = 0; f < F; ++f)
                 acc[f][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
         }
-        shrink_part<DT, F, J, kManyWaves>(s.H, wave, xr, ar, live, acc);
+        shrink_part<DT, F, J, kManyWaves>(s.H, wave, xr, ar, acc);
 #pragma unroll
         for (int f = 0; f < F; ++f)
 #pragma unroll
@@ -360,7 +378,9 @@ shrink_many_kernel(AShape s, const uint16_t *__restrict__ x, const int32_t *__re
 // Expand: adds the adapters' term of 16 rows (the lane's: row) to the sums of
 // 16 NF columns from n0 (in column_of's order).
 // ---------------------------------------------------------------------------
-template <int DT, int NF>
+// 64 of the rank at a time: the rows' v as hi and lo, then the adapters among
+// the rows, GB at a time with their B in flight together.
+template <int DT, int NF, int GB>
 __device__ __forceinline__ void expand(const AShape &s, const float *__restrict__ v,
                                        const uint16_t *__restrict__ b,
                                        const float *__restrict__ scale, const Row &row, int n0,
@@ -368,10 +388,13 @@ __device__ __forceinline__ void expand(const AShape &s, const float *__restrict_
 {
     const int lane = threadIdx.x & 63;
     const int k0 = 8 * (lane >> 4);
-    uint32_t todo = (uint32_t)__ballot(row.id >= 0) & 0xffffu;
-    if (!todo)
+    const uint32_t rows = (uint32_t)__ballot(row.id >= 0) & 0xffffu;
+    if (!rows)
         return;
     const float *vr = v + (size_t)row.t * s.r + k0;
+    float sc = 1.0f;
+    if (scale && row.id >= 0)
+        sc = scale[row.id];
     int ex = 0;
     if constexpr (DT == MOE_DT_F16) {
         float top = 0.0f;
@@ -384,51 +407,72 @@ __device__ __forceinline__ void expand(const AShape &s, const float *__restrict_
         if (top > 0.0f && top < INFINITY)
             (void)frexpf(top, &ex);
     }
-    size_t col[NF];
+    uint32_t col[NF]; // element of B_l; N * rank is below 2^28
 #pragma unroll
     for (int f = 0; f < NF; ++f)
-        col[f] = (size_t)min(n0 + column_of<NF>(f, lane & 15), s.N - 1) * s.r + k0;
-    do {
-        const int g = __builtin_amdgcn_readlane(row.id, __builtin_ctz(todo));
-        const bool mine = row.id == g;
-        todo &= ~(uint32_t)__ballot(mine);
-        const uint16_t *bg = b + (size_t)g * s.N * s.r;
-        const float sc = scale ? scale[g] : 1.0f;
-        v4f d[NF];
+        col[f] = (uint32_t)min(n0 + column_of<NF>(f, lane & 15), s.N - 1) * s.r;
+    for (int c = 0; c < s.r; c += 64) {
+        uint4 hi[2], lo[2];
+        bool there[2];
 #pragma unroll
-        for (int f = 0; f < NF; ++f)
-            d[f] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-        for (int k = 0; k < s.r; k += 32) {
-            const bool there = k + k0 < s.r;
+        for (int k = 0; k < 2; ++k) {
+            there[k] = c + 32 * k + k0 < s.r;
             float f8[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 f8[i] = 0.0f;
-            if (there && mine) {
-                const v4f v0 = *reinterpret_cast<const v4f *>(vr + k);
-                const v4f v1 = *reinterpret_cast<const v4f *>(vr + k + 4);
+            if (there[k] && row.id >= 0) {
+                const v4f v0 = *reinterpret_cast<const v4f *>(vr + c + 32 * k);
+                const v4f v1 = *reinterpret_cast<const v4f *>(vr + c + 32 * k + 4);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     f8[i] = DT == MOE_DT_F16 ? ldexpf(v0[i], -ex) : v0[i];
                     f8[i + 4] = DT == MOE_DT_F16 ? ldexpf(v1[i], -ex) : v1[i];
                 }
             }
-            uint4 hi, lo;
-            split8<DT>(f8, hi, lo);
-#pragma unroll
-            for (int f = 0; f < NF; ++f) {
-                const uint4 bq = there ? piece(bg + col[f] + k) : uint4{0, 0, 0, 0};
-                d[f] = mfma<DT>(bq, hi, d[f]);
-                d[f] = mfma<DT>(bq, lo, d[f]);
-            }
+            split8<DT>(f8, hi[k], lo[k]);
         }
-        if (mine)
+        uint32_t todo = rows;
+        do {
+            int g[GB];
+            uint4 bq[GB][2][NF];
 #pragma unroll
-            for (int f = 0; f < NF; ++f)
+            for (int q = 0; q < GB; ++q) {
+                g[q] = -1;
+                if (todo) {
+                    g[q] = __builtin_amdgcn_readlane(row.id, __builtin_ctz(todo));
+                    todo &= ~(uint32_t)__ballot(row.id == g[q]);
+                }
+                // (past the rank a lane reads the chunk's first piece, unused)
+                const uint16_t *bg = b + (size_t)max(g[q], 0) * s.N * s.r + c;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    acc[f][i] += sc * (DT == MOE_DT_F16 ? ldexpf(d[f][i], ex) : d[f][i]);
-    } while (todo);
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int f = 0; f < NF; ++f)
+                        if (g[q] >= 0)
+                            bq[q][k][f] = piece(bg + col[f] + (there[k] ? 32 * k + k0 : 0));
+            }
+#pragma unroll
+            for (int q = 0; q < GB; ++q) {
+                if (g[q] < 0)
+                    break;
+#pragma unroll
+                for (int f = 0; f < NF; ++f) {
+                    v4f d = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint4 bk = there[k] ? bq[q][k][f] : uint4{0, 0, 0, 0};
+                        d = mfma<DT>(bk, hi[k], d);
+                        d = mfma<DT>(bk, lo[k], d);
+                    }
+                    if (row.id == g[q])
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            acc[f][i] += sc * (DT == MOE_DT_F16 ? ldexpf(d[i], ex) : d[i]);
+                }
+            }
+        } while (todo);
+    }
 }
 
 // The 4 NF neighbouring columns of one row that a lane holds, rounded and
@@ -489,38 +533,29 @@ project_skinny_kernel(AShape s, const uint16_t *__restrict__ x, const uint16_t *
 #pragma unroll
         for (int f = 0; f < NF; ++f)
             acc[m][f] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    const int steps = s.H / 64;
     uint4 wq[D][NF][2], xq[D][MF][2];
-    const auto load = [&](int d, int i) {
-        const int h = 64 * min(i, steps - 1);
+    stream_steps<kSkinnyWaves, D>(
+        s.H / 64, wave,
+        [&](int d, int step) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+            for (int k = 0; k < 2; ++k) {
 #pragma unroll
-            for (int f = 0; f < NF; ++f)
-                wq[d][f][k] = piece(wr[f] + h + 32 * k);
+                for (int f = 0; f < NF; ++f)
+                    wq[d][f][k] = piece(wr[f] + 64 * step + 32 * k);
 #pragma unroll
-            for (int m = 0; m < MF; ++m)
-                xq[d][m][k] = piece(xr[m] + h + 32 * k);
-        }
-    };
+                for (int m = 0; m < MF; ++m)
+                    xq[d][m][k] = piece(xr[m] + 64 * step + 32 * k);
+            }
+        },
+        [&](int d) {
 #pragma unroll
-    for (int d = 0; d < D; ++d)
-        load(d, wave + d * kSkinnyWaves);
-    for (int i0 = wave; i0 < steps; i0 += D * kSkinnyWaves) {
+            for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int d = 0; d < D; ++d) {
-            const int i = i0 + d * kSkinnyWaves;
-            if (i < steps)
+                for (int m = 0; m < MF; ++m)
 #pragma unroll
-                for (int k = 0; k < 2; ++k)
-#pragma unroll
-                    for (int m = 0; m < MF; ++m)
-#pragma unroll
-                        for (int f = 0; f < NF; ++f)
-                            acc[m][f] = mfma<DT>(wq[d][f][k], xq[d][m][k], acc[m][f]);
-            load(d, i + D * kSkinnyWaves);
-        }
-    }
+                    for (int f = 0; f < NF; ++f)
+                        acc[m][f] = mfma<DT>(wq[d][f][k], xq[d][m][k], acc[m][f]);
+        });
 #pragma unroll
     for (int m = 0; m < MF; ++m)
 #pragma unroll
@@ -539,58 +574,66 @@ project_skinny_kernel(AShape s, const uint16_t *__restrict__ x, const uint16_t *
         for (int q = 1; q < kSkinnyWaves; ++q)
             sum[f] += part[q][wave][f][lane];
     }
-    expand<DT, NF>(s, v, b, scale, row, n0, sum);
+    expand<DT, NF, 4>(s, v, b, scale, row, n0, sum);
     if (i < s.T)
         store_cols<DT, NF>(s, out, row.t, n0 + 4 * NF * (lane >> 4), sum);
 }
 
 // ---------------------------------------------------------------------------
 // Project, many rows: BM places x BN columns per workgroup, WM x WN
-// wavefronts of 16 MF rows x 64 columns.  K steps of 64 values (128 bytes a
-// row) go from global memory to LDS without registers, two stages; the
-// loads of step k + 1 are in flight while step k multiplies.  A row's eight
-// 16-byte pieces are stored at piece ^ (row / 2 mod 8): the 16 rows that one
-// operand read touches then lie in different banks.
+// wavefronts of 16 MF rows x 16 NF columns.  K steps of 64 values (128 bytes
+// a row) go from global memory to LDS without registers, two stages.  A
+// row's eight 16-byte pieces are stored at piece ^ (row / 2 mod 8): the 16
+// rows that one operand read touches then lie in different banks.
+//
+// Operands are read from LDS one phase ahead of their matrix instructions,
+// into a second set of registers, a few reads between every few matrix
+// instructions.  The last phase of a step reads the next stage and sends off
+// the loads of the step after it, into the stage that all wavefronts have
+// just finished reading: one barrier a step, and a step's time for its loads.
 // ---------------------------------------------------------------------------
-template <int BM, int BN>
-struct Tile {
-    static constexpr int kRow = 128;                       // bytes of a row's step
-    static constexpr int kStage = (BM + BN) * kRow;
-};
 
-// Tile index of a workgroup: neighbouring workgroups run on different XCDs,
-// so each XCD gets a contiguous run of tiles; inside it, tiles go down 8 row
-// tiles before the next column tile, so the tiles that run together on an
-// XCD share rows and columns in its L2.
-__device__ __forceinline__ void tile_of(int b, int tm, int tn, int *im, int *in)
+// Place of workgroup b of n in a run that gives each XCD (neighbouring
+// workgroups run on different ones) a contiguous part.
+__device__ __forceinline__ int xcd_run(int b, int n)
 {
-    const int total = tm * tn, xcd = b & 7, idx = b >> 3;
-    const int base = total >> 3, rem = total & 7;
-    const int q = xcd * base + min(xcd, rem) + idx;
+    const int xcd = b & 7;
+    return xcd * (n >> 3) + min(xcd, n & 7) + (b >> 3);
+}
+
+// Tile q of tm x tn: down 8 row tiles before the next column tile, so the
+// tiles that run together on an XCD share rows and columns in its L2.
+__device__ __forceinline__ void tile_of(int q, int tm, int tn, int *im, int *in)
+{
     const int group = q / (8 * tn), first = group * 8;
     const int rows = min(8, tm - first), in_group = q - group * 8 * tn;
     *im = first + in_group % rows;
     *in = in_group / rows;
 }
 
+// s_waitcnt vmcnt(0) lgkmcnt(0).
+__device__ __forceinline__ void wait_all() { __builtin_amdgcn_s_waitcnt(0x7 << 4); }
+
+constexpr int kRowBytes = 128; // of a row's step
+
+struct ProjectArgs {
+    const uint16_t *x, *w;
+    const int32_t *ids, *order;
+    const uint16_t *b;
+    const float *scale, *v;
+    uint16_t *out;
+};
+
+// The rows of places m0 .. m0 + BM - 1 by the columns n0 .. n0 + BN - 1.
 template <int DT, int BM, int BN, int WM, int WN>
-__global__ void __launch_bounds__(64 * WM * WN)
-project_tiled_kernel(AShape s, int tm, int tn, const uint16_t *__restrict__ x,
-                     const uint16_t *__restrict__ w, const int32_t *__restrict__ ids,
-                     const int32_t *__restrict__ order, const uint16_t *__restrict__ b,
-                     const float *__restrict__ scale, const float *__restrict__ v,
-                     uint16_t *__restrict__ out)
+__device__ __forceinline__ void project_tile(const AShape &s, const ProjectArgs &p, long m0,
+                                             int n0, uint8_t *lds)
 {
-    constexpr int NW = WM * WN, MF = BM / WM / 16, NF = 4;
-    static_assert(BN == 64 * WN && (BM + BN) % (8 * NW) == 0, "wavefronts cover the tile");
+    constexpr int NW = WM * WN, MF = BM / WM / 16, NF = BN / WN / 16;
+    static_assert(NF % 4 == 0 && (BM + BN) % (8 * NW) == 0, "wavefronts cover the tile");
     constexpr int U = (BM + BN) / 8 / NW; // 1 KiB loads per wavefront and step
-    using Tl = Tile<BM, BN>;
-    __shared__ __align__(1024) uint8_t lds[2 * Tl::kStage];
+    constexpr int kStage = (BM + BN) * kRowBytes;
     const int lane = threadIdx.x & 63, wave = wave_of();
-    int im, in;
-    tile_of(blockIdx.x, tm, tn, &im, &in);
-    const long m0 = (long)im * BM;
-    const int n0 = in * BN;
 
     // this lane's byte offsets: load u covers 8 LDS rows, x's first
     uint32_t voff[U];
@@ -601,79 +644,149 @@ project_tiled_kernel(AShape s, int tm, int tn, const uint16_t *__restrict__ x,
         const int at = ((lane & 7) ^ ((row >> 1) & 7)) * 16;
         if ((wave * U + u) * 8 < BM) {
             const long i = min(m0 + row, (long)s.T - 1);
-            const int t = order ? order[i] : (int)i;
+            const int t = p.order ? p.order[i] : (int)i;
             voff[u] = (uint32_t)t * (uint32_t)(2 * s.H) + at;
-            base[u] = reinterpret_cast<const uint8_t *>(x);
+            base[u] = reinterpret_cast<const uint8_t *>(p.x);
         } else {
             const int rw = row - BM;
-            const int n = (rw & ~63) + column_of<NF>((rw >> 4) & 3, rw & 15);
+            const int n = (rw & ~63) + column_of<4>((rw >> 4) & 3, rw & 15);
             const int nc = min(n, s.N - 1 - n0);
             voff[u] = (uint32_t)nc * (uint32_t)(2 * s.H) + at;
-            base[u] = reinterpret_cast<const uint8_t *>(w + (size_t)n0 * s.H);
+            base[u] = reinterpret_cast<const uint8_t *>(p.w + (size_t)n0 * s.H);
         }
     }
     const uint32_t l0 = lds_addr(lds);
-    const auto load = [&](int step, int buf) {
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            g2lds<16>(base[u] + (size_t)step * Tl::kRow, voff[u],
-                      l0 + buf * Tl::kStage + (wave * U + u) * 1024);
+    const auto load = [&](int u, int step, int buf) {
+        g2lds<16>(base[u] + (size_t)step * kRowBytes, voff[u],
+                  l0 + buf * kStage + (wave * U + u) * 1024);
     };
 
     const int wm = wave / WN, wn = wave % WN;
-    const int swz = (lane & 15) >> 1;
-    const int off0 = (lane & 15) * Tl::kRow + (((lane >> 4) ^ swz) * 16);
-    const int xoff = wm * MF * 16 * Tl::kRow, woff = (BM + wn * 64) * Tl::kRow;
+    const int off = (lane & 15) * kRowBytes + (((lane >> 4) ^ ((lane & 15) >> 1)) * 16);
+    const uint8_t *xl = lds + wm * MF * 16 * kRowBytes;
+    const uint8_t *wl = lds + (BM + wn * NF * 16) * kRowBytes;
     v4f acc[MF][NF];
 #pragma unroll
     for (int m = 0; m < MF; ++m)
 #pragma unroll
         for (int f = 0; f < NF; ++f)
             acc[m][f] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    const int steps = s.H / 64; // even: H is a multiple of 128
-    const auto multiply = [&](int buf) {
-        const uint8_t *st = lds + buf * Tl::kStage;
+    // The phases of a step: half k of its 64 values, a group of 4 of the
+    // wavefront's row blocks.  Phase p multiplies the operands in sets p mod 2
+    // (x) and k (w) and reads those of phase p + 1 into the other sets.
+    constexpr int G = MF / 4, P = 2 * G;
+    static_assert(MF % 4 == 0, "row blocks in groups of four");
+    uint4 xo[2][4], wo[2][NF];
+    const auto read_x = [&](int q, int ph, int buf) {
+        xo[ph & 1][q] = *reinterpret_cast<const uint4 *>(
+            xl + buf * kStage + ((ph % G) * 4 + q) * 16 * kRowBytes + (off ^ (64 * (ph / G))));
+    };
+    const auto read_w = [&](int f, int k, int buf) {
+        wo[k][f] = *reinterpret_cast<const uint4 *>(wl + buf * kStage + f * 16 * kRowBytes +
+                                                    (off ^ (64 * k)));
+    };
+    // step k in stage buf: the other stage holds step k + 1 before the last
+    // phase, which also sends off the loads of step k + 2 into this stage
+    const auto step_of = [&](int k, int buf, int last) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int o = off0 ^ (64 * k);
-            uint4 wq[NF];
+        for (int ph = 0; ph < P; ++ph) {
+            const bool end = ph + 1 == P;
+            const int np = end ? 0 : ph + 1, nbuf = end ? buf ^ 1 : buf;
+            if (end) {
+                wait_all();
+                raw_barrier();
+            }
 #pragma unroll
-            for (int f = 0; f < NF; ++f)
-                wq[f] = *reinterpret_cast<const uint4 *>(st + woff + f * 16 * Tl::kRow + o);
+            for (int q = 0; q < 4; ++q) {
+                read_x(q, np, nbuf);
+                if (np % G == 0)
 #pragma unroll
-            for (int m = 0; m < MF; ++m) {
-                const uint4 xq =
-                    *reinterpret_cast<const uint4 *>(st + xoff + m * 16 * Tl::kRow + o);
+                    for (int f = q * NF / 4; f < (q + 1) * NF / 4; ++f)
+                        read_w(f, np / G, nbuf);
+                if (end)
 #pragma unroll
-                for (int f = 0; f < NF; ++f)
-                    acc[m][f] = mfma<DT>(wq[f], xq, acc[m][f]);
+                    for (int u = q * U / 4; u < (q + 1) * U / 4; ++u)
+                        load(u, min(k + 2, last), buf);
+#pragma unroll
+                for (int f = 0; f < NF; ++f) {
+                    v4f &a = acc[(ph % G) * 4 + q][f];
+                    a = mfma<DT>(wo[ph / G][f], xo[ph & 1][q], a);
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
     };
-    load(0, 0);
+    static_assert(P % 2 == 0, "the next step starts with x's set 0");
+    const int steps = s.H / 64; // even: H is a multiple of 128
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        load(u, 0, 0);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        load(u, 1, 1);
+    wait_vmcnt<U>();
+    raw_barrier();
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        read_x(q, 0, 0);
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+        read_w(f, 0, 0);
+    // (the loads past the last step repeat it, unused)
     for (int k = 0; k < steps; k += 2) {
-        wait_vmcnt<0>();
-        raw_barrier();
-        load(k + 1, 1);
-        multiply(0);
-        wait_vmcnt<0>();
-        raw_barrier();
-        if (k + 2 < steps)
-            load(k + 2, 0);
-        multiply(1);
+        step_of(k, 0, steps - 1);
+        step_of(k + 1, 1, steps - 1);
     }
+    wait_all();
 
-    // 16 rows at a time, in order (their loads would not fit in registers
-    // beside the sums all at once)
+    // 16 rows x 64 columns at a time, in order (their loads would not fit in
+    // registers beside the sums all at once)
+    Row row[MF];
+#pragma unroll
+    for (int m = 0; m < MF; ++m)
+        row[m] = row_at(s, p.order, p.ids, m0 + (wm * MF + m) * 16 + (lane & 15));
 #pragma unroll
     for (int m = 0; m < MF; ++m) {
-        const long i = m0 + (wm * MF + m) * 16 + (lane & 15);
-        const Row row = row_at(s, order, ids, i);
-        expand<DT, NF>(s, v, b, scale, row, n0 + wn * 64, acc[m]);
-        if (i < s.T)
-            store_cols<DT, NF>(s, out, row.t, n0 + wn * 64 + 16 * (lane >> 4), acc[m]);
-        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int f = 0; f < NF; f += 4) {
+            const int n = n0 + (wn * NF + f) * 16;
+            __builtin_amdgcn_sched_barrier(0);
+            expand<DT, 4, 1>(s, p.v, p.b, p.scale, row[m], n, acc[m] + f);
+            if (m0 + (wm * MF + m) * 16 + (lane & 15) < s.T)
+                store_cols<DT, 4>(s, p.out, row[m].t, n + 16 * (lane >> 4), acc[m] + f);
+        }
     }
+}
+
+// `whole` tiles of 256 x 256, then, where the tiles left over would keep less
+// than half the CUs busy for a tile's time, each of them as two of 128 rows.
+template <int DT>
+__global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2)))
+project_large_kernel(AShape s, int tm, int tn, int whole, ProjectArgs p)
+{
+    __shared__ __align__(1024) uint8_t lds[2 * 512 * kRowBytes];
+    const int b = blockIdx.x;
+    int im, in;
+    if (b < whole) {
+        tile_of(xcd_run(b, whole), tm, tn, &im, &in);
+        project_tile<DT, 256, 256, 2, 4>(s, p, (long)im * 256, in * 256, lds);
+        return;
+    }
+    const int h = xcd_run(b - whole, gridDim.x - whole);
+    tile_of(whole + (h >> 1), tm, tn, &im, &in);
+    const long m0 = (long)im * 256 + 128 * (h & 1);
+    if (m0 < s.T)
+        project_tile<DT, 128, 256, 2, 4>(s, p, m0, in * 256, lds);
+}
+
+template <int DT>
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2)))
+project_small_kernel(AShape s, int tm, int tn, ProjectArgs p)
+{
+    __shared__ __align__(1024) uint8_t lds[2 * 256 * kRowBytes];
+    int im, in;
+    tile_of(xcd_run(blockIdx.x, tm * tn), tm, tn, &im, &in);
+    project_tile<DT, 128, 128, 2, 2>(s, p, (long)im * 128, in * 128, lds);
 }
 
 // ---------------------------------------------------------------------------
@@ -708,7 +821,7 @@ add_kernel(AShape s, const uint16_t *base, const int32_t *__restrict__ ids,
             acc[2 * p + 1][e] = f[4 + e];
         }
     }
-    expand<DT, NF>(s, v, b, scale, row, n0, acc);
+    expand<DT, NF, 2>(s, v, b, scale, row, n0, acc);
     if (i < s.T)
         store_cols<DT, NF>(s, out, row.t, n, acc);
 }
@@ -801,14 +914,18 @@ hipError_t adapter_of_type(const moe_adapter_shape &sh, const void *x_, const vo
         skinny(c4, c2);
     else if (s.T <= kFewRows)
         skinny(c8, c2);
-    else if ((long)up(s.T, 256) * up(s.N, 256) >= device_cu_count()) {
-        const int tm = up(s.T, 256), tn = up(s.N, 256);
-        project_tiled_kernel<DT, 256, 256, 2, 4><<<tm * tn, 512, 0, st>>>(
-            s, tm, tn, x, w, ids, order, b, scale, v, out);
-    } else {
-        const int tm = up(s.T, 128), tn = up(s.N, 128);
-        project_tiled_kernel<DT, 128, 128, 2, 2><<<tm * tn, 256, 0, st>>>(
-            s, tm, tn, x, w, ids, order, b, scale, v, out);
+    else {
+        const ProjectArgs p{x, w, ids, order, b, scale, v, out};
+        const int cus = device_cu_count();
+        const int tm = up(s.T, 256), tn = up(s.N, 256), left = tm * tn % cus;
+        if (tm * tn >= cus) {
+            const int halves = 2 * left <= cus ? left : 0;
+            project_large_kernel<DT><<<tm * tn + halves, 512, 0, st>>>(s, tm, tn,
+                                                                      tm * tn - halves, p);
+        } else {
+            const int sm = up(s.T, 128), sn = up(s.N, 128);
+            project_small_kernel<DT><<<sm * sn, 256, 0, st>>>(s, sm, sn, p);
+        }
     }
     return hipGetLastError();
 }

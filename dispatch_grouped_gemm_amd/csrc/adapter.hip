@@ -176,99 +176,151 @@ order_kernel(AShape s, const int32_t *__restrict__ ids, int32_t *__restrict__ or
     }
 }
 
-// Steps wave, wave + NW, ... of `steps` for one wavefront, D of them in
-// flight: mul(d) multiplies the operands that load(d, step) sent for.  The
-// barriers keep the loads where they stand (left alone, the compiler moves
-// each next to its use and waits for it there); loads past the last step
-// repeat it, so that the count of loads in flight is always known.
-template <int NW, int D, typename Load, typename Mul>
-__device__ __forceinline__ void stream_steps(int steps, int wave, Load load, Mul mul)
+// ---------------------------------------------------------------------------
+// Stream: BM rows of x by BN rows of a weight (W or A), bound by reading
+// them.  Steps of 128 values, 256 bytes of a row: a load instruction moves
+// four whole rows of a step from global memory to LDS, so it asks for whole
+// cache lines (a wavefront reading its operands straight into registers
+// touches 16 rows by 64 bytes at a time, and half lines come from the L2 at
+// a third of the rate: 36 against 105 KB/us a CU).  NS stages keep NS - 1
+// steps in flight.  A row's sixteen 16-byte pieces are stored at piece ^ (row
+// mod 16): the 16 rows that one operand read touches lie in different banks.
+//
+// Wavefront (m, k): quarter k of every step for rows (BM / WM) m ..; the
+// four quarters meet in LDS at the end, in a fixed order.
+// ---------------------------------------------------------------------------
+template <int BM, int BN, int WM, int NS>
+struct Stream {
+    static constexpr int kWaves = 4 * WM, MF = BM / WM / 16, NF = BN / 16;
+    static constexpr int U = (BM + BN) / 4 / kWaves; // 1 KiB loads per wavefront and step
+    static constexpr int kRow = 256, kStage = (BM + BN) * kRow;
+    static constexpr int kLds = NS * kStage;
+    static_assert((BM + BN) % (4 * kWaves) == 0 && BM % (16 * WM) == 0, "whole loads, blocks");
+    static_assert(4 * (BM / 16) * NF * 1024 <= kLds, "the quarters' sums reuse the stages");
+};
+
+// Rows [0, BM) come from x, rows [BM, BM + BN) from w: xrow(i) and wrow(i)
+// give a row's number, w's within 2^31 bytes of its base.  Afterwards
+// wavefront m < BM / 16 holds rows 16 m .. 16 m + 15 in sum.
+template <int DT, int BM, int BN, int WM, int NS, typename XRow, typename WRow>
+__device__ __forceinline__ void stream_tile(int H, const uint16_t *__restrict__ x, XRow xrow,
+                                            const uint16_t *__restrict__ w, WRow wrow,
+                                            uint8_t *lds, v4f *sum)
 {
-    const int n = wave < steps ? (steps - wave + NW - 1) / NW : 0;
+    using S = Stream<BM, BN, WM, NS>;
+    constexpr int U = S::U, MF = S::MF, NF = S::NF;
+    const int lane = threadIdx.x & 63, wave = wave_of();
+    uint32_t voff[U];
+    const uint8_t *base[U];
 #pragma unroll
-    for (int d = 0; d < D; ++d) {
-        load(d, min(wave + d * NW, steps - 1));
-        __builtin_amdgcn_sched_barrier(0);
+    for (int u = 0; u < U; ++u) {
+        const int row = (wave * U + u) * 4 + (lane >> 4);
+        const int at = ((lane & 15) ^ (row & 15)) * 16;
+        const bool of_x = (wave * U + u) * 4 < BM;
+        const int r = of_x ? xrow(row) : wrow(row - BM);
+        voff[u] = (uint32_t)r * (uint32_t)(2 * H) + at;
+        base[u] = reinterpret_cast<const uint8_t *>(of_x ? x : w);
     }
-    int i = 0;
-    for (; i + D <= n; i += D) {
+    const uint32_t l0 = lds_addr(lds);
+    const auto load = [&](int step, int slot) {
 #pragma unroll
-        for (int d = 0; d < D; ++d) {
-            mul(d);
-            __builtin_amdgcn_sched_barrier(0);
-            load(d, min(wave + (i + d + D) * NW, steps - 1));
-            __builtin_amdgcn_sched_barrier(0);
+        for (int u = 0; u < U; ++u)
+            g2lds<16>(base[u] + (size_t)step * S::kRow, voff[u],
+                      l0 + slot * S::kStage + (wave * U + u) * 1024);
+    };
+    const int kq = wave & 3, wm = wave >> 2;
+    const int off = (lane & 15) * S::kRow + (((4 * kq + (lane >> 4)) ^ (lane & 15)) * 16);
+    v4f acc[MF][NF];
+#pragma unroll
+    for (int m = 0; m < MF; ++m)
+#pragma unroll
+        for (int f = 0; f < NF; ++f)
+            acc[m][f] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    const auto multiply = [&](int slot) {
+        const uint8_t *st = lds + slot * S::kStage + off;
+        uint4 xq[MF], wq[NF];
+#pragma unroll
+        for (int f = 0; f < NF; ++f)
+            wq[f] = *reinterpret_cast<const uint4 *>(st + (BM + 16 * f) * S::kRow);
+#pragma unroll
+        for (int m = 0; m < MF; ++m)
+            xq[m] = *reinterpret_cast<const uint4 *>(st + 16 * (wm * MF + m) * S::kRow);
+#pragma unroll
+        for (int m = 0; m < MF; ++m)
+#pragma unroll
+            for (int f = 0; f < NF; ++f)
+                acc[m][f] = mfma<DT>(wq[f], xq[m], acc[m][f]);
+    };
+    const int steps = H / 128;
+    int slot = 0;
+    if (steps >= NS) {
+#pragma unroll
+        for (int k = 0; k < NS - 1; ++k)
+            load(k, k);
+        for (int k = 0; k + NS <= steps; ++k) {
+            // step k has landed; step k - 1, whose stage is refilled, is done
+            wait_vmcnt<(NS - 2) * U>();
+            raw_barrier();
+            load(k + NS - 1, slot == 0 ? NS - 1 : slot - 1);
+            multiply(slot);
+            slot = slot + 1 == NS ? 0 : slot + 1;
+        }
+    } else {
+        for (int k = 0; k < steps; ++k)
+            load(k, k);
+    }
+    wait_vmcnt<0>();
+    raw_barrier();
+    for (int k = min(steps, NS - 1); k > 0; --k) {
+        multiply(slot);
+        slot = slot + 1 == NS ? 0 : slot + 1;
+    }
+    __syncthreads();
+    v4f *part = reinterpret_cast<v4f *>(lds);
+#pragma unroll
+    for (int m = 0; m < MF; ++m)
+#pragma unroll
+        for (int f = 0; f < NF; ++f)
+            part[((kq * (BM / 16) + wm * MF + m) * NF + f) * 64 + lane] = acc[m][f];
+    __syncthreads();
+    if (wave < BM / 16) {
+#pragma unroll
+        for (int f = 0; f < NF; ++f) {
+            sum[f] = part[(wave * NF + f) * 64 + lane];
+#pragma unroll
+            for (int k = 1; k < 4; ++k)
+                sum[f] += part[((k * (BM / 16) + wave) * NF + f) * 64 + lane];
         }
     }
-#pragma unroll
-    for (int d = 0; d + 1 < D; ++d)
-        if (i + d < n)
-            mul(d);
 }
 
 // ---------------------------------------------------------------------------
-// Shrink.  Both forms: a workgroup's wavefronts split H, each summing its
-// part for all of the workgroup's rows and rank values straight from global
-// memory, and the parts meet in LDS in a fixed order.
+// Shrink, few rows: workgroup (t, block of 16 of the rank).  Row t works for
+// itself and the next 15 rows of its adapter if the rows before it of the
+// same adapter fill whole sixteens, else it has nothing to do: every
+// adapter's A is read by as few workgroups as its rows allow, in whatever
+// order they come.
 // ---------------------------------------------------------------------------
-
-// The sums over one wavefront's part of H: row pieces xr (per 16 rows) with
-// rows of A, J blocks of 16.
-template <int DT, int F, int J, int NW>
-__device__ __forceinline__ void shrink_part(int H, int wave, const uint16_t *const *xr,
-                                            const uint16_t *const *ar, v4f (*acc)[J])
-{
-    constexpr int D = F + J > 4 ? 3 : 4;
-    uint4 xq[D][F][2], aq[D][J][2];
-    stream_steps<NW, D>(
-        H / 64, wave,
-        [&](int d, int step) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-#pragma unroll
-                for (int f = 0; f < F; ++f)
-                    xq[d][f][k] = piece(xr[f] + 64 * step + 32 * k);
-#pragma unroll
-                for (int j = 0; j < J; ++j)
-                    aq[d][j][k] = piece(ar[j] + 64 * step + 32 * k);
-            }
-        },
-        [&](int d) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-#pragma unroll
-                for (int f = 0; f < F; ++f)
-#pragma unroll
-                    for (int j = 0; j < J; ++j)
-                        acc[f][j] = mfma<DT>(aq[d][j][k], xq[d][f][k], acc[f][j]);
-        });
-}
-
-// Few rows: workgroup (t, block of 16 of the rank).  Row t works for the
-// next 16 rows of its adapter if the rows before it of the same adapter
-// fill whole sixteens, else it has nothing to do: every adapter's A is read
-// by as few workgroups as its rows allow, in whatever order they come.
-constexpr int kFewWaves = 16;
+constexpr int kFewStages = 8;
+using FewStream = Stream<16, 16, 1, kFewStages>;
 
 template <int DT>
-__global__ void __launch_bounds__(64 * kFewWaves)
+__global__ void __launch_bounds__(64 * FewStream::kWaves)
 shrink_few_kernel(AShape s, const uint16_t *__restrict__ x, const int32_t *__restrict__ ids,
                   const uint16_t *__restrict__ a, float *__restrict__ v)
 {
+    static_assert(64 * FewStream::kWaves == kFewRows, "a thread looks at one row");
+    __shared__ __align__(1024) uint8_t lds[FewStream::kLds];
     __shared__ uint64_t mask[kFewRows / 64];
     __shared__ int member[16];
-    __shared__ v4f part[kFewWaves][64];
     const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = wave_of();
     const int id = ids[t];
     if ((unsigned)id >= (unsigned)s.L)
         return;
-    bool same = false;
-    if (tid < kFewRows) {
-        same = tid < s.T && ids[tid] == id;
-        const uint64_t m = __ballot(same);
-        if (lane == 0)
-            mask[wave] = m;
-    }
+    const bool same = tid < s.T && ids[tid] == id;
+    const uint64_t mine = __ballot(same);
+    if (lane == 0)
+        mask[wave] = mine;
     if (tid < 16)
         member[tid] = -1;
     __syncthreads();
@@ -291,84 +343,43 @@ shrink_few_kernel(AShape s, const uint16_t *__restrict__ x, const int32_t *__res
             member[at] = tid;
     }
     __syncthreads();
-    const int row = member[lane & 15];
-    const int j = blockIdx.y * 16 + (lane & 15);
-    const uint16_t *xr[1] = {x + (size_t)(row < 0 ? t : row) * s.H + 8 * (lane >> 4)};
-    const uint16_t *ar[1] = {a + ((size_t)id * s.r + min(j, s.r - 1)) * s.H + 8 * (lane >> 4)};
-    v4f acc[1][1] = {{v4f{0.0f, 0.0f, 0.0f, 0.0f}}};
-    shrink_part<DT, 1, 1, kFewWaves>(s.H, wave, xr, ar, acc);
-    part[wave][lane] = acc[0][0];
-    __syncthreads();
-    const int j0 = blockIdx.y * 16 + 4 * (lane >> 4);
-    if (wave == 0 && row >= 0 && j0 < s.r) {
-        v4f sum = part[0][lane];
-        for (int w = 1; w < kFewWaves; ++w)
-            sum += part[w][lane];
-        *reinterpret_cast<v4f *>(v + (size_t)row * s.r + j0) = sum;
-    }
+    const int j0 = blockIdx.y * 16;
+    v4f sum[1];
+    stream_tile<DT, 16, 16, 1, kFewStages>(
+        s.H, x, [&](int i) { return member[i] < 0 ? t : member[i]; },
+        a + (size_t)id * s.r * s.H, [&](int i) { return min(j0 + i, s.r - 1); }, lds, sum);
+    const int row = member[lane & 15], j = j0 + 4 * (lane >> 4);
+    if (wave == 0 && row >= 0 && j < s.r)
+        *reinterpret_cast<v4f *>(v + (size_t)row * s.r + j) = sum[0];
 }
 
-// Many rows, ordered: workgroup (16 F places, 16 J of the rank).
-constexpr int kManyWaves = 8;
-
-template <int DT, int F, int J>
-__global__ void __launch_bounds__(64 * kManyWaves)
+// Shrink, many rows, ordered: workgroup (32 places, BN of the rank).
+template <int DT, int BN, int NS>
+__global__ void __launch_bounds__((64 * Stream<32, BN, 2, NS>::kWaves))
 shrink_many_kernel(AShape s, const uint16_t *__restrict__ x, const int32_t *__restrict__ ids,
                    const int32_t *__restrict__ order, const uint16_t *__restrict__ a,
                    float *__restrict__ v)
 {
-    __shared__ v4f part[kManyWaves][F * J][64];
+    __shared__ __align__(1024) uint8_t lds[Stream<32, BN, 2, NS>::kLds];
     const int lane = threadIdx.x & 63, wave = wave_of();
-    Row row[F];
-    const uint16_t *xr[F];
-    uint32_t todo[F];
+    const long i0 = (long)blockIdx.x * 32;
+    const Row row = row_at(s, order, ids, i0 + (lane & 31));
+    const int j0 = blockIdx.y * BN;
+    uint32_t todo = (uint32_t)__ballot(row.id >= 0);
+    while (todo) {
+        const int g = __builtin_amdgcn_readlane(row.id, __builtin_ctz(todo));
+        todo &= ~(uint32_t)__ballot(row.id == g);
+        v4f sum[BN / 16];
+        stream_tile<DT, 32, BN, 2, NS>(
+            s.H, x, [&](int i) { return row_at(s, order, ids, i0 + i).t; },
+            a + (size_t)g * s.r * s.H, [&](int i) { return min(j0 + i, s.r - 1); }, lds, sum);
+        const Row mine = row_at(s, order, ids, i0 + 16 * wave + (lane & 15));
+        if (wave < 2 && mine.id == g)
 #pragma unroll
-    for (int f = 0; f < F; ++f) {
-        row[f] = row_at(s, order, ids, (long)blockIdx.x * 16 * F + 16 * f + (lane & 15));
-        xr[f] = x + (size_t)row[f].t * s.H + 8 * (lane >> 4);
-        todo[f] = (uint32_t)__ballot(row[f].id >= 0) & 0xffffu;
-    }
-    while (true) {
-        int g = -1;
-#pragma unroll
-        for (int f = F - 1; f >= 0; --f)
-            if (todo[f])
-                g = __builtin_amdgcn_readlane(row[f].id, __builtin_ctz(todo[f]));
-        if (g < 0)
-            return;
-#pragma unroll
-        for (int f = 0; f < F; ++f)
-            todo[f] &= ~(uint32_t)__ballot(row[f].id == g);
-        const uint16_t *ar[J];
-        v4f acc[F][J];
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-            const int at = (blockIdx.y * J + j) * 16 + (lane & 15);
-            ar[j] = a + ((size_t)g * s.r + min(at, s.r - 1)) * s.H + 8 * (lane >> 4);
-#pragma unroll
-            for (int f = 0; f < F; ++f)
-                acc[f][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-        }
-        shrink_part<DT, F, J, kManyWaves>(s.H, wave, xr, ar, acc);
-#pragma unroll
-        for (int f = 0; f < F; ++f)
-#pragma unroll
-            for (int j = 0; j < J; ++j)
-                part[wave][f * J + j][lane] = acc[f][j];
-        __syncthreads();
-#pragma unroll
-        for (int f = 0; f < F; ++f)
-#pragma unroll
-            for (int j = 0; j < J; ++j) {
-                if ((f * J + j) % kManyWaves != wave)
-                    continue;
-                const int j0 = (blockIdx.y * J + j) * 16 + 4 * (lane >> 4);
-                if (row[f].id == g && j0 < s.r) {
-                    v4f sum = part[0][f * J + j][lane];
-                    for (int w = 1; w < kManyWaves; ++w)
-                        sum += part[w][f * J + j][lane];
-                    *reinterpret_cast<v4f *>(v + (size_t)row[f].t * s.r + j0) = sum;
-                }
+            for (int f = 0; f < BN / 16; ++f) {
+                const int j = j0 + 16 * f + 4 * (lane >> 4);
+                if (j < s.r)
+                    *reinterpret_cast<v4f *>(v + (size_t)mine.t * s.r + j) = sum[f];
             }
         __syncthreads();
     }
@@ -500,80 +511,28 @@ __device__ __forceinline__ void store_cols(const AShape &s, uint16_t *out, int t
 }
 
 // ---------------------------------------------------------------------------
-// Project, few rows: bound by reading W once.  A workgroup holds 16 MF rows
-// and 16 NF columns; its wavefronts split H (interleaved 128-byte pieces of
-// each row) and read W and x straight into registers, D steps in flight;
-// their sums meet in LDS in a fixed order, wavefront m finishing rows 16 m.
+// Project, few rows: all rows (up to BM) by 32 columns per workgroup, so W is
+// read once and x by every workgroup, from the L2.
 // ---------------------------------------------------------------------------
-constexpr int kSkinnyWaves = 8;
-
-template <int DT, int MF, int NF>
-__global__ void __launch_bounds__(64 * kSkinnyWaves)
-project_skinny_kernel(AShape s, const uint16_t *__restrict__ x, const uint16_t *__restrict__ w,
-                      const int32_t *__restrict__ ids, const uint16_t *__restrict__ b,
-                      const float *__restrict__ scale, const float *__restrict__ v,
-                      uint16_t *__restrict__ out)
+template <int DT, int BM, int WM, int NS>
+__global__ void __launch_bounds__((64 * Stream<BM, 32, WM, NS>::kWaves))
+project_few_kernel(AShape s, const uint16_t *__restrict__ x, const uint16_t *__restrict__ w,
+                   const int32_t *__restrict__ ids, const uint16_t *__restrict__ b,
+                   const float *__restrict__ scale, const float *__restrict__ v,
+                   uint16_t *__restrict__ out)
 {
-    constexpr int D = MF >= 8 ? 2 : MF >= 4 ? 3 : MF >= 2 ? 4 : 6;
-    __shared__ v4f part[kSkinnyWaves][MF][NF][64];
+    constexpr int NF = 2;
+    __shared__ __align__(1024) uint8_t lds[Stream<BM, 32, WM, NS>::kLds];
     const int lane = threadIdx.x & 63, wave = wave_of();
-    const long m0 = (long)blockIdx.y * 16 * MF;
-    const int n0 = blockIdx.x * 16 * NF;
-    const uint16_t *xr[MF], *wr[NF];
-#pragma unroll
-    for (int m = 0; m < MF; ++m)
-        xr[m] = x + (size_t)min(m0 + 16 * m + (lane & 15), (long)s.T - 1) * s.H + 8 * (lane >> 4);
-#pragma unroll
-    for (int f = 0; f < NF; ++f)
-        wr[f] = w + (size_t)min(n0 + column_of<NF>(f, lane & 15), s.N - 1) * s.H +
-                8 * (lane >> 4);
-    v4f acc[MF][NF];
-#pragma unroll
-    for (int m = 0; m < MF; ++m)
-#pragma unroll
-        for (int f = 0; f < NF; ++f)
-            acc[m][f] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    uint4 wq[D][NF][2], xq[D][MF][2];
-    stream_steps<kSkinnyWaves, D>(
-        s.H / 64, wave,
-        [&](int d, int step) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-#pragma unroll
-                for (int f = 0; f < NF; ++f)
-                    wq[d][f][k] = piece(wr[f] + 64 * step + 32 * k);
-#pragma unroll
-                for (int m = 0; m < MF; ++m)
-                    xq[d][m][k] = piece(xr[m] + 64 * step + 32 * k);
-            }
-        },
-        [&](int d) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-#pragma unroll
-                for (int m = 0; m < MF; ++m)
-#pragma unroll
-                    for (int f = 0; f < NF; ++f)
-                        acc[m][f] = mfma<DT>(wq[d][f][k], xq[d][m][k], acc[m][f]);
-        });
-#pragma unroll
-    for (int m = 0; m < MF; ++m)
-#pragma unroll
-        for (int f = 0; f < NF; ++f)
-            part[wave][m][f][lane] = acc[m][f];
-    __syncthreads();
-    if (wave >= MF)
-        return;
-    const long i = m0 + 16 * wave + (lane & 15);
-    const Row row = row_at(s, nullptr, ids, i);
+    const int n0 = blockIdx.x * 32;
     v4f sum[NF];
-#pragma unroll
-    for (int f = 0; f < NF; ++f) {
-        sum[f] = part[0][wave][f][lane];
-#pragma unroll
-        for (int q = 1; q < kSkinnyWaves; ++q)
-            sum[f] += part[q][wave][f][lane];
-    }
+    stream_tile<DT, BM, 32, WM, NS>(
+        s.H, x, [&](int i) { return min(i, s.T - 1); }, w + (size_t)n0 * s.H,
+        [&](int i) { return min(column_of<NF>(i >> 4, i & 15), s.N - 1 - n0); }, lds, sum);
+    if (wave >= BM / 16)
+        return;
+    const long i = 16 * wave + (lane & 15);
+    const Row row = row_at(s, nullptr, ids, i);
     expand<DT, NF, 4>(s, v, b, scale, row, n0, sum);
     if (i < s.T)
         store_cols<DT, NF>(s, out, row.t, n0 + 4 * NF * (lane >> 4), sum);
@@ -838,31 +797,19 @@ template <int DT>
 hipError_t shrink_many(const AShape &s, const uint16_t *x, const int32_t *ids,
                        const int32_t *order, const uint16_t *a, float *v, hipStream_t st)
 {
-    const int cus = device_cu_count();
-    const int rb = up(s.r, 16);
-    const auto go = [&](auto f, auto j) {
-        constexpr int F = decltype(f)::value, J = decltype(j)::value;
-        shrink_many_kernel<DT, F, J><<<dim3(up(s.T, 16 * F), up(rb, J)), 64 * kManyWaves, 0, st>>>(
-            s, x, ids, order, a, v);
+    const auto go = [&](auto bn, auto ns) {
+        constexpr int BN = decltype(bn)::value, NS = decltype(ns)::value;
+        shrink_many_kernel<DT, BN, NS>
+            <<<dim3(up(s.T, 32), up(s.r, BN)), 64 * Stream<32, BN, 2, NS>::kWaves, 0, st>>>(
+                s, x, ids, order, a, v);
     };
-    std::integral_constant<int, 1> c1;
-    std::integral_constant<int, 2> c2;
-    std::integral_constant<int, 4> c4;
-    // blocks as large as leave every CU a workgroup: x is read once per
-    // block of the rank, A once per block of rows
-    const int t1 = up(s.T, 16), t2 = up(s.T, 32);
-    if (rb >= 3 && t2 >= cus)
-        go(c2, c4);
-    else if (rb >= 3 && t1 >= cus)
-        go(c1, c4);
-    else if (rb >= 2 && t2 >= cus)
-        go(c2, c2);
-    else if (rb >= 2 && t1 * up(rb, 2) >= cus)
-        go(c1, c2);
-    else if (rb == 1 && t2 >= cus)
-        go(c2, c1);
+    // as much of the rank per workgroup as there is (x is read once per
+    // block of the rank), but a workgroup for every CU
+    const int cus = device_cu_count(), t = up(s.T, 32);
+    if (s.r > 32 && t * up(s.r, 64) >= cus)
+        go(std::integral_constant<int, 64>{}, std::integral_constant<int, 6>{});
     else
-        go(c1, c1);
+        go(std::integral_constant<int, 32>{}, std::integral_constant<int, 5>{});
     return hipGetLastError();
 }
 
@@ -884,7 +831,8 @@ hipError_t adapter_of_type(const moe_adapter_shape &sh, const void *x_, const vo
             return e;
     }
     if (s.T <= kFewRows) {
-        shrink_few_kernel<DT><<<dim3(s.T, up(s.r, 16)), 64 * kFewWaves, 0, st>>>(s, x, ids, a, v);
+        shrink_few_kernel<DT>
+            <<<dim3(s.T, up(s.r, 16)), 64 * FewStream::kWaves, 0, st>>>(s, x, ids, a, v);
         e = hipGetLastError();
     } else {
         e = shrink_many<DT>(s, x, ids, order, a, v, st);
@@ -896,24 +844,25 @@ hipError_t adapter_of_type(const moe_adapter_shape &sh, const void *x_, const vo
             s, static_cast<const uint16_t *>(base), ids, order, b, scale, v, out);
         return hipGetLastError();
     }
-    const auto skinny = [&](auto m, auto n) {
-        constexpr int MF = decltype(m)::value, NF = decltype(n)::value;
-        project_skinny_kernel<DT, MF, NF>
-            <<<dim3(up(s.N, 16 * NF), up(s.T, 16 * MF)), 64 * kSkinnyWaves, 0, st>>>(
-                s, x, w, ids, b, scale, v, out);
+    const auto few = [&](auto bm, auto wm, auto ns) {
+        constexpr int BM = decltype(bm)::value, WM = decltype(wm)::value,
+                      NS = decltype(ns)::value;
+        project_few_kernel<DT, BM, WM, NS>
+            <<<up(s.N, 32), 64 * Stream<BM, 32, WM, NS>::kWaves, 0, st>>>(s, x, w, ids, b, scale,
+                                                                          v, out);
     };
-    std::integral_constant<int, 1> c1;
-    std::integral_constant<int, 2> c2;
-    std::integral_constant<int, 4> c4;
-    std::integral_constant<int, 8> c8;
     if (s.T <= 16)
-        skinny(c1, c1);
+        few(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{},
+            std::integral_constant<int, 8>{});
     else if (s.T <= 32)
-        skinny(c2, c2);
+        few(std::integral_constant<int, 32>{}, std::integral_constant<int, 2>{},
+            std::integral_constant<int, 8>{});
     else if (s.T <= 64)
-        skinny(c4, c2);
-    else if (s.T <= kFewRows)
-        skinny(c8, c2);
+        few(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{},
+            std::integral_constant<int, 6>{});
+    else if (s.T <= 128)
+        few(std::integral_constant<int, 128>{}, std::integral_constant<int, 2>{},
+            std::integral_constant<int, 4>{});
     else {
         const ProjectArgs p{x, w, ids, order, b, scale, v, out};
         const int cus = device_cu_count();

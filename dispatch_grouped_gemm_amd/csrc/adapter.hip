@@ -201,11 +201,12 @@ struct Stream {
 
 // Rows [0, BM) come from x, rows [BM, BM + BN) from w: xrow(i) and wrow(i)
 // give a row's number, w's within 2^31 bytes of its base.  Afterwards
-// wavefront m < BM / 16 holds rows 16 m .. 16 m + 15 in sum.
-template <int DT, int BM, int BN, int WM, int NS, typename XRow, typename WRow>
+// wavefront m < BM / 16 has added rows 16 m .. 16 m + 15 to sum.  meanwhile()
+// runs once the first loads are on their way.
+template <int DT, int BM, int BN, int WM, int NS, typename XRow, typename WRow, typename Mean>
 __device__ __forceinline__ void stream_tile(int H, const uint16_t *__restrict__ x, XRow xrow,
                                             const uint16_t *__restrict__ w, WRow wrow,
-                                            uint8_t *lds, v4f *sum)
+                                            uint8_t *lds, Mean meanwhile, v4f *sum)
 {
     using S = Stream<BM, BN, WM, NS>;
     constexpr int U = S::U, MF = S::MF, NF = S::NF;
@@ -253,21 +254,16 @@ __device__ __forceinline__ void stream_tile(int H, const uint16_t *__restrict__ 
     };
     const int steps = H / 128;
     int slot = 0;
-    if (steps >= NS) {
-#pragma unroll
-        for (int k = 0; k < NS - 1; ++k)
-            load(k, k);
-        for (int k = 0; k + NS <= steps; ++k) {
-            // step k has landed; step k - 1, whose stage is refilled, is done
-            wait_vmcnt<(NS - 2) * U>();
-            raw_barrier();
-            load(k + NS - 1, slot == 0 ? NS - 1 : slot - 1);
-            multiply(slot);
-            slot = slot + 1 == NS ? 0 : slot + 1;
-        }
-    } else {
-        for (int k = 0; k < steps; ++k)
-            load(k, k);
+    for (int k = 0; k < min(steps, NS - 1); ++k)
+        load(k, k);
+    meanwhile();
+    for (int k = 0; k + NS <= steps; ++k) {
+        // step k has landed; step k - 1, whose stage is refilled, is done
+        wait_vmcnt<(NS - 2) * U>();
+        raw_barrier();
+        load(k + NS - 1, slot == 0 ? NS - 1 : slot - 1);
+        multiply(slot);
+        slot = slot + 1 == NS ? 0 : slot + 1;
     }
     wait_vmcnt<0>();
     raw_barrier();
@@ -286,10 +282,11 @@ __device__ __forceinline__ void stream_tile(int H, const uint16_t *__restrict__ 
     if (wave < BM / 16) {
 #pragma unroll
         for (int f = 0; f < NF; ++f) {
-            sum[f] = part[(wave * NF + f) * 64 + lane];
+            v4f q = part[(wave * NF + f) * 64 + lane];
 #pragma unroll
             for (int k = 1; k < 4; ++k)
-                sum[f] += part[((k * (BM / 16) + wave) * NF + f) * 64 + lane];
+                q += part[((k * (BM / 16) + wave) * NF + f) * 64 + lane];
+            sum[f] += q;
         }
     }
 }
@@ -344,10 +341,10 @@ shrink_few_kernel(AShape s, const uint16_t *__restrict__ x, const int32_t *__res
     }
     __syncthreads();
     const int j0 = blockIdx.y * 16;
-    v4f sum[1];
+    v4f sum[1] = {v4f{0.0f, 0.0f, 0.0f, 0.0f}};
     stream_tile<DT, 16, 16, 1, kFewStages>(
         s.H, x, [&](int i) { return member[i] < 0 ? t : member[i]; },
-        a + (size_t)id * s.r * s.H, [&](int i) { return min(j0 + i, s.r - 1); }, lds, sum);
+        a + (size_t)id * s.r * s.H, [&](int i) { return min(j0 + i, s.r - 1); }, lds, [] {}, sum);
     const int row = member[lane & 15], j = j0 + 4 * (lane >> 4);
     if (wave == 0 && row >= 0 && j < s.r)
         *reinterpret_cast<v4f *>(v + (size_t)row * s.r + j) = sum[0];
@@ -370,9 +367,12 @@ shrink_many_kernel(AShape s, const uint16_t *__restrict__ x, const int32_t *__re
         const int g = __builtin_amdgcn_readlane(row.id, __builtin_ctz(todo));
         todo &= ~(uint32_t)__ballot(row.id == g);
         v4f sum[BN / 16];
+#pragma unroll
+        for (int f = 0; f < BN / 16; ++f)
+            sum[f] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
         stream_tile<DT, 32, BN, 2, NS>(
             s.H, x, [&](int i) { return row_at(s, order, ids, i0 + i).t; },
-            a + (size_t)g * s.r * s.H, [&](int i) { return min(j0 + i, s.r - 1); }, lds, sum);
+            a + (size_t)g * s.r * s.H, [&](int i) { return min(j0 + i, s.r - 1); }, lds, [] {}, sum);
         const Row mine = row_at(s, order, ids, i0 + 16 * wave + (lane & 15));
         if (wave < 2 && mine.id == g)
 #pragma unroll
@@ -390,7 +390,9 @@ shrink_many_kernel(AShape s, const uint16_t *__restrict__ x, const int32_t *__re
 // 16 NF columns from n0 (in column_of's order).
 // ---------------------------------------------------------------------------
 // 64 of the rank at a time: the rows' v as hi and lo, then the adapters among
-// the rows, GB at a time with their B in flight together.
+// the rows, GB at a time with their B in flight together.  No load stands
+// behind a branch (a lane or a place without work reads a valid address and
+// drops the product): behind one the compiler waits for each by itself.
 template <int DT, int NF, int GB>
 __device__ __forceinline__ void expand(const AShape &s, const float *__restrict__ v,
                                        const uint16_t *__restrict__ b,
@@ -399,20 +401,27 @@ __device__ __forceinline__ void expand(const AShape &s, const float *__restrict_
 {
     const int lane = threadIdx.x & 63;
     const int k0 = 8 * (lane >> 4);
-    const uint32_t rows = (uint32_t)__ballot(row.id >= 0) & 0xffffu;
+    const bool has = row.id >= 0;
+    const uint32_t rows = (uint32_t)__ballot(has) & 0xffffu;
     if (!rows)
         return;
-    const float *vr = v + (size_t)row.t * s.r + k0;
+    const float *vr = v + (size_t)row.t * s.r;
     float sc = 1.0f;
-    if (scale && row.id >= 0)
-        sc = scale[row.id];
+    if (scale)
+        sc = scale[max(row.id, 0)];
     int ex = 0;
     if constexpr (DT == MOE_DT_F16) {
         float top = 0.0f;
-        if (row.id >= 0)
-            for (int k = 0; k + k0 < s.r; k += 32)
-                for (int i = 0; i < 8; ++i)
-                    top = fmaxf(top, fabsf(vr[k + i]));
+        for (int k = 0; k < s.r; k += 32) {
+            const float *p = vr + min(k + k0, s.r - 8);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const v4f q = *reinterpret_cast<const v4f *>(p + 4 * h);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    top = fmaxf(top, has ? fabsf(q[i]) : 0.0f);
+            }
+        }
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
         if (top > 0.0f && top < INFINITY)
@@ -423,50 +432,50 @@ __device__ __forceinline__ void expand(const AShape &s, const float *__restrict_
     for (int f = 0; f < NF; ++f)
         col[f] = (uint32_t)min(n0 + column_of<NF>(f, lane & 15), s.N - 1) * s.r;
     for (int c = 0; c < s.r; c += 64) {
-        uint4 hi[2], lo[2];
+        int at[2];
         bool there[2];
+        v4f vq[2][2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             there[k] = c + 32 * k + k0 < s.r;
+            at[k] = there[k] ? c + 32 * k + k0 : 0;
+            vq[k][0] = *reinterpret_cast<const v4f *>(vr + at[k]);
+            vq[k][1] = *reinterpret_cast<const v4f *>(vr + at[k] + 4);
+        }
+        uint4 hi[2], lo[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
             float f8[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                f8[i] = 0.0f;
-            if (there[k] && row.id >= 0) {
-                const v4f v0 = *reinterpret_cast<const v4f *>(vr + c + 32 * k);
-                const v4f v1 = *reinterpret_cast<const v4f *>(vr + c + 32 * k + 4);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    f8[i] = DT == MOE_DT_F16 ? ldexpf(v0[i], -ex) : v0[i];
-                    f8[i + 4] = DT == MOE_DT_F16 ? ldexpf(v1[i], -ex) : v1[i];
-                }
+            for (int i = 0; i < 8; ++i) {
+                const float q = there[k] && has ? vq[k][i >> 2][i & 3] : 0.0f;
+                f8[i] = DT == MOE_DT_F16 ? ldexpf(q, -ex) : q;
             }
             split8<DT>(f8, hi[k], lo[k]);
         }
         uint32_t todo = rows;
         do {
-            int g[GB];
+            int g[GB], n = 0;
             uint4 bq[GB][2][NF];
 #pragma unroll
             for (int q = 0; q < GB; ++q) {
-                g[q] = -1;
-                if (todo) {
-                    g[q] = __builtin_amdgcn_readlane(row.id, __builtin_ctz(todo));
-                    todo &= ~(uint32_t)__ballot(row.id == g[q]);
-                }
-                // (past the rank a lane reads the chunk's first piece, unused)
-                const uint16_t *bg = b + (size_t)max(g[q], 0) * s.N * s.r + c;
+                const int next = __builtin_amdgcn_readlane(row.id, todo ? __builtin_ctz(todo) : 0);
+                g[q] = q == 0 || todo ? next : g[0];
+                n += todo ? 1 : 0;
+                todo &= ~(uint32_t)__ballot(row.id == g[q]);
+            }
+#pragma unroll
+            for (int q = 0; q < GB; ++q) {
+                const uint16_t *bg = b + (size_t)g[q] * s.N * s.r;
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
                     for (int f = 0; f < NF; ++f)
-                        if (g[q] >= 0)
-                            bq[q][k][f] = piece(bg + col[f] + (there[k] ? 32 * k + k0 : 0));
+                        bq[q][k][f] = piece(bg + col[f] + at[k]);
             }
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int q = 0; q < GB; ++q) {
-                if (g[q] < 0)
-                    break;
 #pragma unroll
                 for (int f = 0; f < NF; ++f) {
                     v4f d = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -476,10 +485,10 @@ __device__ __forceinline__ void expand(const AShape &s, const float *__restrict_
                         d = mfma<DT>(bk, hi[k], d);
                         d = mfma<DT>(bk, lo[k], d);
                     }
-                    if (row.id == g[q])
+                    const bool take = row.id == g[q] && q < n;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            acc[f][i] += sc * (DT == MOE_DT_F16 ? ldexpf(d[i], ex) : d[i]);
+                    for (int i = 0; i < 4; ++i)
+                        acc[f][i] += !take ? 0.0f : sc * (DT == MOE_DT_F16 ? ldexpf(d[i], ex) : d[i]);
                 }
             }
         } while (todo);
@@ -512,7 +521,9 @@ __device__ __forceinline__ void store_cols(const AShape &s, uint16_t *out, int t
 
 // ---------------------------------------------------------------------------
 // Project, few rows: all rows (up to BM) by 32 columns per workgroup, so W is
-// read once and x by every workgroup, from the L2.
+// read once and x by every workgroup, from the L2.  The adapters' term comes
+// first, while the first steps of W are on their way: at the end its chain
+// of loads (ids, v, B) would stand alone.
 // ---------------------------------------------------------------------------
 template <int DT, int BM, int WM, int NS>
 __global__ void __launch_bounds__((64 * Stream<BM, 32, WM, NS>::kWaves))
@@ -525,17 +536,21 @@ project_few_kernel(AShape s, const uint16_t *__restrict__ x, const uint16_t *__r
     __shared__ __align__(1024) uint8_t lds[Stream<BM, 32, WM, NS>::kLds];
     const int lane = threadIdx.x & 63, wave = wave_of();
     const int n0 = blockIdx.x * 32;
-    v4f sum[NF];
-    stream_tile<DT, BM, 32, WM, NS>(
-        s.H, x, [&](int i) { return min(i, s.T - 1); }, w + (size_t)n0 * s.H,
-        [&](int i) { return min(column_of<NF>(i >> 4, i & 15), s.N - 1 - n0); }, lds, sum);
-    if (wave >= BM / 16)
-        return;
     const long i = 16 * wave + (lane & 15);
-    const Row row = row_at(s, nullptr, ids, i);
-    expand<DT, NF, 4>(s, v, b, scale, row, n0, sum);
-    if (i < s.T)
-        store_cols<DT, NF>(s, out, row.t, n0 + 4 * NF * (lane >> 4), sum);
+    v4f sum[NF];
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+        sum[f] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    stream_tile<DT, BM, 32, WM, NS>(
+        s.H, x, [&](int r) { return min(r, s.T - 1); }, w + (size_t)n0 * s.H,
+        [&](int r) { return min(column_of<NF>(r >> 4, r & 15), s.N - 1 - n0); }, lds,
+        [&] {
+            if (wave < BM / 16)
+                expand<DT, NF, 4>(s, v, b, scale, row_at(s, nullptr, ids, i), n0, sum);
+        },
+        sum);
+    if (wave < BM / 16 && i < s.T)
+        store_cols<DT, NF>(s, out, (int)i, n0 + 4 * NF * (lane >> 4), sum);
 }
 
 // ---------------------------------------------------------------------------

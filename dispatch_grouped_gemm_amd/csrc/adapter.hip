@@ -182,53 +182,86 @@ order_kernel(AShape s, const int32_t *__restrict__ ids, int32_t *__restrict__ or
 // four whole rows of a step from global memory to LDS, so it asks for whole
 // cache lines (a wavefront reading its operands straight into registers
 // touches 16 rows by 64 bytes at a time, and half lines come from the L2 at
-// a third of the rate: 36 against 105 KB/us a CU).  NS stages keep NS - 1
-// steps in flight.  A row's sixteen 16-byte pieces are stored at piece ^ (row
-// mod 16): the 16 rows that one operand read touches lie in different banks.
+// a third of the rate: 36 against 105 KB/us a CU).  A row's sixteen 16-byte
+// pieces are stored at piece ^ (row mod 16): the 16 rows that one operand
+// read touches lie in different banks.
+//
+// Half the wavefronts load x, half the weight, each into its own ring of
+// stages (NX, NR): a wavefront's loads end in order, so in one ring the
+// operand that comes from the L2 would wait for the one that comes from
+// memory, and the rings' depths could not differ.
 //
 // Wavefront (m, k): quarter k of every step for rows (BM / WM) m ..; the
 // four quarters meet in LDS at the end, in a fixed order.
 // ---------------------------------------------------------------------------
-template <int BM, int BN, int WM, int NS>
+template <int BM, int BN, int WM, int NX, int NR>
 struct Stream {
-    static constexpr int kWaves = 4 * WM, MF = BM / WM / 16, NF = BN / 16;
-    static constexpr int U = (BM + BN) / 4 / kWaves; // 1 KiB loads per wavefront and step
-    static constexpr int kRow = 256, kStage = (BM + BN) * kRow;
-    static constexpr int kLds = NS * kStage;
-    static_assert((BM + BN) % (4 * kWaves) == 0 && BM % (16 * WM) == 0, "whole loads, blocks");
+    static constexpr int kWaves = 4 * WM, kThreads = 64 * kWaves, MF = BM / WM / 16, NF = BN / 16;
+    // 1 KiB loads per wavefront and step
+    static constexpr int UX = BM / 4 / (kWaves / 2), UR = BN / 4 / (kWaves / 2);
+    static constexpr int kRow = 256, kX = BM * kRow, kR = BN * kRow; // bytes of a stage
+    static constexpr int kLds = NX * kX + NR * kR;
+    static_assert(BM % (2 * kWaves) == 0 && BN % (2 * kWaves) == 0 && BM % (16 * WM) == 0,
+                  "whole loads, whole blocks");
     static_assert(4 * (BM / 16) * NF * 1024 <= kLds, "the quarters' sums reuse the stages");
 };
 
-// Rows [0, BM) come from x, rows [BM, BM + BN) from w: xrow(i) and wrow(i)
-// give a row's number, w's within 2^31 bytes of its base.  Afterwards
+// One wavefront's loads into one ring: U a step, N stages of kStage bytes
+// from lds0.  Loads past the last step repeat it into stages that nobody
+// reads again, so the number in flight stays the same to the end.
+template <int U, int N, int kStage, int kRow>
+struct Ring {
+    const uint8_t *next;
+    uint32_t voff[U], lds0, slot;
+    int left; // steps after the next one
+
+    // `first`: this wavefront's first load of a stage; row(i): number of the
+    // stage's row i in the array at p
+    template <typename Row>
+    __device__ __forceinline__ Ring(const uint16_t *p, int H, int first, uint32_t lds, Row row)
+        : next(reinterpret_cast<const uint8_t *>(p)), lds0(lds + first * 1024), slot(0),
+          left(H / 128 - 1)
+    {
+        const int lane = threadIdx.x & 63;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = (first + u) * 4 + (lane >> 4);
+            voff[u] = (uint32_t)row(i) * (uint32_t)(2 * H) + ((lane & 15) ^ (i & 15)) * 16;
+        }
+    }
+    __device__ __forceinline__ void load()
+    {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            g2lds<16>(next, voff[u], lds0 + slot + u * 1024);
+        slot = slot + kStage == N * kStage ? 0 : slot + kStage;
+        next += left > 0 ? kRow : 0;
+        --left;
+    }
+    __device__ __forceinline__ void start()
+    {
+        for (int k = 0; k < N - 1; ++k)
+            load();
+    }
+    // this wavefront's part of the oldest step has landed
+    __device__ __forceinline__ void wait() { wait_vmcnt<(N - 2) * U>(); }
+};
+
+// Rows [0, BM) come from x, columns [0, BN) from the rows of w: xrow(i) and
+// wrow(i) give their numbers, w's within 2^31 bytes of its base.  Afterwards
 // wavefront m < BM / 16 has added rows 16 m .. 16 m + 15 to sum.  meanwhile()
 // runs once the first loads are on their way.
-template <int DT, int BM, int BN, int WM, int NS, typename XRow, typename WRow, typename Mean>
-__device__ __forceinline__ void stream_tile(int H, const uint16_t *__restrict__ x, XRow xrow,
+template <int DT, int BM, int BN, int WM, int NX, int NR, typename XRow, typename WRow,
+          typename Mean>
+__device__ __forceinline__ void stream_tile(Stream<BM, BN, WM, NX, NR>, int H,
+                                            const uint16_t *__restrict__ x, XRow xrow,
                                             const uint16_t *__restrict__ w, WRow wrow,
                                             uint8_t *lds, Mean meanwhile, v4f *sum)
 {
-    using S = Stream<BM, BN, WM, NS>;
-    constexpr int U = S::U, MF = S::MF, NF = S::NF;
+    using S = Stream<BM, BN, WM, NX, NR>;
+    constexpr int MF = S::MF, NF = S::NF, kHalf = S::kWaves / 2;
     const int lane = threadIdx.x & 63, wave = wave_of();
-    uint32_t voff[U];
-    const uint8_t *base[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int row = (wave * U + u) * 4 + (lane >> 4);
-        const int at = ((lane & 15) ^ (row & 15)) * 16;
-        const bool of_x = (wave * U + u) * 4 < BM;
-        const int r = of_x ? xrow(row) : wrow(row - BM);
-        voff[u] = (uint32_t)r * (uint32_t)(2 * H) + at;
-        base[u] = reinterpret_cast<const uint8_t *>(of_x ? x : w);
-    }
     const uint32_t l0 = lds_addr(lds);
-    const auto load = [&](int step, int slot) {
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            g2lds<16>(base[u] + (size_t)step * S::kRow, voff[u],
-                      l0 + slot * S::kStage + (wave * U + u) * 1024);
-    };
     const int kq = wave & 3, wm = wave >> 2;
     const int off = (lane & 15) * S::kRow + (((4 * kq + (lane >> 4)) ^ (lane & 15)) * 16);
     v4f acc[MF][NF];
@@ -237,40 +270,38 @@ __device__ __forceinline__ void stream_tile(int H, const uint16_t *__restrict__ 
 #pragma unroll
         for (int f = 0; f < NF; ++f)
             acc[m][f] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    const auto multiply = [&](int slot) {
-        const uint8_t *st = lds + slot * S::kStage + off;
-        uint4 xq[MF], wq[NF];
-#pragma unroll
-        for (int f = 0; f < NF; ++f)
-            wq[f] = *reinterpret_cast<const uint4 *>(st + (BM + 16 * f) * S::kRow);
-#pragma unroll
-        for (int m = 0; m < MF; ++m)
-            xq[m] = *reinterpret_cast<const uint4 *>(st + 16 * (wm * MF + m) * S::kRow);
-#pragma unroll
-        for (int m = 0; m < MF; ++m)
+    const auto go = [&](auto ring) {
+        ring.start();
+        meanwhile();
+        const uint8_t *xl = lds + off + wm * MF * 16 * S::kRow, *wl = lds + off + NX * S::kX;
+        int xs = 0, ws = 0;
+        for (int k = H / 128; k > 0; --k) {
+            // the step has landed, and the one before it is done with
+            // everywhere: its stage takes the next load
+            ring.wait();
+            raw_barrier();
+            uint4 xq[MF], wq[NF];
 #pragma unroll
             for (int f = 0; f < NF; ++f)
-                acc[m][f] = mfma<DT>(wq[f], xq[m], acc[m][f]);
+                wq[f] = *reinterpret_cast<const uint4 *>(wl + ws + 16 * f * S::kRow);
+#pragma unroll
+            for (int m = 0; m < MF; ++m)
+                xq[m] = *reinterpret_cast<const uint4 *>(xl + xs + 16 * m * S::kRow);
+            ring.load();
+            xs = xs + S::kX == NX * S::kX ? 0 : xs + S::kX;
+            ws = ws + S::kR == NR * S::kR ? 0 : ws + S::kR;
+#pragma unroll
+            for (int m = 0; m < MF; ++m)
+#pragma unroll
+                for (int f = 0; f < NF; ++f)
+                    acc[m][f] = mfma<DT>(wq[f], xq[m], acc[m][f]);
+        }
     };
-    const int steps = H / 128;
-    int slot = 0;
-    for (int k = 0; k < min(steps, NS - 1); ++k)
-        load(k, k);
-    meanwhile();
-    for (int k = 0; k + NS <= steps; ++k) {
-        // step k has landed; step k - 1, whose stage is refilled, is done
-        wait_vmcnt<(NS - 2) * U>();
-        raw_barrier();
-        load(k + NS - 1, slot == 0 ? NS - 1 : slot - 1);
-        multiply(slot);
-        slot = slot + 1 == NS ? 0 : slot + 1;
-    }
+    if (wave < kHalf)
+        go(Ring<S::UX, NX, S::kX, S::kRow>(x, H, wave * S::UX, l0, xrow));
+    else
+        go(Ring<S::UR, NR, S::kR, S::kRow>(w, H, (wave - kHalf) * S::UR, l0 + NX * S::kX, wrow));
     wait_vmcnt<0>();
-    raw_barrier();
-    for (int k = min(steps, NS - 1); k > 0; --k) {
-        multiply(slot);
-        slot = slot + 1 == NS ? 0 : slot + 1;
-    }
     __syncthreads();
     v4f *part = reinterpret_cast<v4f *>(lds);
 #pragma unroll
@@ -298,15 +329,14 @@ __device__ __forceinline__ void stream_tile(int H, const uint16_t *__restrict__ 
 // adapter's A is read by as few workgroups as its rows allow, in whatever
 // order they come.
 // ---------------------------------------------------------------------------
-constexpr int kFewStages = 8;
-using FewStream = Stream<16, 16, 1, kFewStages>;
+using FewStream = Stream<16, 16, 1, 16, 16>;
 
 template <int DT>
-__global__ void __launch_bounds__(64 * FewStream::kWaves)
+__global__ void __launch_bounds__(FewStream::kThreads)
 shrink_few_kernel(AShape s, const uint16_t *__restrict__ x, const int32_t *__restrict__ ids,
                   const uint16_t *__restrict__ a, float *__restrict__ v)
 {
-    static_assert(64 * FewStream::kWaves == kFewRows, "a thread looks at one row");
+    static_assert(FewStream::kThreads == kFewRows, "a thread looks at one row");
     __shared__ __align__(1024) uint8_t lds[FewStream::kLds];
     __shared__ uint64_t mask[kFewRows / 64];
     __shared__ int member[16];
@@ -342,8 +372,8 @@ shrink_few_kernel(AShape s, const uint16_t *__restrict__ x, const int32_t *__res
     __syncthreads();
     const int j0 = blockIdx.y * 16;
     v4f sum[1] = {v4f{0.0f, 0.0f, 0.0f, 0.0f}};
-    stream_tile<DT, 16, 16, 1, kFewStages>(
-        s.H, x, [&](int i) { return member[i] < 0 ? t : member[i]; },
+    stream_tile<DT>(
+        FewStream{}, s.H, x, [&](int i) { return member[i] < 0 ? t : member[i]; },
         a + (size_t)id * s.r * s.H, [&](int i) { return min(j0 + i, s.r - 1); }, lds, [] {}, sum);
     const int row = member[lane & 15], j = j0 + 4 * (lane >> 4);
     if (wave == 0 && row >= 0 && j < s.r)
@@ -351,13 +381,14 @@ shrink_few_kernel(AShape s, const uint16_t *__restrict__ x, const int32_t *__res
 }
 
 // Shrink, many rows, ordered: workgroup (32 places, BN of the rank).
-template <int DT, int BN, int NS>
-__global__ void __launch_bounds__((64 * Stream<32, BN, 2, NS>::kWaves))
+template <int DT, int BN, int NX, int NR>
+__global__ void __launch_bounds__((Stream<32, BN, 2, NX, NR>::kThreads))
 shrink_many_kernel(AShape s, const uint16_t *__restrict__ x, const int32_t *__restrict__ ids,
                    const int32_t *__restrict__ order, const uint16_t *__restrict__ a,
                    float *__restrict__ v)
 {
-    __shared__ __align__(1024) uint8_t lds[Stream<32, BN, 2, NS>::kLds];
+    using S = Stream<32, BN, 2, NX, NR>;
+    __shared__ __align__(1024) uint8_t lds[S::kLds];
     const int lane = threadIdx.x & 63, wave = wave_of();
     const long i0 = (long)blockIdx.x * 32;
     const Row row = row_at(s, order, ids, i0 + (lane & 31));
@@ -370,8 +401,8 @@ shrink_many_kernel(AShape s, const uint16_t *__restrict__ x, const int32_t *__re
 #pragma unroll
         for (int f = 0; f < BN / 16; ++f)
             sum[f] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-        stream_tile<DT, 32, BN, 2, NS>(
-            s.H, x, [&](int i) { return row_at(s, order, ids, i0 + i).t; },
+        stream_tile<DT>(
+            S{}, s.H, x, [&](int i) { return row_at(s, order, ids, i0 + i).t; },
             a + (size_t)g * s.r * s.H, [&](int i) { return min(j0 + i, s.r - 1); }, lds, [] {}, sum);
         const Row mine = row_at(s, order, ids, i0 + 16 * wave + (lane & 15));
         if (wave < 2 && mine.id == g)
@@ -493,6 +524,9 @@ __device__ __forceinline__ void expand(const AShape &s, const float *__restrict_
             }
         } while (todo);
     }
+    // leave no load of this function's in flight: the compiler would look
+    // after it with a wait in the caller's loop
+    wait_vmcnt<0>();
 }
 
 // The 4 NF neighbouring columns of one row that a lane holds, rounded and
@@ -525,15 +559,15 @@ __device__ __forceinline__ void store_cols(const AShape &s, uint16_t *out, int t
 // first, while the first steps of W are on their way: at the end its chain
 // of loads (ids, v, B) would stand alone.
 // ---------------------------------------------------------------------------
-template <int DT, int BM, int WM, int NS>
-__global__ void __launch_bounds__((64 * Stream<BM, 32, WM, NS>::kWaves))
+template <int DT, typename S, int BM>
+__global__ void __launch_bounds__(S::kThreads)
 project_few_kernel(AShape s, const uint16_t *__restrict__ x, const uint16_t *__restrict__ w,
                    const int32_t *__restrict__ ids, const uint16_t *__restrict__ b,
                    const float *__restrict__ scale, const float *__restrict__ v,
                    uint16_t *__restrict__ out)
 {
     constexpr int NF = 2;
-    __shared__ __align__(1024) uint8_t lds[Stream<BM, 32, WM, NS>::kLds];
+    __shared__ __align__(1024) uint8_t lds[S::kLds];
     const int lane = threadIdx.x & 63, wave = wave_of();
     const int n0 = blockIdx.x * 32;
     const long i = 16 * wave + (lane & 15);
@@ -541,8 +575,8 @@ project_few_kernel(AShape s, const uint16_t *__restrict__ x, const uint16_t *__r
 #pragma unroll
     for (int f = 0; f < NF; ++f)
         sum[f] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    stream_tile<DT, BM, 32, WM, NS>(
-        s.H, x, [&](int r) { return min(r, s.T - 1); }, w + (size_t)n0 * s.H,
+    stream_tile<DT>(
+        S{}, s.H, x, [&](int r) { return min(r, s.T - 1); }, w + (size_t)n0 * s.H,
         [&](int r) { return min(column_of<NF>(r >> 4, r & 15), s.N - 1 - n0); }, lds,
         [&] {
             if (wave < BM / 16)
@@ -812,19 +846,16 @@ template <int DT>
 hipError_t shrink_many(const AShape &s, const uint16_t *x, const int32_t *ids,
                        const int32_t *order, const uint16_t *a, float *v, hipStream_t st)
 {
-    const auto go = [&](auto bn, auto ns) {
-        constexpr int BN = decltype(bn)::value, NS = decltype(ns)::value;
-        shrink_many_kernel<DT, BN, NS>
-            <<<dim3(up(s.T, 32), up(s.r, BN)), 64 * Stream<32, BN, 2, NS>::kWaves, 0, st>>>(
-                s, x, ids, order, a, v);
-    };
     // as much of the rank per workgroup as there is (x is read once per
-    // block of the rank), but a workgroup for every CU
+    // block of the rank), but a workgroup for every CU; x comes from memory
+    // and gets the deeper ring
     const int cus = device_cu_count(), t = up(s.T, 32);
     if (s.r > 32 && t * up(s.r, 64) >= cus)
-        go(std::integral_constant<int, 64>{}, std::integral_constant<int, 6>{});
+        shrink_many_kernel<DT, 64, 8, 6>
+            <<<dim3(t, up(s.r, 64)), 512, 0, st>>>(s, x, ids, order, a, v);
     else
-        go(std::integral_constant<int, 32>{}, std::integral_constant<int, 5>{});
+        shrink_many_kernel<DT, 32, 10, 8>
+            <<<dim3(t, up(s.r, 32)), 512, 0, st>>>(s, x, ids, order, a, v);
     return hipGetLastError();
 }
 
@@ -847,7 +878,7 @@ hipError_t adapter_of_type(const moe_adapter_shape &sh, const void *x_, const vo
     }
     if (s.T <= kFewRows) {
         shrink_few_kernel<DT>
-            <<<dim3(s.T, up(s.r, 16)), 64 * FewStream::kWaves, 0, st>>>(s, x, ids, a, v);
+            <<<dim3(s.T, up(s.r, 16)), FewStream::kThreads, 0, st>>>(s, x, ids, a, v);
         e = hipGetLastError();
     } else {
         e = shrink_many<DT>(s, x, ids, order, a, v, st);
@@ -859,25 +890,20 @@ hipError_t adapter_of_type(const moe_adapter_shape &sh, const void *x_, const vo
             s, static_cast<const uint16_t *>(base), ids, order, b, scale, v, out);
         return hipGetLastError();
     }
-    const auto few = [&](auto bm, auto wm, auto ns) {
-        constexpr int BM = decltype(bm)::value, WM = decltype(wm)::value,
-                      NS = decltype(ns)::value;
-        project_few_kernel<DT, BM, WM, NS>
-            <<<up(s.N, 32), 64 * Stream<BM, 32, WM, NS>::kWaves, 0, st>>>(s, x, w, ids, b, scale,
-                                                                          v, out);
+    // W comes from memory and gets the deeper ring
+    const auto few = [&](auto stream, auto bm) {
+        using S = decltype(stream);
+        project_few_kernel<DT, S, decltype(bm)::value>
+            <<<up(s.N, 32), S::kThreads, 0, st>>>(s, x, w, ids, b, scale, v, out);
     };
     if (s.T <= 16)
-        few(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{},
-            std::integral_constant<int, 8>{});
+        few(Stream<16, 32, 1, 6, 16>{}, std::integral_constant<int, 16>{});
     else if (s.T <= 32)
-        few(std::integral_constant<int, 32>{}, std::integral_constant<int, 2>{},
-            std::integral_constant<int, 8>{});
+        few(Stream<32, 32, 2, 4, 15>{}, std::integral_constant<int, 32>{});
     else if (s.T <= 64)
-        few(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{},
-            std::integral_constant<int, 6>{});
+        few(Stream<64, 32, 2, 3, 13>{}, std::integral_constant<int, 64>{});
     else if (s.T <= 128)
-        few(std::integral_constant<int, 128>{}, std::integral_constant<int, 2>{},
-            std::integral_constant<int, 4>{});
+        few(Stream<128, 32, 2, 3, 8>{}, std::integral_constant<int, 128>{});
     else {
         const ProjectArgs p{x, w, ids, order, b, scale, v, out};
         const int cus = device_cu_count();

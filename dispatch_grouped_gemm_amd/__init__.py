@@ -114,8 +114,15 @@ class TileEntry(ctypes.Structure):
         return {n: int(getattr(self, n)) for n, _ in self._fields_}
 
 
+class _Shape:
+    """What a shape object keeps for its calls (_kept) stays out of its copies."""
+
+    def __getstate__(self):
+        return {k: v for k, v in self.__dict__.items() if not k.startswith("_")}
+
+
 @dataclass(frozen=True)
-class MoeShape:
+class MoeShape(_Shape):
     T: int
     H: int
     I: int
@@ -142,7 +149,7 @@ class MoeShape:
 
 
 @dataclass(frozen=True)
-class AdapterShape:
+class AdapterShape(_Shape):
     """Sizes of moe_adapter_project: T rows of H values to N, L adapters of `rank`."""
     T: int
     H: int
@@ -793,29 +800,62 @@ def moe_forward_persistent(shape: MoeShape, x_fp8, x_scale, topk_ids, topk_w, w1
 # ---- the router, the rows to their experts and back, the adapters -----------------
 
 _ELEM = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-_I32 = {torch.int32}
-_F32 = {torch.float32}
 
 
-def _elem(t: torch.Tensor, name: str, allowed=(0, 1, 2)):
-    """The element code, dtype set and device that a call's other tensors share."""
+def _elem(t: torch.Tensor, name: str, most: int = 2):
+    """The element code, dtype and device that a call's other tensors share."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a tensor" % name)
-    code = _ELEM.get(t.dtype)
-    if code not in allowed:
-        raise TypeError("%s has dtype %s" % (name, t.dtype))
-    if t.device.type != "cuda":
-        raise ValueError("%s is on %s, expected a GPU" % (name, t.device))
-    return code, {t.dtype}, t.device
+    dt, dev = t.dtype, t.device
+    code = _ELEM.get(dt, 9)
+    if code > most:
+        raise TypeError("%s has dtype %s" % (name, dt))
+    if dev.type != "cuda":
+        raise ValueError("%s is on %s, expected a GPU" % (name, dev))
+    return code, dt, dev
 
 
-def _launch(fn, where: str, device, *args):
-    """Call fn(*args) with the tensors' device current."""
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args), where)
+def _at(t, name: str, shape: tuple, dtype, device) -> int:
+    """_ptr for one dtype; these calls are short enough for its time to count."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device
+            and t.shape == shape and t.is_contiguous()):
+        return t.data_ptr()
+    return _ptr(t, name, shape, {dtype}, device)
+
+
+def _kept(shape, name: str, make):
+    """make(shape), kept with the (immutable) shape object."""
+    got = shape.__dict__.get(name)
+    if got is None:
+        got = make(shape)
+        object.__setattr__(shape, name, got)
+    return got
+
+
+def _ref(shape):
+    return _kept(shape, "_c_ref", lambda s: ctypes.byref(s.c()))
+
+
+def _row_sizes(shape: MoeShape):
+    """(T, H), (row capacity, H), (T*K,) and (T, K), as alloc_dispatch sizes them."""
+    return _kept(shape, "_rows", lambda s: (
+        (s.T, s.H), (max(moe_row_capacity(s), 1), s.H), (max(s.T * s.K, 1),), (s.T, s.K)))
+
+
+def _launch(name: str, device, stream, *args):
+    """Call the C function on `stream` with the tensors' device current."""
+    fn = getattr(_lib or lib(), name)
+    if stream is None:
+        st = torch._C._cuda_getCurrentRawStream(device.index)
+    else:
+        st = _stream(stream, device)
+    if device.index == torch._C._cuda_getDevice():
+        rc = fn(*args, st)
     else:
         with torch.cuda.device(device):
-            _check(fn(*args), where)
+            rc = fn(*args, st)
+    if rc:
+        raise MoeError(rc, name)
 
 
 def moe_route(shape: MoeShape, logits, topk_ids, topk_w, renormalize: bool = True, stream=None):
@@ -823,69 +863,57 @@ def moe_route(shape: MoeShape, logits, topk_ids, topk_w, renormalize: bool = Tru
     [T, K], the K largest in falling order (equal ones by the lower id), weights the
     softmax over them (renormalize) or over all experts.  -inf and NaN are never
     chosen; slots left over get -1 and 0."""
-    code, dts, dev = _elem(logits, "logits")
-    T, K = shape.T, shape.K
-    args = [_ptr(logits, "logits", (T, shape.E_total), dts, dev), 1 if renormalize else 0,
-            _ptr(topk_ids, "topk_ids", (T, K), _I32, dev),
-            _ptr(topk_w, "topk_w", (T, K), _F32, dev)]
-    _launch(lib().moe_route, "moe_route", dev, ctypes.byref(shape.c()), code, *args,
-            _stream(stream, dev))
+    code, dt, dev = _elem(logits, "logits")
+    tk = (shape.T, shape.K)
+    _launch("moe_route", dev, stream, _ref(shape), code,
+            _at(logits, "logits", (shape.T, shape.E_total), dt, dev), 1 if renormalize else 0,
+            _at(topk_ids, "topk_ids", tk, torch.int32, dev),
+            _at(topk_w, "topk_w", tk, torch.float32, dev))
 
 
 def moe_route_backward(shape: MoeShape, logits, topk_ids, topk_w, dtopk_w, dlogits,
                        renormalize: bool = True, stream=None):
     """dlogits [T, E_total] from dtopk_w [T, K] and moe_route's ids and weights; logits
     may be None when the weights were renormalised."""
-    code, dts, dev = _elem(dlogits, "dlogits")
-    T, K, E = shape.T, shape.K, shape.E_total
+    code, dt, dev = _elem(dlogits, "dlogits")
+    te, tk = (shape.T, shape.E_total), (shape.T, shape.K)
     lp = None
     if logits is not None or not renormalize:
-        lp = _ptr(logits, "logits", (T, E), dts, dev)
-    args = [lp, 1 if renormalize else 0, _ptr(topk_ids, "topk_ids", (T, K), _I32, dev),
-            _ptr(topk_w, "topk_w", (T, K), _F32, dev),
-            _ptr(dtopk_w, "dtopk_w", (T, K), _F32, dev),
-            _ptr(dlogits, "dlogits", (T, E), dts, dev)]
-    _launch(lib().moe_route_backward, "moe_route_backward", dev, ctypes.byref(shape.c()), code,
-            *args, _stream(stream, dev))
-
-
-def _row_sizes(shape: MoeShape):
-    """(T, H), (row capacity, H) and (T*K,), as alloc_dispatch sizes them."""
-    return ((shape.T, shape.H), (max(moe_row_capacity(shape), 1), shape.H),
-            (max(shape.T * shape.K, 1),))
+        lp = _at(logits, "logits", te, dt, dev)
+    _launch("moe_route_backward", dev, stream, _ref(shape), code, lp, 1 if renormalize else 0,
+            _at(topk_ids, "topk_ids", tk, torch.int32, dev),
+            _at(topk_w, "topk_w", tk, torch.float32, dev),
+            _at(dtopk_w, "dtopk_w", tk, torch.float32, dev),
+            _at(dlogits, "dlogits", te, dt, dev))
 
 
 def moe_permute(shape: MoeShape, x, route_row, rows, stream=None):
     """rows[route_row[t, k]] = x[t]: token rows [T, H] to the rows [R, H] of their
     experts (route_row of moe_dispatch); rows without a route are left as they are."""
-    code, dts, dev = _elem(x, "x")
-    tok, row, slots = _row_sizes(shape)
-    args = [_ptr(x, "x", tok, dts, dev), _ptr(route_row, "route_row", slots, _I32, dev),
-            _ptr(rows, "rows", row, dts, dev)]
-    _launch(lib().moe_permute, "moe_permute", dev, ctypes.byref(shape.c()), code, *args,
-            _stream(stream, dev))
+    code, dt, dev = _elem(x, "x")
+    tok, row, slots, _ = _row_sizes(shape)
+    _launch("moe_permute", dev, stream, _ref(shape), code, _at(x, "x", tok, dt, dev),
+            _at(route_row, "route_row", slots, torch.int32, dev),
+            _at(rows, "rows", row, dt, dev))
 
 
 def moe_permute_backward(shape: MoeShape, drows, route_row, dx, stream=None):
     """dx[t] = sum over k of drows[route_row[t, k]]: moe_permute's gradient."""
-    code, dts, dev = _elem(drows, "drows")
-    tok, row, slots = _row_sizes(shape)
-    args = [_ptr(drows, "drows", row, dts, dev), _ptr(route_row, "route_row", slots, _I32, dev),
-            _ptr(dx, "dx", tok, dts, dev)]
-    _launch(lib().moe_permute_backward, "moe_permute_backward", dev, ctypes.byref(shape.c()),
-            code, *args, _stream(stream, dev))
+    code, dt, dev = _elem(drows, "drows")
+    tok, row, slots, _ = _row_sizes(shape)
+    _launch("moe_permute_backward", dev, stream, _ref(shape), code,
+            _at(drows, "drows", row, dt, dev),
+            _at(route_row, "route_row", slots, torch.int32, dev), _at(dx, "dx", tok, dt, dev))
 
 
 def moe_unpermute(shape: MoeShape, rows, topk_w, route_row, out, stream=None):
     """out[t] = sum over k of topk_w[t, k] rows[route_row[t, k]] (topk_w None: weights
     of 1), in float32, k ascending, rounded once."""
-    code, dts, dev = _elem(rows, "rows")
-    tok, row, slots = _row_sizes(shape)
-    wp = None if topk_w is None else _ptr(topk_w, "topk_w", (shape.T, shape.K), _F32, dev)
-    args = [_ptr(rows, "rows", row, dts, dev), wp,
-            _ptr(route_row, "route_row", slots, _I32, dev), _ptr(out, "out", tok, dts, dev)]
-    _launch(lib().moe_unpermute, "moe_unpermute", dev, ctypes.byref(shape.c()), code, *args,
-            _stream(stream, dev))
+    code, dt, dev = _elem(rows, "rows")
+    tok, row, slots, tk = _row_sizes(shape)
+    _launch("moe_unpermute", dev, stream, _ref(shape), code, _at(rows, "rows", row, dt, dev),
+            None if topk_w is None else _at(topk_w, "topk_w", tk, torch.float32, dev),
+            _at(route_row, "route_row", slots, torch.int32, dev), _at(out, "out", tok, dt, dev))
 
 
 def moe_unpermute_backward(shape: MoeShape, dout, rows, topk_w, route_row, drows, dtopk_w,
@@ -893,27 +921,25 @@ def moe_unpermute_backward(shape: MoeShape, dout, rows, topk_w, route_row, drows
     """moe_unpermute's gradients: drows[route_row[t, k]] = topk_w[t, k] dout[t] and
     dtopk_w[t, k] = <dout[t], rows[route_row[t, k]]> (0 for skipped slots).  drows or
     dtopk_w may be None; rows may be None without dtopk_w."""
-    code, dts, dev = _elem(dout, "dout")
-    tok, row, slots = _row_sizes(shape)
-    tk = (shape.T, shape.K)
+    code, dt, dev = _elem(dout, "dout")
+    tok, row, slots, tk = _row_sizes(shape)
     if drows is None and dtopk_w is None:
         raise ValueError("moe_unpermute_backward: give drows, dtopk_w or both")
-    args = [_ptr(dout, "dout", tok, dts, dev),
-            None if rows is None and dtopk_w is None else _ptr(rows, "rows", row, dts, dev),
-            None if topk_w is None else _ptr(topk_w, "topk_w", tk, _F32, dev),
-            _ptr(route_row, "route_row", slots, _I32, dev),
-            None if drows is None else _ptr(drows, "drows", row, dts, dev),
-            None if dtopk_w is None else _ptr(dtopk_w, "dtopk_w", tk, _F32, dev)]
-    _launch(lib().moe_unpermute_backward, "moe_unpermute_backward", dev,
-            ctypes.byref(shape.c()), code, *args, _stream(stream, dev))
+    _launch("moe_unpermute_backward", dev, stream, _ref(shape), code,
+            _at(dout, "dout", tok, dt, dev),
+            None if rows is None and dtopk_w is None else _at(rows, "rows", row, dt, dev),
+            None if topk_w is None else _at(topk_w, "topk_w", tk, torch.float32, dev),
+            _at(route_row, "route_row", slots, torch.int32, dev),
+            None if drows is None else _at(drows, "drows", row, dt, dev),
+            None if dtopk_w is None else _at(dtopk_w, "dtopk_w", tk, torch.float32, dev))
 
 
 def moe_adapter_check(shape: AdapterShape) -> int:
-    return lib().moe_adapter_check(ctypes.byref(shape.c()))
+    return lib().moe_adapter_check(_ref(shape))
 
 
 def moe_adapter_workspace_size(shape: AdapterShape) -> int:
-    return int(lib().moe_adapter_workspace_size(ctypes.byref(shape.c())))
+    return int(lib().moe_adapter_workspace_size(_ref(shape)))
 
 
 def alloc_adapter_workspace(shape: AdapterShape, device) -> torch.Tensor:
@@ -928,17 +954,15 @@ def moe_adapter_project(shape: AdapterShape, x, w, adapter_ids, a, b, scale, out
     adapter), base = x W^T for a shared weight w [N, H], or the given base [T, N] (w
     None; base may be out).  x [T, H], a [L, rank, H], b [L, N, rank], scale float32
     [L] or None, out [T, N], bf16 or fp16; workspace of alloc_adapter_workspace."""
-    code, dts, dev = _elem(x, "x", (0, 1))
+    code, dt, dev = _elem(x, "x", 1)
     T, H, N, L, r = shape.T, shape.H, shape.N, shape.L, shape.rank
     if (w is None) == (base is None):
         raise ValueError("moe_adapter_project: give w or base")
-    args = [_ptr(x, "x", (T, H), dts, dev),
-            None if w is None else _ptr(w, "w", (N, H), dts, dev),
-            None if base is None else _ptr(base, "base", (T, N), dts, dev),
-            _ptr(adapter_ids, "adapter_ids", (T,), _I32, dev),
-            _ptr(a, "a", (L, r, H), dts, dev), _ptr(b, "b", (L, N, r), dts, dev),
-            None if scale is None else _ptr(scale, "scale", (L,), _F32, dev),
-            _ptr(out, "out", (T, N), dts, dev)]
-    ws = _ptr(workspace, "workspace", None, {torch.uint8}, dev)
-    _launch(lib().moe_adapter_project, "moe_adapter_project", dev, ctypes.byref(shape.c()), code,
-            *args, ws, workspace.numel(), _stream(stream, dev))
+    _launch("moe_adapter_project", dev, stream, _ref(shape), code, _at(x, "x", (T, H), dt, dev),
+            None if w is None else _at(w, "w", (N, H), dt, dev),
+            None if base is None else _at(base, "base", (T, N), dt, dev),
+            _at(adapter_ids, "adapter_ids", (T,), torch.int32, dev),
+            _at(a, "a", (L, r, H), dt, dev), _at(b, "b", (L, N, r), dt, dev),
+            None if scale is None else _at(scale, "scale", (L,), torch.float32, dev),
+            _at(out, "out", (T, N), dt, dev),
+            _ptr(workspace, "workspace", None, {torch.uint8}, dev), workspace.numel())

@@ -18,6 +18,8 @@
 // the sum of two 16-bit values, hi = round(v) and lo = round(v - hi).  fp16
 // lacks float32's range, so there v is first divided by a power of two that
 // puts the row's largest magnitude below 1, and the product multiplied by it.
+#include <algorithm>
+
 #include "elem.hpp"
 
 namespace moe {
@@ -218,9 +220,10 @@ struct Ring {
     // `first`: this wavefront's first load of a stage; row(i): number of the
     // stage's row i in the array at p
     template <typename Row>
-    __device__ __forceinline__ Ring(const uint16_t *p, int H, int first, uint32_t lds, Row row)
+    __device__ __forceinline__ Ring(const uint16_t *p, int H, int steps, int first, uint32_t lds,
+                                    Row row)
         : next(reinterpret_cast<const uint8_t *>(p)), lds0(lds + first * 1024), slot(0),
-          left(H / 128 - 1)
+          left(steps - 1)
     {
         const int lane = threadIdx.x & 63;
 #pragma unroll
@@ -247,16 +250,15 @@ struct Ring {
     __device__ __forceinline__ void wait() { wait_vmcnt<(N - 2) * U>(); }
 };
 
-// Rows [0, BM) come from x, columns [0, BN) from the rows of w: xrow(i) and
-// wrow(i) give their numbers, w's within 2^31 bytes of its base.  Afterwards
-// wavefront m < BM / 16 has added rows 16 m .. 16 m + 15 to sum.  meanwhile()
-// runs once the first loads are on their way.
-template <int DT, int BM, int BN, int WM, int NX, int NR, typename XRow, typename WRow,
-          typename Mean>
-__device__ __forceinline__ void stream_tile(Stream<BM, BN, WM, NX, NR>, int H,
+// `steps` steps from x and w on.  Rows [0, BM) come from x, columns [0, BN)
+// from the rows of w: xrow(i) and wrow(i) give their numbers, w's within
+// 2^31 bytes of its base.  Afterwards wavefront m < BM / 16 (of the first
+// kWaves, in turn) has rows 16 m .. 16 m + 15 in sum.
+template <int DT, int BM, int BN, int WM, int NX, int NR, typename XRow, typename WRow>
+__device__ __forceinline__ void stream_tile(Stream<BM, BN, WM, NX, NR>, int H, int steps,
                                             const uint16_t *__restrict__ x, XRow xrow,
                                             const uint16_t *__restrict__ w, WRow wrow,
-                                            uint8_t *lds, Mean meanwhile, v4f *sum)
+                                            uint8_t *lds, v4f *sum)
 {
     using S = Stream<BM, BN, WM, NX, NR>;
     constexpr int MF = S::MF, NF = S::NF, kHalf = S::kWaves / 2;
@@ -272,10 +274,9 @@ __device__ __forceinline__ void stream_tile(Stream<BM, BN, WM, NX, NR>, int H,
             acc[m][f] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     const auto go = [&](auto ring) {
         ring.start();
-        meanwhile();
         const uint8_t *xl = lds + off + wm * MF * 16 * S::kRow, *wl = lds + off + NX * S::kX;
         int xs = 0, ws = 0;
-        for (int k = H / 128; k > 0; --k) {
+        for (int k = steps; k > 0; --k) {
             // the step has landed, and the one before it is done with
             // everywhere: its stage takes the next load
             ring.wait();
@@ -298,9 +299,10 @@ __device__ __forceinline__ void stream_tile(Stream<BM, BN, WM, NX, NR>, int H,
         }
     };
     if (wave < kHalf)
-        go(Ring<S::UX, NX, S::kX, S::kRow>(x, H, wave * S::UX, l0, xrow));
+        go(Ring<S::UX, NX, S::kX, S::kRow>(x, H, steps, wave * S::UX, l0, xrow));
     else
-        go(Ring<S::UR, NR, S::kR, S::kRow>(w, H, (wave - kHalf) * S::UR, l0 + NX * S::kX, wrow));
+        go(Ring<S::UR, NR, S::kR, S::kRow>(w, H, steps, (wave - kHalf) * S::UR,
+                                           l0 + NX * S::kX, wrow));
     wait_vmcnt<0>();
     __syncthreads();
     v4f *part = reinterpret_cast<v4f *>(lds);
@@ -310,14 +312,19 @@ __device__ __forceinline__ void stream_tile(Stream<BM, BN, WM, NX, NR>, int H,
         for (int f = 0; f < NF; ++f)
             part[((kq * (BM / 16) + wm * MF + m) * NF + f) * 64 + lane] = acc[m][f];
     __syncthreads();
-    if (wave < BM / 16) {
+    // block of 16 rows q * kWaves + wave in sum + q * NF
+#pragma unroll
+    for (int q = 0; q * S::kWaves < BM / 16; ++q) {
+        const int m = q * S::kWaves + wave;
+        if (m >= BM / 16)
+            break;
 #pragma unroll
         for (int f = 0; f < NF; ++f) {
-            v4f q = part[(wave * NF + f) * 64 + lane];
+            v4f a = part[(m * NF + f) * 64 + lane];
 #pragma unroll
             for (int k = 1; k < 4; ++k)
-                q += part[((k * (BM / 16) + wave) * NF + f) * 64 + lane];
-            sum[f] += q;
+                a += part[((k * (BM / 16) + m) * NF + f) * 64 + lane];
+            sum[q * NF + f] = a;
         }
     }
 }
@@ -332,15 +339,15 @@ __device__ __forceinline__ void stream_tile(Stream<BM, BN, WM, NX, NR>, int H,
 using FewStream = Stream<16, 16, 1, 16, 16>;
 
 template <int DT>
-__global__ void __launch_bounds__(FewStream::kThreads)
-shrink_few_kernel(AShape s, const uint16_t *__restrict__ x, const int32_t *__restrict__ ids,
-                  const uint16_t *__restrict__ a, float *__restrict__ v)
+__device__ __forceinline__ void shrink_few(const AShape &s, const uint16_t *__restrict__ x,
+                                           const int32_t *__restrict__ ids,
+                                           const uint16_t *__restrict__ a, float *__restrict__ v,
+                                           int t, int j0, uint8_t *lds)
 {
     static_assert(FewStream::kThreads == kFewRows, "a thread looks at one row");
-    __shared__ __align__(1024) uint8_t lds[FewStream::kLds];
     __shared__ uint64_t mask[kFewRows / 64];
     __shared__ int member[16];
-    const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = wave_of();
+    const int tid = threadIdx.x, lane = tid & 63, wave = wave_of();
     const int id = ids[t];
     if ((unsigned)id >= (unsigned)s.L)
         return;
@@ -370,42 +377,48 @@ shrink_few_kernel(AShape s, const uint16_t *__restrict__ x, const int32_t *__res
             member[at] = tid;
     }
     __syncthreads();
-    const int j0 = blockIdx.y * 16;
-    v4f sum[1] = {v4f{0.0f, 0.0f, 0.0f, 0.0f}};
+    v4f sum[1];
     stream_tile<DT>(
-        FewStream{}, s.H, x, [&](int i) { return member[i] < 0 ? t : member[i]; },
-        a + (size_t)id * s.r * s.H, [&](int i) { return min(j0 + i, s.r - 1); }, lds, [] {}, sum);
+        FewStream{}, s.H, s.H / 128, x, [&](int i) { return member[i] < 0 ? t : member[i]; },
+        a + (size_t)id * s.r * s.H, [&](int i) { return min(j0 + i, s.r - 1); }, lds, sum);
     const int row = member[lane & 15], j = j0 + 4 * (lane >> 4);
     if (wave == 0 && row >= 0 && j < s.r)
         *reinterpret_cast<v4f *>(v + (size_t)row * s.r + j) = sum[0];
 }
 
-// Shrink, many rows, ordered: workgroup (32 places, BN of the rank).
-template <int DT, int BN, int NX, int NR>
-__global__ void __launch_bounds__((Stream<32, BN, 2, NX, NR>::kThreads))
+template <int DT>
+__global__ void __launch_bounds__(FewStream::kThreads)
+shrink_few_kernel(AShape s, const uint16_t *__restrict__ x, const int32_t *__restrict__ ids,
+                  const uint16_t *__restrict__ a, float *__restrict__ v)
+{
+    __shared__ __align__(1024) uint8_t lds[FewStream::kLds];
+    shrink_few<DT>(s, x, ids, a, v, blockIdx.x, blockIdx.y * 16, lds);
+}
+
+// Shrink, many rows, ordered: workgroup (BM places, BN of the rank).
+template <int DT, int BM, int BN, int WM, int NX, int NR>
+__global__ void __launch_bounds__((Stream<BM, BN, WM, NX, NR>::kThreads))
 shrink_many_kernel(AShape s, const uint16_t *__restrict__ x, const int32_t *__restrict__ ids,
                    const int32_t *__restrict__ order, const uint16_t *__restrict__ a,
                    float *__restrict__ v)
 {
-    using S = Stream<32, BN, 2, NX, NR>;
+    using S = Stream<BM, BN, WM, NX, NR>;
+    static_assert(BM <= 32, "the rows' adapters in one mask");
     __shared__ __align__(1024) uint8_t lds[S::kLds];
     const int lane = threadIdx.x & 63, wave = wave_of();
-    const long i0 = (long)blockIdx.x * 32;
-    const Row row = row_at(s, order, ids, i0 + (lane & 31));
+    const long i0 = (long)blockIdx.x * BM;
+    const Row row = row_at(s, order, ids, i0 + (lane & (BM - 1)));
     const int j0 = blockIdx.y * BN;
     uint32_t todo = (uint32_t)__ballot(row.id >= 0);
     while (todo) {
         const int g = __builtin_amdgcn_readlane(row.id, __builtin_ctz(todo));
         todo &= ~(uint32_t)__ballot(row.id == g);
         v4f sum[BN / 16];
-#pragma unroll
-        for (int f = 0; f < BN / 16; ++f)
-            sum[f] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
         stream_tile<DT>(
-            S{}, s.H, x, [&](int i) { return row_at(s, order, ids, i0 + i).t; },
-            a + (size_t)g * s.r * s.H, [&](int i) { return min(j0 + i, s.r - 1); }, lds, [] {}, sum);
+            S{}, s.H, s.H / 128, x, [&](int i) { return row_at(s, order, ids, i0 + i).t; },
+            a + (size_t)g * s.r * s.H, [&](int i) { return min(j0 + i, s.r - 1); }, lds, sum);
         const Row mine = row_at(s, order, ids, i0 + 16 * wave + (lane & 15));
-        if (wave < 2 && mine.id == g)
+        if (wave < BM / 16 && mine.id == g)
 #pragma unroll
             for (int f = 0; f < BN / 16; ++f) {
                 const int j = j0 + 16 * f + 4 * (lane >> 4);
@@ -419,29 +432,35 @@ shrink_many_kernel(AShape s, const uint16_t *__restrict__ x, const int32_t *__re
 // ---------------------------------------------------------------------------
 // Expand: adds the adapters' term of 16 rows (the lane's: row) to the sums of
 // 16 NF columns from n0 (in column_of's order).
-// ---------------------------------------------------------------------------
 // 64 of the rank at a time: the rows' v as hi and lo, then the adapters among
 // the rows, GB at a time with their B in flight together.  No load stands
 // behind a branch (a lane or a place without work reads a valid address and
 // drops the product): behind one the compiler waits for each by itself.
-template <int DT, int NF, int GB>
-__device__ __forceinline__ void expand(const AShape &s, const float *__restrict__ v,
-                                       const uint16_t *__restrict__ b,
-                                       const float *__restrict__ scale, const Row &row, int n0,
-                                       v4f *acc)
+// ---------------------------------------------------------------------------
+
+// 64 of the rank of the lane's row, from c: pieces k0 + 32 k of 8.
+struct Low {
+    uint4 hi[2], lo[2];
+    int at[2];
+    bool there[2];
+};
+
+// What a row needs besides: its scale, and fp16's power of two.
+struct Gain {
+    float sc;
+    int ex;
+};
+
+template <int DT>
+__device__ __forceinline__ Gain gain_of(const AShape &s, const float *__restrict__ v,
+                                        const float *__restrict__ scale, const Row &row)
 {
-    const int lane = threadIdx.x & 63;
-    const int k0 = 8 * (lane >> 4);
-    const bool has = row.id >= 0;
-    const uint32_t rows = (uint32_t)__ballot(has) & 0xffffu;
-    if (!rows)
-        return;
-    const float *vr = v + (size_t)row.t * s.r;
-    float sc = 1.0f;
+    Gain g{1.0f, 0};
     if (scale)
-        sc = scale[max(row.id, 0)];
-    int ex = 0;
+        g.sc = scale[max(row.id, 0)];
     if constexpr (DT == MOE_DT_F16) {
+        const float *vr = v + (size_t)row.t * s.r;
+        const int k0 = 8 * ((threadIdx.x & 63) >> 4);
         float top = 0.0f;
         for (int k = 0; k < s.r; k += 32) {
             const float *p = vr + min(k + k0, s.r - 8);
@@ -450,141 +469,170 @@ __device__ __forceinline__ void expand(const AShape &s, const float *__restrict_
                 const v4f q = *reinterpret_cast<const v4f *>(p + 4 * h);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    top = fmaxf(top, has ? fabsf(q[i]) : 0.0f);
+                    top = fmaxf(top, row.id >= 0 ? fabsf(q[i]) : 0.0f);
             }
         }
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
         if (top > 0.0f && top < INFINITY)
-            (void)frexpf(top, &ex);
+            (void)frexpf(top, &g.ex);
     }
+    return g;
+}
+
+template <int DT>
+__device__ __forceinline__ Low low_of(const AShape &s, const float *__restrict__ v,
+                                      const Row &row, const Gain &g, int c)
+{
+    const float *vr = v + (size_t)row.t * s.r;
+    const int k0 = 8 * ((threadIdx.x & 63) >> 4);
+    Low low;
+    v4f vq[2][2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        low.there[k] = c + 32 * k + k0 < s.r;
+        low.at[k] = low.there[k] ? c + 32 * k + k0 : 0;
+        vq[k][0] = *reinterpret_cast<const v4f *>(vr + low.at[k]);
+        vq[k][1] = *reinterpret_cast<const v4f *>(vr + low.at[k] + 4);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        float f8[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float q = low.there[k] && row.id >= 0 ? vq[k][i >> 2][i & 3] : 0.0f;
+            f8[i] = DT == MOE_DT_F16 ? ldexpf(q, -g.ex) : q;
+        }
+        split8<DT>(f8, low.hi[k], low.lo[k]);
+    }
+    return low;
+}
+
+// Adds 64 of the rank; rows: which of the 16 rows have an adapter (not 0).
+template <int DT, int NF, int GB>
+__device__ __forceinline__ void expand_part(const AShape &s, const uint16_t *__restrict__ b,
+                                            const Row &row, uint32_t rows, const Gain &gain,
+                                            const Low &low, int n0, v4f *acc)
+{
+    const int lane = threadIdx.x & 63;
     uint32_t col[NF]; // element of B_l; N * rank is below 2^28
 #pragma unroll
     for (int f = 0; f < NF; ++f)
         col[f] = (uint32_t)min(n0 + column_of<NF>(f, lane & 15), s.N - 1) * s.r;
-    for (int c = 0; c < s.r; c += 64) {
-        int at[2];
-        bool there[2];
-        v4f vq[2][2];
+    uint32_t todo = rows;
+    do {
+        int g[GB], n = 0;
+        uint4 bq[GB][2][NF];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            there[k] = c + 32 * k + k0 < s.r;
-            at[k] = there[k] ? c + 32 * k + k0 : 0;
-            vq[k][0] = *reinterpret_cast<const v4f *>(vr + at[k]);
-            vq[k][1] = *reinterpret_cast<const v4f *>(vr + at[k] + 4);
+        for (int q = 0; q < GB; ++q) {
+            const int next = __builtin_amdgcn_readlane(row.id, todo ? __builtin_ctz(todo) : 0);
+            g[q] = q == 0 || todo ? next : g[0];
+            n += todo ? 1 : 0;
+            todo &= ~(uint32_t)__ballot(row.id == g[q]);
         }
-        uint4 hi[2], lo[2];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            float f8[8];
+        for (int q = 0; q < GB; ++q) {
+            const uint16_t *bg = b + (size_t)g[q] * s.N * s.r;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float q = there[k] && has ? vq[k][i >> 2][i & 3] : 0.0f;
-                f8[i] = DT == MOE_DT_F16 ? ldexpf(q, -ex) : q;
-            }
-            split8<DT>(f8, hi[k], lo[k]);
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int f = 0; f < NF; ++f)
+                    bq[q][k][f] = piece(bg + col[f] + low.at[k]);
         }
-        uint32_t todo = rows;
-        do {
-            int g[GB], n = 0;
-            uint4 bq[GB][2][NF];
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int q = 0; q < GB; ++q) {
-                const int next = __builtin_amdgcn_readlane(row.id, todo ? __builtin_ctz(todo) : 0);
-                g[q] = q == 0 || todo ? next : g[0];
-                n += todo ? 1 : 0;
-                todo &= ~(uint32_t)__ballot(row.id == g[q]);
-            }
+        for (int q = 0; q < GB; ++q) {
+            const bool take = row.id == g[q] && q < n;
 #pragma unroll
-            for (int q = 0; q < GB; ++q) {
-                const uint16_t *bg = b + (size_t)g[q] * s.N * s.r;
+            for (int f = 0; f < NF; ++f) {
+                v4f d = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int k = 0; k < 2; ++k)
-#pragma unroll
-                    for (int f = 0; f < NF; ++f)
-                        bq[q][k][f] = piece(bg + col[f] + at[k]);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int q = 0; q < GB; ++q) {
-#pragma unroll
-                for (int f = 0; f < NF; ++f) {
-                    v4f d = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const uint4 bk = there[k] ? bq[q][k][f] : uint4{0, 0, 0, 0};
-                        d = mfma<DT>(bk, hi[k], d);
-                        d = mfma<DT>(bk, lo[k], d);
-                    }
-                    const bool take = row.id == g[q] && q < n;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        acc[f][i] += !take ? 0.0f : sc * (DT == MOE_DT_F16 ? ldexpf(d[i], ex) : d[i]);
+                for (int k = 0; k < 2; ++k) {
+                    const uint4 bk = low.there[k] ? bq[q][k][f] : uint4{0, 0, 0, 0};
+                    d = mfma<DT>(bk, low.hi[k], d);
+                    d = mfma<DT>(bk, low.lo[k], d);
                 }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    acc[f][i] +=
+                        !take ? 0.0f : gain.sc * (DT == MOE_DT_F16 ? ldexpf(d[i], gain.ex) : d[i]);
             }
-        } while (todo);
-    }
-    // leave no load of this function's in flight: the compiler would look
-    // after it with a wait in the caller's loop
-    wait_vmcnt<0>();
+        }
+    } while (todo);
+}
+
+template <int DT, int NF, int GB>
+__device__ __forceinline__ void expand(const AShape &s, const float *__restrict__ v,
+                                       const uint16_t *__restrict__ b,
+                                       const float *__restrict__ scale, const Row &row, int n0,
+                                       v4f *acc)
+{
+    const uint32_t rows = (uint32_t)__ballot(row.id >= 0) & 0xffffu;
+    if (!rows)
+        return;
+    const Gain gain = gain_of<DT>(s, v, scale, row);
+    for (int c = 0; c < s.r; c += 64)
+        expand_part<DT, NF, GB>(s, b, row, rows, gain, low_of<DT>(s, v, row, gain, c), n0, acc);
 }
 
 // The 4 NF neighbouring columns of one row that a lane holds, rounded and
-// stored (or the base's values loaded): columns from n, in pieces of 8 (N is
-// a multiple of 8; NF = 1 has pieces of 4).
+// stored, in pieces of 8 (N is a multiple of 8).
 template <int DT, int NF>
 __device__ __forceinline__ void store_cols(const AShape &s, uint16_t *out, int t, int n,
                                            const v4f *acc)
 {
     uint16_t *o = out + (size_t)t * s.N + n;
-    if constexpr (NF == 1) {
-        const float f[8] = {acc[0][0], acc[0][1], acc[0][2], acc[0][3], 0.0f, 0.0f, 0.0f, 0.0f};
-        const uint4 q = Elem<DT>::pack(f);
-        if (n < s.N)
-            *reinterpret_cast<uint2 *>(o) = uint2{q.x, q.y};
-    } else {
 #pragma unroll
-        for (int p = 0; p < NF / 2; ++p) {
-            const v4f a = acc[2 * p], b = acc[2 * p + 1];
-            const float f[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-            if (n + 8 * p < s.N)
-                *reinterpret_cast<uint4 *>(o + 8 * p) = Elem<DT>::pack(f);
-        }
+    for (int p = 0; p < NF / 2; ++p) {
+        const v4f a = acc[2 * p], b = acc[2 * p + 1];
+        const float f[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+        if (n + 8 * p < s.N)
+            *reinterpret_cast<uint4 *>(o + 8 * p) = Elem<DT>::pack(f);
     }
 }
 
 // ---------------------------------------------------------------------------
-// Project, few rows: all rows (up to BM) by 32 columns per workgroup, so W is
-// read once and x by every workgroup, from the L2.  The adapters' term comes
-// first, while the first steps of W are on their way: at the end its chain
-// of loads (ids, v, B) would stand alone.
+// Project, few rows: W is read once.  One launch makes v (its workgroups
+// first) and, beside it, parts of x W^T: a workgroup takes all rows (up to
+// BM), 64 columns and one of `splits` parts of H, and leaves float32 sums;
+// the add launch joins the parts in order and adds the adapters' term.
+// Splitting H gives every CU work without more copies of x than columns ask
+// for, and the adapters' chain of loads does not stand at the end of W's.
 // ---------------------------------------------------------------------------
 template <int DT, typename S, int BM>
 __global__ void __launch_bounds__(S::kThreads)
-project_few_kernel(AShape s, const uint16_t *__restrict__ x, const uint16_t *__restrict__ w,
-                   const int32_t *__restrict__ ids, const uint16_t *__restrict__ b,
-                   const float *__restrict__ scale, const float *__restrict__ v,
-                   uint16_t *__restrict__ out)
+few_kernel(AShape s, int shrinks, int tn, int splits, const uint16_t *__restrict__ x,
+           const uint16_t *__restrict__ w, const int32_t *__restrict__ ids,
+           const uint16_t *__restrict__ a, float *__restrict__ v, float *__restrict__ parts)
 {
-    constexpr int NF = 2;
-    __shared__ __align__(1024) uint8_t lds[S::kLds];
-    const int lane = threadIdx.x & 63, wave = wave_of();
-    const int n0 = blockIdx.x * 32;
-    const long i = 16 * wave + (lane & 15);
-    v4f sum[NF];
-#pragma unroll
-    for (int f = 0; f < NF; ++f)
-        sum[f] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    static_assert(S::kThreads == FewStream::kThreads && S::NF == 4, "one launch for both");
+    constexpr int kLds = S::kLds > FewStream::kLds ? S::kLds : FewStream::kLds;
+    __shared__ __align__(1024) uint8_t lds[kLds];
+    int q = blockIdx.x;
+    if (q < shrinks) {
+        shrink_few<DT>(s, x, ids, a, v, q % s.T, q / s.T * 16, lds);
+        return;
+    }
+    q -= shrinks;
+    const int n0 = q % tn * 64, part = q / tn;
+    const int all = s.H / 128, first = (long)all * part / splits;
+    const int steps = (int)((long)all * (part + 1) / splits) - first;
+    v4f sum[S::NF * ((BM / 16 + S::kWaves - 1) / S::kWaves)];
     stream_tile<DT>(
-        S{}, s.H, x, [&](int r) { return min(r, s.T - 1); }, w + (size_t)n0 * s.H,
-        [&](int r) { return min(column_of<NF>(r >> 4, r & 15), s.N - 1 - n0); }, lds,
-        [&] {
-            if (wave < BM / 16)
-                expand<DT, NF, 4>(s, v, b, scale, row_at(s, nullptr, ids, i), n0, sum);
-        },
-        sum);
-    if (wave < BM / 16 && i < s.T)
-        store_cols<DT, NF>(s, out, (int)i, n0 + 4 * NF * (lane >> 4), sum);
+        S{}, s.H, steps, x + 128 * first, [&](int r) { return min(r, s.T - 1); },
+        w + (size_t)n0 * s.H + 128 * first,
+        [&](int r) { return min(column_of<4>(r >> 4, r & 15), s.N - 1 - n0); }, lds, sum);
+    const int lane = threadIdx.x & 63, n = n0 + 16 * (lane >> 4);
+#pragma unroll
+    for (int m = 0; m * S::kWaves < BM / 16; ++m) {
+        const int t = 16 * (m * S::kWaves + wave_of()) + (lane & 15);
+        if (t < min(s.T, BM))
+#pragma unroll
+            for (int f = 0; f < 4; ++f)
+                if (n + 4 * f < s.N)
+                    *reinterpret_cast<v4f *>(parts + ((size_t)part * s.T + t) * s.N + n + 4 * f) =
+                        sum[m * 4 + f];
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -798,46 +846,88 @@ project_small_kernel(AShape s, int tm, int tn, ProjectArgs p)
 }
 
 // ---------------------------------------------------------------------------
-// A given base: bound by reading it and writing out.  A wavefront takes 16
-// places x 64 columns.
+// Add: out = base + the adapters' term, base a given projection, or the sum
+// of `parts` float32 planes.  Bound by reading the base and writing out.  A
+// wavefront takes 16 places and `blocks` blocks of 64 columns: their v is
+// read once for all of them (up to a rank of 64).
 // ---------------------------------------------------------------------------
 constexpr int kAddWaves = 4;
 
-template <int DT>
+template <int DT, bool kParts>
 __global__ void __launch_bounds__(64 * kAddWaves)
-add_kernel(AShape s, const uint16_t *base, const int32_t *__restrict__ ids,
+add_kernel(AShape s, int blocks, int parts, const void *base, const int32_t *__restrict__ ids,
            const int32_t *__restrict__ order, const uint16_t *__restrict__ b,
            const float *__restrict__ scale, const float *__restrict__ v, uint16_t *out)
 {
     constexpr int NF = 4;
     const int lane = threadIdx.x & 63, wave = wave_of();
-    const int n0 = (blockIdx.y * kAddWaves + wave) * 16 * NF;
+    int n0 = (blockIdx.y * kAddWaves + wave) * 64 * blocks;
     const long i = (long)blockIdx.x * 16 + (lane & 15);
-    if (n0 >= s.N)
-        return;
     const Row row = row_at(s, order, ids, i);
-    const int n = n0 + 4 * NF * (lane >> 4);
-    v4f acc[NF];
+    const uint32_t rows = (uint32_t)__ballot(row.id >= 0) & 0xffffu;
+    const Gain gain = gain_of<DT>(s, v, scale, row);
+    const Low low = low_of<DT>(s, v, row, gain, 0);
+    for (int k = 0; k < blocks && n0 < s.N; ++k, n0 += 64) {
+        const int n = n0 + 16 * (lane >> 4);
+        v4f acc[NF];
+        if constexpr (kParts) {
+            const float *p = static_cast<const float *>(base) + (size_t)row.t * s.N;
 #pragma unroll
-    for (int p = 0; p < NF / 2; ++p) {
-        float f[8] = {};
-        if (n + 8 * p < s.N)
-            Elem<DT>::unpack(piece(base + (size_t)row.t * s.N + n + 8 * p), f);
+            for (int f = 0; f < NF; ++f)
+                acc[f] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int q = 0; q < parts; ++q, p += (size_t)s.T * s.N)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            acc[2 * p][e] = f[e];
-            acc[2 * p + 1][e] = f[4 + e];
+                for (int f = 0; f < NF; ++f)
+                    acc[f] += *reinterpret_cast<const v4f *>(p + min(n + 4 * f, s.N - 4));
+        } else {
+            const uint16_t *p = static_cast<const uint16_t *>(base) + (size_t)row.t * s.N;
+#pragma unroll
+            for (int h = 0; h < NF / 2; ++h) {
+                float f[8];
+                Elem<DT>::unpack(piece(p + min(n + 8 * h, s.N - 8)), f);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    acc[2 * h][e] = f[e];
+                    acc[2 * h + 1][e] = f[4 + e];
+                }
+            }
         }
+        if (rows) {
+            expand_part<DT, NF, kParts ? 4 : 1>(s, b, row, rows, gain, low, n0, acc);
+            for (int c = 64; c < s.r; c += 64)
+                expand_part<DT, NF, 1>(s, b, row, rows, gain, low_of<DT>(s, v, row, gain, c), n0,
+                                       acc);
+        }
+        if (i < s.T)
+            store_cols<DT, NF>(s, out, row.t, n, acc);
     }
-    expand<DT, NF, 2>(s, v, b, scale, row, n0, acc);
-    if (i < s.T)
-        store_cols<DT, NF>(s, out, row.t, n, acc);
+}
+
+constexpr int kFewProject = 128; // rows projected by few_kernel
+
+// Parts of H of few_kernel for a shape: enough workgroups for every CU, up
+// to 8 and the steps there are.
+int few_splits(const moe_adapter_shape &s)
+{
+    const int tn = (s.N + 63) / 64, want = s.T > 64 ? 224 : 384;
+    return std::max(1, std::min({(want + tn - 1) / tn, 8, s.H / 128}));
+}
+
+size_t parts_bytes(const moe_adapter_shape &s)
+{
+    return s.T > kFewProject ? 0 : (size_t)few_splits(s) * s.T * s.N * sizeof(float);
 }
 
 size_t order_bytes(const moe_adapter_shape &s)
 {
     return s.T > kFewRows && s.L < kOrderKeys ? ((size_t)s.T * sizeof(int32_t) + 255) / 256 * 256
                                               : 0;
+}
+
+// x A^T of every row, 256-byte aligned ends.
+size_t v_bytes(const moe_adapter_shape &s)
+{
+    return order_bytes(s) + ((size_t)s.T * s.rank * sizeof(float) + 255) / 256 * 256;
 }
 
 int up(long n, int by) { return (int)((n + by - 1) / by); }
@@ -851,11 +941,14 @@ hipError_t shrink_many(const AShape &s, const uint16_t *x, const int32_t *ids,
     // and gets the deeper ring
     const int cus = device_cu_count(), t = up(s.T, 32);
     if (s.r > 32 && t * up(s.r, 64) >= cus)
-        shrink_many_kernel<DT, 64, 8, 6>
+        shrink_many_kernel<DT, 32, 64, 2, 8, 6>
             <<<dim3(t, up(s.r, 64)), 512, 0, st>>>(s, x, ids, order, a, v);
-    else
-        shrink_many_kernel<DT, 32, 10, 8>
+    else if (s.r > 16 && t * up(s.r, 32) >= cus)
+        shrink_many_kernel<DT, 32, 32, 2, 10, 8>
             <<<dim3(t, up(s.r, 32)), 512, 0, st>>>(s, x, ids, order, a, v);
+    else
+        shrink_many_kernel<DT, 16, 16, 1, 10, 10>
+            <<<dim3(up(s.T, 16), up(s.r, 16)), 256, 0, st>>>(s, x, ids, order, a, v);
     return hipGetLastError();
 }
 
@@ -870,7 +963,35 @@ hipError_t adapter_of_type(const moe_adapter_shape &sh, const void *x_, const vo
     auto *out = static_cast<uint16_t *>(out_);
     int32_t *order = order_bytes(sh) ? reinterpret_cast<int32_t *>(ws) : nullptr;
     float *v = reinterpret_cast<float *>(ws + order_bytes(sh));
+    const auto add = [&](auto parts_given, const void *from, int parts) {
+        // blocks of 64 columns a wavefront: one where the rows are few
+        const int blocks = s.T > kFewProject ? 4 : 1;
+        add_kernel<DT, decltype(parts_given)::value>
+            <<<dim3(up(s.T, 16), up(s.N, 64 * kAddWaves * blocks)), 64 * kAddWaves, 0, st>>>(
+                s, blocks, parts, from, ids, order, b, scale, v, out);
+        return hipGetLastError();
+    };
     hipError_t e;
+    if (s.T <= kFewProject && w) {
+        float *parts = reinterpret_cast<float *>(ws + v_bytes(sh));
+        const int tn = up(s.N, 64), splits = few_splits(sh), shrinks = s.T * up(s.r, 16);
+        const auto few = [&](auto stream, auto bm) {
+            using S = decltype(stream);
+            few_kernel<DT, S, decltype(bm)::value><<<shrinks + tn * splits, S::kThreads, 0, st>>>(
+                s, shrinks, tn, splits, x, w, ids, a, v, parts);
+        };
+        if (s.T <= 16)
+            few(Stream<16, 64, 1, 4, 8>{}, std::integral_constant<int, 16>{});
+        else if (s.T <= 32)
+            few(Stream<32, 64, 1, 3, 8>{}, std::integral_constant<int, 32>{});
+        else if (s.T <= 64)
+            few(Stream<64, 64, 1, 3, 6>{}, std::integral_constant<int, 64>{});
+        else
+            few(Stream<128, 64, 1, 3, 3>{}, std::integral_constant<int, 128>{});
+        if ((e = hipGetLastError()) != hipSuccess)
+            return e;
+        return add(std::true_type{}, parts, splits);
+    }
     if (order) {
         order_kernel<<<1, kOrderThreads, (s.L + 1) * sizeof(int), st>>>(s, ids, order);
         if ((e = hipGetLastError()) != hipSuccess)
@@ -885,37 +1006,18 @@ hipError_t adapter_of_type(const moe_adapter_shape &sh, const void *x_, const vo
     }
     if (e != hipSuccess)
         return e;
-    if (!w) {
-        add_kernel<DT><<<dim3(up(s.T, 16), up(s.N, 64 * kAddWaves)), 64 * kAddWaves, 0, st>>>(
-            s, static_cast<const uint16_t *>(base), ids, order, b, scale, v, out);
-        return hipGetLastError();
-    }
-    // W comes from memory and gets the deeper ring
-    const auto few = [&](auto stream, auto bm) {
-        using S = decltype(stream);
-        project_few_kernel<DT, S, decltype(bm)::value>
-            <<<up(s.N, 32), S::kThreads, 0, st>>>(s, x, w, ids, b, scale, v, out);
-    };
-    if (s.T <= 16)
-        few(Stream<16, 32, 1, 6, 16>{}, std::integral_constant<int, 16>{});
-    else if (s.T <= 32)
-        few(Stream<32, 32, 2, 4, 15>{}, std::integral_constant<int, 32>{});
-    else if (s.T <= 64)
-        few(Stream<64, 32, 2, 3, 13>{}, std::integral_constant<int, 64>{});
-    else if (s.T <= 128)
-        few(Stream<128, 32, 2, 3, 8>{}, std::integral_constant<int, 128>{});
-    else {
-        const ProjectArgs p{x, w, ids, order, b, scale, v, out};
-        const int cus = device_cu_count();
-        const int tm = up(s.T, 256), tn = up(s.N, 256), left = tm * tn % cus;
-        if (tm * tn >= cus) {
-            const int halves = 2 * left <= cus ? left : 0;
-            project_large_kernel<DT><<<tm * tn + halves, 512, 0, st>>>(s, tm, tn,
-                                                                      tm * tn - halves, p);
-        } else {
-            const int sm = up(s.T, 128), sn = up(s.N, 128);
-            project_small_kernel<DT><<<sm * sn, 256, 0, st>>>(s, sm, sn, p);
-        }
+    if (!w)
+        return add(std::false_type{}, base, 0);
+    const ProjectArgs p{x, w, ids, order, b, scale, v, out};
+    const int cus = device_cu_count();
+    const int tm = up(s.T, 256), tn = up(s.N, 256), left = tm * tn % cus;
+    if (tm * tn >= cus) {
+        const int halves = 2 * left <= cus ? left : 0;
+        project_large_kernel<DT>
+            <<<tm * tn + halves, 512, 0, st>>>(s, tm, tn, tm * tn - halves, p);
+    } else {
+        const int sm = up(s.T, 128), sn = up(s.N, 128);
+        project_small_kernel<DT><<<sm * sn, 256, 0, st>>>(s, sm, sn, p);
     }
     return hipGetLastError();
 }
@@ -924,7 +1026,7 @@ hipError_t adapter_of_type(const moe_adapter_shape &sh, const void *x_, const vo
 
 size_t adapter_workspace_bytes(const moe_adapter_shape &s)
 {
-    return order_bytes(s) + (size_t)s.T * s.rank * sizeof(float);
+    return v_bytes(s) + parts_bytes(s);
 }
 
 hipError_t launch_adapter_project(const moe_adapter_shape &s, int dtype, const void *x,

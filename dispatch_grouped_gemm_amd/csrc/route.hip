@@ -13,8 +13,12 @@
 //   dl_e = p_e (g_e - sum_k w_k g_k).
 //
 // Choosing is exact: a logit becomes a whole number that orders as the
-// floats do (-0 made +0 first), so ties are ties.  Bound by memory for many
-// tokens, by launch latency for few.
+// floats do (-0 made +0 first), so ties are ties.
+//
+// Sixteen lanes share a token and hold its logits in registers: a reduction
+// then takes four lane rotations inside a row of the wavefront, and four
+// tokens share every instruction.  Bound by memory for many tokens, by
+// launch latency for few.
 #include "elem.hpp"
 
 namespace moe {
@@ -22,75 +26,145 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kLanes = 16; // of a token
 constexpr int kMaxK = 8;
-constexpr int kMaxPer = 16; // 64 lanes x 16: up to 1024 experts
+constexpr int kMaxPer = 64; // 16 lanes x 64: up to 1024 experts
 
-// Order-preserving whole number of an eligible logit (never 0); 0 for -inf
-// and NaN.
-__device__ __forceinline__ uint32_t key_of(float v)
+// Value of the lane N places on in the same row of 16.
+template <int N>
+__device__ __forceinline__ uint32_t ror(uint32_t v)
 {
-    if (!(v > -INFINITY))
-        return 0u;
-    const uint32_t u = __float_as_uint(v + 0.0f);
-    return u & 0x80000000u ? ~u : u | 0x80000000u;
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x120 + N, 0xf, 0xf, true);
 }
 
-__device__ __forceinline__ float value_of(uint32_t key)
+template <typename F>
+__device__ __forceinline__ uint32_t row_reduce(uint32_t v, F f)
 {
-    return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+    v = f(v, ror<8>(v));
+    v = f(v, ror<4>(v));
+    v = f(v, ror<2>(v));
+    return f(v, ror<1>(v));
 }
 
+__device__ __forceinline__ uint32_t row_max(uint32_t v)
+{
+    return row_reduce(v, [](uint32_t a, uint32_t b) { return max(a, b); });
+}
+
+__device__ __forceinline__ uint32_t row_min(uint32_t v)
+{
+    return row_reduce(v, [](uint32_t a, uint32_t b) { return min(a, b); });
+}
+
+__device__ __forceinline__ float row_sum(float v)
+{
+    return __uint_as_float(row_reduce(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+        return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+    }));
+}
+
+// exp(v - m), 1 at v = m whatever m is.  The hardware exponential of
+// (v - m) log2 e: off by |v - m| 2^-24 and an ulp, relatively.
 __device__ __forceinline__ float exp_to_max(float v, float m)
 {
-    return expf(v == m ? 0.0f : v - m);
+    return __expf(v == m ? 0.0f : v - m);
 }
 
-__device__ __forceinline__ float wave_sum_f(float v)
+// Which expert register i of a lane holds: whole 16-byte pieces where the
+// rows allow them (kVec), else single logits.
+template <int DT, bool kVec>
+__device__ __forceinline__ int expert_of(int i, int lane)
 {
-#pragma unroll
-    for (int d = 32; d; d >>= 1)
-        v += __shfl_xor(v, d);
-    return v;
+    constexpr int V = Elem<DT>::kVec;
+    return kVec ? ((i / V) * kLanes + lane) * V + i % V : i * kLanes + lane;
 }
 
-// One wavefront per token, expert e in lane e mod 64.
-template <int DT, int PER>
+// A token's logits; -inf past the last expert.
+template <int DT, int PER, bool kVec>
+__device__ __forceinline__ void load_logits(const void *logits, size_t row, int E, int lane,
+                                            float *l)
+{
+    const auto *p = static_cast<const typename Elem<DT>::type *>(logits) + row * E;
+    if constexpr (kVec) {
+        constexpr int V = Elem<DT>::kVec;
+#pragma unroll
+        for (int j = 0; j < PER / V; ++j) {
+            const int e = (j * kLanes + lane) * V;
+            if (e < E) {
+                Elem<DT>::unpack(*reinterpret_cast<const uint4 *>(p + e), l + j * V);
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    l[j * V + i] = -INFINITY;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int e = i * kLanes + lane;
+            l[i] = e < E ? Elem<DT>::load(p + e) : -INFINITY;
+        }
+    }
+}
+
+template <int DT, int PER, bool kVec>
 __global__ void __launch_bounds__(kThreads)
 route_kernel(int T, int E, int K, bool renorm, const void *__restrict__ logits,
              int32_t *__restrict__ ids, float *__restrict__ w)
 {
-    const int t = blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
-    const int lane = threadIdx.x & 63;
+    const int lane = threadIdx.x & (kLanes - 1);
+    const int t = blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
     if (t >= T)
-        return;
-    const auto *l = static_cast<const typename Elem<DT>::type *>(logits) + (size_t)t * E;
+        return; // a whole row of lanes
+    float l[PER];
+    load_logits<DT, PER, kVec>(logits, t, E, lane, l);
+    // the ordering keys; 0: not eligible (-inf, NaN, past the last expert).
+    // A 16-bit logit's key takes the high half and its expert, complemented,
+    // the low one: one maximum finds the winner and settles ties.
+    constexpr bool kWide = DT == MOE_DT_F32;
     uint32_t key[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const int e = i * 64 + lane;
-        key[i] = e < E ? key_of(Elem<DT>::load(l + e)) : 0u;
+        uint32_t u;
+        if constexpr (kWide) {
+            u = __float_as_uint(l[i] + 0.0f);
+            u = u & 0x80000000u ? ~u : u | 0x80000000u;
+        } else {
+            const float z = l[i] + 0.0f;
+            const uint32_t b = DT == MOE_DT_BF16 ? __float_as_uint(z) >> 16
+                                                 : Elem<MOE_DT_F16>::bits_of(z);
+            u = (b & 0x8000u ? ~b & 0xffffu : b | 0x8000u) << 16 |
+                (0xffffu - expert_of<DT, kVec>(i, lane));
+        }
+        key[i] = l[i] > -INFINITY ? u : 0u;
     }
-    float all = 0.0f, m = 0.0f, mine = 0.0f, sum = 0.0f;
+    const auto value_of = [](uint32_t k) {
+        if constexpr (kWide) {
+            return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+        } else {
+            const uint32_t b = k & 0x80000000u ? (k >> 16) & 0x7fffu : ~(k >> 16) & 0xffffu;
+            return DT == MOE_DT_BF16 ? __uint_as_float(b << 16) : Elem<MOE_DT_F16>::half_of(b);
+        }
+    };
+    float m = 0.0f, all = 0.0f, mine = 0.0f;
     int my_id = -1;
     for (int k = 0; k < K; ++k) {
         uint32_t best = 0u;
-        int at = 0;
 #pragma unroll
         for (int i = 0; i < PER; ++i)
-            if (key[i] > best) {
-                best = key[i];
-                at = i * 64 + lane;
-            }
-        uint64_t b = ((uint64_t)best << 32) | (uint32_t)~at;
+            best = max(best, key[i]);
+        const uint32_t won = row_max(best);
+        int e;
+        if constexpr (kWide) {
+            uint32_t at = ~0u;
 #pragma unroll
-        for (int d = 32; d; d >>= 1) {
-            const uint64_t o = __shfl_xor((unsigned long long)b, d);
-            b = o > b ? o : b;
+            for (int i = 0; i < PER; ++i)
+                if (key[i] == won)
+                    at = min(at, (uint32_t)expert_of<DT, kVec>(i, lane));
+            e = (int)row_min(at);
+        } else {
+            e = 0xffff - (int)(won & 0xffffu);
         }
-        const uint32_t won = (uint32_t)(b >> 32);
-        if (won == 0u)
-            break;
-        const int e = (int)~(uint32_t)b;
         const float v = value_of(won);
         if (k == 0) {
             m = v;
@@ -98,95 +172,102 @@ route_kernel(int T, int E, int K, bool renorm, const void *__restrict__ logits,
                 float s = 0.0f;
 #pragma unroll
                 for (int i = 0; i < PER; ++i)
-                    if (key[i])
-                        s += exp_to_max(value_of(key[i]), m);
-                all = wave_sum_f(s);
+                    s += key[i] ? exp_to_max(l[i], m) : 0.0f;
+                all = row_sum(s);
             }
         }
 #pragma unroll
         for (int i = 0; i < PER; ++i)
-            if (e == i * 64 + lane)
+            if (key[i] == won && (!kWide || expert_of<DT, kVec>(i, lane) == e))
                 key[i] = 0u;
-        const float ek = exp_to_max(v, m);
-        sum += ek;
-        if (lane == k) {
-            mine = ek;
+        if (lane == k && won) {
+            mine = expf(v == m ? 0.0f : v - m);
             my_id = e;
         }
     }
+    const float sum = renorm ? row_sum(mine) : all;
     if (lane < K) {
         const size_t o = (size_t)t * K + lane;
         ids[o] = my_id;
-        w[o] = my_id >= 0 ? mine / (renorm ? sum : all) : 0.0f;
+        w[o] = my_id >= 0 ? mine / sum : 0.0f;
     }
 }
 
-template <int DT, int PER>
+template <int DT, int PER, bool kVec>
 __global__ void __launch_bounds__(kThreads)
 route_backward_kernel(int T, int E, int K, bool renorm, const void *__restrict__ logits,
                       const int32_t *__restrict__ ids, const float *__restrict__ w,
                       const float *__restrict__ dw, void *__restrict__ dlogits)
 {
-    const int t = blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
-    const int lane = threadIdx.x & 63;
+    constexpr int V = Elem<DT>::kVec;
+    const int lane = threadIdx.x & (kLanes - 1);
+    const int t = blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
     if (t >= T)
         return;
-    int id[kMaxK];
-    float wk[kMaxK], g[kMaxK], dot = 0.0f;
-#pragma unroll
-    for (int k = 0; k < kMaxK; ++k) {
-        const size_t o = (size_t)t * K + k;
-        id[k] = k < K ? ids[o] : -1;
-        if ((unsigned)id[k] >= (unsigned)E)
-            id[k] = -1;
-        wk[k] = id[k] >= 0 ? w[o] : 0.0f;
-        g[k] = id[k] >= 0 ? dw[o] : 0.0f;
-        dot += wk[k] * g[k];
+    // lane k: the slot k
+    int id = -1;
+    float wk = 0.0f, g = 0.0f;
+    if (lane < K) {
+        const size_t o = (size_t)t * K + lane;
+        id = ids[o];
+        if ((unsigned)id < (unsigned)E) {
+            wk = w[o];
+            g = dw[o];
+        } else {
+            id = -1;
+        }
     }
-    auto *dl = static_cast<typename Elem<DT>::type *>(dlogits) + (size_t)t * E;
-    if (renorm) {
+    const float dot = row_sum(wk * g);
+    float d[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        d[i] = 0.0f;
+    // what slot k adds to its expert: w (g - dot), or g alone
+    const float add = renorm ? wk * (g - dot) : g;
+    for (int k = 0; k < K; ++k) {
+        const int e = __shfl(id, k, kLanes);
+        const float a = __shfl(add, k, kLanes);
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            d[i] += e == expert_of<DT, kVec>(i, lane) ? a : 0.0f;
+    }
+    if (!renorm) {
+        float l[PER];
+        load_logits<DT, PER, kVec>(logits, t, E, lane, l);
+        float m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            m = l[i] > m ? l[i] : m; // (passes NaN over)
+        m = __uint_as_float(row_reduce(__float_as_uint(m), [](uint32_t a, uint32_t b) {
+            return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+        }));
+        float s = 0.0f;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int e = i * 64 + lane;
-            float d = 0.0f;
-#pragma unroll
-            for (int k = 0; k < kMaxK; ++k)
-                if (id[k] == e)
-                    d += wk[k] * (g[k] - dot);
-            if (e < E)
-                Elem<DT>::store(dl + e, d);
+            l[i] = l[i] > -INFINITY ? exp_to_max(l[i], m) : 0.0f;
+            s += l[i];
         }
-        return;
+        s = row_sum(s);
+        const float r = s > 0.0f ? 1.0f / s : 0.0f;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            d[i] = l[i] > 0.0f ? l[i] * r * (d[i] - dot) : 0.0f;
     }
-    const auto *l = static_cast<const typename Elem<DT>::type *>(logits) + (size_t)t * E;
-    float v[PER], m = -INFINITY;
+    auto *dl = static_cast<typename Elem<DT>::type *>(dlogits) + (size_t)t * E;
+    if constexpr (kVec) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int e = i * 64 + lane;
-        v[i] = e < E ? Elem<DT>::load(l + e) : -INFINITY;
-        if (v[i] > m)
-            m = v[i];
-    }
+        for (int j = 0; j < PER / V; ++j) {
+            const int e = (j * kLanes + lane) * V;
+            if (e < E)
+                *reinterpret_cast<uint4 *>(dl + e) = Elem<DT>::pack(d + j * V);
+        }
+    } else {
 #pragma unroll
-    for (int d = 32; d; d >>= 1)
-        m = fmaxf(m, __shfl_xor(m, d));
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        v[i] = v[i] > -INFINITY ? exp_to_max(v[i], m) : 0.0f;
-        s += v[i];
-    }
-    s = wave_sum_f(s);
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int e = i * 64 + lane;
-        float ge = 0.0f;
-#pragma unroll
-        for (int k = 0; k < kMaxK; ++k)
-            if (id[k] == e)
-                ge += g[k];
-        if (e < E)
-            Elem<DT>::store(dl + e, v[i] > 0.0f ? v[i] / s * (ge - dot) : 0.0f);
+        for (int i = 0; i < PER; ++i) {
+            const int e = i * kLanes + lane;
+            if (e < E)
+                Elem<DT>::store(dl + e, d[i]);
+        }
     }
 }
 
@@ -194,30 +275,45 @@ route_backward_kernel(int T, int E, int K, bool renorm, const void *__restrict__
 template <typename F>
 void per_lane(int E, F f)
 {
-    const int per = (E + 63) / 64;
-    if (per <= 2)
-        f(std::integral_constant<int, 2>{});
-    else if (per <= 4)
-        f(std::integral_constant<int, 4>{});
-    else if (per <= 8)
+    const int per = (E + kLanes - 1) / kLanes;
+    if (per <= 8)
         f(std::integral_constant<int, 8>{});
+    else if (per <= 16)
+        f(std::integral_constant<int, 16>{});
+    else if (per <= 24)
+        f(std::integral_constant<int, 24>{});
+    else if (per <= 32)
+        f(std::integral_constant<int, 32>{});
     else
         f(std::integral_constant<int, kMaxPer>{});
 }
 
-unsigned grid_of(const moe_shape &s) { return ((unsigned)s.T + 3) / 4; }
+// Whether the rows of E logits are whole 16-byte pieces on 16-byte borders.
+bool whole_pieces(int E, int dtype, const void *p, const void *q)
+{
+    return E * elem_bytes(dtype) % 16 == 0 && (((uintptr_t)p | (uintptr_t)q) & 15) == 0;
+}
+
+unsigned grid_of(const moe_shape &s)
+{
+    constexpr unsigned per = kThreads / kLanes;
+    return ((unsigned)s.T + per - 1) / per;
+}
 
 } // namespace
 
-bool route_supported(const moe_shape &s) { return s.E_total <= 64 * kMaxPer; }
+bool route_supported(const moe_shape &s) { return s.E_total <= kLanes * kMaxPer; }
 
 hipError_t launch_route(const moe_shape &s, int dtype, bool renorm, const void *logits,
                         int32_t *ids, float *w, hipStream_t st)
 {
     with_elem(dtype, [&](auto dt) {
         per_lane(s.E_total, [&](auto per) {
-            route_kernel<decltype(dt)::value, decltype(per)::value>
-                <<<grid_of(s), kThreads, 0, st>>>(s.T, s.E_total, s.K, renorm, logits, ids, w);
+            constexpr int DT = decltype(dt)::value, PER = decltype(per)::value;
+            const auto k = whole_pieces(s.E_total, dtype, logits, nullptr)
+                               ? route_kernel<DT, PER, true>
+                               : route_kernel<DT, PER, false>;
+            k<<<grid_of(s), kThreads, 0, st>>>(s.T, s.E_total, s.K, renorm, logits, ids, w);
         });
     });
     return hipGetLastError();
@@ -229,9 +325,12 @@ hipError_t launch_route_backward(const moe_shape &s, int dtype, bool renorm, con
 {
     with_elem(dtype, [&](auto dt) {
         per_lane(s.E_total, [&](auto per) {
-            route_backward_kernel<decltype(dt)::value, decltype(per)::value>
-                <<<grid_of(s), kThreads, 0, st>>>(s.T, s.E_total, s.K, renorm, logits, ids, w, dw,
-                                                  dlogits);
+            constexpr int DT = decltype(dt)::value, PER = decltype(per)::value;
+            const auto k = whole_pieces(s.E_total, dtype, logits, dlogits)
+                               ? route_backward_kernel<DT, PER, true>
+                               : route_backward_kernel<DT, PER, false>;
+            k<<<grid_of(s), kThreads, 0, st>>>(s.T, s.E_total, s.K, renorm, logits, ids, w, dw,
+                                               dlogits);
         });
     });
     return hipGetLastError();

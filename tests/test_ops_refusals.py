@@ -140,3 +140,16 @@ def test_binding_refuses_tensors(lib):
         moe.moe_adapter_project(a, x.float(), None, rr, rows, rows, None, x, rr)
     with pytest.raises(ValueError):
         moe.moe_adapter_project(a, x, None, rr, rows, rows, None, x, rr)
+
+
+def test_shapes_copy_after_use(lib):
+    """What a shape object keeps for its calls does not stand in the way of copies."""
+    import copy
+    import pickle
+    s = moe.AdapterShape(**AD)
+    assert moe.moe_adapter_check(s) == 0
+    m = moe.MoeShape(**V4)
+    assert moe._row_sizes(m)[1] == (128 * 6, 7168) and moe._ref(m) is moe._ref(m)
+    for v in (s, m):
+        for w in (copy.deepcopy(v), pickle.loads(pickle.dumps(v))):
+            assert w == v and hash(w) == hash(v)

@@ -180,38 +180,51 @@ order_kernel(AShape s, const int32_t *__restrict__ ids, int32_t *__restrict__ or
 
 // ---------------------------------------------------------------------------
 // Stream: BM rows of x by BN rows of a weight (W or A), bound by reading
-// them.  Steps of 128 values, 256 bytes of a row: a load instruction moves
-// four whole rows of a step from global memory to LDS, so it asks for whole
-// cache lines (a wavefront reading its operands straight into registers
-// touches 16 rows by 64 bytes at a time, and half lines come from the L2 at
-// a third of the rate: 36 against 105 KB/us a CU).  A row's sixteen 16-byte
-// pieces are stored at piece ^ (row mod 16): the 16 rows that one operand
-// read touches lie in different banks.
+// them.  A step is KB bytes (128 or 256) of every row; a load instruction
+// moves whole KB-byte pieces of 1024 / KB rows from global memory to LDS, so
+// it asks for whole cache lines (a wavefront reading its operands straight
+// into registers touches 16 rows by 64 bytes at a time, and half lines come
+// from the L2 at a third of the rate: 36 against 105 KB/us a CU).  The 16-byte
+// pieces of a row are stored where the 16 rows that one operand read touches
+// lie in different banks.
 //
 // Half the wavefronts load x, half the weight, each into its own ring of
 // stages (NX, NR): a wavefront's loads end in order, so in one ring the
 // operand that comes from the L2 would wait for the one that comes from
-// memory, and the rings' depths could not differ.
+// memory, and the rings' depths could not differ.  Little's law sets them:
+// about 2 us of latency from memory at 25 KB/us a CU.
 //
-// Wavefront (m, k): quarter k of every step for rows (BM / WM) m ..; the
-// four quarters meet in LDS at the end, in a fixed order.
+// A wavefront multiplies 64 bytes of every step (one matrix instruction deep)
+// for a block of WM x WN of the tile; the KB / 64 sums of a block meet in LDS
+// at the end, in a fixed order.
 // ---------------------------------------------------------------------------
-template <int BM, int BN, int WM, int NX, int NR>
+template <int BM, int BN, int WM, int WN, int NX, int NR, int KB>
 struct Stream {
-    static constexpr int kWaves = 4 * WM, kThreads = 64 * kWaves, MF = BM / WM / 16, NF = BN / 16;
-    // 1 KiB loads per wavefront and step
-    static constexpr int UX = BM / 4 / (kWaves / 2), UR = BN / 4 / (kWaves / 2);
-    static constexpr int kRow = 256, kX = BM * kRow, kR = BN * kRow; // bytes of a stage
+    static_assert(KB == 128 || KB == 256, "one or two cache lines of a row");
+    static constexpr int kSlices = KB / 64, kWaves = kSlices * WM * WN, kThreads = 64 * kWaves;
+    static constexpr int MF = BM / WM / 16, NF = BN / WN / 16;
+    static constexpr int kRows = 1024 / KB; // rows of a load
+    // loads per wavefront and step
+    static constexpr int UX = BM / kRows / (kWaves / 2), UR = BN / kRows / (kWaves / 2);
+    static constexpr int kX = BM * KB, kR = BN * KB; // bytes of a stage
     static constexpr int kLds = NX * kX + NR * kR;
-    static_assert(BM % (2 * kWaves) == 0 && BN % (2 * kWaves) == 0 && BM % (16 * WM) == 0,
-                  "whole loads, whole blocks");
-    static_assert(4 * (BM / 16) * NF * 1024 <= kLds, "the quarters' sums reuse the stages");
+    static_assert(UX * kRows * kWaves / 2 == BM && UR * kRows * kWaves / 2 == BN, "whole loads");
+    static_assert(MF * WM * 16 == BM && NF * WN * 16 == BN, "whole blocks");
+    static_assert((NX - 2) * UX < 64 && (NR - 2) * UR < 64, "loads that vmcnt can count");
+    static_assert(kSlices * (BM / 16) * (BN / 16) * 1024 <= kLds, "the sums reuse the stages");
 };
+
+// Place of the 16-byte piece c of row i.
+template <int KB>
+__device__ __forceinline__ int place_of(int c, int i)
+{
+    return KB == 256 ? c ^ (i & 15) : c ^ ((i >> 1) & 7);
+}
 
 // One wavefront's loads into one ring: U a step, N stages of kStage bytes
 // from lds0.  Loads past the last step repeat it into stages that nobody
 // reads again, so the number in flight stays the same to the end.
-template <int U, int N, int kStage, int kRow>
+template <int U, int N, int kStage, int KB>
 struct Ring {
     const uint8_t *next;
     uint32_t voff[U], lds0, slot;
@@ -226,10 +239,12 @@ struct Ring {
           left(steps - 1)
     {
         const int lane = threadIdx.x & 63;
+        constexpr int kPieces = KB / 16;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int i = (first + u) * 4 + (lane >> 4);
-            voff[u] = (uint32_t)row(i) * (uint32_t)(2 * H) + ((lane & 15) ^ (i & 15)) * 16;
+            const int i = (first + u) * (1024 / KB) + lane / kPieces;
+            voff[u] = (uint32_t)row(i) * (uint32_t)(2 * H) +
+                      place_of<KB>(lane & (kPieces - 1), i) * 16;
         }
     }
     __device__ __forceinline__ void load()
@@ -238,7 +253,7 @@ struct Ring {
         for (int u = 0; u < U; ++u)
             g2lds<16>(next, voff[u], lds0 + slot + u * 1024);
         slot = slot + kStage == N * kStage ? 0 : slot + kStage;
-        next += left > 0 ? kRow : 0;
+        next += left > 0 ? KB : 0;
         --left;
     }
     __device__ __forceinline__ void start()
@@ -252,20 +267,22 @@ struct Ring {
 
 // `steps` steps from x and w on.  Rows [0, BM) come from x, columns [0, BN)
 // from the rows of w: xrow(i) and wrow(i) give their numbers, w's within
-// 2^31 bytes of its base.  Afterwards wavefront m < BM / 16 (of the first
-// kWaves, in turn) has rows 16 m .. 16 m + 15 in sum.
-template <int DT, int BM, int BN, int WM, int NX, int NR, typename XRow, typename WRow>
-__device__ __forceinline__ void stream_tile(Stream<BM, BN, WM, NX, NR>, int H, int steps,
+// 2^31 bytes of its base.  Afterwards wavefront v holds the blocks of 16
+// rows v, v + kWaves, ... in sum, BN / 16 values a block.
+template <int DT, int BM, int BN, int WM, int WN, int NX, int NR, int KB, typename XRow,
+          typename WRow>
+__device__ __forceinline__ void stream_tile(Stream<BM, BN, WM, WN, NX, NR, KB>, int H, int steps,
                                             const uint16_t *__restrict__ x, XRow xrow,
                                             const uint16_t *__restrict__ w, WRow wrow,
                                             uint8_t *lds, v4f *sum)
 {
-    using S = Stream<BM, BN, WM, NX, NR>;
+    using S = Stream<BM, BN, WM, WN, NX, NR, KB>;
     constexpr int MF = S::MF, NF = S::NF, kHalf = S::kWaves / 2;
     const int lane = threadIdx.x & 63, wave = wave_of();
     const uint32_t l0 = lds_addr(lds);
-    const int kq = wave & 3, wm = wave >> 2;
-    const int off = (lane & 15) * S::kRow + (((4 * kq + (lane >> 4)) ^ (lane & 15)) * 16);
+    const int slice = wave % S::kSlices, block = wave / S::kSlices;
+    const int wm = block / WN, wn = block % WN;
+    const int off = (lane & 15) * KB + place_of<KB>(4 * slice + (lane >> 4), lane & 15) * 16;
     v4f acc[MF][NF];
 #pragma unroll
     for (int m = 0; m < MF; ++m)
@@ -274,7 +291,8 @@ __device__ __forceinline__ void stream_tile(Stream<BM, BN, WM, NX, NR>, int H, i
             acc[m][f] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     const auto go = [&](auto ring) {
         ring.start();
-        const uint8_t *xl = lds + off + wm * MF * 16 * S::kRow, *wl = lds + off + NX * S::kX;
+        const uint8_t *xl = lds + off + wm * MF * 16 * KB;
+        const uint8_t *wl = lds + NX * S::kX + off + wn * NF * 16 * KB;
         int xs = 0, ws = 0;
         for (int k = steps; k > 0; --k) {
             // the step has landed, and the one before it is done with
@@ -284,10 +302,10 @@ __device__ __forceinline__ void stream_tile(Stream<BM, BN, WM, NX, NR>, int H, i
             uint4 xq[MF], wq[NF];
 #pragma unroll
             for (int f = 0; f < NF; ++f)
-                wq[f] = *reinterpret_cast<const uint4 *>(wl + ws + 16 * f * S::kRow);
+                wq[f] = *reinterpret_cast<const uint4 *>(wl + ws + 16 * f * KB);
 #pragma unroll
             for (int m = 0; m < MF; ++m)
-                xq[m] = *reinterpret_cast<const uint4 *>(xl + xs + 16 * m * S::kRow);
+                xq[m] = *reinterpret_cast<const uint4 *>(xl + xs + 16 * m * KB);
             ring.load();
             xs = xs + S::kX == NX * S::kX ? 0 : xs + S::kX;
             ws = ws + S::kR == NR * S::kR ? 0 : ws + S::kR;
@@ -299,32 +317,32 @@ __device__ __forceinline__ void stream_tile(Stream<BM, BN, WM, NX, NR>, int H, i
         }
     };
     if (wave < kHalf)
-        go(Ring<S::UX, NX, S::kX, S::kRow>(x, H, steps, wave * S::UX, l0, xrow));
+        go(Ring<S::UX, NX, S::kX, KB>(x, H, steps, wave * S::UX, l0, xrow));
     else
-        go(Ring<S::UR, NR, S::kR, S::kRow>(w, H, steps, (wave - kHalf) * S::UR,
-                                           l0 + NX * S::kX, wrow));
+        go(Ring<S::UR, NR, S::kR, KB>(w, H, steps, (wave - kHalf) * S::UR, l0 + NX * S::kX,
+                                      wrow));
     wait_vmcnt<0>();
     __syncthreads();
+    constexpr int MB = BM / 16, NB = BN / 16;
     v4f *part = reinterpret_cast<v4f *>(lds);
 #pragma unroll
     for (int m = 0; m < MF; ++m)
 #pragma unroll
         for (int f = 0; f < NF; ++f)
-            part[((kq * (BM / 16) + wm * MF + m) * NF + f) * 64 + lane] = acc[m][f];
+            part[((slice * MB + wm * MF + m) * NB + wn * NF + f) * 64 + lane] = acc[m][f];
     __syncthreads();
-    // block of 16 rows q * kWaves + wave in sum + q * NF
 #pragma unroll
-    for (int q = 0; q * S::kWaves < BM / 16; ++q) {
+    for (int q = 0; q * S::kWaves < MB; ++q) {
         const int m = q * S::kWaves + wave;
-        if (m >= BM / 16)
+        if (m >= MB)
             break;
 #pragma unroll
-        for (int f = 0; f < NF; ++f) {
-            v4f a = part[(m * NF + f) * 64 + lane];
+        for (int f = 0; f < NB; ++f) {
+            v4f a = part[(m * NB + f) * 64 + lane];
 #pragma unroll
-            for (int k = 1; k < 4; ++k)
-                a += part[((k * (BM / 16) + m) * NF + f) * 64 + lane];
-            sum[q * NF + f] = a;
+            for (int k = 1; k < S::kSlices; ++k)
+                a += part[((k * MB + m) * NB + f) * 64 + lane];
+            sum[q * NB + f] = a;
         }
     }
 }
@@ -336,7 +354,7 @@ __device__ __forceinline__ void stream_tile(Stream<BM, BN, WM, NX, NR>, int H, i
 // adapter's A is read by as few workgroups as its rows allow, in whatever
 // order they come.
 // ---------------------------------------------------------------------------
-using FewStream = Stream<16, 16, 1, 16, 16>;
+using FewStream = Stream<16, 16, 1, 1, 16, 16, 256>;
 
 template <int DT>
 __device__ __forceinline__ void shrink_few(const AShape &s, const uint16_t *__restrict__ x,
@@ -397,12 +415,12 @@ shrink_few_kernel(AShape s, const uint16_t *__restrict__ x, const int32_t *__res
 
 // Shrink, many rows, ordered: workgroup (BM places, BN of the rank).
 template <int DT, int BM, int BN, int WM, int NX, int NR>
-__global__ void __launch_bounds__((Stream<BM, BN, WM, NX, NR>::kThreads))
+__global__ void __launch_bounds__((Stream<BM, BN, WM, 1, NX, NR, 256>::kThreads))
 shrink_many_kernel(AShape s, const uint16_t *__restrict__ x, const int32_t *__restrict__ ids,
                    const int32_t *__restrict__ order, const uint16_t *__restrict__ a,
                    float *__restrict__ v)
 {
-    using S = Stream<BM, BN, WM, NX, NR>;
+    using S = Stream<BM, BN, WM, 1, NX, NR, 256>;
     static_assert(BM <= 32, "the rows' adapters in one mask");
     __shared__ __align__(1024) uint8_t lds[S::kLds];
     const int lane = threadIdx.x & 63, wave = wave_of();
@@ -432,17 +450,18 @@ shrink_many_kernel(AShape s, const uint16_t *__restrict__ x, const int32_t *__re
 // ---------------------------------------------------------------------------
 // Expand: adds the adapters' term of 16 rows (the lane's: row) to the sums of
 // 16 NF columns from n0 (in column_of's order).
-// 64 of the rank at a time: the rows' v as hi and lo, then the adapters among
+// 32 KK of the rank at a time: the rows' v as hi and lo, then the adapters among
 // the rows, GB at a time with their B in flight together.  No load stands
 // behind a branch (a lane or a place without work reads a valid address and
 // drops the product): behind one the compiler waits for each by itself.
 // ---------------------------------------------------------------------------
 
-// 64 of the rank of the lane's row, from c: pieces k0 + 32 k of 8.
+// 32 KK of the rank of the lane's row, from c: pieces k0 + 32 k of 8.
+template <int KK>
 struct Low {
-    uint4 hi[2], lo[2];
-    int at[2];
-    bool there[2];
+    uint4 hi[KK], lo[KK];
+    int at[KK];
+    bool there[KK];
 };
 
 // What a row needs besides: its scale, and fp16's power of two.
@@ -480,23 +499,23 @@ __device__ __forceinline__ Gain gain_of(const AShape &s, const float *__restrict
     return g;
 }
 
-template <int DT>
-__device__ __forceinline__ Low low_of(const AShape &s, const float *__restrict__ v,
+template <int DT, int KK>
+__device__ __forceinline__ Low<KK> low_of(const AShape &s, const float *__restrict__ v,
                                       const Row &row, const Gain &g, int c)
 {
     const float *vr = v + (size_t)row.t * s.r;
     const int k0 = 8 * ((threadIdx.x & 63) >> 4);
-    Low low;
-    v4f vq[2][2];
+    Low<KK> low;
+    v4f vq[KK][2];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
+    for (int k = 0; k < KK; ++k) {
         low.there[k] = c + 32 * k + k0 < s.r;
         low.at[k] = low.there[k] ? c + 32 * k + k0 : 0;
         vq[k][0] = *reinterpret_cast<const v4f *>(vr + low.at[k]);
         vq[k][1] = *reinterpret_cast<const v4f *>(vr + low.at[k] + 4);
     }
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
+    for (int k = 0; k < KK; ++k) {
         float f8[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -508,11 +527,11 @@ __device__ __forceinline__ Low low_of(const AShape &s, const float *__restrict__
     return low;
 }
 
-// Adds 64 of the rank; rows: which of the 16 rows have an adapter (not 0).
-template <int DT, int NF, int GB>
+// Adds 32 KK of the rank; rows: which of the 16 rows have an adapter (not 0).
+template <int DT, int NF, int GB, int KK>
 __device__ __forceinline__ void expand_part(const AShape &s, const uint16_t *__restrict__ b,
                                             const Row &row, uint32_t rows, const Gain &gain,
-                                            const Low &low, int n0, v4f *acc)
+                                            const Low<KK> &low, int n0, v4f *acc)
 {
     const int lane = threadIdx.x & 63;
     uint32_t col[NF]; // element of B_l; N * rank is below 2^28
@@ -522,7 +541,7 @@ __device__ __forceinline__ void expand_part(const AShape &s, const uint16_t *__r
     uint32_t todo = rows;
     do {
         int g[GB], n = 0;
-        uint4 bq[GB][2][NF];
+        uint4 bq[GB][KK][NF];
 #pragma unroll
         for (int q = 0; q < GB; ++q) {
             const int next = __builtin_amdgcn_readlane(row.id, todo ? __builtin_ctz(todo) : 0);
@@ -534,7 +553,7 @@ __device__ __forceinline__ void expand_part(const AShape &s, const uint16_t *__r
         for (int q = 0; q < GB; ++q) {
             const uint16_t *bg = b + (size_t)g[q] * s.N * s.r;
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
+            for (int k = 0; k < KK; ++k)
 #pragma unroll
                 for (int f = 0; f < NF; ++f)
                     bq[q][k][f] = piece(bg + col[f] + low.at[k]);
@@ -547,7 +566,7 @@ __device__ __forceinline__ void expand_part(const AShape &s, const uint16_t *__r
             for (int f = 0; f < NF; ++f) {
                 v4f d = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
+                for (int k = 0; k < KK; ++k) {
                     const uint4 bk = low.there[k] ? bq[q][k][f] : uint4{0, 0, 0, 0};
                     d = mfma<DT>(bk, low.hi[k], d);
                     d = mfma<DT>(bk, low.lo[k], d);
@@ -561,7 +580,7 @@ __device__ __forceinline__ void expand_part(const AShape &s, const uint16_t *__r
     } while (todo);
 }
 
-template <int DT, int NF, int GB>
+template <int DT, int NF>
 __device__ __forceinline__ void expand(const AShape &s, const float *__restrict__ v,
                                        const uint16_t *__restrict__ b,
                                        const float *__restrict__ scale, const Row &row, int n0,
@@ -572,7 +591,8 @@ __device__ __forceinline__ void expand(const AShape &s, const float *__restrict_
         return;
     const Gain gain = gain_of<DT>(s, v, scale, row);
     for (int c = 0; c < s.r; c += 64)
-        expand_part<DT, NF, GB>(s, b, row, rows, gain, low_of<DT>(s, v, row, gain, c), n0, acc);
+        expand_part<DT, NF, 1, 2>(s, b, row, rows, gain, low_of<DT, 2>(s, v, row, gain, c), n0,
+                                  acc);
 }
 
 // The 4 NF neighbouring columns of one row that a lane holds, rounded and
@@ -605,7 +625,7 @@ few_kernel(AShape s, int shrinks, int tn, int splits, const uint16_t *__restrict
            const uint16_t *__restrict__ w, const int32_t *__restrict__ ids,
            const uint16_t *__restrict__ a, float *__restrict__ v, float *__restrict__ parts)
 {
-    static_assert(S::kThreads == FewStream::kThreads && S::NF == 4, "one launch for both");
+    static_assert(S::kThreads == FewStream::kThreads, "one launch for both");
     constexpr int kLds = S::kLds > FewStream::kLds ? S::kLds : FewStream::kLds;
     __shared__ __align__(1024) uint8_t lds[kLds];
     int q = blockIdx.x;
@@ -615,12 +635,12 @@ few_kernel(AShape s, int shrinks, int tn, int splits, const uint16_t *__restrict
     }
     q -= shrinks;
     const int n0 = q % tn * 64, part = q / tn;
-    const int all = s.H / 128, first = (long)all * part / splits;
+    const int all = s.H / 64, first = (long)all * part / splits;
     const int steps = (int)((long)all * (part + 1) / splits) - first;
-    v4f sum[S::NF * ((BM / 16 + S::kWaves - 1) / S::kWaves)];
+    v4f sum[4 * ((BM / 16 + S::kWaves - 1) / S::kWaves)];
     stream_tile<DT>(
-        S{}, s.H, steps, x + 128 * first, [&](int r) { return min(r, s.T - 1); },
-        w + (size_t)n0 * s.H + 128 * first,
+        S{}, s.H, steps, x + 64 * first, [&](int r) { return min(r, s.T - 1); },
+        w + (size_t)n0 * s.H + 64 * first,
         [&](int r) { return min(column_of<4>(r >> 4, r & 15), s.N - 1 - n0); }, lds, sum);
     const int lane = threadIdx.x & 63, n = n0 + 16 * (lane >> 4);
 #pragma unroll
@@ -807,7 +827,7 @@ __device__ __forceinline__ void project_tile(const AShape &s, const ProjectArgs 
         for (int f = 0; f < NF; f += 4) {
             const int n = n0 + (wn * NF + f) * 16;
             __builtin_amdgcn_sched_barrier(0);
-            expand<DT, 4, 1>(s, p.v, p.b, p.scale, row[m], n, acc[m] + f);
+            expand<DT, 4>(s, p.v, p.b, p.scale, row[m], n, acc[m] + f);
             if (m0 + (wm * MF + m) * 16 + (lane & 15) < s.T)
                 store_cols<DT, 4>(s, p.out, row[m].t, n + 16 * (lane >> 4), acc[m] + f);
         }
@@ -846,39 +866,49 @@ project_small_kernel(AShape s, int tm, int tn, ProjectArgs p)
 }
 
 // ---------------------------------------------------------------------------
-// Add: out = base + the adapters' term, base a given projection, or the sum
-// of `parts` float32 planes.  Bound by reading the base and writing out.  A
-// wavefront takes 16 places and `blocks` blocks of 64 columns: their v is
-// read once for all of them (up to a rank of 64).
+// Add: out = base + the adapters' term, base a given projection, or (kParts)
+// the sum of `parts` float32 planes.  Bound by reading the base and writing
+// out.  A wavefront takes 16 places and `blocks` blocks of 16 NF columns:
+// their v is read once for all of them, up to a rank of 32 KK.
 // ---------------------------------------------------------------------------
 constexpr int kAddWaves = 4;
 
-template <int DT, bool kParts>
+template <int DT, int NF, int GB, int KK, bool kParts>
 __global__ void __launch_bounds__(64 * kAddWaves)
 add_kernel(AShape s, int blocks, int parts, const void *base, const int32_t *__restrict__ ids,
            const int32_t *__restrict__ order, const uint16_t *__restrict__ b,
            const float *__restrict__ scale, const float *__restrict__ v, uint16_t *out)
 {
-    constexpr int NF = 4;
     const int lane = threadIdx.x & 63, wave = wave_of();
-    int n0 = (blockIdx.y * kAddWaves + wave) * 64 * blocks;
+    int n0 = (blockIdx.y * kAddWaves + wave) * 16 * NF * blocks;
     const long i = (long)blockIdx.x * 16 + (lane & 15);
     const Row row = row_at(s, order, ids, i);
     const uint32_t rows = (uint32_t)__ballot(row.id >= 0) & 0xffffu;
     const Gain gain = gain_of<DT>(s, v, scale, row);
-    const Low low = low_of<DT>(s, v, row, gain, 0);
-    for (int k = 0; k < blocks && n0 < s.N; ++k, n0 += 64) {
-        const int n = n0 + 16 * (lane >> 4);
+    const Low<KK> low = low_of<DT, KK>(s, v, row, gain, 0);
+    for (int k = 0; k < blocks && n0 < s.N; ++k, n0 += 16 * NF) {
+        const int n = n0 + 4 * NF * (lane >> 4);
         v4f acc[NF];
         if constexpr (kParts) {
             const float *p = static_cast<const float *>(base) + (size_t)row.t * s.N;
+            const size_t plane = (size_t)s.T * s.N;
+            v4f q[4][NF];
 #pragma unroll
             for (int f = 0; f < NF; ++f)
                 acc[f] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-            for (int q = 0; q < parts; ++q, p += (size_t)s.T * s.N)
+            for (int h = 0; h < parts; h += 4) {
 #pragma unroll
-                for (int f = 0; f < NF; ++f)
-                    acc[f] += *reinterpret_cast<const v4f *>(p + min(n + 4 * f, s.N - 4));
+                for (int u = 0; u < 4; ++u)
+#pragma unroll
+                    for (int f = 0; f < NF; ++f)
+                        q[u][f] = *reinterpret_cast<const v4f *>(
+                            p + min(h + u, parts - 1) * plane + min(n + 4 * f, s.N - 4));
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+#pragma unroll
+                    for (int f = 0; f < NF; ++f)
+                        acc[f] += h + u < parts ? q[u][f] : v4f{0.0f, 0.0f, 0.0f, 0.0f};
+            }
         } else {
             const uint16_t *p = static_cast<const uint16_t *>(base) + (size_t)row.t * s.N;
 #pragma unroll
@@ -893,10 +923,10 @@ add_kernel(AShape s, int blocks, int parts, const void *base, const int32_t *__r
             }
         }
         if (rows) {
-            expand_part<DT, NF, kParts ? 4 : 1>(s, b, row, rows, gain, low, n0, acc);
-            for (int c = 64; c < s.r; c += 64)
-                expand_part<DT, NF, 1>(s, b, row, rows, gain, low_of<DT>(s, v, row, gain, c), n0,
-                                       acc);
+            expand_part<DT, NF, GB, KK>(s, b, row, rows, gain, low, n0, acc);
+            for (int c = 32 * KK; c < s.r; c += 32 * KK)
+                expand_part<DT, NF, GB, KK>(s, b, row, rows, gain,
+                                            low_of<DT, KK>(s, v, row, gain, c), n0, acc);
         }
         if (i < s.T)
             store_cols<DT, NF>(s, out, row.t, n, acc);
@@ -905,12 +935,12 @@ add_kernel(AShape s, int blocks, int parts, const void *base, const int32_t *__r
 
 constexpr int kFewProject = 128; // rows projected by few_kernel
 
-// Parts of H of few_kernel for a shape: enough workgroups for every CU, up
-// to 8 and the steps there are.
+// Parts of H of few_kernel for a shape: as many workgroups as run at once
+// (one a CU), at most 8 parts of at least two steps.
 int few_splits(const moe_adapter_shape &s)
 {
-    const int tn = (s.N + 63) / 64, want = s.T > 64 ? 224 : 384;
-    return std::max(1, std::min({(want + tn - 1) / tn, 8, s.H / 128}));
+    const int tn = (s.N + 63) / 64;
+    return std::max(1, std::min({256 / tn, 8, s.H / 128}));
 }
 
 size_t parts_bytes(const moe_adapter_shape &s)
@@ -963,14 +993,22 @@ hipError_t adapter_of_type(const moe_adapter_shape &sh, const void *x_, const vo
     auto *out = static_cast<uint16_t *>(out_);
     int32_t *order = order_bytes(sh) ? reinterpret_cast<int32_t *>(ws) : nullptr;
     float *v = reinterpret_cast<float *>(ws + order_bytes(sh));
-    const auto add = [&](auto parts_given, const void *from, int parts) {
-        // blocks of 64 columns a wavefront: one where the rows are few
-        const int blocks = s.T > kFewProject ? 4 : 1;
-        add_kernel<DT, decltype(parts_given)::value>
-            <<<dim3(up(s.T, 16), up(s.N, 64 * kAddWaves * blocks)), 64 * kAddWaves, 0, st>>>(
+    const auto add = [&](auto nf, auto gb, auto given, int blocks, const void *from, int parts) {
+        constexpr int NF = decltype(nf)::value, GB = decltype(gb)::value;
+        constexpr bool kParts = !decltype(given)::value;
+        const dim3 grid(up(s.T, 16), up(s.N, 16 * NF * kAddWaves * blocks));
+        if (s.r <= 32)
+            add_kernel<DT, NF, GB, 1, kParts><<<grid, 64 * kAddWaves, 0, st>>>(
+                s, blocks, parts, from, ids, order, b, scale, v, out);
+        else
+            add_kernel<DT, NF, GB, 2, kParts><<<grid, 64 * kAddWaves, 0, st>>>(
                 s, blocks, parts, from, ids, order, b, scale, v, out);
         return hipGetLastError();
     };
+    const std::integral_constant<int, 1> c1;
+    const std::integral_constant<int, 2> c2;
+    const std::integral_constant<int, 4> c4;
+    const std::integral_constant<int, 8> c8;
     hipError_t e;
     if (s.T <= kFewProject && w) {
         float *parts = reinterpret_cast<float *>(ws + v_bytes(sh));
@@ -981,16 +1019,17 @@ hipError_t adapter_of_type(const moe_adapter_shape &sh, const void *x_, const vo
                 s, shrinks, tn, splits, x, w, ids, a, v, parts);
         };
         if (s.T <= 16)
-            few(Stream<16, 64, 1, 4, 8>{}, std::integral_constant<int, 16>{});
+            few(Stream<16, 64, 1, 2, 8, 15, 128>{}, std::integral_constant<int, 16>{});
         else if (s.T <= 32)
-            few(Stream<32, 64, 1, 3, 8>{}, std::integral_constant<int, 32>{});
+            few(Stream<32, 64, 2, 1, 6, 15, 128>{}, std::integral_constant<int, 32>{});
         else if (s.T <= 64)
-            few(Stream<64, 64, 1, 3, 6>{}, std::integral_constant<int, 64>{});
+            few(Stream<64, 64, 2, 1, 6, 12, 128>{}, std::integral_constant<int, 64>{});
         else
-            few(Stream<128, 64, 1, 3, 3>{}, std::integral_constant<int, 128>{});
+            few(Stream<128, 64, 2, 1, 5, 9, 128>{}, std::integral_constant<int, 128>{});
         if ((e = hipGetLastError()) != hipSuccess)
             return e;
-        return add(std::true_type{}, parts, splits);
+        // few rows: many short wavefronts, any mix of adapters
+        return add(c2, c8, std::false_type{}, 1, parts, splits);
     }
     if (order) {
         order_kernel<<<1, kOrderThreads, (s.L + 1) * sizeof(int), st>>>(s, ids, order);
@@ -1007,7 +1046,7 @@ hipError_t adapter_of_type(const moe_adapter_shape &sh, const void *x_, const vo
     if (e != hipSuccess)
         return e;
     if (!w)
-        return add(std::false_type{}, base, 0);
+        return add(c4, c1, std::true_type{}, s.T > kFewProject ? 4 : 1, base, 0);
     const ProjectArgs p{x, w, ids, order, b, scale, v, out};
     const int cus = device_cu_count();
     const int tm = up(s.T, 256), tn = up(s.N, 256), left = tm * tn % cus;

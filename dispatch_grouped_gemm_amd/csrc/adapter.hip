@@ -202,7 +202,7 @@ template <int BM, int BN, int WM, int WN, int NX, int NR, int KB>
 struct Stream {
     static_assert(KB == 128 || KB == 256, "one or two cache lines of a row");
     static constexpr int kSlices = KB / 64, kWaves = kSlices * WM * WN, kThreads = 64 * kWaves;
-    static constexpr int MF = BM / WM / 16, NF = BN / WN / 16;
+    static constexpr int kBM = BM, kBN = BN, MF = BM / WM / 16, NF = BN / WN / 16;
     static constexpr int kRows = 1024 / KB; // rows of a load
     // loads per wavefront and step
     static constexpr int UX = BM / kRows / (kWaves / 2), UR = BN / kRows / (kWaves / 2);
@@ -222,9 +222,10 @@ __device__ __forceinline__ int place_of(int c, int i)
 }
 
 // One wavefront's loads into one ring: U a step, N stages of kStage bytes
-// from lds0.  Loads past the last step repeat it into stages that nobody
-// reads again, so the number in flight stays the same to the end.
-template <int U, int N, int kStage, int KB>
+// from lds0; kOnce: read once, to leave the L2 first.  Loads past the last
+// step repeat it into stages that nobody reads again, so the number in flight
+// stays the same to the end.
+template <int U, int N, int kStage, int KB, bool kOnce>
 struct Ring {
     const uint8_t *next;
     uint32_t voff[U], lds0, slot;
@@ -251,7 +252,7 @@ struct Ring {
     {
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            g2lds<16>(next, voff[u], lds0 + slot + u * 1024);
+            g2lds<16, kOnce>(next, voff[u], lds0 + slot + u * 1024);
         slot = slot + kStage == N * kStage ? 0 : slot + kStage;
         next += left > 0 ? KB : 0;
         --left;
@@ -317,10 +318,10 @@ __device__ __forceinline__ void stream_tile(Stream<BM, BN, WM, WN, NX, NR, KB>, 
         }
     };
     if (wave < kHalf)
-        go(Ring<S::UX, NX, S::kX, KB>(x, H, steps, wave * S::UX, l0, xrow));
+        go(Ring<S::UX, NX, S::kX, KB, false>(x, H, steps, wave * S::UX, l0, xrow));
     else
-        go(Ring<S::UR, NR, S::kR, KB>(w, H, steps, (wave - kHalf) * S::UR, l0 + NX * S::kX,
-                                      wrow));
+        go(Ring<S::UR, NR, S::kR, KB, true>(w, H, steps, (wave - kHalf) * S::UR,
+                                           l0 + NX * S::kX, wrow));
     wait_vmcnt<0>();
     __syncthreads();
     constexpr int MB = BM / 16, NB = BN / 16;
@@ -348,60 +349,73 @@ __device__ __forceinline__ void stream_tile(Stream<BM, BN, WM, WN, NX, NR, KB>, 
 }
 
 // ---------------------------------------------------------------------------
-// Shrink, few rows: workgroup (t, block of 16 of the rank).  Row t works for
-// itself and the next 15 rows of its adapter if the rows before it of the
-// same adapter fill whole sixteens, else it has nothing to do: every
-// adapter's A is read by as few workgroups as its rows allow, in whatever
-// order they come.
+// Shrink, few rows (up to kFewRows, in any order): a task is up to 16 rows of
+// one adapter by the S::kBN of the rank, and a workgroup takes every blocks-th
+// task.  The first of each sixteen rows of an adapter stands for it, so
+// every adapter's A is read as few times as its rows allow.
 // ---------------------------------------------------------------------------
-using FewStream = Stream<16, 16, 1, 1, 16, 16, 256>;
+using FewStream = Stream<16, 16, 1, 1, 16, 16, 256>;  // four wavefronts
+using FewStream8 = Stream<16, 32, 1, 2, 8, 12, 256>;  // eight
 
-template <int DT>
+template <int DT, typename S>
 __device__ __forceinline__ void shrink_few(const AShape &s, const uint16_t *__restrict__ x,
                                            const int32_t *__restrict__ ids,
                                            const uint16_t *__restrict__ a, float *__restrict__ v,
-                                           int t, int j0, uint8_t *lds)
+                                           int block, int blocks, uint8_t *lds)
 {
-    static_assert(FewStream::kThreads == kFewRows, "a thread looks at one row");
-    __shared__ uint64_t mask[kFewRows / 64];
-    __shared__ int member[16];
+    static_assert(S::kThreads >= kFewRows, "a thread looks at one row");
+    constexpr int kGroups = kFewRows / 64;
+    __shared__ int32_t id_of[kFewRows];
+    __shared__ uint64_t firsts[kGroups];
+    __shared__ int lead[kFewRows], member[16];
     const int tid = threadIdx.x, lane = tid & 63, wave = wave_of();
-    const int id = ids[t];
-    if ((unsigned)id >= (unsigned)s.L)
-        return;
-    const bool same = tid < s.T && ids[tid] == id;
-    const uint64_t mine = __ballot(same);
-    if (lane == 0)
-        mask[wave] = mine;
-    if (tid < 16)
-        member[tid] = -1;
+    int id = -1;
+    if (tid < s.T && (unsigned)ids[tid] < (unsigned)s.L)
+        id = ids[tid];
+    if (tid < kFewRows)
+        id_of[tid] = id;
     __syncthreads();
-    // rows of this adapter before row i
-    const auto before = [&](int i) {
-        int n = 0;
-        for (int w = 0; w < kFewRows / 64; ++w) {
-            const int b = i - 64 * w;
-            if (b > 0)
-                n += __builtin_popcountll(b >= 64 ? mask[w] : mask[w] & ((1ull << b) - 1));
-        }
-        return n;
-    };
-    const int first = before(t);
-    if (first % 16)
-        return;
-    if (same) {
-        const int at = before(tid) - first;
-        if (at >= 0 && at < 16)
-            member[at] = tid;
+    // rows of the same adapter before this one
+    int rank = 0;
+    for (int u = 0; u < min(tid, s.T); ++u)
+        rank += id_of[u] == id;
+    const bool leads = id >= 0 && rank % 16 == 0;
+    const uint64_t m = __ballot(leads);
+    if (lane == 0 && wave < kGroups)
+        firsts[wave] = m;
+    __syncthreads();
+    int n = 0, at = 0;
+    for (int w = 0; w < kGroups; ++w) {
+        at += w < wave ? __builtin_popcountll(firsts[w]) : 0;
+        n += __builtin_popcountll(firsts[w]);
     }
-    __syncthreads();
-    v4f sum[1];
-    stream_tile<DT>(
-        FewStream{}, s.H, s.H / 128, x, [&](int i) { return member[i] < 0 ? t : member[i]; },
-        a + (size_t)id * s.r * s.H, [&](int i) { return min(j0 + i, s.r - 1); }, lds, sum);
-    const int row = member[lane & 15], j = j0 + 4 * (lane >> 4);
-    if (wave == 0 && row >= 0 && j < s.r)
-        *reinterpret_cast<v4f *>(v + (size_t)row * s.r + j) = sum[0];
+    if (leads)
+        lead[at + __builtin_popcountll(m & ((1ull << lane) - 1))] = tid | rank << 16;
+    const int nj = (s.r + S::kBN - 1) / S::kBN;
+    for (int task = block; task < n * nj; task += blocks) {
+        if (tid < 16)
+            member[tid] = -1;
+        __syncthreads();
+        const int first = __builtin_amdgcn_readfirstlane(lead[task / nj]);
+        const int t = first & 0xffff, g = __builtin_amdgcn_readfirstlane(id_of[t]);
+        if (id == g && (unsigned)(rank - (first >> 16)) < 16u)
+            member[rank - (first >> 16)] = tid;
+        __syncthreads();
+        const int j0 = task % nj * S::kBN;
+        v4f sum[S::kBN / 16];
+        stream_tile<DT>(
+            S{}, s.H, s.H / 128, x, [&](int i) { return member[i] < 0 ? t : member[i]; },
+            a + (size_t)g * s.r * s.H, [&](int i) { return min(j0 + i, s.r - 1); }, lds, sum);
+        const int row = member[lane & 15];
+        if (wave == 0 && row >= 0)
+#pragma unroll
+            for (int f = 0; f < S::kBN / 16; ++f) {
+                const int j = j0 + 16 * f + 4 * (lane >> 4);
+                if (j < s.r)
+                    *reinterpret_cast<v4f *>(v + (size_t)row * s.r + j) = sum[f];
+            }
+        __syncthreads();
+    }
 }
 
 template <int DT>
@@ -410,7 +424,7 @@ shrink_few_kernel(AShape s, const uint16_t *__restrict__ x, const int32_t *__res
                   const uint16_t *__restrict__ a, float *__restrict__ v)
 {
     __shared__ __align__(1024) uint8_t lds[FewStream::kLds];
-    shrink_few<DT>(s, x, ids, a, v, blockIdx.x, blockIdx.y * 16, lds);
+    shrink_few<DT, FewStream>(s, x, ids, a, v, blockIdx.x, gridDim.x, lds);
 }
 
 // Shrink, many rows, ordered: workgroup (BM places, BN of the rank).
@@ -613,45 +627,50 @@ __device__ __forceinline__ void store_cols(const AShape &s, uint16_t *out, int t
 
 // ---------------------------------------------------------------------------
 // Project, few rows: W is read once.  One launch makes v (its workgroups
-// first) and, beside it, parts of x W^T: a workgroup takes all rows (up to
+// last) and, beside it, parts of x W^T: a workgroup takes all rows (up to
 // BM), 64 columns and one of `splits` parts of H, and leaves float32 sums;
 // the add launch joins the parts in order and adds the adapters' term.
 // Splitting H gives every CU work without more copies of x than columns ask
 // for, and the adapters' chain of loads does not stand at the end of W's.
 // ---------------------------------------------------------------------------
-template <int DT, typename S, int BM>
+template <int DT, typename S, typename F>
 __global__ void __launch_bounds__(S::kThreads)
-few_kernel(AShape s, int shrinks, int tn, int splits, const uint16_t *__restrict__ x,
+few_kernel(AShape s, int tn, int splits, const uint16_t *__restrict__ x,
            const uint16_t *__restrict__ w, const int32_t *__restrict__ ids,
            const uint16_t *__restrict__ a, float *__restrict__ v, float *__restrict__ parts)
 {
-    static_assert(S::kThreads == FewStream::kThreads, "one launch for both");
-    constexpr int kLds = S::kLds > FewStream::kLds ? S::kLds : FewStream::kLds;
+    static_assert(S::kThreads == F::kThreads, "one launch for both");
+    constexpr int kLds = S::kLds > F::kLds ? S::kLds : F::kLds, BM = S::kBM;
     __shared__ __align__(1024) uint8_t lds[kLds];
-    int q = blockIdx.x;
-    if (q < shrinks) {
-        shrink_few<DT>(s, x, ids, a, v, q % s.T, q / s.T * 16, lds);
+    const int q = blockIdx.x;
+    if (q >= tn * splits) {
+        shrink_few<DT, F>(s, x, ids, a, v, q - tn * splits, gridDim.x - tn * splits, lds);
         return;
     }
-    q -= shrinks;
-    const int n0 = q % tn * 64, part = q / tn;
+    const int n0 = q % tn * S::kBN, part = q / tn;
     const int all = s.H / 64, first = (long)all * part / splits;
     const int steps = (int)((long)all * (part + 1) / splits) - first;
-    v4f sum[4 * ((BM / 16 + S::kWaves - 1) / S::kWaves)];
+    constexpr int NB = S::kBN / 16;
+    v4f sum[NB * ((BM / 16 + S::kWaves - 1) / S::kWaves)];
     stream_tile<DT>(
         S{}, s.H, steps, x + 64 * first, [&](int r) { return min(r, s.T - 1); },
         w + (size_t)n0 * s.H + 64 * first,
-        [&](int r) { return min(column_of<4>(r >> 4, r & 15), s.N - 1 - n0); }, lds, sum);
-    const int lane = threadIdx.x & 63, n = n0 + 16 * (lane >> 4);
+        [&](int r) {
+            return min((r & ~63) + column_of<4>((r >> 4) & 3, r & 15), s.N - 1 - n0);
+        },
+        lds, sum);
+    const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int m = 0; m * S::kWaves < BM / 16; ++m) {
         const int t = 16 * (m * S::kWaves + wave_of()) + (lane & 15);
         if (t < min(s.T, BM))
 #pragma unroll
-            for (int f = 0; f < 4; ++f)
-                if (n + 4 * f < s.N)
-                    *reinterpret_cast<v4f *>(parts + ((size_t)part * s.T + t) * s.N + n + 4 * f) =
-                        sum[m * 4 + f];
+            for (int f = 0; f < NB; ++f) {
+                const int n = n0 + 64 * (f / 4) + 16 * (lane >> 4) + 4 * (f % 4);
+                if (n < s.N)
+                    *reinterpret_cast<v4f *>(parts + ((size_t)part * s.T + t) * s.N + n) =
+                        sum[m * NB + f];
+            }
     }
 }
 
@@ -935,11 +954,14 @@ add_kernel(AShape s, int blocks, int parts, const void *base, const int32_t *__r
 
 constexpr int kFewProject = 128; // rows projected by few_kernel
 
+// Columns of a workgroup of few_kernel.
+int few_columns(const moe_adapter_shape &s) { return s.T > 64 ? 128 : 64; }
+
 // Parts of H of few_kernel for a shape: as many workgroups as run at once
 // (one a CU), at most 8 parts of at least two steps.
 int few_splits(const moe_adapter_shape &s)
 {
-    const int tn = (s.N + 63) / 64;
+    const int tn = (s.N + few_columns(s) - 1) / few_columns(s);
     return std::max(1, std::min({256 / tn, 8, s.H / 128}));
 }
 
@@ -1012,20 +1034,26 @@ hipError_t adapter_of_type(const moe_adapter_shape &sh, const void *x_, const vo
     hipError_t e;
     if (s.T <= kFewProject && w) {
         float *parts = reinterpret_cast<float *>(ws + v_bytes(sh));
-        const int tn = up(s.N, 64), splits = few_splits(sh), shrinks = s.T * up(s.r, 16);
-        const auto few = [&](auto stream, auto bm) {
+        const int tn = up(s.N, few_columns(sh)), splits = few_splits(sh);
+        const auto few = [&](auto stream, auto shrink) {
             using S = decltype(stream);
-            few_kernel<DT, S, decltype(bm)::value><<<shrinks + tn * splits, S::kThreads, 0, st>>>(
-                s, shrinks, tn, splits, x, w, ids, a, v, parts);
+            using F = decltype(shrink);
+            // the shrink's workgroups come last and find the CUs that the
+            // parts leave, at most four tasks each
+            const int tasks = s.T * up(s.r, F::kBN);
+            const int shrinks =
+                std::min(tasks, std::max(device_cu_count() - tn * splits, up(tasks, 4)));
+            few_kernel<DT, S, F><<<tn * splits + shrinks, S::kThreads, 0, st>>>(
+                s, tn, splits, x, w, ids, a, v, parts);
         };
         if (s.T <= 16)
-            few(Stream<16, 64, 1, 2, 8, 15, 128>{}, std::integral_constant<int, 16>{});
+            few(Stream<16, 64, 1, 2, 8, 15, 128>{}, FewStream{});
         else if (s.T <= 32)
-            few(Stream<32, 64, 2, 1, 6, 15, 128>{}, std::integral_constant<int, 32>{});
+            few(Stream<32, 64, 2, 1, 6, 15, 128>{}, FewStream{});
         else if (s.T <= 64)
-            few(Stream<64, 64, 2, 1, 6, 12, 128>{}, std::integral_constant<int, 64>{});
+            few(Stream<64, 64, 2, 1, 6, 12, 128>{}, FewStream{});
         else
-            few(Stream<128, 64, 2, 1, 5, 9, 128>{}, std::integral_constant<int, 128>{});
+            few(Stream<128, 128, 2, 2, 4, 5, 128>{}, FewStream8{});
         if ((e = hipGetLastError()) != hipSuccess)
             return e;
         // few rows: many short wavefronts, any mix of adapters
@@ -1038,7 +1066,8 @@ hipError_t adapter_of_type(const moe_adapter_shape &sh, const void *x_, const vo
     }
     if (s.T <= kFewRows) {
         shrink_few_kernel<DT>
-            <<<dim3(s.T, up(s.r, 16)), FewStream::kThreads, 0, st>>>(s, x, ids, a, v);
+            <<<std::min(s.T * up(s.r, FewStream::kBN), 2 * device_cu_count()),
+               FewStream::kThreads, 0, st>>>(s, x, ids, a, v);
         e = hipGetLastError();
     } else {
         e = shrink_many<DT>(s, x, ids, order, a, v, st);

@@ -118,25 +118,28 @@ route_kernel(int T, int E, int K, bool renorm, const void *__restrict__ logits,
         return; // a whole row of lanes
     float l[PER];
     load_logits<DT, PER, kVec>(logits, t, E, lane, l);
-    // the ordering keys; 0: not eligible (-inf, NaN, past the last expert).
-    // A 16-bit logit's key takes the high half and its expert, complemented,
-    // the low one: one maximum finds the winner and settles ties.
+    // The ordering keys, a NaN as -inf; 0 once chosen.  A 16-bit logit's key
+    // takes the high half and its expert, complemented, the low one: one
+    // maximum finds the winner and settles ties.
     constexpr bool kWide = DT == MOE_DT_F32;
+    // the largest key of a logit of -inf
+    constexpr uint32_t kNone = kWide                  ? 0x007fffffu
+                               : DT == MOE_DT_BF16 ? 0x007fffffu
+                                                      : 0x03ffffffu;
     uint32_t key[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        uint32_t u;
-        if constexpr (kWide) {
-            u = __float_as_uint(l[i] + 0.0f);
-            u = u & 0x80000000u ? ~u : u | 0x80000000u;
+        l[i] = fmaxf(l[i], -INFINITY); // the other operand of a NaN
+        const float z = l[i] + 0.0f;
+        if constexpr (DT == MOE_DT_F16) {
+            const uint32_t b = Elem<MOE_DT_F16>::bits_of(z) << 16;
+            key[i] = ((b ^ (uint32_t)((int32_t)b >> 31)) | (~b & 0x80000000u)) & 0xffff0000u;
         } else {
-            const float z = l[i] + 0.0f;
-            const uint32_t b = DT == MOE_DT_BF16 ? __float_as_uint(z) >> 16
-                                                 : Elem<MOE_DT_F16>::bits_of(z);
-            u = (b & 0x8000u ? ~b & 0xffffu : b | 0x8000u) << 16 |
-                (0xffffu - expert_of<DT, kVec>(i, lane));
+            const uint32_t b = __float_as_uint(z);
+            key[i] = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
         }
-        key[i] = l[i] > -INFINITY ? u : 0u;
+        if constexpr (!kWide)
+            key[i] = (key[i] & 0xffff0000u) | (0xffffu - expert_of<DT, kVec>(i, lane));
     }
     const auto value_of = [](uint32_t k) {
         if constexpr (kWide) {
@@ -154,33 +157,45 @@ route_kernel(int T, int E, int K, bool renorm, const void *__restrict__ logits,
         for (int i = 0; i < PER; ++i)
             best = max(best, key[i]);
         const uint32_t won = row_max(best);
+        const bool found = won > kNone;
         int e;
         if constexpr (kWide) {
-            uint32_t at = ~0u;
+            // the lane's first register of that key, then the lowest expert;
+            // only that register of that lane is done with
+            int at = PER;
+#pragma unroll
+            for (int i = PER - 1; i >= 0; --i)
+                at = key[i] == won ? i : at;
+            const uint32_t mine_e = at < PER ? (uint32_t)expert_of<DT, kVec>(at, lane) : ~0u;
+            e = (int)row_min(mine_e);
+            at = mine_e == (uint32_t)e ? at : PER;
 #pragma unroll
             for (int i = 0; i < PER; ++i)
-                if (key[i] == won)
-                    at = min(at, (uint32_t)expert_of<DT, kVec>(i, lane));
-            e = (int)row_min(at);
+                key[i] = at == i ? 0u : key[i];
         } else {
             e = 0xffff - (int)(won & 0xffffu);
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                key[i] = key[i] == won ? 0u : key[i];
         }
         const float v = value_of(won);
         if (k == 0) {
             m = v;
             if (!renorm) {
                 float s = 0.0f;
+                if (__any(m == INFINITY)) {
 #pragma unroll
-                for (int i = 0; i < PER; ++i)
-                    s += key[i] ? exp_to_max(l[i], m) : 0.0f;
+                    for (int i = 0; i < PER; ++i)
+                        s += exp_to_max(l[i], m);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < PER; ++i)
+                        s += __expf(l[i] - m);
+                }
                 all = row_sum(s);
             }
         }
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (key[i] == won && (!kWide || expert_of<DT, kVec>(i, lane) == e))
-                key[i] = 0u;
-        if (lane == k && won) {
+        if (lane == k && found) {
             mine = expf(v == m ? 0.0f : v - m);
             my_id = e;
         }

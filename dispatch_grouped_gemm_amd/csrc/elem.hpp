@@ -13,8 +13,8 @@ inline size_t elem_bytes(int dtype) { return dtype == MOE_DT_F32 ? 4 : 2; }
 template <int DT>
 struct Elem;
 
-// One 16-byte piece as kVec float32 values and back (round to nearest even;
-// bf16 through f32_to_bf16, fp16 by the hardware conversion).
+// One 16-byte piece as kVec float32 values and back, by the hardware
+// conversions (round to nearest even).
 template <>
 struct Elem<MOE_DT_BF16> {
     typedef uint16_t type;
@@ -23,7 +23,12 @@ struct Elem<MOE_DT_BF16> {
     {
         return __uint_as_float((uint32_t)*p << 16);
     }
-    static __device__ __forceinline__ void store(type *p, float v) { *p = (type)f32_to_bf16(v); }
+    static __device__ __forceinline__ uint32_t bits_of(float lo, float hi)
+    {
+        typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+        return __builtin_bit_cast(uint32_t, v2bf{(__bf16)lo, (__bf16)hi});
+    }
+    static __device__ __forceinline__ void store(type *p, float v) { *p = (type)bits_of(v, v); }
     static __device__ __forceinline__ void unpack(const uint4 &q, float *f)
     {
         const uint32_t w[4] = {q.x, q.y, q.z, q.w};
@@ -38,7 +43,7 @@ struct Elem<MOE_DT_BF16> {
         uint32_t o[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            o[i] = f32_to_bf16(f[2 * i]) | (f32_to_bf16(f[2 * i + 1]) << 16);
+            o[i] = bits_of(f[2 * i], f[2 * i + 1]);
         return uint4{o[0], o[1], o[2], o[3]};
     }
 };

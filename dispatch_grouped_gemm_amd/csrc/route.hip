@@ -63,11 +63,35 @@ __device__ __forceinline__ float row_sum(float v)
     }));
 }
 
-// exp(v - m), 1 at v = m whatever m is.  The hardware exponential of
-// (v - m) log2 e: off by |v - m| 2^-24 and an ulp, relatively.
-__device__ __forceinline__ float exp_to_max(float v, float m)
+// Value of lane k of the same row of 16.
+template <int k>
+__device__ __forceinline__ uint32_t row_lane(uint32_t v)
 {
-    return __expf(v == m ? 0.0f : v - m);
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x150 + k, 0xf, 0xf, true);
+}
+
+// exp(l - m) of a lane's logits in place (0 for -inf) and their sum; m the
+// largest of the token.  The hardware exponential of (l - m) log2 e: off by
+// |l - m| 2^-24 and an ulp, relatively.
+template <int PER>
+__device__ __forceinline__ float exps(float *l, float m)
+{
+    float s = 0.0f;
+    if (__any(m == INFINITY)) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            l[i] = __expf(l[i] == m ? 0.0f : l[i] - m);
+            s += l[i];
+        }
+    } else {
+        const float z = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            l[i] = __expf(l[i] - z);
+            s += l[i];
+        }
+    }
+    return s;
 }
 
 // Which expert register i of a lane holds: whole 16-byte pieces where the
@@ -77,6 +101,20 @@ __device__ __forceinline__ int expert_of(int i, int lane)
 {
     constexpr int V = Elem<DT>::kVec;
     return kVec ? ((i / V) * kLanes + lane) * V + i % V : i * kLanes + lane;
+}
+
+// The lane that holds expert e (16 or more for e < 0), and its register.
+template <int DT, bool kVec>
+__device__ __forceinline__ int lane_of(int e)
+{
+    const int l = kVec ? e / Elem<DT>::kVec % kLanes : e % kLanes;
+    return e < 0 ? kLanes : l;
+}
+template <int DT, bool kVec>
+__device__ __forceinline__ int register_of(int e)
+{
+    constexpr int V = Elem<DT>::kVec;
+    return kVec ? e / (V * kLanes) * V + e % V : e / kLanes;
 }
 
 // A token's logits; -inf past the last expert.
@@ -182,17 +220,7 @@ route_kernel(int T, int E, int K, bool renorm, const void *__restrict__ logits,
         if (k == 0) {
             m = v;
             if (!renorm) {
-                float s = 0.0f;
-                if (__any(m == INFINITY)) {
-#pragma unroll
-                    for (int i = 0; i < PER; ++i)
-                        s += exp_to_max(l[i], m);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < PER; ++i)
-                        s += __expf(l[i] - m);
-                }
-                all = row_sum(s);
+                all = row_sum(exps<PER>(l, m));
             }
         }
         if (lane == k && found) {
@@ -219,7 +247,7 @@ route_backward_kernel(int T, int E, int K, bool renorm, const void *__restrict__
     const int t = blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
     if (t >= T)
         return;
-    // lane k: the slot k
+    // lane k: the slot k; no expert in the lanes past K
     int id = -1;
     float wk = 0.0f, g = 0.0f;
     if (lane < K) {
@@ -239,34 +267,47 @@ route_backward_kernel(int T, int E, int K, bool renorm, const void *__restrict__
         d[i] = 0.0f;
     // what slot k adds to its expert: w (g - dot), or g alone
     const float add = renorm ? wk * (g - dot) : g;
-    for (int k = 0; k < K; ++k) {
-        const int e = __shfl(id, k, kLanes);
-        const float a = __shfl(add, k, kLanes);
+    // the slots whose expert this lane holds, and one of them a turn: a lane
+    // rarely holds more than two, and a turn costs what a slot would
+    uint32_t held = 0;
+#define MOE_SLOT(k)                                                                              \
+    held |= (uint32_t)(lane_of<DT, kVec>((int)row_lane<k>((uint32_t)id)) == lane) << k
+    MOE_SLOT(0);
+    MOE_SLOT(1);
+    MOE_SLOT(2);
+    MOE_SLOT(3);
+    MOE_SLOT(4);
+    MOE_SLOT(5);
+    MOE_SLOT(6);
+    MOE_SLOT(7);
+#undef MOE_SLOT
+    while (__any(held != 0)) {
+        const int k = __ffs(held) - 1;
+        const int e = __shfl(id, max(k, 0), kLanes);
+        const float a = __shfl(add, max(k, 0), kLanes);
+        const int at = k >= 0 ? register_of<DT, kVec>(e) : PER;
 #pragma unroll
         for (int i = 0; i < PER; ++i)
-            d[i] += e == expert_of<DT, kVec>(i, lane) ? a : 0.0f;
+            d[i] += at == i ? a : 0.0f;
+        held &= held - 1;
     }
     if (!renorm) {
         float l[PER];
         load_logits<DT, PER, kVec>(logits, t, E, lane, l);
         float m = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < PER; ++i)
-            m = l[i] > m ? l[i] : m; // (passes NaN over)
+        for (int i = 0; i < PER; ++i) {
+            l[i] = fmaxf(l[i], -INFINITY); // a NaN is not eligible
+            m = fmaxf(m, l[i]);
+        }
         m = __uint_as_float(row_reduce(__float_as_uint(m), [](uint32_t a, uint32_t b) {
             return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
         }));
-        float s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            l[i] = l[i] > -INFINITY ? exp_to_max(l[i], m) : 0.0f;
-            s += l[i];
-        }
-        s = row_sum(s);
+        const float s = row_sum(exps<PER>(l, m));
         const float r = s > 0.0f ? 1.0f / s : 0.0f;
 #pragma unroll
         for (int i = 0; i < PER; ++i)
-            d[i] = l[i] > 0.0f ? l[i] * r * (d[i] - dot) : 0.0f;
+            d[i] = l[i] * r * (d[i] - dot);
     }
     auto *dl = static_cast<typename Elem<DT>::type *>(dlogits) + (size_t)t * E;
     if constexpr (kVec) {

@@ -11,8 +11,8 @@
 // ids among them: an adapter's product is formed for 16 rows at a time (the
 // matrix instruction costs the same for one) and taken only where the id
 // matches, so no row ever sees another adapter's values, infinite or NaN.
-// Past kFewRows rows, a first launch orders the rows by adapter, so that a
-// tile holds few of them; results do not depend on that order.
+// Past kFewRows rows a first launch orders the rows by adapter, so that a
+// tile holds few of them; results do not depend on the places inside one.
 //
 // v keeps float32's precision through the matrix instruction: it enters as
 // the sum of two 16-bit values, hi = round(v) and lo = round(v - hi).  fp16
@@ -34,7 +34,7 @@ struct AShape {
 };
 
 constexpr int kFewRows = 256;       // rows shrunk without an order
-constexpr int kOrderKeys = 1 << 13; // adapters the ordering launch counts in LDS
+constexpr int kOrderKeys = 1 << 13; // adapters that the order counts in LDS
 
 // D(16x16) += A(16x32) B(32x16): lane l holds A's row / B's column l mod 16
 // at k = 8 (l div 16) .. + 7, and D's column l mod 16 at rows
@@ -100,18 +100,33 @@ __device__ __forceinline__ int column_of(int f, int i)
 }
 
 // ---------------------------------------------------------------------------
-// Order: the rows by adapter, those without one last, as a list of rows.
-// One workgroup: a histogram in LDS, its scan, and a claim of a place per
-// row (places inside an adapter in whatever order the claims land).  A
-// wavefront whose rows share an adapter claims with one atomic.
+// Order: the rows by adapter, those without one last, as a list of rows
+// (places inside an adapter in whatever order the claims land), and the
+// blocks of up to `block` places that hold one adapter each.  One workgroup:
+// a histogram (in LDS, or in the workspace past kOrderKeys adapters), its
+// scan, and a claim of a place per row.  A wavefront whose rows share an
+// adapter claims with one atomic.
 // ---------------------------------------------------------------------------
-constexpr int kOrderThreads = 1024;
+constexpr int kOrderThreads = 1024, kOrderBatch = 8;
+
+// Places first .. first + rows - 1 hold rows of one adapter.
+struct Block {
+    int id, first, rows, pad;
+};
+
+struct OrderOut {
+    int32_t *order;  // T
+    int32_t *blocks; // how many
+    Block *block;    // T / rows + L at most
+    int32_t *count;  // L + 1 of scratch, or null: in LDS
+};
 
 __global__ void __launch_bounds__(kOrderThreads)
-order_kernel(AShape s, const int32_t *__restrict__ ids, int32_t *__restrict__ order)
+order_kernel(AShape s, int rows, const int32_t *__restrict__ ids, OrderOut o)
 {
-    extern __shared__ int count[]; // L + 1
-    __shared__ int wsum[kOrderThreads / 64];
+    extern __shared__ int lds_count[]; // L + 1
+    __shared__ int wsum[2][kOrderThreads / 64];
+    int *count = o.count ? o.count : lds_count;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int keys = s.L + 1;
     for (int i = tid; i < keys; i += kOrderThreads)
@@ -133,49 +148,65 @@ order_kernel(AShape s, const int32_t *__restrict__ ids, int32_t *__restrict__ or
         }
         return in ? atomicAdd(&count[k], 1) : 0;
     };
-    const auto key = [&](long t) {
-        const int id = ids[t];
-        return (unsigned)id < (unsigned)s.L ? id : s.L;
+    // f(row, its key, whether there is such a row), kOrderBatch loads at once
+    const auto walk = [&](auto f) {
+        for (long b = 0; b < s.T; b += kOrderThreads * kOrderBatch) {
+            int id[kOrderBatch];
+#pragma unroll
+            for (int q = 0; q < kOrderBatch; ++q)
+                id[q] = ids[min(b + q * kOrderThreads + tid, (long)s.T - 1)];
+#pragma unroll
+            for (int q = 0; q < kOrderBatch; ++q) {
+                const long t = b + q * kOrderThreads + tid;
+                f((int)t, (unsigned)id[q] < (unsigned)s.L ? id[q] : s.L, t < s.T);
+            }
+        }
     };
-    const long rounds = ((long)s.T + kOrderThreads - 1) / kOrderThreads;
-    for (long q = 0; q < rounds; ++q) {
-        const long t = q * kOrderThreads + tid;
-        const bool in = t < s.T;
-        claim(in ? key(t) : 0, in);
-    }
+    walk([&](int, int k, bool in) { (void)claim(k, in); });
     __syncthreads();
-    // exclusive scan of the counts, per keys of each thread
+    // exclusive scans of the counts and of the blocks, a run of keys a thread
     const int per = (keys + kOrderThreads - 1) / kOrderThreads;
     const int b = min(keys, tid * per), e = min(keys, b + per);
-    int sum = 0;
-    for (int i = b; i < e; ++i)
-        sum += count[i];
-    int inc = sum;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int o = __shfl_up(inc, d);
-        if (lane >= d)
-            inc += o;
+    int sum[2] = {0, 0};
+    for (int i = b; i < e; ++i) {
+        const int c = count[i];
+        sum[0] += c;
+        sum[1] += i < s.L ? (c + rows - 1) / rows : 0;
     }
-    if (lane == 63)
-        wsum[wave] = inc;
+    int inc[2] = {sum[0], sum[1]};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int u = __shfl_up(inc[h], d);
+            if (lane >= d)
+                inc[h] += u;
+        }
+        if (lane == 63)
+            wsum[h][wave] = inc[h];
+    }
     __syncthreads();
-    int run = inc - sum;
-    for (int w = 0; w < wave; ++w)
-        run += wsum[w];
+    int run = inc[0] - sum[0], at = inc[1] - sum[1];
+    for (int w = 0; w < wave; ++w) {
+        run += wsum[0][w];
+        at += wsum[1][w];
+    }
     for (int i = b; i < e; ++i) {
         const int c = count[i];
         count[i] = run;
+        if (i < s.L)
+            for (int q = 0; q < c; q += rows)
+                o.block[at++] = Block{i, run + q, min(rows, c - q), 0};
         run += c;
     }
+    if (tid == kOrderThreads - 1)
+        *o.blocks = at;
     __syncthreads();
-    for (long q = 0; q < rounds; ++q) {
-        const long t = q * kOrderThreads + tid;
-        const bool in = t < s.T;
-        const int at = claim(in ? key(t) : 0, in);
+    walk([&](int t, int k, bool in) {
+        const int place = claim(k, in);
         if (in)
-            order[at] = (int)t;
-    }
+            o.order[place] = t;
+    });
 }
 
 // ---------------------------------------------------------------------------
@@ -427,37 +458,33 @@ shrink_few_kernel(AShape s, const uint16_t *__restrict__ x, const int32_t *__res
     shrink_few<DT, FewStream>(s, x, ids, a, v, blockIdx.x, gridDim.x, lds);
 }
 
-// Shrink, many rows, ordered: workgroup (BM places, BN of the rank).
+// Shrink, many rows, ordered: workgroup (a block of up to BM places of one
+// adapter, BN of the rank).
 template <int DT, int BM, int BN, int WM, int NX, int NR>
 __global__ void __launch_bounds__((Stream<BM, BN, WM, 1, NX, NR, 256>::kThreads))
-shrink_many_kernel(AShape s, const uint16_t *__restrict__ x, const int32_t *__restrict__ ids,
-                   const int32_t *__restrict__ order, const uint16_t *__restrict__ a,
-                   float *__restrict__ v)
+shrink_many_kernel(AShape s, const uint16_t *__restrict__ x, OrderOut o,
+                   const uint16_t *__restrict__ a, float *__restrict__ v)
 {
     using S = Stream<BM, BN, WM, 1, NX, NR, 256>;
-    static_assert(BM <= 32, "the rows' adapters in one mask");
     __shared__ __align__(1024) uint8_t lds[S::kLds];
+    if ((int)blockIdx.x >= *o.blocks)
+        return;
+    const Block b = o.block[blockIdx.x];
     const int lane = threadIdx.x & 63, wave = wave_of();
-    const long i0 = (long)blockIdx.x * BM;
-    const Row row = row_at(s, order, ids, i0 + (lane & (BM - 1)));
     const int j0 = blockIdx.y * BN;
-    uint32_t todo = (uint32_t)__ballot(row.id >= 0);
-    while (todo) {
-        const int g = __builtin_amdgcn_readlane(row.id, __builtin_ctz(todo));
-        todo &= ~(uint32_t)__ballot(row.id == g);
-        v4f sum[BN / 16];
-        stream_tile<DT>(
-            S{}, s.H, s.H / 128, x, [&](int i) { return row_at(s, order, ids, i0 + i).t; },
-            a + (size_t)g * s.r * s.H, [&](int i) { return min(j0 + i, s.r - 1); }, lds, sum);
-        const Row mine = row_at(s, order, ids, i0 + 16 * wave + (lane & 15));
-        if (wave < BM / 16 && mine.id == g)
+    v4f sum[BN / 16];
+    stream_tile<DT>(
+        S{}, s.H, s.H / 128, x, [&](int i) { return o.order[b.first + min(i, b.rows - 1)]; },
+        a + (size_t)b.id * s.r * s.H, [&](int i) { return min(j0 + i, s.r - 1); }, lds, sum);
+    const int i = 16 * wave + (lane & 15);
+    if (wave < BM / 16 && i < b.rows) {
+        float *vr = v + (size_t)o.order[b.first + i] * s.r;
 #pragma unroll
-            for (int f = 0; f < BN / 16; ++f) {
-                const int j = j0 + 16 * f + 4 * (lane >> 4);
-                if (j < s.r)
-                    *reinterpret_cast<v4f *>(v + (size_t)mine.t * s.r + j) = sum[f];
-            }
-        __syncthreads();
+        for (int f = 0; f < BN / 16; ++f) {
+            const int j = j0 + 16 * f + 4 * (lane >> 4);
+            if (j < s.r)
+                *reinterpret_cast<v4f *>(vr + j) = sum[f];
+        }
     }
 }
 
@@ -970,37 +997,64 @@ size_t parts_bytes(const moe_adapter_shape &s)
     return s.T > kFewProject ? 0 : (size_t)few_splits(s) * s.T * s.N * sizeof(float);
 }
 
-size_t order_bytes(const moe_adapter_shape &s)
+// The order's arrays in the workspace, from its start; order null where there
+// is none (few rows).
+struct OrderLayout {
+    OrderOut out;
+    size_t bytes;
+};
+
+OrderLayout order_layout(const moe_adapter_shape &s, uint8_t *ws)
 {
-    return s.T > kFewRows && s.L < kOrderKeys ? ((size_t)s.T * sizeof(int32_t) + 255) / 256 * 256
-                                              : 0;
+    OrderLayout l{};
+    if (s.T <= kFewRows)
+        return l;
+    const auto take = [&](size_t n) {
+        uint8_t *p = ws + l.bytes;
+        l.bytes += (n + 255) / 256 * 256;
+        return p;
+    };
+    l.out.order = reinterpret_cast<int32_t *>(take(sizeof(int32_t) * s.T));
+    l.out.blocks = reinterpret_cast<int32_t *>(take(sizeof(int32_t)));
+    l.out.block = reinterpret_cast<Block *>(
+        take(sizeof(Block) * ((s.T + 15u) / 16u + (size_t)std::min(s.T, s.L))));
+    if (s.L >= kOrderKeys)
+        l.out.count = reinterpret_cast<int32_t *>(take(sizeof(int32_t) * ((size_t)s.L + 1)));
+    return l;
 }
 
 // x A^T of every row, 256-byte aligned ends.
 size_t v_bytes(const moe_adapter_shape &s)
 {
-    return order_bytes(s) + ((size_t)s.T * s.rank * sizeof(float) + 255) / 256 * 256;
+    return order_layout(s, nullptr).bytes + ((size_t)s.T * s.rank * sizeof(float) + 255) / 256 * 256;
 }
 
 int up(long n, int by) { return (int)((n + by - 1) / by); }
 
+// The order, and x A^T of its blocks.
 template <int DT>
-hipError_t shrink_many(const AShape &s, const uint16_t *x, const int32_t *ids,
-                       const int32_t *order, const uint16_t *a, float *v, hipStream_t st)
+hipError_t shrink_many(const AShape &s, const uint16_t *x, const int32_t *ids, const OrderOut &o,
+                       const uint16_t *a, float *v, hipStream_t st)
 {
     // as much of the rank per workgroup as there is (x is read once per
     // block of the rank), but a workgroup for every CU; x comes from memory
     // and gets the deeper ring
-    const int cus = device_cu_count(), t = up(s.T, 32);
-    if (s.r > 32 && t * up(s.r, 64) >= cus)
+    const int cus = device_cu_count(), t = up(s.T, 32), more = std::min(s.T, s.L);
+    const bool wide = s.r > 16 && t * up(s.r, 32) >= cus;
+    order_kernel<<<1, kOrderThreads, o.count ? 0 : (s.L + 1) * sizeof(int), st>>>(
+        s, wide ? 32 : 16, ids, o);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess)
+        return e;
+    if (wide && s.r > 32 && t * up(s.r, 64) >= cus)
         shrink_many_kernel<DT, 32, 64, 2, 8, 6>
-            <<<dim3(t, up(s.r, 64)), 512, 0, st>>>(s, x, ids, order, a, v);
-    else if (s.r > 16 && t * up(s.r, 32) >= cus)
+            <<<dim3(t + more, up(s.r, 64)), 512, 0, st>>>(s, x, o, a, v);
+    else if (wide)
         shrink_many_kernel<DT, 32, 32, 2, 10, 8>
-            <<<dim3(t, up(s.r, 32)), 512, 0, st>>>(s, x, ids, order, a, v);
+            <<<dim3(t + more, up(s.r, 32)), 512, 0, st>>>(s, x, o, a, v);
     else
         shrink_many_kernel<DT, 16, 16, 1, 10, 10>
-            <<<dim3(up(s.T, 16), up(s.r, 16)), 256, 0, st>>>(s, x, ids, order, a, v);
+            <<<dim3(up(s.T, 16) + more, up(s.r, 16)), 256, 0, st>>>(s, x, o, a, v);
     return hipGetLastError();
 }
 
@@ -1013,8 +1067,9 @@ hipError_t adapter_of_type(const moe_adapter_shape &sh, const void *x_, const vo
     const auto *x = static_cast<const uint16_t *>(x_), *w = static_cast<const uint16_t *>(w_);
     const auto *a = static_cast<const uint16_t *>(a_), *b = static_cast<const uint16_t *>(b_);
     auto *out = static_cast<uint16_t *>(out_);
-    int32_t *order = order_bytes(sh) ? reinterpret_cast<int32_t *>(ws) : nullptr;
-    float *v = reinterpret_cast<float *>(ws + order_bytes(sh));
+    const OrderLayout ol = order_layout(sh, ws);
+    const int32_t *order = ol.out.order;
+    float *v = reinterpret_cast<float *>(ws + ol.bytes);
     const auto add = [&](auto nf, auto gb, auto given, int blocks, const void *from, int parts) {
         constexpr int NF = decltype(nf)::value, GB = decltype(gb)::value;
         constexpr bool kParts = !decltype(given)::value;
@@ -1059,18 +1114,13 @@ hipError_t adapter_of_type(const moe_adapter_shape &sh, const void *x_, const vo
         // few rows: many short wavefronts, any mix of adapters
         return add(c2, c8, std::false_type{}, 1, parts, splits);
     }
-    if (order) {
-        order_kernel<<<1, kOrderThreads, (s.L + 1) * sizeof(int), st>>>(s, ids, order);
-        if ((e = hipGetLastError()) != hipSuccess)
-            return e;
-    }
     if (s.T <= kFewRows) {
         shrink_few_kernel<DT>
             <<<std::min(s.T * up(s.r, FewStream::kBN), 2 * device_cu_count()),
                FewStream::kThreads, 0, st>>>(s, x, ids, a, v);
         e = hipGetLastError();
     } else {
-        e = shrink_many<DT>(s, x, ids, order, a, v, st);
+        e = shrink_many<DT>(s, x, ids, ol.out, a, v, st);
     }
     if (e != hipSuccess)
         return e;

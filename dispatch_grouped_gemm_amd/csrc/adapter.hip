@@ -99,6 +99,14 @@ __device__ __forceinline__ int column_of(int f, int i)
     return 4 * NF * (i >> 2) + 4 * f + (i & 3);
 }
 
+// Place of workgroup b of n in a run that gives each XCD (neighbouring
+// workgroups run on different ones) a contiguous part.
+__device__ __forceinline__ int xcd_run(int b, int n)
+{
+    const int xcd = b & 7;
+    return xcd * (n >> 3) + min(xcd, n & 7) + (b >> 3);
+}
+
 // ---------------------------------------------------------------------------
 // Order: the rows by adapter, those without one last, as a list of rows
 // (places inside an adapter in whatever order the claims land), and the
@@ -467,9 +475,11 @@ shrink_many_kernel(AShape s, const uint16_t *__restrict__ x, OrderOut o,
 {
     using S = Stream<BM, BN, WM, 1, NX, NR, 256>;
     __shared__ __align__(1024) uint8_t lds[S::kLds];
-    if ((int)blockIdx.x >= *o.blocks)
+    const int n = *o.blocks;
+    if ((int)blockIdx.x >= n)
         return;
-    const Block b = o.block[blockIdx.x];
+    // an XCD's blocks lie together: few adapters' A in its L2
+    const Block b = o.block[xcd_run(blockIdx.x, n)];
     const int lane = threadIdx.x & 63, wave = wave_of();
     const int j0 = blockIdx.y * BN;
     v4f sum[BN / 16];
@@ -714,14 +724,6 @@ few_kernel(AShape s, int tn, int splits, const uint16_t *__restrict__ x,
 // the loads of the step after it, into the stage that all wavefronts have
 // just finished reading: one barrier a step, and a step's time for its loads.
 // ---------------------------------------------------------------------------
-
-// Place of workgroup b of n in a run that gives each XCD (neighbouring
-// workgroups run on different ones) a contiguous part.
-__device__ __forceinline__ int xcd_run(int b, int n)
-{
-    const int xcd = b & 7;
-    return xcd * (n >> 3) + min(xcd, n & 7) + (b >> 3);
-}
 
 // Tile q of tm x tn: down 8 row tiles before the next column tile, so the
 // tiles that run together on an XCD share rows and columns in its L2.

@@ -90,13 +90,12 @@ __device__ __forceinline__ Row row_at(const AShape &s, const int32_t *__restrict
     return Row{t, i < s.T && (unsigned)id < (unsigned)s.L ? id : -1};
 }
 
-// Column of the output that row i (0..15) of block f (of NF) of 16 weight
-// rows stands for, within the 16 NF columns of a wavefront: a lane then
-// holds 4 NF neighbouring columns of its token.
-template <int NF>
+// Column of the output that row i (0..15) of the block f of 16 weight rows
+// stands for: a lane then holds 8 neighbouring columns of its token in two
+// blocks' sums, and the four lanes of a token 32 (64 whole bytes).
 __device__ __forceinline__ int column_of(int f, int i)
 {
-    return 4 * NF * (i >> 2) + 4 * f + (i & 3);
+    return 32 * (f >> 1) + 8 * (i >> 2) + 4 * (f & 1) + (i & 3);
 }
 
 // Place of workgroup b of n in a run that gives each XCD (neighbouring
@@ -156,7 +155,7 @@ order_kernel(AShape s, int rows, const int32_t *__restrict__ ids, OrderOut o)
         }
         return in ? atomicAdd(&count[k], 1) : 0;
     };
-    // f(row, its key, whether there is such a row), kOrderBatch loads at once
+    // f(q, row, its key, whether there is such a row), kOrderBatch loads at once
     const auto walk = [&](auto f) {
         for (long b = 0; b < s.T; b += kOrderThreads * kOrderBatch) {
             int id[kOrderBatch];
@@ -166,11 +165,21 @@ order_kernel(AShape s, int rows, const int32_t *__restrict__ ids, OrderOut o)
 #pragma unroll
             for (int q = 0; q < kOrderBatch; ++q) {
                 const long t = b + q * kOrderThreads + tid;
-                f((int)t, (unsigned)id[q] < (unsigned)s.L ? id[q] : s.L, t < s.T);
+                f(q, (int)t, (unsigned)id[q] < (unsigned)s.L ? id[q] : s.L, t < s.T);
             }
         }
     };
-    walk([&](int, int k, bool in) { (void)claim(k, in); });
+    // a claim's answer is the row's place inside its adapter: up to one batch
+    // of rows keeps it, more claim a second time, from the adapters' places on
+    const bool one = s.T <= kOrderThreads * kOrderBatch;
+    int place[kOrderBatch], key[kOrderBatch];
+    walk([&](int q, int, int k, bool in) {
+        const int at = claim(k, in);
+        if (one) {
+            place[q] = at;
+            key[q] = k;
+        }
+    });
     __syncthreads();
     // exclusive scans of the counts and of the blocks, a run of keys a thread
     const int per = (keys + kOrderThreads - 1) / kOrderThreads;
@@ -210,10 +219,19 @@ order_kernel(AShape s, int rows, const int32_t *__restrict__ ids, OrderOut o)
     if (tid == kOrderThreads - 1)
         *o.blocks = at;
     __syncthreads();
-    walk([&](int t, int k, bool in) {
-        const int place = claim(k, in);
+    if (one) {
+#pragma unroll
+        for (int q = 0; q < kOrderBatch; ++q) {
+            const int t = q * kOrderThreads + tid;
+            if (t < s.T)
+                o.order[count[key[q]] + place[q]] = t;
+        }
+        return;
+    }
+    walk([&](int, int t, int k, bool in) {
+        const int at = claim(k, in);
         if (in)
-            o.order[place] = t;
+            o.order[at] = t;
     });
 }
 
@@ -235,9 +253,10 @@ order_kernel(AShape s, int rows, const int32_t *__restrict__ ids, OrderOut o)
 //
 // A wavefront multiplies 64 bytes of every step (one matrix instruction deep)
 // for a block of WM x WN of the tile; the KB / 64 sums of a block meet in LDS
-// at the end, in a fixed order.
+// at the end, in a fixed order.  kOnce: the weight is read by no other
+// workgroup and leaves the L2 first.
 // ---------------------------------------------------------------------------
-template <int BM, int BN, int WM, int WN, int NX, int NR, int KB>
+template <int BM, int BN, int WM, int WN, int NX, int NR, int KB, bool kOnce = true>
 struct Stream {
     static_assert(KB == 128 || KB == 256, "one or two cache lines of a row");
     static constexpr int kSlices = KB / 64, kWaves = kSlices * WM * WN, kThreads = 64 * kWaves;
@@ -309,14 +328,14 @@ struct Ring {
 // from the rows of w: xrow(i) and wrow(i) give their numbers, w's within
 // 2^31 bytes of its base.  Afterwards wavefront v holds the blocks of 16
 // rows v, v + kWaves, ... in sum, BN / 16 values a block.
-template <int DT, int BM, int BN, int WM, int WN, int NX, int NR, int KB, typename XRow,
-          typename WRow>
-__device__ __forceinline__ void stream_tile(Stream<BM, BN, WM, WN, NX, NR, KB>, int H, int steps,
+template <int DT, int BM, int BN, int WM, int WN, int NX, int NR, int KB, bool kOnce,
+          typename XRow, typename WRow>
+__device__ __forceinline__ void stream_tile(Stream<BM, BN, WM, WN, NX, NR, KB, kOnce>, int H, int steps,
                                             const uint16_t *__restrict__ x, XRow xrow,
                                             const uint16_t *__restrict__ w, WRow wrow,
                                             uint8_t *lds, v4f *sum)
 {
-    using S = Stream<BM, BN, WM, WN, NX, NR, KB>;
+    using S = Stream<BM, BN, WM, WN, NX, NR, KB, kOnce>;
     constexpr int MF = S::MF, NF = S::NF, kHalf = S::kWaves / 2;
     const int lane = threadIdx.x & 63, wave = wave_of();
     const uint32_t l0 = lds_addr(lds);
@@ -359,7 +378,7 @@ __device__ __forceinline__ void stream_tile(Stream<BM, BN, WM, WN, NX, NR, KB>, 
     if (wave < kHalf)
         go(Ring<S::UX, NX, S::kX, KB, false>(x, H, steps, wave * S::UX, l0, xrow));
     else
-        go(Ring<S::UR, NR, S::kR, KB, true>(w, H, steps, (wave - kHalf) * S::UR,
+        go(Ring<S::UR, NR, S::kR, KB, kOnce>(w, H, steps, (wave - kHalf) * S::UR,
                                            l0 + NX * S::kX, wrow));
     wait_vmcnt<0>();
     __syncthreads();
@@ -469,11 +488,11 @@ shrink_few_kernel(AShape s, const uint16_t *__restrict__ x, const int32_t *__res
 // Shrink, many rows, ordered: workgroup (a block of up to BM places of one
 // adapter, BN of the rank).
 template <int DT, int BM, int BN, int WM, int NX, int NR>
-__global__ void __launch_bounds__((Stream<BM, BN, WM, 1, NX, NR, 256>::kThreads))
+__global__ void __launch_bounds__((Stream<BM, BN, WM, 1, NX, NR, 256, false>::kThreads))
 shrink_many_kernel(AShape s, const uint16_t *__restrict__ x, OrderOut o,
                    const uint16_t *__restrict__ a, float *__restrict__ v)
 {
-    using S = Stream<BM, BN, WM, 1, NX, NR, 256>;
+    using S = Stream<BM, BN, WM, 1, NX, NR, 256, false>;
     __shared__ __align__(1024) uint8_t lds[S::kLds];
     const int n = *o.blocks;
     if ((int)blockIdx.x >= n)
@@ -588,7 +607,7 @@ __device__ __forceinline__ void expand_part(const AShape &s, const uint16_t *__r
     uint32_t col[NF]; // element of B_l; N * rank is below 2^28
 #pragma unroll
     for (int f = 0; f < NF; ++f)
-        col[f] = (uint32_t)min(n0 + column_of<NF>(f, lane & 15), s.N - 1) * s.r;
+        col[f] = (uint32_t)min(n0 + column_of(f, lane & 15), s.N - 1) * s.r;
     uint32_t todo = rows;
     do {
         int g[GB], n = 0;
@@ -646,19 +665,20 @@ __device__ __forceinline__ void expand(const AShape &s, const float *__restrict_
                                   acc);
 }
 
-// The 4 NF neighbouring columns of one row that a lane holds, rounded and
-// stored, in pieces of 8 (N is a multiple of 8).
+// A lane's sums of 16 NF columns from n0 of row t, rounded and stored in
+// pieces of 8 (N is a multiple of 8).
 template <int DT, int NF>
-__device__ __forceinline__ void store_cols(const AShape &s, uint16_t *out, int t, int n,
+__device__ __forceinline__ void store_cols(const AShape &s, uint16_t *out, int t, int n0,
                                            const v4f *acc)
 {
+    const int n = n0 + 8 * ((threadIdx.x & 63) >> 4);
     uint16_t *o = out + (size_t)t * s.N + n;
 #pragma unroll
     for (int p = 0; p < NF / 2; ++p) {
         const v4f a = acc[2 * p], b = acc[2 * p + 1];
         const float f[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-        if (n + 8 * p < s.N)
-            *reinterpret_cast<uint4 *>(o + 8 * p) = Elem<DT>::pack(f);
+        if (n + 32 * p < s.N)
+            *reinterpret_cast<uint4 *>(o + 32 * p) = Elem<DT>::pack(f);
     }
 }
 
@@ -693,7 +713,7 @@ few_kernel(AShape s, int tn, int splits, const uint16_t *__restrict__ x,
         S{}, s.H, steps, x + 64 * first, [&](int r) { return min(r, s.T - 1); },
         w + (size_t)n0 * s.H + 64 * first,
         [&](int r) {
-            return min((r & ~63) + column_of<4>((r >> 4) & 3, r & 15), s.N - 1 - n0);
+            return min(column_of(r >> 4, r & 15), s.N - 1 - n0);
         },
         lds, sum);
     const int lane = threadIdx.x & 63;
@@ -703,7 +723,7 @@ few_kernel(AShape s, int tn, int splits, const uint16_t *__restrict__ x,
         if (t < min(s.T, BM))
 #pragma unroll
             for (int f = 0; f < NB; ++f) {
-                const int n = n0 + 64 * (f / 4) + 16 * (lane >> 4) + 4 * (f % 4);
+                const int n = n0 + column_of(f, 4 * (lane >> 4));
                 if (n < s.N)
                     *reinterpret_cast<v4f *>(parts + ((size_t)part * s.T + t) * s.N + n) =
                         sum[m * NB + f];
@@ -773,7 +793,7 @@ __device__ __forceinline__ void project_tile(const AShape &s, const ProjectArgs 
             base[u] = reinterpret_cast<const uint8_t *>(p.x);
         } else {
             const int rw = row - BM;
-            const int n = (rw & ~63) + column_of<4>((rw >> 4) & 3, rw & 15);
+            const int n = column_of(rw >> 4, rw & 15);
             const int nc = min(n, s.N - 1 - n0);
             voff[u] = (uint32_t)nc * (uint32_t)(2 * s.H) + at;
             base[u] = reinterpret_cast<const uint8_t *>(p.w + (size_t)n0 * s.H);
@@ -877,7 +897,7 @@ __device__ __forceinline__ void project_tile(const AShape &s, const ProjectArgs 
             __builtin_amdgcn_sched_barrier(0);
             expand<DT, 4>(s, p.v, p.b, p.scale, row[m], n, acc[m] + f);
             if (m0 + (wm * MF + m) * 16 + (lane & 15) < s.T)
-                store_cols<DT, 4>(s, p.out, row[m].t, n + 16 * (lane >> 4), acc[m] + f);
+                store_cols<DT, 4>(s, p.out, row[m].t, n, acc[m] + f);
         }
     }
 }
@@ -934,8 +954,17 @@ add_kernel(AShape s, int blocks, int parts, const void *base, const int32_t *__r
     const uint32_t rows = (uint32_t)__ballot(row.id >= 0) & 0xffffu;
     const Gain gain = gain_of<DT>(s, v, scale, row);
     const Low<KK> low = low_of<DT, KK>(s, v, row, gain, 0);
+    // a given base's pieces of the block at n0, loaded one block ahead
+    uint4 ahead[NF / 2];
+    const auto load_base = [&](int at) {
+        const uint16_t *p = static_cast<const uint16_t *>(base) + (size_t)row.t * s.N;
+#pragma unroll
+        for (int h = 0; h < NF / 2; ++h)
+            ahead[h] = piece(p + min(at + 32 * h + 8 * (lane >> 4), s.N - 8));
+    };
+    if constexpr (!kParts)
+        load_base(n0);
     for (int k = 0; k < blocks && n0 < s.N; ++k, n0 += 16 * NF) {
-        const int n = n0 + 4 * NF * (lane >> 4);
         v4f acc[NF];
         if constexpr (kParts) {
             const float *p = static_cast<const float *>(base) + (size_t)row.t * s.N;
@@ -950,7 +979,8 @@ add_kernel(AShape s, int blocks, int parts, const void *base, const int32_t *__r
 #pragma unroll
                     for (int f = 0; f < NF; ++f)
                         q[u][f] = *reinterpret_cast<const v4f *>(
-                            p + min(h + u, parts - 1) * plane + min(n + 4 * f, s.N - 4));
+                            p + min(h + u, parts - 1) * plane +
+                            min(n0 + column_of(f, 4 * (lane >> 4)), s.N - 4));
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
 #pragma unroll
@@ -958,17 +988,18 @@ add_kernel(AShape s, int blocks, int parts, const void *base, const int32_t *__r
                         acc[f] += h + u < parts ? q[u][f] : v4f{0.0f, 0.0f, 0.0f, 0.0f};
             }
         } else {
-            const uint16_t *p = static_cast<const uint16_t *>(base) + (size_t)row.t * s.N;
 #pragma unroll
             for (int h = 0; h < NF / 2; ++h) {
                 float f[8];
-                Elem<DT>::unpack(piece(p + min(n + 8 * h, s.N - 8)), f);
+                Elem<DT>::unpack(ahead[h], f);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     acc[2 * h][e] = f[e];
                     acc[2 * h + 1][e] = f[4 + e];
                 }
             }
+            // (past the wavefront's columns a repeat, dropped)
+            load_base(min(n0 + 16 * NF, s.N - 8));
         }
         if (rows) {
             expand_part<DT, NF, GB, KK>(s, b, row, rows, gain, low, n0, acc);
@@ -977,7 +1008,7 @@ add_kernel(AShape s, int blocks, int parts, const void *base, const int32_t *__r
                                             low_of<DT, KK>(s, v, row, gain, c), n0, acc);
         }
         if (i < s.T)
-            store_cols<DT, NF>(s, out, row.t, n, acc);
+            store_cols<DT, NF>(s, out, row.t, n0, acc);
     }
 }
 
@@ -1127,7 +1158,7 @@ hipError_t adapter_of_type(const moe_adapter_shape &sh, const void *x_, const vo
     if (e != hipSuccess)
         return e;
     if (!w)
-        return add(c4, c1, std::true_type{}, s.T > kFewProject ? 4 : 1, base, 0);
+        return add(c4, c1, std::true_type{}, s.T > kFewProject ? 2 : 1, base, 0);
     const ProjectArgs p{x, w, ids, order, b, scale, v, out};
     const int cus = device_cu_count();
     const int tm = up(s.T, 256), tn = up(s.N, 256), left = tm * tn % cus;

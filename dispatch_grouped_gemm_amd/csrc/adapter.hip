@@ -76,18 +76,25 @@ __device__ __forceinline__ void split8(const float *v, uint4 &hi, uint4 &lo)
     lo = Elem<DT>::pack(d);
 }
 
-// The row at place i (order: the rows sorted by adapter, or null), clamped
-// to the last place, and its adapter; -1 where there is none.
+// A row and its adapter (-1: none).
 struct Row {
     int t, id;
 };
-__device__ __forceinline__ Row row_at(const AShape &s, const int32_t *__restrict__ order,
+
+// What place i holds, clamped to the last place, there without its adapter;
+// order: the places' rows sorted by adapter, or null.
+__device__ __forceinline__ Row row_at(const AShape &s, const Row *__restrict__ order,
                                       const int32_t *__restrict__ ids, long i)
 {
     const long c = i < s.T ? i : s.T - 1;
-    const int t = order ? order[c] : (int)c;
-    const int id = ids[t];
-    return Row{t, i < s.T && (unsigned)id < (unsigned)s.L ? id : -1};
+    Row r;
+    if (order) {
+        r = order[c];
+    } else {
+        r = Row{(int)c, ids[c]};
+        r.id = (unsigned)r.id < (unsigned)s.L ? r.id : -1;
+    }
+    return Row{r.t, i < s.T ? r.id : -1};
 }
 
 // Column of the output that row i (0..15) of the block f of 16 weight rows
@@ -122,7 +129,7 @@ struct Block {
 };
 
 struct OrderOut {
-    int32_t *order;  // T
+    Row *order;      // T
     int32_t *blocks; // how many
     Block *block;    // T / rows + L at most
     int32_t *count;  // L + 1 of scratch, or null: in LDS
@@ -224,14 +231,14 @@ order_kernel(AShape s, int rows, const int32_t *__restrict__ ids, OrderOut o)
         for (int q = 0; q < kOrderBatch; ++q) {
             const int t = q * kOrderThreads + tid;
             if (t < s.T)
-                o.order[count[key[q]] + place[q]] = t;
+                o.order[count[key[q]] + place[q]] = Row{t, key[q] < s.L ? key[q] : -1};
         }
         return;
     }
     walk([&](int, int t, int k, bool in) {
         const int at = claim(k, in);
         if (in)
-            o.order[at] = t;
+            o.order[at] = Row{t, k < s.L ? k : -1};
     });
 }
 
@@ -503,11 +510,11 @@ shrink_many_kernel(AShape s, const uint16_t *__restrict__ x, OrderOut o,
     const int j0 = blockIdx.y * BN;
     v4f sum[BN / 16];
     stream_tile<DT>(
-        S{}, s.H, s.H / 128, x, [&](int i) { return o.order[b.first + min(i, b.rows - 1)]; },
+        S{}, s.H, s.H / 128, x, [&](int i) { return o.order[b.first + min(i, b.rows - 1)].t; },
         a + (size_t)b.id * s.r * s.H, [&](int i) { return min(j0 + i, s.r - 1); }, lds, sum);
     const int i = 16 * wave + (lane & 15);
     if (wave < BM / 16 && i < b.rows) {
-        float *vr = v + (size_t)o.order[b.first + i] * s.r;
+        float *vr = v + (size_t)o.order[b.first + i].t * s.r;
 #pragma unroll
         for (int f = 0; f < BN / 16; ++f) {
             const int j = j0 + 16 * f + 4 * (lane >> 4);
@@ -762,7 +769,8 @@ constexpr int kRowBytes = 128; // of a row's step
 
 struct ProjectArgs {
     const uint16_t *x, *w;
-    const int32_t *ids, *order;
+    const int32_t *ids;
+    const Row *order;
     const uint16_t *b;
     const float *scale, *v;
     uint16_t *out;
@@ -788,7 +796,7 @@ __device__ __forceinline__ void project_tile(const AShape &s, const ProjectArgs 
         const int at = ((lane & 7) ^ ((row >> 1) & 7)) * 16;
         if ((wave * U + u) * 8 < BM) {
             const long i = min(m0 + row, (long)s.T - 1);
-            const int t = p.order ? p.order[i] : (int)i;
+            const int t = p.order ? p.order[i].t : (int)i;
             voff[u] = (uint32_t)t * (uint32_t)(2 * s.H) + at;
             base[u] = reinterpret_cast<const uint8_t *>(p.x);
         } else {
@@ -944,7 +952,7 @@ constexpr int kAddWaves = 4;
 template <int DT, int NF, int GB, int KK, bool kParts>
 __global__ void __launch_bounds__(64 * kAddWaves)
 add_kernel(AShape s, int blocks, int parts, const void *base, const int32_t *__restrict__ ids,
-           const int32_t *__restrict__ order, const uint16_t *__restrict__ b,
+           const Row *__restrict__ order, const uint16_t *__restrict__ b,
            const float *__restrict__ scale, const float *__restrict__ v, uint16_t *out)
 {
     const int lane = threadIdx.x & 63, wave = wave_of();
@@ -952,8 +960,6 @@ add_kernel(AShape s, int blocks, int parts, const void *base, const int32_t *__r
     const long i = (long)blockIdx.x * 16 + (lane & 15);
     const Row row = row_at(s, order, ids, i);
     const uint32_t rows = (uint32_t)__ballot(row.id >= 0) & 0xffffu;
-    const Gain gain = gain_of<DT>(s, v, scale, row);
-    const Low<KK> low = low_of<DT, KK>(s, v, row, gain, 0);
     // a given base's pieces of the block at n0, loaded one block ahead
     uint4 ahead[NF / 2];
     const auto load_base = [&](int at) {
@@ -964,6 +970,8 @@ add_kernel(AShape s, int blocks, int parts, const void *base, const int32_t *__r
     };
     if constexpr (!kParts)
         load_base(n0);
+    const Gain gain = gain_of<DT>(s, v, scale, row);
+    const Low<KK> low = low_of<DT, KK>(s, v, row, gain, 0);
     for (int k = 0; k < blocks && n0 < s.N; ++k, n0 += 16 * NF) {
         v4f acc[NF];
         if constexpr (kParts) {
@@ -1047,7 +1055,7 @@ OrderLayout order_layout(const moe_adapter_shape &s, uint8_t *ws)
         l.bytes += (n + 255) / 256 * 256;
         return p;
     };
-    l.out.order = reinterpret_cast<int32_t *>(take(sizeof(int32_t) * s.T));
+    l.out.order = reinterpret_cast<Row *>(take(sizeof(Row) * s.T));
     l.out.blocks = reinterpret_cast<int32_t *>(take(sizeof(int32_t)));
     l.out.block = reinterpret_cast<Block *>(
         take(sizeof(Block) * ((s.T + 15u) / 16u + (size_t)std::min(s.T, s.L))));
@@ -1101,7 +1109,7 @@ hipError_t adapter_of_type(const moe_adapter_shape &sh, const void *x_, const vo
     const auto *a = static_cast<const uint16_t *>(a_), *b = static_cast<const uint16_t *>(b_);
     auto *out = static_cast<uint16_t *>(out_);
     const OrderLayout ol = order_layout(sh, ws);
-    const int32_t *order = ol.out.order;
+    const Row *order = ol.out.order;
     float *v = reinterpret_cast<float *>(ws + ol.bytes);
     const auto add = [&](auto nf, auto gb, auto given, int blocks, const void *from, int parts) {
         constexpr int NF = decltype(nf)::value, GB = decltype(gb)::value;

@@ -101,6 +101,13 @@ struct Elem<MOE_DT_F32> {
     }
 };
 
+// A 16-byte store that leaves the L2 first.
+__device__ __forceinline__ void store_once(void *p, const uint4 &q)
+{
+    typedef unsigned int u4v __attribute__((ext_vector_type(4)));
+    __builtin_nontemporal_store(u4v{q.x, q.y, q.z, q.w}, static_cast<u4v *>(p));
+}
+
 // A row index from a route table, or -1 where it names no row of the R rows
 // (a slot of -1; an index past the buffers is never followed).
 __device__ __forceinline__ int checked_row(int row, long R)

@@ -40,16 +40,14 @@ __device__ __forceinline__ Place place_of(int T, int pieces)
     }
 }
 
-typedef unsigned int u4v __attribute__((ext_vector_type(4)));
-
-// A store that leaves the L2 first: what these kernels write is large and
-// next read by another kernel, which would else find its own reads behind
-// the lines still to be written (permute and its gradient, one after the
-// other at 8,192 tokens of 7,168 bf16 values and 6 experts each: 312 us, with
-// ordinary stores 362; unpermute and its gradients 465, and 485).
-__device__ __forceinline__ void store_once(void *base, size_t piece, const uint4 &q)
+// The stores leave the L2 first: what these kernels write is large and read
+// by another kernel, which would else find its own reads behind the lines
+// still to be written (permute and its gradient, one after the other at 8,192
+// tokens of 7,168 bf16 values and 6 experts each: 312 us, with ordinary
+// stores 362; unpermute and its gradients 465, and 485).
+__device__ __forceinline__ void store_piece(void *base, size_t piece, const uint4 &q)
 {
-    __builtin_nontemporal_store(u4v{q.x, q.y, q.z, q.w}, static_cast<u4v *>(base) + piece);
+    store_once(static_cast<uint4 *>(base) + piece, q);
 }
 
 // A thread stores its pieces of a token's row K times.
@@ -72,7 +70,7 @@ permute_kernel(int T, int H, int K, long R, const void *__restrict__ x,
         if (row >= 0)
 #pragma unroll
             for (int j = 0; j < P; ++j)
-                store_once(rows, (size_t)row * pieces + at.p + 64 * j, v[j]);
+                store_piece(rows, (size_t)row * pieces + at.p + 64 * j, v[j]);
     }
 }
 
@@ -128,7 +126,7 @@ unpermute_kernel(int T, int H, int K, long R, const void *__restrict__ rows,
     }
 #pragma unroll
     for (int j = 0; j < P; ++j)
-        store_once(out, (size_t)at.t * pieces + at.p + 64 * j, Elem<DT>::pack(acc[j]));
+        store_piece(out, (size_t)at.t * pieces + at.p + 64 * j, Elem<DT>::pack(acc[j]));
 }
 
 // A workgroup takes one token: its dout row read once, its expert rows read
@@ -173,7 +171,7 @@ unpermute_backward_kernel(int T, int H, int K, long R, const void *__restrict__ 
 #pragma unroll
                     for (int j = 0; j < V; ++j)
                         d[j] = kWeights ? wk[k] * g[j] : g[j];
-                    store_once(drows, at, Elem<DT>::pack(d));
+                    store_piece(drows, at, Elem<DT>::pack(d));
                 }
             }
         }

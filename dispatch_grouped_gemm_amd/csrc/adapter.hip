@@ -604,27 +604,39 @@ __device__ __forceinline__ Low<KK> low_of(const AShape &s, const float *__restri
     return low;
 }
 
-// Adds 32 KK of the rank; rows: which of the 16 rows have an adapter (not 0).
-template <int DT, int NF, int GB, int KK>
+// Adds 32 KK of the rank to M blocks of 16 rows; rows[m]: which rows of block
+// m have an adapter.  An adapter's B is loaded once for all the blocks.
+template <int DT, int M, int NF, int GB, int KK>
 __device__ __forceinline__ void expand_part(const AShape &s, const uint16_t *__restrict__ b,
-                                            const Row &row, uint32_t rows, const Gain &gain,
-                                            const Low<KK> &low, int n0, v4f *acc)
+                                            const Row *row, const uint32_t *rows,
+                                            const Gain *gain, const Low<KK> *low, int n0,
+                                            v4f (*acc)[NF])
 {
     const int lane = threadIdx.x & 63;
     uint32_t col[NF]; // element of B_l; N * rank is below 2^28
 #pragma unroll
     for (int f = 0; f < NF; ++f)
         col[f] = (uint32_t)min(n0 + column_of(f, lane & 15), s.N - 1) * s.r;
-    uint32_t todo = rows;
-    do {
+    uint32_t todo[M], any = 0;
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+        any |= todo[m] = rows[m];
+    while (any) {
         int g[GB], n = 0;
         uint4 bq[GB][KK][NF];
 #pragma unroll
         for (int q = 0; q < GB; ++q) {
-            const int next = __builtin_amdgcn_readlane(row.id, todo ? __builtin_ctz(todo) : 0);
-            g[q] = q == 0 || todo ? next : g[0];
-            n += todo ? 1 : 0;
-            todo &= ~(uint32_t)__ballot(row.id == g[q]);
+            int next = -1;
+#pragma unroll
+            for (int m = M - 1; m >= 0; --m)
+                if (todo[m])
+                    next = __builtin_amdgcn_readlane(row[m].id, __builtin_ctz(todo[m]));
+            n += next >= 0 ? 1 : 0;
+            g[q] = next >= 0 ? next : g[0];
+            any = 0;
+#pragma unroll
+            for (int m = 0; m < M; ++m)
+                any |= todo[m] &= ~(uint32_t)__ballot(row[m].id == g[q]);
         }
 #pragma unroll
         for (int q = 0; q < GB; ++q) {
@@ -633,43 +645,60 @@ __device__ __forceinline__ void expand_part(const AShape &s, const uint16_t *__r
             for (int k = 0; k < KK; ++k)
 #pragma unroll
                 for (int f = 0; f < NF; ++f)
-                    bq[q][k][f] = piece(bg + col[f] + low.at[k]);
+                    bq[q][k][f] = piece(bg + col[f] + low[0].at[k]);
         }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int q = 0; q < GB; ++q) {
-            const bool take = row.id == g[q] && q < n;
+        for (int q = 0; q < GB; ++q)
 #pragma unroll
-            for (int f = 0; f < NF; ++f) {
-                v4f d = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int m = 0; m < M; ++m) {
+                const bool take = row[m].id == g[q] && q < n;
+                if (M > 1 && !__any(take))
+                    continue;
 #pragma unroll
-                for (int k = 0; k < KK; ++k) {
-                    const uint4 bk = low.there[k] ? bq[q][k][f] : uint4{0, 0, 0, 0};
-                    d = mfma<DT>(bk, low.hi[k], d);
-                    d = mfma<DT>(bk, low.lo[k], d);
+                for (int f = 0; f < NF; ++f) {
+                    v4f d = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int k = 0; k < KK; ++k) {
+                        const uint4 bk = low[0].there[k] ? bq[q][k][f] : uint4{0, 0, 0, 0};
+                        d = mfma<DT>(bk, low[m].hi[k], d);
+                        d = mfma<DT>(bk, low[m].lo[k], d);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        acc[m][f][i] += !take ? 0.0f
+                                              : gain[m].sc * (DT == MOE_DT_F16
+                                                                  ? ldexpf(d[i], gain[m].ex)
+                                                                  : d[i]);
                 }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    acc[f][i] +=
-                        !take ? 0.0f : gain.sc * (DT == MOE_DT_F16 ? ldexpf(d[i], gain.ex) : d[i]);
             }
-        }
-    } while (todo);
+    }
 }
 
-template <int DT, int NF>
+// The whole term for M blocks of 16 rows.
+template <int DT, int M, int NF, int GB>
 __device__ __forceinline__ void expand(const AShape &s, const float *__restrict__ v,
                                        const uint16_t *__restrict__ b,
-                                       const float *__restrict__ scale, const Row &row, int n0,
-                                       v4f *acc)
+                                       const float *__restrict__ scale, const Row *row, int n0,
+                                       v4f (*acc)[NF])
 {
-    const uint32_t rows = (uint32_t)__ballot(row.id >= 0) & 0xffffu;
-    if (!rows)
+    uint32_t rows[M], any = 0;
+    Gain gain[M];
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+        any |= rows[m] = (uint32_t)__ballot(row[m].id >= 0) & 0xffffu;
+    if (!any)
         return;
-    const Gain gain = gain_of<DT>(s, v, scale, row);
-    for (int c = 0; c < s.r; c += 64)
-        expand_part<DT, NF, 1, 2>(s, b, row, rows, gain, low_of<DT, 2>(s, v, row, gain, c), n0,
-                                  acc);
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+        gain[m] = gain_of<DT>(s, v, scale, row[m]);
+    for (int c = 0; c < s.r; c += 64) {
+        Low<2> low[M];
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+            low[m] = low_of<DT, 2>(s, v, row[m], gain[m], c);
+        expand_part<DT, M, NF, GB, 2>(s, b, row, rows, gain, low, n0, acc);
+    }
 }
 
 // A lane's sums of 16 NF columns from n0 of row t, rounded and stored in
@@ -897,8 +926,6 @@ __device__ __forceinline__ void project_tile(const AShape &s, const ProjectArgs 
     }
     wait_all();
 
-    // 16 rows x 64 columns at a time, in order (their loads would not fit in
-    // registers beside the sums all at once)
     Row row[MF];
 #pragma unroll
     for (int m = 0; m < MF; ++m)
@@ -918,16 +945,16 @@ __device__ __forceinline__ void project_tile(const AShape &s, const ProjectArgs 
         }
         return;
     }
+    static_assert(NF == 4 && MF % 4 == 0, "four blocks of rows at a time");
 #pragma unroll
-    for (int m = 0; m < MF; ++m) {
+    for (int m = 0; m < MF; m += 4) {
+        const int n = n0 + wn * NF * 16;
+        __builtin_amdgcn_sched_barrier(0);
+        expand<DT, 4, NF, MF == 4 ? 2 : 1>(s, p.v, p.b, p.scale, row + m, n, acc + m);
 #pragma unroll
-        for (int f = 0; f < NF; f += 4) {
-            const int n = n0 + (wn * NF + f) * 16;
-            __builtin_amdgcn_sched_barrier(0);
-            expand<DT, 4>(s, p.v, p.b, p.scale, row[m], n, acc[m] + f);
-            if (m0 + (wm * MF + m) * 16 + (lane & 15) < s.T)
-                store_cols<DT, 4>(s, p.out, row[m].t, n, acc[m] + f);
-        }
+        for (int q = m; q < m + 4; ++q)
+            if (m0 + (wm * MF + q) * 16 + (lane & 15) < s.T)
+                store_cols<DT, NF>(s, p.out, row[q].t, n, acc[q]);
     }
 }
 
@@ -1037,10 +1064,11 @@ add_kernel(AShape s, int blocks, int parts, const void *base, const int32_t *__r
             load_base(min(n0 + 16 * NF, s.N - 8));
         }
         if (rows) {
-            expand_part<DT, NF, GB, KK>(s, b, row, rows, gain, low, n0, acc);
-            for (int c = 32 * KK; c < s.r; c += 32 * KK)
-                expand_part<DT, NF, GB, KK>(s, b, row, rows, gain,
-                                            low_of<DT, KK>(s, v, row, gain, c), n0, acc);
+            expand_part<DT, 1, NF, GB, KK>(s, b, &row, &rows, &gain, &low, n0, &acc);
+            for (int c = 32 * KK; c < s.r; c += 32 * KK) {
+                const Low<KK> more = low_of<DT, KK>(s, v, row, gain, c);
+                expand_part<DT, 1, NF, GB, KK>(s, b, &row, &rows, &gain, &more, n0, &acc);
+            }
         }
         if (i < s.T)
             store_cols<DT, NF>(s, out, row.t, n0, acc);

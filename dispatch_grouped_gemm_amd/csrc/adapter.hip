@@ -794,8 +794,12 @@ __device__ __forceinline__ void tile_of(int q, int tm, int tn, int *im, int *in)
     *in = in_group / rows;
 }
 
-// s_waitcnt vmcnt(0) lgkmcnt(0).
-__device__ __forceinline__ void wait_all() { __builtin_amdgcn_s_waitcnt(0x7 << 4); }
+// s_waitcnt vmcnt(N) lgkmcnt(0).
+template <int N>
+__device__ __forceinline__ void wait_but()
+{
+    __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4));
+}
 
 constexpr int kRowBytes = 128; // of a row's step
 
@@ -812,7 +816,7 @@ struct ProjectArgs {
 // The rows of places m0 .. m0 + BM - 1 by the columns n0 .. n0 + BN - 1: out,
 // or (kParts) the float32 sums over `steps` steps (even) from `first` on, as
 // plane `part` of p.parts.
-template <int DT, int BM, int BN, int WM, int WN, bool kParts = false>
+template <int DT, int BM, int BN, int WM, int WN, int NS = 2, bool kParts = false>
 __device__ __forceinline__ void project_tile(const AShape &s, const ProjectArgs &p, long m0,
                                              int n0, uint8_t *lds, int first, int steps,
                                              int part = 0)
@@ -873,15 +877,15 @@ __device__ __forceinline__ void project_tile(const AShape &s, const ProjectArgs 
         wo[k][f] = *reinterpret_cast<const uint4 *>(wl + buf * kStage + f * 16 * kRowBytes +
                                                     (off ^ (64 * k)));
     };
-    // step k in stage buf: the other stage holds step k + 1 before the last
-    // phase, which also sends off the loads of step k + 2 into this stage
-    const auto step_of = [&](int k, int buf, int last) {
+    // step k in stage buf: the next stage holds step k + 1 before the last
+    // phase, which also sends off the loads of step k + NS into this stage
+    const auto step_of = [&](int k, int buf, int next, int last) {
 #pragma unroll
         for (int ph = 0; ph < P; ++ph) {
             const bool end = ph + 1 == P;
-            const int np = end ? 0 : ph + 1, nbuf = end ? buf ^ 1 : buf;
+            const int np = end ? 0 : ph + 1, nbuf = end ? next : buf;
             if (end) {
-                wait_all();
+                wait_but<(NS - 2) * U>();
                 raw_barrier();
             }
 #pragma unroll
@@ -894,7 +898,7 @@ __device__ __forceinline__ void project_tile(const AShape &s, const ProjectArgs 
                 if (end)
 #pragma unroll
                     for (int u = q * U / 4; u < (q + 1) * U / 4; ++u)
-                        load(u, min(k + 2, last), buf);
+                        load(u, min(k + NS, last), buf);
 #pragma unroll
                 for (int f = 0; f < NF; ++f) {
                     v4f &a = acc[(ph % G) * 4 + q][f];
@@ -905,13 +909,13 @@ __device__ __forceinline__ void project_tile(const AShape &s, const ProjectArgs 
         }
     };
     static_assert(P % 2 == 0, "the next step starts with x's set 0");
+    // (loads past the last step repeat it, unused)
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-        load(u, 0, 0);
+    for (int k = 0; k < NS; ++k)
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-        load(u, 1, 1);
-    wait_vmcnt<U>();
+        for (int u = 0; u < U; ++u)
+            load(u, min(k, steps - 1), k);
+    wait_vmcnt<(NS - 1) * U>();
     raw_barrier();
 #pragma unroll
     for (int q = 0; q < 4; ++q)
@@ -919,12 +923,20 @@ __device__ __forceinline__ void project_tile(const AShape &s, const ProjectArgs 
 #pragma unroll
     for (int f = 0; f < NF; ++f)
         read_w(f, 0, 0);
-    // (the loads past the last step repeat it, unused)
-    for (int k = 0; k < steps; k += 2) {
-        step_of(k, 0, steps - 1);
-        step_of(k + 1, 1, steps - 1);
+    if constexpr (NS == 2) {
+        for (int k = 0; k < steps; k += 2) {
+            step_of(k, 0, 1, steps - 1);
+            step_of(k + 1, 1, 0, steps - 1);
+        }
+    } else {
+        int buf = 0;
+        for (int k = 0; k < steps; ++k) {
+            const int next = buf + 1 == NS ? 0 : buf + 1;
+            step_of(k, buf, next, steps - 1);
+            buf = next;
+        }
     }
-    wait_all();
+    wait_but<0>();
 
     Row row[MF];
 #pragma unroll
@@ -979,20 +991,21 @@ project_large_kernel(AShape s, int tm, int tn, int whole, ProjectArgs p)
         project_tile<DT, 128, 256, 2, 4>(s, p, m0, in * 256, lds, 0, s.H / 64);
 }
 
-// Tiles of 128 x 128, two workgroups a CU; splits > 1 (kParts) parts of H for
-// shapes with too few tiles, joined by the add launch.
-template <int DT, bool kParts>
+// Tiles of 128 x 128: with NS = 2 stages two workgroups a CU, with 4 one,
+// three steps ahead of memory, where there are no more tiles than CUs;
+// kParts: `splits` parts of H for fewer still, joined by the add launch.
+template <int DT, int NS, bool kParts>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2)))
 project_small_kernel(AShape s, int tm, int tn, int splits, ProjectArgs p)
 {
-    __shared__ __align__(1024) uint8_t lds[2 * 256 * kRowBytes];
+    __shared__ __align__(1024) uint8_t lds[NS * 256 * kRowBytes];
     const int q = xcd_run(blockIdx.x, tm * tn * splits);
     const int part = q / (tm * tn), pairs = s.H / 128; // steps go in pairs
     const int a = (long)pairs * part / splits, b = (long)pairs * (part + 1) / splits;
     int im, in;
     tile_of(q - part * tm * tn, tm, tn, &im, &in);
-    project_tile<DT, 128, 128, 2, 2, kParts>(s, p, (long)im * 128, in * 128, lds, 2 * a,
-                                             2 * (b - a), part);
+    project_tile<DT, 128, 128, 2, 2, NS, kParts>(s, p, (long)im * 128, in * 128, lds, 2 * a,
+                                                 2 * (b - a), part);
 }
 
 // ---------------------------------------------------------------------------
@@ -1088,14 +1101,21 @@ int few_splits(const moe_adapter_shape &s)
     return std::max(1, std::min({256 / tn, 8, s.H / 128}));
 }
 
-// Parts of H of project_small_kernel: two workgroups a CU, where the tiles
-// are fewer than two thirds of the CUs; parts of at least four steps.
+// Tiles of 128 x 128, and the parts of H that project_small_kernel makes of
+// few of them: two workgroups a CU, parts of at least four steps.  At 384 x
+// 7,168 x 7,168 (168 tiles) three parts take 86 us, one deep workgroup a CU 103;
+// at 512 rows (224 tiles) two parts' planes cost more than they give, and the
+// deep form takes 103, the two-stage form 129.
+long small_tiles(const moe_adapter_shape &s)
+{
+    return (long)((s.T + 127) / 128) * ((s.N + 127) / 128);
+}
+
 int small_splits(const moe_adapter_shape &s)
 {
-    const long tiles = (long)((s.T + 127) / 128) * ((s.N + 127) / 128);
-    if (tiles > 170)
+    if (small_tiles(s) > 170)
         return 1;
-    return (int)std::max(1l, std::min({512 / tiles, 8l, (long)s.H / 256}));
+    return (int)std::max(1l, std::min({512 / small_tiles(s), 8l, (long)s.H / 256}));
 }
 
 size_t parts_bytes(const moe_adapter_shape &s)
@@ -1239,7 +1259,7 @@ hipError_t adapter_of_type(const moe_adapter_shape &sh, const void *x_, const vo
     const int tm = up(s.T, 256), tn = up(s.N, 256), left = tm * tn % cus;
     const int sm = up(s.T, 128), sn = up(s.N, 128), splits = small_splits(sh);
     if (splits > 1) {
-        project_small_kernel<DT, true>
+        project_small_kernel<DT, 2, true>
             <<<sm * sn * splits, 256, 0, st>>>(s, sm, sn, splits, p);
         if ((e = hipGetLastError()) != hipSuccess)
             return e;
@@ -1249,8 +1269,10 @@ hipError_t adapter_of_type(const moe_adapter_shape &sh, const void *x_, const vo
         const int halves = 2 * left <= cus ? left : 0;
         project_large_kernel<DT>
             <<<tm * tn + halves, 512, 0, st>>>(s, tm, tn, tm * tn - halves, p);
+    } else if (sm * sn > cus) {
+        project_small_kernel<DT, 2, false><<<sm * sn, 256, 0, st>>>(s, sm, sn, 1, p);
     } else {
-        project_small_kernel<DT, false><<<sm * sn, 256, 0, st>>>(s, sm, sn, 1, p);
+        project_small_kernel<DT, 4, false><<<sm * sn, 256, 0, st>>>(s, sm, sn, 1, p);
     }
     return hipGetLastError();
 }

@@ -59,7 +59,11 @@ SIZES = [
     (511, 768, 768, 6, 64),
     (700, 256, 2304, 3, 16),
     (1025, 384, 392, 12, 48),
-    (300, 128, 64, 9000, 8),                       # more adapters than the order counts
+    (130, 2048, 200, 6, 16),                       # parts of H by tiles
+    (700, 1536, 3000, 20, 40),                     # no more tiles than CUs
+    (1300, 256, 4100 - 4, 7, 8),                   # more
+    (9000, 128, 40, 70, 8),                        # more rows than a batch of the order
+    (300, 128, 64, 9000, 8),                       # more adapters than the order counts in LDS
     (4111, 128, 4104, 9, 16),                      # the largest tiles
 ]
 

@@ -58,6 +58,13 @@ __device__ __forceinline__ int wave_of()
     return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 }
 
+// s_waitcnt vmcnt(N) lgkmcnt(0).
+template <int N>
+__device__ __forceinline__ void wait_but()
+{
+    __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4));
+}
+
 __device__ __forceinline__ const uint4 &piece(const uint16_t *p)
 {
     return *reinterpret_cast<const uint4 *>(p);
@@ -327,8 +334,9 @@ struct Ring {
         for (int k = 0; k < N - 1; ++k)
             load();
     }
-    // this wavefront's part of the oldest step has landed
-    __device__ __forceinline__ void wait() { wait_vmcnt<(N - 2) * U>(); }
+    // this wavefront's part of the oldest step has landed, and what it read
+    // of the step before is in registers
+    __device__ __forceinline__ void wait() { wait_but<(N - 2) * U>(); }
 };
 
 // `steps` steps from x and w on.  Rows [0, BM) come from x, columns [0, BN)
@@ -501,26 +509,27 @@ shrink_many_kernel(AShape s, const uint16_t *__restrict__ x, OrderOut o,
 {
     using S = Stream<BM, BN, WM, 1, NX, NR, 256, false>;
     __shared__ __align__(1024) uint8_t lds[S::kLds];
-    const int n = *o.blocks;
-    if ((int)blockIdx.x >= n)
-        return;
-    // an XCD's blocks lie together: few adapters' A in its L2
-    const Block b = o.block[xcd_run(blockIdx.x, n)];
-    const int lane = threadIdx.x & 63, wave = wave_of();
+    const int n = *o.blocks, lane = threadIdx.x & 63, wave = wave_of();
     const int j0 = blockIdx.y * BN;
-    v4f sum[BN / 16];
-    stream_tile<DT>(
-        S{}, s.H, s.H / 128, x, [&](int i) { return o.order[b.first + min(i, b.rows - 1)].t; },
-        a + (size_t)b.id * s.r * s.H, [&](int i) { return min(j0 + i, s.r - 1); }, lds, sum);
-    const int i = 16 * wave + (lane & 15);
-    if (wave < BM / 16 && i < b.rows) {
-        float *vr = v + (size_t)o.order[b.first + i].t * s.r;
+    for (int q = blockIdx.x; q < n; q += gridDim.x) {
+        // an XCD's blocks lie together: few adapters' A in its L2
+        const Block b = o.block[n <= (int)gridDim.x ? xcd_run(q, n) : q];
+        v4f sum[BN / 16];
+        stream_tile<DT>(
+            S{}, s.H, s.H / 128, x,
+            [&](int i) { return o.order[b.first + min(i, b.rows - 1)].t; },
+            a + (size_t)b.id * s.r * s.H, [&](int i) { return min(j0 + i, s.r - 1); }, lds, sum);
+        const int i = 16 * wave + (lane & 15);
+        if (wave < BM / 16 && i < b.rows) {
+            float *vr = v + (size_t)o.order[b.first + i].t * s.r;
 #pragma unroll
-        for (int f = 0; f < BN / 16; ++f) {
-            const int j = j0 + 16 * f + 4 * (lane >> 4);
-            if (j < s.r)
-                *reinterpret_cast<v4f *>(vr + j) = sum[f];
+            for (int f = 0; f < BN / 16; ++f) {
+                const int j = j0 + 16 * f + 4 * (lane >> 4);
+                if (j < s.r)
+                    *reinterpret_cast<v4f *>(vr + j) = sum[f];
+            }
         }
+        __syncthreads();
     }
 }
 
@@ -792,13 +801,6 @@ __device__ __forceinline__ void tile_of(int q, int tm, int tn, int *im, int *in)
     const int rows = min(8, tm - first), in_group = q - group * 8 * tn;
     *im = first + in_group % rows;
     *in = in_group / rows;
-}
-
-// s_waitcnt vmcnt(N) lgkmcnt(0).
-template <int N>
-__device__ __forceinline__ void wait_but()
-{
-    __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4));
 }
 
 constexpr int kRowBytes = 128; // of a row's step
@@ -1166,7 +1168,11 @@ hipError_t shrink_many(const AShape &s, const uint16_t *x, const int32_t *ids, c
     // as much of the rank per workgroup as there is (x is read once per
     // block of the rank), but a workgroup for every CU; x comes from memory
     // and gets the deeper ring
-    const int cus = device_cu_count(), t = up(s.T, 32), more = std::min(s.T, s.L);
+    const int cus = device_cu_count(), t = up(s.T, 32);
+    // blocks there may be (a workgroup takes several past 2^20)
+    const auto blocks = [&](int rows) {
+        return (int)std::min(up(s.T, rows) + (long)std::min(s.T, s.L), 1l << 20);
+    };
     const bool wide = s.r > 16 && t * up(s.r, 32) >= cus;
     order_kernel<<<1, kOrderThreads, o.count ? 0 : (s.L + 1) * sizeof(int), st>>>(
         s, wide ? 32 : 16, ids, o);
@@ -1175,13 +1181,13 @@ hipError_t shrink_many(const AShape &s, const uint16_t *x, const int32_t *ids, c
         return e;
     if (wide && s.r > 32 && t * up(s.r, 64) >= cus)
         shrink_many_kernel<DT, 32, 64, 2, 8, 6>
-            <<<dim3(t + more, up(s.r, 64)), 512, 0, st>>>(s, x, o, a, v);
+            <<<dim3(blocks(32), up(s.r, 64)), 512, 0, st>>>(s, x, o, a, v);
     else if (wide)
         shrink_many_kernel<DT, 32, 32, 2, 10, 8>
-            <<<dim3(t + more, up(s.r, 32)), 512, 0, st>>>(s, x, o, a, v);
+            <<<dim3(blocks(32), up(s.r, 32)), 512, 0, st>>>(s, x, o, a, v);
     else
         shrink_many_kernel<DT, 16, 16, 1, 10, 10>
-            <<<dim3(up(s.T, 16) + more, up(s.r, 16)), 256, 0, st>>>(s, x, o, a, v);
+            <<<dim3(blocks(16), up(s.r, 16)), 256, 0, st>>>(s, x, o, a, v);
     return hipGetLastError();
 }
 

@@ -724,7 +724,8 @@ int moe_adapter_check(const moe_adapter_shape *s)
     if (!s || s->T < 0 || s->H <= 0 || s->N <= 0 || s->L < 1 || s->rank < 1)
         return MOE_EINVAL;
     if (s->H % 128 != 0 || s->H > (1 << 17) || s->N % 8 != 0 || s->N > (1 << 20) ||
-        s->rank % 8 != 0 || s->rank > 256 || (long long)s->T * s->H >= (1ll << 31) ||
+        s->L > (1 << 24) || s->rank % 8 != 0 || s->rank > 256 ||
+        (long long)s->T * s->H >= (1ll << 31) ||
         (long long)s->T * s->N >= (1ll << 32))
         return MOE_ENOTSUP;
     return MOE_OK;

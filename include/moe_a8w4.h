@@ -551,7 +551,7 @@ typedef struct moe_adapter_shape {
     int32_t T;    /* rows (0 is a valid no-op); T*H below 2^31, T*N below 2^32 */
     int32_t H;    /* input size, a multiple of 128, at most 2^17 */
     int32_t N;    /* output size, a multiple of 8, at most 2^20 */
-    int32_t L;    /* adapters, at least 1 */
+    int32_t L;    /* adapters, 1 to 2^24 */
     int32_t rank; /* a multiple of 8, at most 256 */
 } moe_adapter_shape;
 

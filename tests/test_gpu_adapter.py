@@ -63,6 +63,7 @@ SIZES = [
     (700, 1536, 3000, 20, 40),                     # no more tiles than CUs
     (1300, 256, 4100 - 4, 7, 8),                   # more
     (9000, 128, 40, 70, 8),                        # more rows than a batch of the order
+    (9000, 128, 16, 9000, 8),                      # both
     (300, 128, 64, 9000, 8),                       # more adapters than the order counts in LDS
     (4111, 128, 4104, 9, 16),                      # the largest tiles
 ]
@@ -82,6 +83,8 @@ def test_whole_numbers(size, dt):
     scale = (2.0 ** torch.randint(-1, 3, (L,), generator=g)).to(DEV)
     base = whole(g, (T, N), -50, 50, dt)
     for kind in ("mixed", "requests", "none", "one", "outside"):
+        if T * L > 1 << 24 and kind != "mixed":
+            continue                               # the reference walks the adapters
         ids = ids_of(kind, T, L, g).to(DEV)
         for ww, bb, sc in ((w, None, scale), (None, base, None)):
             say("adapter", size, dt, kind, ww is not None)

@@ -82,6 +82,7 @@ def test_adapter_shapes(lib):
     bad = [({"T": -1}, -1), ({"H": 0}, -1), ({"N": 0}, -1), ({"L": 0}, -1), ({"rank": 0}, -1),
            ({"H": 192}, -2), ({"H": (1 << 17) + 128}, -2), ({"N": 12}, -2),
            ({"N": (1 << 20) + 8}, -2), ({"rank": 12}, -2), ({"rank": 264}, -2),
+           ({"L": (1 << 24) + 1}, -2),
            ({"T": 1 << 23, "H": 512}, -2), ({"T": 1 << 23, "H": 128, "N": 512}, -2)]
     for kw, code in bad:
         s = moe.AdapterShape(**{**AD, **kw})

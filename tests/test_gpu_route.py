@@ -155,3 +155,58 @@ def test_many_tokens_and_a_captured_graph():
             assert torch.equal(u, v)
     pick = torch.arange(0, T, 1777)
     check_forward(logits[pick.to(DEV)], K, False, ids[pick.to(DEV)], w[pick.to(DEV)])
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("dt", [BF, HF, F32])
+def test_logits_off_16_byte_borders(dt, renorm):
+    """Logits and gradients that start one element into a buffer, and what lies around."""
+    T, E, K = 50, 384, 6
+    say("route off borders", dt, renorm)
+    logits = torch.empty(T * E + 1, dtype=dt, device=DEV)[1:].view(T, E)
+    logits.copy_(draw(T, E, dt, seed=3))
+    assert logits.data_ptr() % 16 and logits.is_contiguous()
+    s, ids, w = run(logits, K, renorm)
+    p, reach = check_forward(logits, K, renorm, ids, w)
+    g = torch.randn(T, K, generator=torch.Generator().manual_seed(6)).to(DEV)
+    g = torch.where(ids < 0, float("nan"), g)
+    room = torch.full((T * E + 2,), 7.0, dtype=dt, device=DEV)
+    dl = room[1:-1].view(T, E)
+    moe.moe_route_backward(s, logits, ids, w, g, dl, renormalize=renorm)
+    d, mag = ref.route_backward(ids, w, p, g, E, renorm)
+    ref.assert_close(dl, d, mag * (ref.U32 * (2 * reach + 60))[:, None] + 2.0 ** -149, "dlogits")
+    assert float(room[0]) == 7.0 and float(room[-1]) == 7.0
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+def test_every_16_bit_pattern(dt):
+    """Every value of the type, both zeros and every NaN, in shuffled rows."""
+    say("route patterns", dt)
+    bits = np.random.default_rng(11).permutation(1 << 16).astype(np.uint16).view(np.int16)
+    logits = torch.from_numpy(bits).view(dt).view(2048, 32).to(DEV)
+    logits[0] = float("nan")
+    logits[1] = -float("nan")
+    logits[2, ::2], logits[2, 1::2] = 0.0, -0.0
+    for renorm in (True, False):
+        s, ids, w = run(logits, 8, renorm)
+        rid = ref.route(logits, 8, renorm)[0]
+        np.testing.assert_array_equal(ids.cpu().numpy(), rid)
+
+
+@pytest.mark.parametrize("dt", [BF, HF, F32])
+@pytest.mark.parametrize("E", [128, 384, 1024])
+def test_the_largest_side_by_side(E, dt):
+    """All the chosen in neighbouring experts or 16 apart, falling, rising and equal."""
+    say("route side by side", E, dt)
+    T, K = 48, 8
+    l = torch.randn(T, E, generator=torch.Generator().manual_seed(E)) * 0.25
+    for t in range(T):
+        step = (1, 16, 8 * 16)[t % 3]
+        at = [(t + step * i) % E for i in range(10)]
+        l[t, at] = torch.tensor([[4.0 - 0.25 * i for i in range(10)],
+                                 [4.0 + 0.25 * i for i in range(10)],
+                                 [4.0] * 10][t // 3 % 3])
+    logits = l.to(dt).to(DEV)
+    for renorm in (True, False):
+        s, ids, w = run(logits, K, renorm)
+        check_forward(logits, K, renorm, ids, w)

@@ -11,8 +11,8 @@
 // ids among them: an adapter's product is formed for 16 rows at a time (the
 // matrix instruction costs the same for one) and taken only where the id
 // matches, so no row ever sees another adapter's values, infinite or NaN.
-// Past kFewRows rows a first launch orders the rows by adapter, so that a
-// tile holds few of them; results do not depend on the places inside one.
+// Past few rows a first launch orders the rows by adapter, so that a tile
+// holds few of them; results do not depend on the places inside one.
 //
 // v keeps float32's precision through the matrix instruction: it enters as
 // the sum of two 16-bit values, hi = round(v) and lo = round(v - hi).  fp16
@@ -33,7 +33,12 @@ struct AShape {
     int T, H, N, L, r;
 };
 
-constexpr int kFewRows = 256;       // rows shrunk without an order
+constexpr int kFewRows = 128;       // rows that few_kernel and shrink_few take, in any order
+// Rows of a given projection from which the order pays for its launch: 16
+// adapters of rank 64 at H = N = 7,168 take 25 us without it and 20 with it at
+// 64 rows, 28 and 20 at 128, 22 and 24 at 33; of rank 16 at 2,048, 12 and 14 at
+// 64 and 128.
+constexpr int kUnordered = 64;
 constexpr int kOrderKeys = 1 << 13; // adapters that the order counts in LDS
 
 // D(16x16) += A(16x32) B(32x16): lane l holds A's row / B's column l mod 16
@@ -1090,17 +1095,29 @@ add_kernel(AShape s, int blocks, int parts, const void *base, const int32_t *__r
     }
 }
 
-constexpr int kFewProject = 128; // rows projected by few_kernel
+// Workgroups of few_kernel for the parts of x W^T, one a CU: an eighth of the
+// CUs stays free for the shrink, which else starts when the first part ends
+// (one row at 4,096 x 4,096 with an adapter of rank 64: 15 us, with 256 31;
+// 65 rows, rank 16: 21 and 28).
+constexpr int kFewGroups = 224;
 
-// Columns of a workgroup of few_kernel.
-int few_columns(const moe_adapter_shape &s) { return s.T > 64 ? 128 : 64; }
+// Columns of a workgroup of few_kernel.  Past 64 rows, 128 read x half as
+// often; 64 make fewer and larger parts of H, whose planes are written and read.
+// 128 win where 64 leave but two parts of a long H (128 rows, H = 7,168,
+// N = 5,120: 34 against 38 us, N = 10,240: 55 and 65), else 64 (H = 1,024,
+// N = 5,120: 18 against 23; H = 7,168, N = 2,304: 24 and 27).
+int few_columns(const moe_adapter_shape &s)
+{
+    const int tn = (s.N + 63) / 64;
+    return s.T > 64 && s.H >= 4096 && 3 * tn > kFewGroups ? 128 : 64;
+}
 
-// Parts of H of few_kernel for a shape: as many workgroups as run at once
-// (one a CU), at most 8 parts of at least two steps.
+// Parts of H of few_kernel: at most 6 (8 gain less than 1% in a short H and
+// lose as much in small N), of at least two steps.
 int few_splits(const moe_adapter_shape &s)
 {
     const int tn = (s.N + few_columns(s) - 1) / few_columns(s);
-    return std::max(1, std::min({256 / tn, 8, s.H / 128}));
+    return std::max(1, std::min({kFewGroups / tn, 6, s.H / 128}));
 }
 
 // Tiles of 128 x 128, and the parts of H that project_small_kernel makes of
@@ -1122,8 +1139,8 @@ int small_splits(const moe_adapter_shape &s)
 
 size_t parts_bytes(const moe_adapter_shape &s)
 {
-    const int splits = s.T <= kFewProject ? few_splits(s) : small_splits(s);
-    return s.T > kFewProject && splits == 1 ? 0 : (size_t)splits * s.T * s.N * sizeof(float);
+    const int splits = s.T <= kFewRows ? few_splits(s) : small_splits(s);
+    return s.T > kFewRows && splits == 1 ? 0 : (size_t)splits * s.T * s.N * sizeof(float);
 }
 
 // The order's arrays in the workspace, from its start; order null where there
@@ -1136,7 +1153,7 @@ struct OrderLayout {
 OrderLayout order_layout(const moe_adapter_shape &s, uint8_t *ws)
 {
     OrderLayout l{};
-    if (s.T <= kFewRows)
+    if (s.T <= kUnordered)
         return l;
     const auto take = [&](size_t n) {
         uint8_t *p = ws + l.bytes;
@@ -1201,7 +1218,8 @@ hipError_t adapter_of_type(const moe_adapter_shape &sh, const void *x_, const vo
     const auto *a = static_cast<const uint16_t *>(a_), *b = static_cast<const uint16_t *>(b_);
     auto *out = static_cast<uint16_t *>(out_);
     const OrderLayout ol = order_layout(sh, ws);
-    const Row *order = ol.out.order;
+    const bool few_rows = w && s.T <= kFewRows;
+    const Row *order = few_rows ? nullptr : ol.out.order;
     float *v = reinterpret_cast<float *>(ws + ol.bytes);
     const auto add = [&](auto nf, auto gb, auto given, int blocks, const void *from, int parts) {
         constexpr int NF = decltype(nf)::value, GB = decltype(gb)::value;
@@ -1220,7 +1238,7 @@ hipError_t adapter_of_type(const moe_adapter_shape &sh, const void *x_, const vo
     const std::integral_constant<int, 4> c4;
     const std::integral_constant<int, 8> c8;
     hipError_t e;
-    if (s.T <= kFewProject && w) {
+    if (few_rows) {
         float *parts = reinterpret_cast<float *>(ws + v_bytes(sh));
         const int tn = up(s.N, few_columns(sh)), splits = few_splits(sh);
         const auto few = [&](auto stream, auto shrink) {
@@ -1240,6 +1258,8 @@ hipError_t adapter_of_type(const moe_adapter_shape &sh, const void *x_, const vo
             few(Stream<32, 64, 2, 1, 6, 15, 128>{}, FewStream{});
         else if (s.T <= 64)
             few(Stream<64, 64, 2, 1, 6, 12, 128>{}, FewStream{});
+        else if (few_columns(sh) == 64)
+            few(Stream<128, 64, 2, 1, 4, 9, 128>{}, FewStream{});
         else
             few(Stream<128, 128, 2, 2, 4, 5, 128>{}, FewStream8{});
         if ((e = hipGetLastError()) != hipSuccess)
@@ -1247,7 +1267,7 @@ hipError_t adapter_of_type(const moe_adapter_shape &sh, const void *x_, const vo
         // few rows: many short wavefronts, any mix of adapters
         return add(c2, c8, std::false_type{}, 1, parts, splits);
     }
-    if (s.T <= kFewRows) {
+    if (s.T <= kUnordered) {
         shrink_few_kernel<DT>
             <<<std::min(s.T * up(s.r, FewStream::kBN), 2 * device_cu_count()),
                FewStream::kThreads, 0, st>>>(s, x, ids, a, v);
@@ -1258,7 +1278,7 @@ hipError_t adapter_of_type(const moe_adapter_shape &sh, const void *x_, const vo
     if (e != hipSuccess)
         return e;
     if (!w)
-        return add(c4, c1, std::true_type{}, s.T > kFewProject ? 2 : 1, base, 0);
+        return add(c4, c1, std::true_type{}, s.T > kFewRows ? 2 : 1, base, 0);
     float *parts = reinterpret_cast<float *>(ws + v_bytes(sh));
     const ProjectArgs p{x, w, ids, order, b, scale, v, out, parts};
     const int cus = device_cu_count();

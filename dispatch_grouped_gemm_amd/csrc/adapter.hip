@@ -6,6 +6,8 @@
 // "Shrink" makes v[t] = x[t] A_l^T in float32.  "Project" computes x W^T in
 // MFMA tiles and, once a tile's sums are complete, adds the adapters' term
 // to them in registers ("expand"), so out is written once and rounded once.
+// Where the tiles are too few for the CUs, they become parts of H, float32
+// planes that a last launch ("add") joins in a fixed order and expands.
 //
 // Rows come in any order.  Whoever owns a set of rows walks the different
 // ids among them: an adapter's product is formed for 16 rows at a time (the
@@ -131,7 +133,8 @@ __device__ __forceinline__ int xcd_run(int b, int n)
 // blocks of up to `block` places that hold one adapter each.  One workgroup:
 // a histogram (in LDS, or in the workspace past kOrderKeys adapters), its
 // scan, and a claim of a place per row.  A wavefront whose rows share an
-// adapter claims with one atomic.
+// adapter claims with one atomic.  Bound by its chain of loads and atomics:
+// 8,191 rows of 16 adapters 8.3 us, 4,097 of 96 5.8.
 // ---------------------------------------------------------------------------
 constexpr int kOrderThreads = 1024, kOrderBatch = 8;
 
@@ -505,7 +508,8 @@ shrink_few_kernel(AShape s, const uint16_t *__restrict__ x, const int32_t *__res
     shrink_few<DT, FewStream>(s, x, ids, a, v, blockIdx.x, gridDim.x, lds);
 }
 
-// Shrink, many rows, ordered: workgroup (a block of up to BM places of one
+// Shrink, many rows, ordered (8,191 rows of 7,168 bf16 values by rank 64: 31 us,
+// 130 MB read at 4.2 TB/s): workgroup (a block of up to BM places of one
 // adapter, BN of the rank).
 template <int DT, int BM, int BN, int WM, int NX, int NR>
 __global__ void __launch_bounds__((Stream<BM, BN, WM, 1, NX, NR, 256, false>::kThreads))
@@ -735,26 +739,56 @@ __device__ __forceinline__ void store_cols(const AShape &s, uint16_t *out, int t
     }
 }
 
+// The order of up to kFewRows rows, by one workgroup: a row's place is the
+// count of rows before it, by adapter and row, those without one last.  The
+// add then meets one or two adapters in 16 rows and reads B once: 128 rows at
+// 1,024 x 6,144 with 32 adapters of rank 64 take 25 us, in the caller's order 33;
+// at rank 16 both are alike.
+__device__ __forceinline__ void order_few(const AShape &s, const int32_t *__restrict__ ids,
+                                          Row *__restrict__ order, int32_t *key)
+{
+    const int tid = threadIdx.x;
+    const int id = tid < s.T && (unsigned)ids[tid] < (unsigned)s.L ? ids[tid] : -1;
+    const uint32_t mine = (uint32_t)id; // -1 orders last
+    if (tid < s.T)
+        key[tid] = id;
+    __syncthreads();
+    int place = 0;
+    for (int u = 0; u < s.T; ++u)
+        place += (uint32_t)key[u] < mine || ((uint32_t)key[u] == mine && u < tid);
+    if (tid < s.T)
+        order[place] = Row{tid, id};
+}
+
 // ---------------------------------------------------------------------------
-// Project, few rows: W is read once.  One launch makes v (its workgroups
-// last) and, beside it, parts of x W^T: a workgroup takes all rows (up to
-// BM), 64 columns and one of `splits` parts of H, and leaves float32 sums;
-// the add launch joins the parts in order and adds the adapters' term.
+// Project, few rows: W is read once.  One launch makes v and the order (its
+// workgroups last) and, beside them, parts of x W^T: a workgroup takes all
+// rows (up to BM), BN columns and one of `splits` parts of H, and leaves
+// float32 sums; the add launch joins the parts and adds the adapters' term.
 // Splitting H gives every CU work without more copies of x than columns ask
 // for, and the adapters' chain of loads does not stand at the end of W's.
+// order is null for 16 rows, whose add is one block in any order.
+// Bound by reading W and A: 1 x 5,120 by 4,608 takes 10 us (4.7 TB/s), 128 x
+// 7,168 by 7,168 with 64 adapters of rank 32 31 us (145 MB, 4.7 TB/s); a step
+// of the 128-row tile multiplies in a fifth of that time.
 // ---------------------------------------------------------------------------
 template <int DT, typename S, typename F>
 __global__ void __launch_bounds__(S::kThreads)
 few_kernel(AShape s, int tn, int splits, const uint16_t *__restrict__ x,
            const uint16_t *__restrict__ w, const int32_t *__restrict__ ids,
-           const uint16_t *__restrict__ a, float *__restrict__ v, float *__restrict__ parts)
+           const uint16_t *__restrict__ a, float *__restrict__ v, float *__restrict__ parts,
+           Row *__restrict__ order)
 {
     static_assert(S::kThreads == F::kThreads, "one launch for both");
     constexpr int kLds = S::kLds > F::kLds ? S::kLds : F::kLds, BM = S::kBM;
     __shared__ __align__(1024) uint8_t lds[kLds];
-    const int q = blockIdx.x;
-    if (q >= tn * splits) {
-        shrink_few<DT, F>(s, x, ids, a, v, q - tn * splits, gridDim.x - tn * splits, lds);
+    const int q = blockIdx.x, other = tn * splits + (order != nullptr);
+    if (q >= other) {
+        shrink_few<DT, F>(s, x, ids, a, v, q - other, gridDim.x - other, lds);
+        return;
+    }
+    if (q == tn * splits) {
+        order_few(s, ids, order, reinterpret_cast<int32_t *>(lds));
         return;
     }
     const int n0 = q % tn * S::kBN, part = q / tn;
@@ -796,6 +830,9 @@ few_kernel(AShape s, int tn, int splits, const uint16_t *__restrict__ x,
 // instructions.  The last phase of a step reads the next stage and sends off
 // the loads of the step after it, into the stage that all wavefronts have
 // just finished reading: one barrier a step, and a step's time for its loads.
+// Bound by the matrix instructions and what of the loads they do not cover: at
+// 8,191 x 7,168 x 7,168 bf16 they hold the matrix cores for two thirds of 700 us
+// (1.2 PFLOP/s with the adapters' term; 896 tiles are 3.5 rounds of 256 CUs).
 // ---------------------------------------------------------------------------
 
 // Tile q of tm x tn: down 8 row tiles before the next column tile, so the
@@ -1017,8 +1054,8 @@ project_small_kernel(AShape s, int tm, int tn, int splits, ProjectArgs p)
 
 // ---------------------------------------------------------------------------
 // Add: out = base + the adapters' term, base a given projection, or (kParts)
-// the sum of `parts` float32 planes.  Bound by reading the base and writing
-// out.  A wavefront takes 16 places and `blocks` blocks of 16 NF columns:
+// the sum of `parts` float32 planes.  Bound by reading the base or the planes
+// and B, and writing out: 4,097 x 5,120 fp16 values 19 us (84 MB, 4.4 TB/s).  A wavefront takes 16 places and `blocks` blocks of 16 NF columns:
 // their v is read once for all of them, up to a rank of 32 KK.
 // ---------------------------------------------------------------------------
 constexpr int kAddWaves = 4;
@@ -1143,8 +1180,7 @@ size_t parts_bytes(const moe_adapter_shape &s)
     return s.T > kFewRows && splits == 1 ? 0 : (size_t)splits * s.T * s.N * sizeof(float);
 }
 
-// The order's arrays in the workspace, from its start; order null where there
-// is none (few rows).
+// The order's arrays in the workspace, from its start; null for one block of rows.
 struct OrderLayout {
     OrderOut out;
     size_t bytes;
@@ -1153,7 +1189,7 @@ struct OrderLayout {
 OrderLayout order_layout(const moe_adapter_shape &s, uint8_t *ws)
 {
     OrderLayout l{};
-    if (s.T <= kUnordered)
+    if (s.T <= 16)
         return l;
     const auto take = [&](size_t n) {
         uint8_t *p = ws + l.bytes;
@@ -1184,7 +1220,9 @@ hipError_t shrink_many(const AShape &s, const uint16_t *x, const int32_t *ids, c
 {
     // as much of the rank per workgroup as there is (x is read once per
     // block of the rank), but a workgroup for every CU; x comes from memory
-    // and gets the deeper ring
+    // and gets the deeper ring (8,191 x 7,168 x 7,168 with rank 64, the whole call:
+    // by 64 717 us, by 32 732, by 16 769; 257 x 5,120 x 4,608 and 1,024 x 5,120 x
+    // 2,048, too few rows for every CU: by 64 54 and 58, by 16 and 32 48 and 54)
     const int cus = device_cu_count(), t = up(s.T, 32);
     // blocks there may be (a workgroup takes several past 2^20)
     const auto blocks = [&](int rows) {
@@ -1219,7 +1257,8 @@ hipError_t adapter_of_type(const moe_adapter_shape &sh, const void *x_, const vo
     auto *out = static_cast<uint16_t *>(out_);
     const OrderLayout ol = order_layout(sh, ws);
     const bool few_rows = w && s.T <= kFewRows;
-    const Row *order = few_rows ? nullptr : ol.out.order;
+    const bool ordered = w || s.T > kUnordered;
+    const Row *order = ordered ? ol.out.order : nullptr;
     float *v = reinterpret_cast<float *>(ws + ol.bytes);
     const auto add = [&](auto nf, auto gb, auto given, int blocks, const void *from, int parts) {
         constexpr int NF = decltype(nf)::value, GB = decltype(gb)::value;
@@ -1244,13 +1283,13 @@ hipError_t adapter_of_type(const moe_adapter_shape &sh, const void *x_, const vo
         const auto few = [&](auto stream, auto shrink) {
             using S = decltype(stream);
             using F = decltype(shrink);
-            // the shrink's workgroups come last and find the CUs that the
-            // parts leave, at most four tasks each
-            const int tasks = s.T * up(s.r, F::kBN);
+            // the order's and the shrink's workgroups come last and find the
+            // CUs that the parts leave, the latter at most four tasks each
+            const int tasks = s.T * up(s.r, F::kBN), other = tn * splits + (order != nullptr);
             const int shrinks =
-                std::min(tasks, std::max(device_cu_count() - tn * splits, up(tasks, 4)));
-            few_kernel<DT, S, F><<<tn * splits + shrinks, S::kThreads, 0, st>>>(
-                s, tn, splits, x, w, ids, a, v, parts);
+                std::min(tasks, std::max(device_cu_count() - other, up(tasks, 4)));
+            few_kernel<DT, S, F><<<other + shrinks, S::kThreads, 0, st>>>(
+                s, tn, splits, x, w, ids, a, v, parts, ol.out.order);
         };
         if (s.T <= 16)
             few(Stream<16, 64, 1, 2, 8, 15, 128>{}, FewStream{});
@@ -1264,10 +1303,10 @@ hipError_t adapter_of_type(const moe_adapter_shape &sh, const void *x_, const vo
             few(Stream<128, 128, 2, 2, 4, 5, 128>{}, FewStream8{});
         if ((e = hipGetLastError()) != hipSuccess)
             return e;
-        // few rows: many short wavefronts, any mix of adapters
+        // few rows: many short wavefronts
         return add(c2, c8, std::false_type{}, 1, parts, splits);
     }
-    if (s.T <= kUnordered) {
+    if (!ordered) {
         shrink_few_kernel<DT>
             <<<std::min(s.T * up(s.r, FewStream::kBN), 2 * device_cu_count()),
                FewStream::kThreads, 0, st>>>(s, x, ids, a, v);
@@ -1278,10 +1317,17 @@ hipError_t adapter_of_type(const moe_adapter_shape &sh, const void *x_, const vo
     if (e != hipSuccess)
         return e;
     if (!w)
+        // two blocks of columns a wavefront read v once, where that leaves
+        // enough of them: 100 rows 18.7 us with two, 13.8 with one; 4,097 rows
+        // 38.3 and 39.5
         return add(c4, c1, std::true_type{}, s.T > kFewRows ? 2 : 1, base, 0);
     float *parts = reinterpret_cast<float *>(ws + v_bytes(sh));
     const ProjectArgs p{x, w, ids, order, b, scale, v, out, parts};
     const int cus = device_cu_count();
+    // 256 x 256 tiles from one a CU on: each value moved from the L2 enters twice
+    // the products of 128 x 128 (4,096 x 4,096 x 4,096 130 against 151 us, 8,191 x
+    // 7,168 x 7,168 714 against 811); the halves: 711 against 739 there, 231 against
+    // 283 at 4,352 x 5,120 x 5,120
     const int tm = up(s.T, 256), tn = up(s.N, 256), left = tm * tn % cus;
     const int sm = up(s.T, 128), sn = up(s.N, 128), splits = small_splits(sh);
     if (splits > 1) {

@@ -8,7 +8,12 @@
 // All four walk the tokens: a token's row is read or written once however
 // many experts it goes to, each of its expert rows once, and no two slots
 // share a row, so there are no atomics and every sum has a fixed order.
-// Sums are float32, k ascending, rounded once.  Bound by memory.
+// Sums are float32, k ascending, rounded once.
+//
+// Bound by memory, HBM bytes those of the formulas (within 2%).  8,192 tokens of
+// 7,168 bf16 values and 6 experts each: permute 157 us (822 MB, 5.2 TB/s), its
+// gradient 147 (5.6), unpermute 146 (5.6), its gradients 313 (1.53 GB, 4.9);
+// a large copy reaches 5.1.  128 tokens take 2.4 to 3.5 us, a launch.
 #include "elem.hpp"
 
 namespace moe {
@@ -18,7 +23,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxK = 8;
 
-// Which pieces of which token a thread takes: P pieces, 64 apart.  Where a
+// Which pieces of which token a thread takes: P pieces, 64 apart (two where the
+// row allows it: half the slots and weights to load, more loads in flight).  Where a
 // row is a multiple of 64 P pieces a wavefront lies inside one token, whose
 // number, slots and weights are then read once per wavefront (scalar loads);
 // else (P = 1) every thread finds its own.

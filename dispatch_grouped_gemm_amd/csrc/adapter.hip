@@ -1055,8 +1055,9 @@ project_small_kernel(AShape s, int tm, int tn, int splits, ProjectArgs p)
 // ---------------------------------------------------------------------------
 // Add: out = base + the adapters' term, base a given projection, or (kParts)
 // the sum of `parts` float32 planes.  Bound by reading the base or the planes
-// and B, and writing out: 4,097 x 5,120 fp16 values 19 us (84 MB, 4.4 TB/s).  A wavefront takes 16 places and `blocks` blocks of 16 NF columns:
-// their v is read once for all of them, up to a rank of 32 KK.
+// and B, and writing out: 4,097 x 5,120 fp16 values 19 us (84 MB, 4.4 TB/s).  A
+// wavefront takes 16 places and `blocks` blocks of 16 NF columns: their v is
+// read once for all of them, up to a rank of 32 KK.
 // ---------------------------------------------------------------------------
 constexpr int kAddWaves = 4;
 

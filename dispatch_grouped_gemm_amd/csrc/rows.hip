@@ -23,27 +23,19 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxK = 8;
 
-// Which pieces of which token a thread takes: P pieces, 64 apart (two where the
-// row allows it: half the slots and weights to load, more loads in flight).  Where a
-// row is a multiple of 64 P pieces a wavefront lies inside one token, whose
-// number, slots and weights are then read once per wavefront (scalar loads);
-// else (P = 1) every thread finds its own.
+// The token and the 16-byte piece of its row that a thread takes (T H < 2^32, so
+// fewer than 2^30 pieces).  The slots come through the vector cache: read once
+// per wavefront, where one lies inside a token, they cost 5 us more at 8,192
+// tokens (unpermute 152 against 147) and 1 us less at 1,024 (17 and 18), and two
+// pieces a thread change nothing.
 struct Place {
     int t, p;
 };
-template <int P, bool kOne>
-__device__ __forceinline__ Place place_of(int T, int pieces)
+__device__ __forceinline__ Place place_of(int pieces)
 {
-    const long i = (long)blockIdx.x * kThreads + threadIdx.x;
-    if constexpr (kOne) {
-        const int per = pieces / (64 * P);
-        const long wave = i >> 6;
-        const int t = __builtin_amdgcn_readfirstlane((int)min(wave / per, (long)T));
-        return Place{t, (int)(wave - (long)t * per) * 64 * P + (int)(threadIdx.x & 63)};
-    } else {
-        const int t = (int)min(i / pieces, (long)T);
-        return Place{t, (int)(i - (long)t * pieces)};
-    }
+    const unsigned i = blockIdx.x * kThreads + threadIdx.x;
+    const unsigned t = i / (unsigned)pieces;
+    return Place{(int)t, (int)(i - t * (unsigned)pieces)};
 }
 
 // The stores leave the L2 first: what these kernels write is large and read
@@ -56,33 +48,28 @@ __device__ __forceinline__ void store_piece(void *base, size_t piece, const uint
     store_once(static_cast<uint4 *>(base) + piece, q);
 }
 
-// A thread stores its pieces of a token's row K times.
-template <int DT, int P, bool kOne>
+// A thread stores its piece of a token's row K times.
+template <int DT>
 __global__ void __launch_bounds__(kThreads)
 permute_kernel(int T, int H, int K, long R, const void *__restrict__ x,
                const int32_t *__restrict__ route_row, void *__restrict__ rows)
 {
     const int pieces = H / Elem<DT>::kVec;
-    const Place at = place_of<P, kOne>(T, pieces);
+    const Place at = place_of(pieces);
     if (at.t >= T)
         return;
-    uint4 v[P];
-#pragma unroll
-    for (int j = 0; j < P; ++j)
-        v[j] = static_cast<const uint4 *>(x)[(size_t)at.t * pieces + at.p + 64 * j];
+    const uint4 v = static_cast<const uint4 *>(x)[(size_t)at.t * pieces + at.p];
 #pragma unroll
     for (int k = 0; k < kMaxK; ++k) {
         const int row = k < K ? checked_row(route_row[(size_t)at.t * K + k], R) : -1;
         if (row >= 0)
-#pragma unroll
-            for (int j = 0; j < P; ++j)
-                store_piece(rows, (size_t)row * pieces + at.p + 64 * j, v[j]);
+            store_piece(rows, (size_t)row * pieces + at.p, v);
     }
 }
 
-// A thread sums its pieces of a token's expert rows: all loaded, then added
+// A thread sums its piece of a token's expert rows: all loaded, then added
 // in ascending k.
-template <int DT, int P, bool kOne, bool kWeights>
+template <int DT, bool kWeights>
 __global__ void __launch_bounds__(kThreads)
 unpermute_kernel(int T, int H, int K, long R, const void *__restrict__ rows,
                  const float *__restrict__ w, const int32_t *__restrict__ route_row,
@@ -91,12 +78,12 @@ unpermute_kernel(int T, int H, int K, long R, const void *__restrict__ rows,
 #pragma clang fp contract(off)
     constexpr int V = Elem<DT>::kVec;
     const int pieces = H / V;
-    const Place at = place_of<P, kOne>(T, pieces);
+    const Place at = place_of(pieces);
     if (at.t >= T)
         return;
     int row[kMaxK];
     float wk[kMaxK];
-    uint4 q[kMaxK][P];
+    uint4 q[kMaxK];
 #pragma unroll
     for (int k = 0; k < kMaxK; ++k) {
         row[k] = k < K ? checked_row(route_row[(size_t)at.t * K + k], R) : -1;
@@ -105,34 +92,24 @@ unpermute_kernel(int T, int H, int K, long R, const void *__restrict__ rows,
 #pragma unroll
     for (int k = 0; k < kMaxK; ++k)
         if (row[k] >= 0)
+            q[k] = static_cast<const uint4 *>(rows)[(size_t)row[k] * pieces + at.p];
+    float acc[V];
 #pragma unroll
-            for (int j = 0; j < P; ++j)
-                q[k][j] =
-                    static_cast<const uint4 *>(rows)[(size_t)row[k] * pieces + at.p + 64 * j];
-    float acc[P][V];
-#pragma unroll
-    for (int j = 0; j < P; ++j)
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            acc[j][i] = 0.0f;
+    for (int i = 0; i < V; ++i)
+        acc[i] = 0.0f;
 #pragma unroll
     for (int k = 0; k < kMaxK; ++k) {
         if (row[k] < 0)
             continue;
+        float f[V];
+        Elem<DT>::unpack(q[k], f);
 #pragma unroll
-        for (int j = 0; j < P; ++j) {
-            float f[V];
-            Elem<DT>::unpack(q[k][j], f);
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float pr = kWeights ? wk[k] * f[i] : f[i];
-                acc[j][i] = acc[j][i] + pr;
-            }
+        for (int i = 0; i < V; ++i) {
+            const float pr = kWeights ? wk[k] * f[i] : f[i];
+            acc[i] = acc[i] + pr;
         }
     }
-#pragma unroll
-    for (int j = 0; j < P; ++j)
-        store_piece(out, (size_t)at.t * pieces + at.p + 64 * j, Elem<DT>::pack(acc[j]));
+    store_piece(out, (size_t)at.t * pieces + at.p, Elem<DT>::pack(acc));
 }
 
 // A workgroup takes one token: its dout row read once, its expert rows read
@@ -204,20 +181,11 @@ unpermute_backward_kernel(int T, int H, int K, long R, const void *__restrict__ 
     }
 }
 
-// Calls f with P and whether a wavefront lies inside one token, and the grid.
-template <typename F>
-void with_place(const moe_shape &s, int dtype, F f)
+// Workgroups for a thread per piece of every token.
+unsigned grid_of(const moe_shape &s, int dtype)
 {
-    const long pieces = s.H * (long)elem_bytes(dtype) / 16;
-    const auto grid = [&](int P) {
-        return (unsigned)((s.T * pieces / P + kThreads - 1) / kThreads);
-    };
-    if (pieces % 128 == 0)
-        f(std::integral_constant<int, 2>{}, std::true_type{}, grid(2));
-    else if (pieces % 64 == 0)
-        f(std::integral_constant<int, 1>{}, std::true_type{}, grid(1));
-    else
-        f(std::integral_constant<int, 1>{}, std::false_type{}, grid(1));
+    const long pieces = s.T * (s.H * (long)elem_bytes(dtype) / 16);
+    return (unsigned)((pieces + kThreads - 1) / kThreads);
 }
 
 } // namespace
@@ -226,14 +194,10 @@ hipError_t launch_permute(const moe_shape &s, int dtype, const void *x, const in
                           void *rows, hipStream_t st)
 {
     const long R = moe_row_capacity(&s);
-    with_place(s, dtype, [&](auto p, auto one, unsigned grid) {
-        constexpr int P = decltype(p)::value;
-        constexpr bool kOne = decltype(one)::value;
-        // a copy: both 16-bit types alike
-        const auto k = dtype == MOE_DT_F32 ? permute_kernel<MOE_DT_F32, P, kOne>
-                                           : permute_kernel<MOE_DT_BF16, P, kOne>;
-        k<<<grid, kThreads, 0, st>>>(s.T, s.H, s.K, R, x, route_row, rows);
-    });
+    // a copy: both 16-bit types alike
+    const auto k =
+        dtype == MOE_DT_F32 ? permute_kernel<MOE_DT_F32> : permute_kernel<MOE_DT_BF16>;
+    k<<<grid_of(s, dtype), kThreads, 0, st>>>(s.T, s.H, s.K, R, x, route_row, rows);
     return hipGetLastError();
 }
 
@@ -242,13 +206,9 @@ hipError_t launch_unpermute(const moe_shape &s, int dtype, const void *rows, con
 {
     const long R = moe_row_capacity(&s);
     with_elem(dtype, [&](auto dt) {
-        with_place(s, dtype, [&](auto p, auto one, unsigned grid) {
-            constexpr int DT = decltype(dt)::value, P = decltype(p)::value;
-            constexpr bool kOne = decltype(one)::value;
-            const auto k = w ? unpermute_kernel<DT, P, kOne, true>
-                             : unpermute_kernel<DT, P, kOne, false>;
-            k<<<grid, kThreads, 0, st>>>(s.T, s.H, s.K, R, rows, w, route_row, out);
-        });
+        constexpr int DT = decltype(dt)::value;
+        const auto k = w ? unpermute_kernel<DT, true> : unpermute_kernel<DT, false>;
+        k<<<grid_of(s, dtype), kThreads, 0, st>>>(s.T, s.H, s.K, R, rows, w, route_row, out);
     });
     return hipGetLastError();
 }

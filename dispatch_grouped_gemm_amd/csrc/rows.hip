@@ -24,19 +24,31 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxK = 8;
 
-// The token and the 16-byte piece of its row that a thread takes (T H < 2^32, so
-// fewer than 2^30 pieces).  The slots come through the vector cache: read once
-// per wavefront, where one lies inside a token, they cost 5 us more at 8,192
-// tokens (unpermute 152 against 147) and 1 us less at 1,024 (17 and 18), and two
-// pieces a thread change nothing.
+// Which 16-byte pieces of which token a thread takes (T H < 2^32, so there are
+// fewer than 2^30).  One piece, wherever it lies; or (kPair) two, 64 apart, where
+// a wavefront lies inside one token: its slots and weights are then read once
+// per wavefront (scalar loads) and skipped slots by scalar branches.
+//
+// kPair is for ranks that hold at most half of the experts, where most slots go
+// elsewhere and a thread's overhead counts: 4,095 tokens of 5,120 float32 values
+// with 23% of the slots here take 30 us to sum, 35 with single pieces.  With
+// every expert here single pieces keep more loads in flight: 8,192 tokens of
+// 7,168 bf16 values 148 us, in pairs 152; 4,096 of 5,120 float32 values 105, 109.
 struct Place {
     int t, p;
 };
-__device__ __forceinline__ Place place_of(int pieces)
+template <bool kPair>
+__device__ __forceinline__ Place place_of(int T, int pieces)
 {
     const unsigned i = blockIdx.x * kThreads + threadIdx.x;
-    const unsigned t = i / (unsigned)pieces;
-    return Place{(int)t, (int)(i - t * (unsigned)pieces)};
+    if constexpr (kPair) {
+        const unsigned per = (unsigned)pieces / 128, wave = i >> 6;
+        const int t = __builtin_amdgcn_readfirstlane((int)min(wave / per, (unsigned)T));
+        return Place{t, (int)((wave - t * per) * 128 + (threadIdx.x & 63))};
+    } else {
+        const unsigned t = i / (unsigned)pieces;
+        return Place{(int)t, (int)(i - t * (unsigned)pieces)};
+    }
 }
 
 // The stores leave the L2 first: what these kernels write is large and read
@@ -49,42 +61,48 @@ __device__ __forceinline__ void store_piece(void *base, size_t piece, const uint
     store_once(static_cast<uint4 *>(base) + piece, q);
 }
 
-// A thread stores its piece of a token's row K times.
-template <int DT>
+// A thread stores its pieces of a token's row K times.
+template <int DT, bool kPair>
 __global__ void __launch_bounds__(kThreads)
 permute_kernel(int T, int H, int K, long R, const void *__restrict__ x,
                const int32_t *__restrict__ route_row, void *__restrict__ rows)
 {
+    constexpr int P = kPair ? 2 : 1;
     const int pieces = H / Elem<DT>::kVec;
-    const Place at = place_of(pieces);
+    const Place at = place_of<kPair>(T, pieces);
     if (at.t >= T)
         return;
-    const uint4 v = static_cast<const uint4 *>(x)[(size_t)at.t * pieces + at.p];
+    uint4 v[P];
+#pragma unroll
+    for (int j = 0; j < P; ++j)
+        v[j] = static_cast<const uint4 *>(x)[(size_t)at.t * pieces + at.p + 64 * j];
 #pragma unroll
     for (int k = 0; k < kMaxK; ++k) {
         const int row = k < K ? checked_row(route_row[(size_t)at.t * K + k], R) : -1;
         if (row >= 0)
-            store_piece(rows, (size_t)row * pieces + at.p, v);
+#pragma unroll
+            for (int j = 0; j < P; ++j)
+                store_piece(rows, (size_t)row * pieces + at.p + 64 * j, v[j]);
     }
 }
 
-// A thread sums its piece of a token's expert rows: all loaded, then added
+// A thread sums its pieces of a token's expert rows: all loaded, then added
 // in ascending k.
-template <int DT, bool kWeights>
+template <int DT, bool kPair, bool kWeights>
 __global__ void __launch_bounds__(kThreads)
 unpermute_kernel(int T, int H, int K, long R, const void *__restrict__ rows,
                  const float *__restrict__ w, const int32_t *__restrict__ route_row,
                  void *__restrict__ out)
 {
 #pragma clang fp contract(off)
-    constexpr int V = Elem<DT>::kVec;
+    constexpr int V = Elem<DT>::kVec, P = kPair ? 2 : 1;
     const int pieces = H / V;
-    const Place at = place_of(pieces);
+    const Place at = place_of<kPair>(T, pieces);
     if (at.t >= T)
         return;
     int row[kMaxK];
     float wk[kMaxK];
-    uint4 q[kMaxK];
+    uint4 q[kMaxK][P];
 #pragma unroll
     for (int k = 0; k < kMaxK; ++k) {
         row[k] = k < K ? checked_row(route_row[(size_t)at.t * K + k], R) : -1;
@@ -93,24 +111,34 @@ unpermute_kernel(int T, int H, int K, long R, const void *__restrict__ rows,
 #pragma unroll
     for (int k = 0; k < kMaxK; ++k)
         if (row[k] >= 0)
-            q[k] = static_cast<const uint4 *>(rows)[(size_t)row[k] * pieces + at.p];
-    float acc[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-        acc[i] = 0.0f;
+            for (int j = 0; j < P; ++j)
+                q[k][j] =
+                    static_cast<const uint4 *>(rows)[(size_t)row[k] * pieces + at.p + 64 * j];
+    float acc[P][V];
+#pragma unroll
+    for (int j = 0; j < P; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            acc[j][i] = 0.0f;
 #pragma unroll
     for (int k = 0; k < kMaxK; ++k) {
         if (row[k] < 0)
             continue;
-        float f[V];
-        Elem<DT>::unpack(q[k], f);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float pr = kWeights ? wk[k] * f[i] : f[i];
-            acc[i] = acc[i] + pr;
+        for (int j = 0; j < P; ++j) {
+            float f[V];
+            Elem<DT>::unpack(q[k][j], f);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float pr = kWeights ? wk[k] * f[i] : f[i];
+                acc[j][i] = acc[j][i] + pr;
+            }
         }
     }
-    store_piece(out, (size_t)at.t * pieces + at.p, Elem<DT>::pack(acc));
+#pragma unroll
+    for (int j = 0; j < P; ++j)
+        store_piece(out, (size_t)at.t * pieces + at.p + 64 * j, Elem<DT>::pack(acc[j]));
 }
 
 // A workgroup takes one token: its dout row read once, its expert rows read
@@ -192,11 +220,18 @@ unpermute_backward_kernel(int T, int H, int K, long R, const void *__restrict__ 
     }
 }
 
-// Workgroups for a thread per piece of every token.
-unsigned grid_of(const moe_shape &s, int dtype)
+// Calls f with whether threads take pairs of pieces, and the grid.
+template <typename F>
+void with_place(const moe_shape &s, int dtype, F f)
 {
-    const long pieces = s.T * (s.H * (long)elem_bytes(dtype) / 16);
-    return (unsigned)((pieces + kThreads - 1) / kThreads);
+    const long pieces = s.H * (long)elem_bytes(dtype) / 16;
+    const auto grid = [&](int P) {
+        return (unsigned)((s.T * pieces / P + kThreads - 1) / kThreads);
+    };
+    if (2l * s.E_local <= s.E_total && pieces % 128 == 0)
+        f(std::true_type{}, grid(2));
+    else
+        f(std::false_type{}, grid(1));
 }
 
 } // namespace
@@ -205,10 +240,13 @@ hipError_t launch_permute(const moe_shape &s, int dtype, const void *x, const in
                           void *rows, hipStream_t st)
 {
     const long R = moe_row_capacity(&s);
-    // a copy: both 16-bit types alike
-    const auto k =
-        dtype == MOE_DT_F32 ? permute_kernel<MOE_DT_F32> : permute_kernel<MOE_DT_BF16>;
-    k<<<grid_of(s, dtype), kThreads, 0, st>>>(s.T, s.H, s.K, R, x, route_row, rows);
+    with_place(s, dtype, [&](auto pair, unsigned grid) {
+        constexpr bool kPair = decltype(pair)::value;
+        // a copy: both 16-bit types alike
+        const auto k = dtype == MOE_DT_F32 ? permute_kernel<MOE_DT_F32, kPair>
+                                           : permute_kernel<MOE_DT_BF16, kPair>;
+        k<<<grid, kThreads, 0, st>>>(s.T, s.H, s.K, R, x, route_row, rows);
+    });
     return hipGetLastError();
 }
 
@@ -217,9 +255,12 @@ hipError_t launch_unpermute(const moe_shape &s, int dtype, const void *rows, con
 {
     const long R = moe_row_capacity(&s);
     with_elem(dtype, [&](auto dt) {
-        constexpr int DT = decltype(dt)::value;
-        const auto k = w ? unpermute_kernel<DT, true> : unpermute_kernel<DT, false>;
-        k<<<grid_of(s, dtype), kThreads, 0, st>>>(s.T, s.H, s.K, R, rows, w, route_row, out);
+        with_place(s, dtype, [&](auto pair, unsigned grid) {
+            constexpr int DT = decltype(dt)::value;
+            constexpr bool kPair = decltype(pair)::value;
+            const auto k = w ? unpermute_kernel<DT, kPair, true> : unpermute_kernel<DT, kPair, false>;
+            k<<<grid, kThreads, 0, st>>>(s.T, s.H, s.K, R, rows, w, route_row, out);
+        });
     });
     return hipGetLastError();
 }

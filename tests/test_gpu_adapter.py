@@ -238,3 +238,23 @@ def test_a_large_weight():
     pick = torch.tensor([0, 1, 2, 777, 131071, 262144, 270001, 299998, 299999])
     want, _ = ref.adapters(x, w[pick.to(DEV)], None, ids, a, b[:, pick.to(DEV)], None)
     assert torch.equal(out[:, pick.to(DEV)].cpu(), want.to(BF))
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("T,N", [(65, 4744), (100, 4800), (128, 15000)])
+def test_few_rows_of_a_wide_weight(T, N, dt):
+    """A long H by many columns, whole numbers as above: exact in float32."""
+    H, L, r = 4096, 5, 24
+    g = torch.Generator().manual_seed(T)
+    x = whole(g, (T, H), -2, 2, dt)
+    x[:, torch.rand(H, generator=g).to(DEV) < 0.5] = 0
+    w = whole(g, (N, H), -1, 1, dt)
+    a, b = whole(g, (L, r, H), -1, 1, dt), whole(g, (L, N, r), -1, 1, dt)
+    base = whole(g, (T, N), -50, 50, dt)
+    for kind in ("mixed", "requests", "none", "one"):
+        ids = ids_of(kind, T, L, g).to(DEV)
+        for ww, bb in ((w, None), (None, base)):
+            say("adapter wide", T, N, dt, kind, ww is not None)
+            out = project(T, H, N, L, r, dt, x, ww, bb, ids, a, b, None)
+            want, _ = ref.adapters(x, ww, bb, ids, a, b, None)
+            assert torch.equal(out.cpu(), want.to(dt)), (kind, ww is not None)

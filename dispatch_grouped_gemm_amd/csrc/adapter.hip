@@ -16,10 +16,10 @@
 // Past few rows a first launch orders the rows by adapter, so that a tile
 // holds few of them; results do not depend on the places inside one.
 //
-// v keeps float32's precision through the matrix instruction: it enters as
-// the sum of two 16-bit values, hi = round(v) and lo = round(v - hi).  fp16
-// lacks float32's range, so there v is first divided by a power of two that
-// puts the row's largest magnitude below 1, and the product multiplied by it.
+// v enters the matrix instruction as it is: as the sum of three bf16 values
+// with eight of float32's 24 bits each, hi, mid and lo.  fp16 lacks float32's
+// range, so there B becomes bf16 instead, the sum of two values (11 bits).
+// Products of bf16 values are exact in float32.
 #include <algorithm>
 
 #include "elem.hpp"
@@ -77,17 +77,25 @@ __device__ __forceinline__ const uint4 &piece(const uint16_t *p)
     return *reinterpret_cast<const uint4 *>(p);
 }
 
-// v as hi + lo, both 16-bit.
-template <int DT>
-__device__ __forceinline__ void split8(const float *v, uint4 &hi, uint4 &lo)
+// v as the sum of N bf16 values, each what the ones before it lack, cut to its
+// upper 16 bits (so none is above that or of another sign); v[i] keeps the rest.
+template <int N>
+__device__ __forceinline__ void cut8(float *v, uint4 *out)
 {
-    float h[8], d[8];
-    hi = Elem<DT>::pack(v);
-    Elem<DT>::unpack(hi, h);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        d[i] = fabsf(h[i]) < INFINITY ? v[i] - h[i] : 0.0f;
-    lo = Elem<DT>::pack(d);
+    for (int n = 0; n < N; ++n) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = __builtin_amdgcn_perm(__float_as_uint(v[2 * i + 1]), __float_as_uint(v[2 * i]),
+                                         0x07060302);
+        out[n] = uint4{w[0], w[1], w[2], w[3]};
+        float h[8];
+        Elem<MOE_DT_BF16>::unpack(out[n], h);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) // (an infinity and a NaN have no rest)
+            v[i] = fabsf(h[i]) < INFINITY ? v[i] - h[i] : 0.0f;
+    }
 }
 
 // A row and its adapter (-1: none).
@@ -545,58 +553,30 @@ shrink_many_kernel(AShape s, const uint16_t *__restrict__ x, OrderOut o,
 // ---------------------------------------------------------------------------
 // Expand: adds the adapters' term of 16 rows (the lane's: row) to the sums of
 // 16 NF columns from n0 (in column_of's order).
-// 32 KK of the rank at a time: the rows' v as hi and lo, then the adapters among
+// 32 KK of the rank at a time: the rows' v in bf16 parts, then the adapters among
 // the rows, GB at a time with their B in flight together.  No load stands
 // behind a branch (a lane or a place without work reads a valid address and
 // drops the product): behind one the compiler waits for each by itself.
 // ---------------------------------------------------------------------------
 
-// 32 KK of the rank of the lane's row, from c: pieces k0 + 32 k of 8.
+// 32 KK of the rank of the lane's row, from c: pieces k0 + 32 k of 8, each as
+// hi, mid and lo.
 template <int KK>
 struct Low {
-    uint4 hi[KK], lo[KK];
+    uint4 v[KK][3];
     int at[KK];
     bool there[KK];
 };
 
-// What a row needs besides: its scale, and fp16's power of two.
-struct Gain {
-    float sc;
-    int ex;
-};
-
-template <int DT>
-__device__ __forceinline__ Gain gain_of(const AShape &s, const float *__restrict__ v,
-                                        const float *__restrict__ scale, const Row &row)
+// The scale of a row's adapter.
+__device__ __forceinline__ float scale_of(const float *__restrict__ scale, const Row &row)
 {
-    Gain g{1.0f, 0};
-    if (scale)
-        g.sc = scale[max(row.id, 0)];
-    if constexpr (DT == MOE_DT_F16) {
-        const float *vr = v + (size_t)row.t * s.r;
-        const int k0 = 8 * ((threadIdx.x & 63) >> 4);
-        float top = 0.0f;
-        for (int k = 0; k < s.r; k += 32) {
-            const float *p = vr + min(k + k0, s.r - 8);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const v4f q = *reinterpret_cast<const v4f *>(p + 4 * h);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    top = fmaxf(top, row.id >= 0 ? fabsf(q[i]) : 0.0f);
-            }
-        }
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
-        if (top > 0.0f && top < INFINITY)
-            (void)frexpf(top, &g.ex);
-    }
-    return g;
+    return scale ? scale[max(row.id, 0)] : 1.0f;
 }
 
-template <int DT, int KK>
+template <int KK>
 __device__ __forceinline__ Low<KK> low_of(const AShape &s, const float *__restrict__ v,
-                                      const Row &row, const Gain &g, int c)
+                                          const Row &row, int c)
 {
     const float *vr = v + (size_t)row.t * s.r;
     const int k0 = 8 * ((threadIdx.x & 63) >> 4);
@@ -613,11 +593,9 @@ __device__ __forceinline__ Low<KK> low_of(const AShape &s, const float *__restri
     for (int k = 0; k < KK; ++k) {
         float f8[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float q = low.there[k] && row.id >= 0 ? vq[k][i >> 2][i & 3] : 0.0f;
-            f8[i] = DT == MOE_DT_F16 ? ldexpf(q, -g.ex) : q;
-        }
-        split8<DT>(f8, low.hi[k], low.lo[k]);
+        for (int i = 0; i < 8; ++i)
+            f8[i] = low.there[k] && row.id >= 0 ? vq[k][i >> 2][i & 3] : 0.0f;
+        cut8<3>(f8, low.v[k]);
     }
     return low;
 }
@@ -627,7 +605,7 @@ __device__ __forceinline__ Low<KK> low_of(const AShape &s, const float *__restri
 template <int DT, int M, int NF, int GB, int KK>
 __device__ __forceinline__ void expand_part(const AShape &s, const uint16_t *__restrict__ b,
                                             const Row *row, const uint32_t *rows,
-                                            const Gain *gain, const Low<KK> *low, int n0,
+                                            const float *scale, const Low<KK> *low, int n0,
                                             v4f (*acc)[NF])
 {
     const int lane = threadIdx.x & 63;
@@ -667,7 +645,22 @@ __device__ __forceinline__ void expand_part(const AShape &s, const uint16_t *__r
         }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int q = 0; q < GB; ++q)
+        for (int q = 0; q < GB; ++q) {
+            constexpr int NB = DT == MOE_DT_F16 ? 2 : 1; // bf16 values of one of B
+            uint4 bk[KK][NF][NB];
+#pragma unroll
+            for (int k = 0; k < KK; ++k)
+#pragma unroll
+                for (int f = 0; f < NF; ++f) {
+                    const uint4 p = low[0].there[k] ? bq[q][k][f] : uint4{0, 0, 0, 0};
+                    if constexpr (DT == MOE_DT_F16) {
+                        float f8[8];
+                        Elem<DT>::unpack(p, f8);
+                        cut8<NB>(f8, bk[k][f]);
+                    } else {
+                        bk[k][f][0] = p;
+                    }
+                }
 #pragma unroll
             for (int m = 0; m < M; ++m) {
                 const bool take = row[m].id == g[q] && q < n;
@@ -675,21 +668,22 @@ __device__ __forceinline__ void expand_part(const AShape &s, const uint16_t *__r
                     continue;
 #pragma unroll
                 for (int f = 0; f < NF; ++f) {
+                    // the smallest products first
                     v4f d = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                    for (int k = 0; k < KK; ++k) {
-                        const uint4 bk = low[0].there[k] ? bq[q][k][f] : uint4{0, 0, 0, 0};
-                        d = mfma<DT>(bk, low[m].hi[k], d);
-                        d = mfma<DT>(bk, low[m].lo[k], d);
-                    }
+                    for (int o = NB + 1; o >= 0; --o)
+#pragma unroll
+                        for (int k = 0; k < KK; ++k)
+#pragma unroll
+                            for (int h = 0; h < NB; ++h)
+                                if (o - h >= 0 && o - h < 3)
+                                    d = mfma<MOE_DT_BF16>(bk[k][f][h], low[m].v[k][o - h], d);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        acc[m][f][i] += !take ? 0.0f
-                                              : gain[m].sc * (DT == MOE_DT_F16
-                                                                  ? ldexpf(d[i], gain[m].ex)
-                                                                  : d[i]);
+                        acc[m][f][i] += take ? scale[m] * d[i] : 0.0f;
                 }
             }
+        }
     }
 }
 
@@ -701,7 +695,7 @@ __device__ __forceinline__ void expand(const AShape &s, const float *__restrict_
                                        v4f (*acc)[NF])
 {
     uint32_t rows[M], any = 0;
-    Gain gain[M];
+    float sc[M];
 #pragma unroll
     for (int m = 0; m < M; ++m)
         any |= rows[m] = (uint32_t)__ballot(row[m].id >= 0) & 0xffffu;
@@ -709,13 +703,15 @@ __device__ __forceinline__ void expand(const AShape &s, const float *__restrict_
         return;
 #pragma unroll
     for (int m = 0; m < M; ++m)
-        gain[m] = gain_of<DT>(s, v, scale, row[m]);
-    for (int c = 0; c < s.r; c += 64) {
-        Low<2> low[M];
+        sc[m] = scale_of(scale, row[m]);
+    // 32 at a time: 64 do not fit the registers beside the tile's sums (8,191 x
+    // 7,168 x 7,168 bf16 with rank 64 take 790 us so, 710 by 32)
+    for (int c = 0; c < s.r; c += 32) {
+        Low<1> low[M];
 #pragma unroll
         for (int m = 0; m < M; ++m)
-            low[m] = low_of<DT, 2>(s, v, row[m], gain[m], c);
-        expand_part<DT, M, NF, GB, 2>(s, b, row, rows, gain, low, n0, acc);
+            low[m] = low_of<1>(s, v, row[m], c);
+        expand_part<DT, M, NF, GB, 1>(s, b, row, rows, sc, low, n0, acc);
     }
 }
 
@@ -1082,8 +1078,8 @@ add_kernel(AShape s, int blocks, int parts, const void *base, const int32_t *__r
     };
     if constexpr (!kParts)
         load_base(n0);
-    const Gain gain = gain_of<DT>(s, v, scale, row);
-    const Low<KK> low = low_of<DT, KK>(s, v, row, gain, 0);
+    const float sc = scale_of(scale, row);
+    const Low<KK> low = low_of<KK>(s, v, row, 0);
     for (int k = 0; k < blocks && n0 < s.N; ++k, n0 += 16 * NF) {
         v4f acc[NF];
         if constexpr (kParts) {
@@ -1122,10 +1118,10 @@ add_kernel(AShape s, int blocks, int parts, const void *base, const int32_t *__r
             load_base(min(n0 + 16 * NF, s.N - 8));
         }
         if (rows) {
-            expand_part<DT, 1, NF, GB, KK>(s, b, &row, &rows, &gain, &low, n0, &acc);
+            expand_part<DT, 1, NF, GB, KK>(s, b, &row, &rows, &sc, &low, n0, &acc);
             for (int c = 32 * KK; c < s.r; c += 32 * KK) {
-                const Low<KK> more = low_of<DT, KK>(s, v, row, gain, c);
-                expand_part<DT, 1, NF, GB, KK>(s, b, &row, &rows, &gain, &more, n0, &acc);
+                const Low<KK> more = low_of<KK>(s, v, row, c);
+                expand_part<DT, 1, NF, GB, KK>(s, b, &row, &rows, &sc, &more, n0, &acc);
             }
         }
         if (i < s.T)

@@ -542,7 +542,7 @@ int moe_unpermute_backward(const moe_shape *shape, int32_t dtype, const void *do
  * is outside [0, L) (-1) has no adapter: its out is base[t].  Rows of one
  * adapter need not be neighbours, though they are faster so.  An adapter of
  * lower rank is padded with zeros.  dtype MOE_DT_BF16 or MOE_DT_F16; every
- * sum in float32, x A^T kept to float32 precision, out rounded once.
+ * sum in float32, x A^T multiplied in all its 24 bits, out rounded once.
  * workspace: moe_adapter_workspace_size bytes of scratch, 256-byte aligned;
  * calls that overlap on one workspace race.  The other buffers are 16-byte
  * aligned (adapter_ids and scale 4-byte).

@@ -1,0 +1,76 @@
+"""The adapters' term where 16 bits of x A^T do not do, and where values are not finite."""
+
+import pytest
+import torch
+
+import dispatch_grouped_gemm_amd as moe
+from gpu_util import DEV, say
+
+pytestmark = pytest.mark.gpu
+BF, HF = torch.bfloat16, torch.float16
+
+# a size for each way through the projection on 256 CUs: 16, 32, 64 and 128 rows at most;
+# tiles in parts of H, one deep workgroup a CU, two, the largest tiles
+SIZES = [(1, 72), (16, 136), (40, 64), (64, 1000), (100, 264), (300, 520), (700, 4352), (1300, 4096),
+         (4111, 4104)]
+
+
+def project(x, w, base, ids, a, b, scale=None):
+    (T, H), (L, N, r) = x.shape, b.shape
+    s = moe.AdapterShape(T=T, H=H, N=N, L=L, rank=r)
+    ws = moe.alloc_adapter_workspace(s, DEV)
+    ws.fill_(255)
+    out = torch.full((T, N), 7.0, dtype=x.dtype, device=DEV)
+    moe.moe_adapter_project(s, x, w, ids, a, b, scale, out, ws, base=base)
+    return out
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("T,N", SIZES)
+def test_all_24_bits_of_v(T, N, dt):
+    """v0 = n, a whole number of 24 bits, and v1 = -n without its last 8: their sum, n mod 256,
+    is left of them only if both products are exact.  Every sum is one of whole numbers
+    below 2^24 (times a power of two that fits the type), so it is exact in float32."""
+    say("24 bits", T, N, dt)
+    H, L, r = 512, 3, 16
+    unit = 1.0 if dt is BF else 2.0 ** -12
+    g = torch.Generator().manual_seed(T)
+    n = torch.randint(1 << 23, 1 << 24, (T,), generator=g)
+    n[0] = (1 << 24) - 1
+    bit = torch.arange(24)
+    x = torch.zeros(T, H)
+    x[:, :24] = (n[:, None] >> bit & 1) * 2.0 ** bit * unit
+    a, b = torch.zeros(L, r, H), torch.zeros(L, N, r)
+    for l in range(L):
+        a[l, 3 + l, :24], a[l, 11 - l, 8:24] = 1.0, -1.0
+        b[l, :, 3 + l] = b[l, :, 11 - l] = 2.0 ** l
+    ids = torch.randint(-1, L, (T,), generator=g)
+    ids[0] = L - 1
+    want = torch.where(ids >= 0, (n % 256) * 2.0 ** ids * unit, 0.0)[:, None].expand(T, N)
+    x, a, b = (t.to(dt).to(DEV) for t in (x, a, b))
+    zero = torch.zeros(N, H, dtype=dt, device=DEV), torch.zeros(T, N, dtype=dt, device=DEV)
+    for w, base in ((zero[0], None), (None, zero[1])):
+        out = project(x, w, base, ids.to(torch.int32).to(DEV), a, b)
+        assert torch.equal(out.cpu(), want.to(dt)), w is not None
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("T,N", SIZES)
+def test_small_values_beside_large_ones(T, N, dt):
+    """A row of v holds 2^25, which B does not use, and k 2^-20, which it multiplies by 2^12:
+    k 2^-8 (k of 8 bits) is exact in both types."""
+    say("small beside large", T, N, dt)
+    H, L, r = 512, 2, 24
+    g = torch.Generator().manual_seed(T)
+    k = torch.randint(0, 256, (T,), generator=g)
+    x = torch.zeros(T, H)
+    x[:, 5], x[:, 77] = 2.0 ** 10, k * 2.0 ** -10
+    a, b = torch.zeros(L, r, H), torch.zeros(L, N, r)
+    a[:, 2, 5], a[:, 17, 77], b[:, :, 17] = 2.0 ** 15, 2.0 ** -10, 2.0 ** 12
+    ids = torch.randint(0, L, (T,), generator=g).to(torch.int32).to(DEV)
+    want = (k * 2.0 ** -8)[:, None].expand(T, N).to(dt)
+    x, a, b = (t.to(dt).to(DEV) for t in (x, a, b))
+    zero = torch.zeros(N, H, dtype=dt, device=DEV), torch.zeros(T, N, dtype=dt, device=DEV)
+    for w, base in ((zero[0], None), (None, zero[1])):
+        out = project(x, w, base, ids, a, b)
+        assert torch.equal(out.cpu(), want), w is not None

@@ -78,7 +78,8 @@ __device__ __forceinline__ const uint4 &piece(const uint16_t *p)
 }
 
 // v as the sum of N bf16 values, each what the ones before it lack, cut to its
-// upper 16 bits (so none is above that or of another sign); v[i] keeps the rest.
+// upper 16 bits (so none is above that or of another sign); v[i] keeps the rest,
+// a NaN where v was infinite.
 template <int N>
 __device__ __forceinline__ void cut8(float *v, uint4 *out)
 {
@@ -93,8 +94,8 @@ __device__ __forceinline__ void cut8(float *v, uint4 *out)
         float h[8];
         Elem<MOE_DT_BF16>::unpack(out[n], h);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) // (an infinity and a NaN have no rest)
-            v[i] = fabsf(h[i]) < INFINITY ? v[i] - h[i] : 0.0f;
+        for (int i = 0; i < 8; ++i)
+            v[i] -= h[i];
     }
 }
 
@@ -600,10 +601,68 @@ __device__ __forceinline__ Low<KK> low_of(const AShape &s, const float *__restri
     return low;
 }
 
+// One block's product with 32 KK of the rank: b as NB bf16 values, v as three,
+// the smallest products first.
+template <int NB, int KK>
+__device__ __forceinline__ v4f product(const uint4 (*b)[NB], const uint4 (*v)[3])
+{
+    v4f d = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int o = NB + 1; o >= 0; --o)
+#pragma unroll
+        for (int k = 0; k < KK; ++k)
+#pragma unroll
+            for (int h = 0; h < NB; ++h)
+                if (o - h >= 0 && o - h < 3)
+                    d = mfma<MOE_DT_BF16>(b[k][h], v[k][o - h], d);
+    return d;
+}
+
+// q's bf16 values, 0 where those of `by` are infinities or NaN.
+__device__ __forceinline__ uint4 where_finite(const uint4 &q, const uint4 &by)
+{
+    const auto one = [](uint32_t x, uint32_t y) {
+        const uint32_t lo = (y & 0x7f80u) == 0x7f80u ? 0u : 0xffffu;
+        const uint32_t hi = (y & 0x7f800000u) == 0x7f800000u ? 0u : 0xffff0000u;
+        return x & (lo | hi);
+    };
+    return uint4{one(q.x, by.x), one(q.y, by.y), one(q.z, by.z), one(q.w, by.w)};
+}
+
+// The same where a factor is infinite or NaN.  Its first bf16 value is too, and
+// multiplies the other factor's first value alone, which is 0 only where that
+// factor is: the values behind may be 0, and 0 times an infinity a NaN.
+template <int NB, int KK>
+__device__ __forceinline__ v4f careful(const uint4 (*b)[NB], const uint4 (*v)[3])
+{
+    uint4 bf[KK][NB], vf[KK][3];
+#pragma unroll
+    for (int k = 0; k < KK; ++k) {
+#pragma unroll
+        for (int h = 0; h < NB; ++h)
+            bf[k][h] = where_finite(b[k][h], b[k][0]);
+#pragma unroll
+        for (int h = 0; h < 3; ++h)
+            vf[k][h] = where_finite(v[k][h], v[k][0]);
+    }
+    v4f d = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int o = NB + 1; o >= 0; --o)
+#pragma unroll
+        for (int k = 0; k < KK; ++k)
+#pragma unroll
+            for (int h = 0; h < NB; ++h)
+                if (o - h >= 0 && o - h < 3)
+                    d = mfma<MOE_DT_BF16>(o ? bf[k][h] : b[k][0], o ? vf[k][o - h] : v[k][0], d);
+    return d;
+}
+
 // Adds 32 KK of the rank to M blocks of 16 rows; rows[m]: which rows of block
-// m have an adapter.  An adapter's B is loaded once for all the blocks.
-template <int DT, int M, int NF, int GB, int KK>
-__device__ __forceinline__ void expand_part(const AShape &s, const uint16_t *__restrict__ b,
+// m have an adapter.  An adapter's B is loaded once for all the blocks.  Returns
+// whether a product of this lane's rows is left out, not being finite: those
+// are added, and nothing else, by a second call (kAgain).
+template <int DT, int M, int NF, int GB, int KK, bool kAgain = false>
+__device__ __forceinline__ bool expand_part(const AShape &s, const uint16_t *__restrict__ b,
                                             const Row *row, const uint32_t *rows,
                                             const float *scale, const Low<KK> *low, int n0,
                                             v4f (*acc)[NF])
@@ -614,6 +673,7 @@ __device__ __forceinline__ void expand_part(const AShape &s, const uint16_t *__r
     for (int f = 0; f < NF; ++f)
         col[f] = (uint32_t)min(n0 + column_of(f, lane & 15), s.N - 1) * s.r;
     uint32_t todo[M], any = 0;
+    bool left_out = false;
 #pragma unroll
     for (int m = 0; m < M; ++m)
         any |= todo[m] = rows[m];
@@ -647,18 +707,18 @@ __device__ __forceinline__ void expand_part(const AShape &s, const uint16_t *__r
 #pragma unroll
         for (int q = 0; q < GB; ++q) {
             constexpr int NB = DT == MOE_DT_F16 ? 2 : 1; // bf16 values of one of B
-            uint4 bk[KK][NF][NB];
+            uint4 bk[NF][KK][NB];
 #pragma unroll
-            for (int k = 0; k < KK; ++k)
+            for (int f = 0; f < NF; ++f)
 #pragma unroll
-                for (int f = 0; f < NF; ++f) {
+                for (int k = 0; k < KK; ++k) {
                     const uint4 p = low[0].there[k] ? bq[q][k][f] : uint4{0, 0, 0, 0};
                     if constexpr (DT == MOE_DT_F16) {
                         float f8[8];
                         Elem<DT>::unpack(p, f8);
-                        cut8<NB>(f8, bk[k][f]);
+                        cut8<NB>(f8, bk[f][k]);
                     } else {
-                        bk[k][f][0] = p;
+                        bk[f][k][0] = p;
                     }
                 }
 #pragma unroll
@@ -668,23 +728,20 @@ __device__ __forceinline__ void expand_part(const AShape &s, const uint16_t *__r
                     continue;
 #pragma unroll
                 for (int f = 0; f < NF; ++f) {
-                    // the smallest products first
-                    v4f d = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int o = NB + 1; o >= 0; --o)
-#pragma unroll
-                        for (int k = 0; k < KK; ++k)
-#pragma unroll
-                            for (int h = 0; h < NB; ++h)
-                                if (o - h >= 0 && o - h < 3)
-                                    d = mfma<MOE_DT_BF16>(bk[k][f][h], low[m].v[k][o - h], d);
+                    v4f d = product<NB, KK>(bk[f], low[m].v);
+                    const bool finite =
+                        fabsf(d[0]) + fabsf(d[1]) + fabsf(d[2]) + fabsf(d[3]) < INFINITY;
+                    left_out |= take && !finite;
+                    if constexpr (kAgain)
+                        d = careful<NB, KK>(bk[f], low[m].v);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        acc[m][f][i] += take ? scale[m] * d[i] : 0.0f;
+                        acc[m][f][i] += take && finite != kAgain ? scale[m] * d[i] : 0.0f;
                 }
             }
         }
     }
+    return left_out;
 }
 
 // The whole term for M blocks of 16 rows.
@@ -706,13 +763,22 @@ __device__ __forceinline__ void expand(const AShape &s, const float *__restrict_
         sc[m] = scale_of(scale, row[m]);
     // 32 at a time: 64 do not fit the registers beside the tile's sums (8,191 x
     // 7,168 x 7,168 bf16 with rank 64 take 790 us so, 710 by 32)
+    bool left_out = false;
     for (int c = 0; c < s.r; c += 32) {
         Low<1> low[M];
 #pragma unroll
         for (int m = 0; m < M; ++m)
             low[m] = low_of<1>(s, v, row[m], c);
-        expand_part<DT, M, NF, GB, 1>(s, b, row, rows, sc, low, n0, acc);
+        left_out |= expand_part<DT, M, NF, GB, 1>(s, b, row, rows, sc, low, n0, acc);
     }
+    if (!__any(left_out))
+        return;
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+        for (int c = 0; c < s.r; c += 32) {
+            const Low<1> low = low_of<1>(s, v, row[m], c);
+            expand_part<DT, 1, NF, 1, 1, true>(s, b, row + m, rows + m, sc + m, &low, n0, acc + m);
+        }
 }
 
 // A lane's sums of 16 NF columns from n0 of row t, rounded and stored in
@@ -1118,11 +1184,17 @@ add_kernel(AShape s, int blocks, int parts, const void *base, const int32_t *__r
             load_base(min(n0 + 16 * NF, s.N - 8));
         }
         if (rows) {
-            expand_part<DT, 1, NF, GB, KK>(s, b, &row, &rows, &sc, &low, n0, &acc);
+            bool left_out =
+                expand_part<DT, 1, NF, GB, KK>(s, b, &row, &rows, &sc, &low, n0, &acc);
             for (int c = 32 * KK; c < s.r; c += 32 * KK) {
                 const Low<KK> more = low_of<KK>(s, v, row, c);
-                expand_part<DT, 1, NF, GB, KK>(s, b, &row, &rows, &sc, &more, n0, &acc);
+                left_out |= expand_part<DT, 1, NF, GB, KK>(s, b, &row, &rows, &sc, &more, n0, &acc);
             }
+            if (__any(left_out))
+                for (int c = 0; c < s.r; c += 32 * KK) {
+                    const Low<KK> more = low_of<KK>(s, v, row, c);
+                    expand_part<DT, 1, NF, 1, KK, true>(s, b, &row, &rows, &sc, &more, n0, &acc);
+                }
         }
         if (i < s.T)
             store_cols<DT, NF>(s, out, row.t, n0, acc);

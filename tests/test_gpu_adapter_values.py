@@ -74,3 +74,52 @@ def test_small_values_beside_large_ones(T, N, dt):
     for w, base in ((zero[0], None), (None, zero[1])):
         out = project(x, w, base, ids, a, b)
         assert torch.equal(out.cpu(), want), w is not None
+
+
+def same(got, want):
+    """Equal, infinities by sign and NaN as NaN."""
+    got, want = got.cpu().double(), want.double()
+    return bool(((got == want) | (got.isnan() & want.isnan())).all())
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("r", [16, 72])
+@pytest.mark.parametrize("T,N", SIZES)
+def test_infinities_and_nan_as_the_definition_has_them(T, N, r, dt):
+    """Whole numbers (every finite sum is exact, and below 2^8, so the outputs are too) with
+    infinities and NaN in B, in A and in x: finite times infinite, infinite times
+    infinite and 0 times infinite come out as in the definition, row by row."""
+    say("infinities", T, N, r, dt)
+    H, L = 512, 5
+    inf, nan = float("inf"), float("nan")
+    g = torch.Generator().manual_seed(T + r)
+    whole = lambda *shape: torch.randint(-1, 2, shape, generator=g).float()
+    x, w, a = torch.zeros(T, H), torch.zeros(N, H), whole(L, r, H)
+    b, base = whole(L, N, r), whole(T, N)
+    x[:, :8], w[:, 1:5] = whole(T, 8), whole(N, 4)
+    b[:, :, 8:] *= (torch.rand(L, N, r - 8, generator=g) < 0.1)
+    # adapter 0 finite; 1: one infinity in every third column; 2: two, of either sign; 3:
+    # an infinite row of A, times all of B; 4: all of B infinite, and a NaN
+    b[1, ::3, 5], b[2, ::2, r - 1], b[2, ::3, 3] = inf, -inf, inf
+    a[3, 2, 6], b[4] = inf, inf * b[4].sign().where(b[4] != 0, torch.ones(()))
+    b[4, 1, 0] = nan
+    ids = torch.randint(-1, L, (T,), generator=g)
+    ids[0] = 2
+    if T > 8:
+        x[5, 7], x[6, 6], x[7, 7] = inf, -inf, nan      # (columns that w does not use)
+        ids[5:8] = torch.tensor([0, 1, 0])
+    d = torch.zeros(T, N, dtype=torch.float64)
+    for l in range(L):
+        at = ids == l
+        v = x[at].double() @ a[l].double().t()
+        d[at] = v @ b[l].double().t()
+    x, w, a, b, base = (t.to(dt).to(DEV) for t in (x, w, a, b, base))
+    xw = x.cpu().double()
+    xw[:, 5:] = 0                                       # 0 times what x holds there
+    idd = ids.to(torch.int32).to(DEV)
+    # x W^T has 0 times infinity in rows 5 to 7, so they are compared with a given base
+    plain = torch.ones(T, dtype=torch.bool)
+    plain[5:8] = False
+    out = project(x, w, None, idd, a, b)
+    assert same(out[plain.to(DEV)], (xw @ w.cpu().double().t() + d)[plain])
+    assert same(project(x, None, base, idd, a, b), base.cpu().double() + d)

@@ -736,7 +736,8 @@ __device__ __forceinline__ bool expand_part(const AShape &s, const uint16_t *__r
                         d = careful<NB, KK>(bk[f], low[m].v);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        acc[m][f][i] += take && finite != kAgain ? scale[m] * d[i] : 0.0f;
+                        if (take && finite != kAgain) // (adding 0 would change a -0)
+                            acc[m][f][i] += scale[m] * d[i];
                 }
             }
         }

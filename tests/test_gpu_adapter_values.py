@@ -123,3 +123,21 @@ def test_infinities_and_nan_as_the_definition_has_them(T, N, r, dt):
     out = project(x, w, None, idd, a, b)
     assert same(out[plain.to(DEV)], (xw @ w.cpu().double().t() + d)[plain])
     assert same(project(x, None, base, idd, a, b), base.cpu().double() + d)
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("T", [2, 40, 100, 300])
+def test_rows_without_an_adapter_are_the_base_to_the_bit(T, dt):
+    """-0 and subnormals among them, whatever the adapters of their neighbours."""
+    say("base bits", T, dt)
+    H, N, L, r = 256, 136, 3, 16
+    g = torch.Generator().manual_seed(T)
+    rn = lambda *shape: torch.randn(*shape, generator=g).to(dt).to(DEV)
+    base = rn(T, N)
+    base[:, ::3], base[:, 1::7] = -0.0, torch.finfo(dt).smallest_normal / 4
+    ids = torch.randint(-1, L, (T,), generator=g).to(torch.int32)
+    ids[0], ids[1] = -1, 0
+    ids = ids.to(DEV)
+    out = project(rn(T, H), None, base, ids, rn(L, r, H), rn(L, N, r))
+    bits = lambda t: t[ids < 0].view(torch.int16)
+    assert torch.equal(bits(out), bits(base))

@@ -745,8 +745,8 @@ __device__ __forceinline__ bool expand_part(const AShape &s, const uint16_t *__r
     return left_out;
 }
 
-// The whole term for M blocks of 16 rows.
-template <int DT, int M, int NF, int GB>
+// The whole term for M blocks of 16 rows, 32 KK of the rank at a time.
+template <int DT, int M, int NF, int GB, int KK>
 __device__ __forceinline__ void expand(const AShape &s, const float *__restrict__ v,
                                        const uint16_t *__restrict__ b,
                                        const float *__restrict__ scale, const Row *row, int n0,
@@ -762,23 +762,22 @@ __device__ __forceinline__ void expand(const AShape &s, const float *__restrict_
 #pragma unroll
     for (int m = 0; m < M; ++m)
         sc[m] = scale_of(scale, row[m]);
-    // 32 at a time: 64 do not fit the registers beside the tile's sums (8,191 x
-    // 7,168 x 7,168 bf16 with rank 64 take 790 us so, 710 by 32)
     bool left_out = false;
-    for (int c = 0; c < s.r; c += 32) {
-        Low<1> low[M];
+    for (int c = 0; c < s.r; c += 32 * KK) {
+        Low<KK> low[M];
 #pragma unroll
         for (int m = 0; m < M; ++m)
-            low[m] = low_of<1>(s, v, row[m], c);
-        left_out |= expand_part<DT, M, NF, GB, 1>(s, b, row, rows, sc, low, n0, acc);
+            low[m] = low_of<KK>(s, v, row[m], c);
+        left_out |= expand_part<DT, M, NF, GB, KK>(s, b, row, rows, sc, low, n0, acc);
     }
     if (!__any(left_out))
         return;
+    // (what is left out is the products of the same 32 KK)
 #pragma unroll
     for (int m = 0; m < M; ++m)
-        for (int c = 0; c < s.r; c += 32) {
-            const Low<1> low = low_of<1>(s, v, row[m], c);
-            expand_part<DT, 1, NF, 1, 1, true>(s, b, row + m, rows + m, sc + m, &low, n0, acc + m);
+        for (int c = 0; c < s.r; c += 32 * KK) {
+            const Low<KK> low = low_of<KK>(s, v, row[m], c);
+            expand_part<DT, 1, NF, 1, KK, true>(s, b, row + m, rows + m, sc + m, &low, n0, acc + m);
         }
 }
 
@@ -1065,11 +1064,16 @@ __device__ __forceinline__ void project_tile(const AShape &s, const ProjectArgs 
         return;
     }
     static_assert(NF == 4 && MF % 4 == 0, "four blocks of rows at a time");
+    // 64 of the rank at a time (whole lines of B) where one workgroup has the CU's
+    // registers (512 mixed rows of 64 adapters of rank 64 120 us, by 32 128), else
+    // 32, which fit beside the sums (8,191 rows 710, by 64 790)
+    constexpr int kRank = NS == 4 ? 2 : 1;
 #pragma unroll
     for (int m = 0; m < MF; m += 4) {
         const int n = n0 + wn * NF * 16;
         __builtin_amdgcn_sched_barrier(0);
-        expand<DT, 4, NF, MF == 4 ? 2 : 1>(s, p.v, p.b, p.scale, row + m, n, acc + m);
+        expand<DT, 4, NF, MF == 4 ? 2 : 1, kRank>(s, p.v, p.b, p.scale, row + m, n,
+                                                  acc + m);
 #pragma unroll
         for (int q = m; q < m + 4; ++q)
             if (m0 + (wm * MF + q) * 16 + (lane & 15) < s.T)

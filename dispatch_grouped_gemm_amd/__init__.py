@@ -920,7 +920,7 @@ def moe_unpermute_backward(shape: MoeShape, dout, rows, topk_w, route_row, drows
                            stream=None):
     """moe_unpermute's gradients: drows[route_row[t, k]] = topk_w[t, k] dout[t] and
     dtopk_w[t, k] = <dout[t], rows[route_row[t, k]]> (0 for skipped slots).  drows or
-    dtopk_w may be None; rows may be None without dtopk_w."""
+    dtopk_w may be None; rows may be None without dtopk_w; drows may be rows itself."""
     code, dt, dev = _elem(dout, "dout")
     tok, row, slots, tk = _row_sizes(shape)
     if drows is None and dtopk_w is None:

@@ -145,12 +145,14 @@ unpermute_kernel(int T, int H, int K, long R, const void *__restrict__ rows,
 // for the weights' gradients (kDots) and their gradients written (kRows).  A
 // piece of every expert row is loaded before the first is used: loaded and used
 // in turn, 8,192 tokens of 2,560 bf16 values take 115 us instead of 93, the
-// weights' gradients alone 63 instead of 47.
+// weights' gradients alone 63 instead of 47.  A thread writes a piece of drows
+// after it has read the same piece of rows, and no other thread reads it: drows
+// may be rows itself.
 template <int DT, bool kRows, bool kDots, bool kWeights>
 __global__ void __launch_bounds__(kThreads)
 unpermute_backward_kernel(int T, int H, int K, long R, const void *__restrict__ dout,
-                          const void *__restrict__ rows, const float *__restrict__ w,
-                          const int32_t *__restrict__ route_row, void *__restrict__ drows,
+                          const void *rows, const float *__restrict__ w,
+                          const int32_t *__restrict__ route_row, void *drows,
                           float *__restrict__ dw)
 {
     constexpr int V = Elem<DT>::kVec;

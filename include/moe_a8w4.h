@@ -518,7 +518,8 @@ int moe_route_backward(const moe_shape *shape, int32_t dtype, const void *logits
  * rounded once (with bf16 rows moe_unpermute gives moe_combine's bits).
  * topk_w NULL means weights of 1.  moe_unpermute_backward writes drows or
  * dtopk_w or both (one may be NULL; rows is read only for dtopk_w).  Rows
- * that hold no route are neither read nor written.  Buffers do not overlap.
+ * that hold no route are neither read nor written.  Buffers do not overlap,
+ * but drows of moe_unpermute_backward may be rows itself (the rows are gone then).
  * x, rows, out and their gradients start on 16-byte boundaries.  T = 0 is a
  * no-op.
  */

@@ -115,10 +115,12 @@ class TileEntry(ctypes.Structure):
 
 
 class _Shape:
-    """What a shape object keeps for its calls (_kept) stays out of its copies."""
+    """What a shape object keeps for its calls is in a slot: it stays out of the object's
+    __dict__ (so vars(shape) is its sizes) and of its copies."""
+    __slots__ = ("_calls",)
 
     def __getstate__(self):
-        return {k: v for k, v in self.__dict__.items() if not k.startswith("_")}
+        return dict(self.__dict__)
 
 
 @dataclass(frozen=True)
@@ -825,20 +827,24 @@ def _at(t, name: str, shape: tuple, dtype, device) -> int:
 
 def _kept(shape, name: str, make):
     """make(shape), kept with the (immutable) shape object."""
-    got = shape.__dict__.get(name)
+    try:
+        calls = shape._calls
+    except AttributeError:
+        calls = {}
+        object.__setattr__(shape, "_calls", calls)
+    got = calls.get(name)
     if got is None:
-        got = make(shape)
-        object.__setattr__(shape, name, got)
+        got = calls[name] = make(shape)
     return got
 
 
 def _ref(shape):
-    return _kept(shape, "_c_ref", lambda s: ctypes.byref(s.c()))
+    return _kept(shape, "c_ref", lambda s: ctypes.byref(s.c()))
 
 
 def _row_sizes(shape: MoeShape):
     """(T, H), (row capacity, H), (T*K,) and (T, K), as alloc_dispatch sizes them."""
-    return _kept(shape, "_rows", lambda s: (
+    return _kept(shape, "rows", lambda s: (
         (s.T, s.H), (max(moe_row_capacity(s), 1), s.H), (max(s.T * s.K, 1),), (s.T, s.K)))
 
 

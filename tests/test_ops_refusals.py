@@ -154,3 +154,17 @@ def test_shapes_copy_after_use(lib):
     for v in (s, m):
         for w in (copy.deepcopy(v), pickle.loads(pickle.dumps(v))):
             assert w == v and hash(w) == hash(v)
+
+
+def test_shapes_keep_only_their_sizes_in_sight(lib):
+    """vars() of a shape that calls have used makes a shape again, and asdict() and replace()
+    do."""
+    import dataclasses
+    for v, n in ((moe.MoeShape(**V4), "T"), (moe.AdapterShape(**AD), "T")):
+        moe._ref(v)
+        if isinstance(v, moe.MoeShape):
+            moe._row_sizes(v)
+        assert type(v)(**vars(v)) == v and type(v)(**dataclasses.asdict(v)) == v
+        other = dataclasses.replace(v, T=v.T + 1)
+        assert moe._ref(other) is not moe._ref(v) and moe._ref(v) is moe._ref(v)
+        assert moe._ref(other)._obj.T == v.T + 1

@@ -880,7 +880,7 @@ def moe_route(shape: MoeShape, logits, topk_ids, topk_w, renormalize: bool = Tru
 def moe_route_backward(shape: MoeShape, logits, topk_ids, topk_w, dtopk_w, dlogits,
                        renormalize: bool = True, stream=None):
     """dlogits [T, E_total] from dtopk_w [T, K] and moe_route's ids and weights; logits
-    may be None when the weights were renormalised."""
+    may be None when the weights were renormalised; dlogits may be logits itself."""
     code, dt, dev = _elem(dlogits, "dlogits")
     te, tk = (shape.T, shape.E_total), (shape.T, shape.K)
     lp = None

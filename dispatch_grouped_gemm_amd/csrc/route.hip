@@ -375,11 +375,12 @@ route_f32_kernel(int T, int E, int K, bool renorm, const void *__restrict__ logi
     store_slots(t, K, lane, renorm, all, my_id, mine, ids, w);
 }
 
+// (dlogits may be logits itself: a lane writes the experts that it has read)
 template <int DT, int PER, bool kVec>
 __global__ void __launch_bounds__(kThreads)
-route_backward_kernel(int T, int E, int K, bool renorm, const void *__restrict__ logits,
+route_backward_kernel(int T, int E, int K, bool renorm, const void *logits,
                       const int32_t *__restrict__ ids, const float *__restrict__ w,
-                      const float *__restrict__ dw, void *__restrict__ dlogits)
+                      const float *__restrict__ dw, void *dlogits)
 {
     constexpr int V = Elem<DT>::kVec;
     const int lane = threadIdx.x & (kLanes - 1);

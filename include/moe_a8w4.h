@@ -498,7 +498,8 @@ int moe_route(const moe_shape *shape, int32_t dtype, const void *logits, int32_t
  * g_e the dtopk_w of the slot that chose e (0 for the rest), p_e the weight of
  * a chosen expert and 0 elsewhere (renormalize != 0; logits may then be NULL),
  * or the softmax over the eligible logits.  Slots whose id is outside
- * [0, E_total) are left out, whatever their weight and gradient hold.
+ * [0, E_total) are left out, whatever their weight and gradient hold.  dlogits
+ * may be logits itself; otherwise the buffers of both calls do not overlap.
  */
 int moe_route_backward(const moe_shape *shape, int32_t dtype, const void *logits,
                        int32_t renormalize, const int32_t *topk_ids, const float *topk_w,

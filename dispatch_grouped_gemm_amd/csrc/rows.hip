@@ -29,11 +29,18 @@ constexpr int kMaxK = 8;
 // a wavefront lies inside one token: its slots and weights are then read once
 // per wavefront (scalar loads) and skipped slots by scalar branches.
 //
-// kPair is for ranks that hold at most half of the experts, where most slots go
-// elsewhere and a thread's overhead counts: 4,095 tokens of 5,120 float32 values
-// with 23% of the slots here take 30 us to sum, 35 with single pieces.  With
-// every expert here single pieces keep more loads in flight: 8,192 tokens of
-// 7,168 bf16 values 148 us, in pairs 152; 4,096 of 5,120 float32 values 105, 109.
+// kPair is for ranks that hold few of the experts, where most slots go elsewhere
+// and a thread's overhead counts; with many here single pieces keep more loads
+// and stores in flight.  The sums take pairs up to half of the experts, the
+// copies up to a quarter (us from memory, six sets of buffers in turn; K 6, even
+// routing; single pieces, then pairs):
+//   experts here             1/8           1/4           1/2           all
+//   8,192 x 7,168 bf16
+//     unpermute              63.3  41.9    70.0  54.9    89.8  87.2    149   154
+//     permute                44.0  39.5    56.3  58.5    88.5  95.2    157   166
+//   4,096 x 5,120 float32
+//     unpermute                            49.0  39.0    63.7  62.5    106   109
+//     permute                              40.1  40.0    61.8  66.1    110   116
 struct Place {
     int t, p;
 };
@@ -222,15 +229,16 @@ unpermute_backward_kernel(int T, int H, int K, long R, const void *__restrict__ 
     }
 }
 
-// Calls f with whether threads take pairs of pieces, and the grid.
+// Calls f with whether threads take pairs of pieces, and the grid; `few`: pairs
+// are for ranks that hold 1 / few of the experts or less.
 template <typename F>
-void with_place(const moe_shape &s, int dtype, F f)
+void with_place(const moe_shape &s, int dtype, int few, F f)
 {
     const long pieces = s.H * (long)elem_bytes(dtype) / 16;
     const auto grid = [&](int P) {
         return (unsigned)((s.T * pieces / P + kThreads - 1) / kThreads);
     };
-    if (2l * s.E_local <= s.E_total && pieces % 128 == 0)
+    if ((long)few * s.E_local <= s.E_total && pieces % 128 == 0)
         f(std::true_type{}, grid(2));
     else
         f(std::false_type{}, grid(1));
@@ -242,7 +250,7 @@ hipError_t launch_permute(const moe_shape &s, int dtype, const void *x, const in
                           void *rows, hipStream_t st)
 {
     const long R = moe_row_capacity(&s);
-    with_place(s, dtype, [&](auto pair, unsigned grid) {
+    with_place(s, dtype, 4, [&](auto pair, unsigned grid) {
         constexpr bool kPair = decltype(pair)::value;
         // a copy: both 16-bit types alike
         const auto k = dtype == MOE_DT_F32 ? permute_kernel<MOE_DT_F32, kPair>
@@ -257,7 +265,7 @@ hipError_t launch_unpermute(const moe_shape &s, int dtype, const void *rows, con
 {
     const long R = moe_row_capacity(&s);
     with_elem(dtype, [&](auto dt) {
-        with_place(s, dtype, [&](auto pair, unsigned grid) {
+        with_place(s, dtype, 2, [&](auto pair, unsigned grid) {
             constexpr int DT = decltype(dt)::value;
             constexpr bool kPair = decltype(pair)::value;
             const auto k = w ? unpermute_kernel<DT, kPair, true> : unpermute_kernel<DT, kPair, false>;

@@ -36,12 +36,23 @@ struct AShape {
 };
 
 constexpr int kFewRows = 128;       // rows that few_kernel and shrink_few take, in any order
-// Rows of a given projection from which the order pays for its launch: 16
-// adapters of rank 64 at H = N = 7,168 take 25 us without it and 20 with it at
-// 64 rows, 28 and 20 at 128, 22 and 24 at 33; of rank 16 at 2,048, 12 and 14 at
-// 64 and 128.
-constexpr int kUnordered = 64;
 constexpr int kOrderKeys = 1 << 13; // adapters that the order counts in LDS
+
+// Whether the order of a given projection's rows pays for its launch: with it the
+// shrink and the add meet few adapters in 16 rows.  H = N, mixed rows, bf16, us
+// without and with it:
+//   rows, adapters, rank     33         48         64         96
+//   H 2,048  16  16        13.3 14.5  14.0 14.5  14.2 14.5  14.9 14.2
+//            64  16        15.3 17.1  15.9 16.5  15.9 16.4  16.7 15.9
+//            16  64        18.7 18.2  20.1 17.3  20.4 16.9  21.8 15.7
+//            64  64        21.7 22.8  24.0 25.8  24.6 24.3  26.6 22.6
+//   H 7,168  16  32        17.7 19.2  21.4 19.7  22.4 18.5  23.9 17.7
+//            16  64        23.6 23.1  25.1 21.0  25.6 20.6  27.6 19.9
+//            64  64        27.7 28.5  28.4 28.4  29.2 27.5  31.1 31.5
+bool order_pays(const AShape &s)
+{
+    return s.T > 64 || (s.T > 40 && (long)s.r * s.H >= 1 << 17);
+}
 
 // D(16x16) += A(16x32) B(32x16): lane l holds A's row / B's column l mod 16
 // at k = 8 (l div 16) .. + 7, and D's column l mod 16 at rows
@@ -1331,7 +1342,7 @@ hipError_t adapter_of_type(const moe_adapter_shape &sh, const void *x_, const vo
     auto *out = static_cast<uint16_t *>(out_);
     const OrderLayout ol = order_layout(sh, ws);
     const bool few_rows = w && s.T <= kFewRows;
-    const bool ordered = w || s.T > kUnordered;
+    const bool ordered = w || order_pays(s);
     const Row *order = ordered ? ol.out.order : nullptr;
     float *v = reinterpret_cast<float *>(ws + ol.bytes);
     const auto add = [&](auto nf, auto gb, auto given, int blocks, const void *from, int parts) {

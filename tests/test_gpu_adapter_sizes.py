@@ -1,4 +1,5 @@
-"""The adapters at sizes for every kernel of many rows: the shrinks of 16 x 16, 32 x 32 and
+"""The adapters at sizes for both forms of few rows of a given projection and for every
+kernel of many rows: the shrinks of 16 x 16, 32 x 32 and
 32 x 64 over many steps, the tiles of every kind over many steps (their rings refilled
 many times), ranks that take several turns, several adapters in every 16 rows.
 
@@ -16,6 +17,9 @@ BF, HF = torch.bfloat16, torch.float16
 
 SIZES = [
     # T, H, N, L, rank
+    (40, 1024, 72, 5, 128),                        # few rows; given projections in any order,
+    (41, 1024, 72, 5, 128),                        # and by adapter
+    (64, 2048, 392, 30, 64),
     (4111, 2304, 264, 13, 128),                    # shrink by 32 x 64; tiles in parts of H
     (4111, 1152, 392, 300, 40),                    # shrink by 32 x 32, most blocks not full
     (8191, 768, 520, 5, 24),                       # the same; two workgroups a CU

@@ -922,8 +922,7 @@ constexpr int kRowBytes = 128; // of a row's step
 
 struct ProjectArgs {
     const uint16_t *x, *w;
-    const int32_t *ids;
-    const Row *order;
+    const Row *order; // tiles are of ordered rows
     const uint16_t *b;
     const float *scale, *v;
     uint16_t *out;
@@ -953,8 +952,7 @@ __device__ __forceinline__ void project_tile(const AShape &s, const ProjectArgs 
         const int at = ((lane & 7) ^ ((row >> 1) & 7)) * 16;
         if ((wave * U + u) * 8 < BM) {
             const long i = min(m0 + row, (long)s.T - 1);
-            const int t = p.order ? p.order[i].t : (int)i;
-            voff[u] = (uint32_t)t * (uint32_t)(2 * s.H) + at;
+            voff[u] = (uint32_t)p.order[i].t * (uint32_t)(2 * s.H) + at;
             base[u] = reinterpret_cast<const uint8_t *>(p.x);
         } else {
             const int rw = row - BM;
@@ -1058,7 +1056,7 @@ __device__ __forceinline__ void project_tile(const AShape &s, const ProjectArgs 
     Row row[MF];
 #pragma unroll
     for (int m = 0; m < MF; ++m)
-        row[m] = row_at(s, p.order, p.ids, m0 + (wm * MF + m) * 16 + (lane & 15));
+        row[m] = row_at(s, p.order, nullptr, m0 + (wm * MF + m) * 16 + (lane & 15));
     if constexpr (kParts) {
 #pragma unroll
         for (int m = 0; m < MF; ++m) {
@@ -1216,6 +1214,9 @@ add_kernel(AShape s, int blocks, int parts, const void *base, const int32_t *__r
             store_cols<DT, NF>(s, out, row.t, n0, acc);
     }
 }
+
+// The numbers of parts below go by the 256 CUs of an MI355X and not by the device,
+// since the workspace's size goes by them and is asked for without one.
 
 // Workgroups of few_kernel for the parts of x W^T, one a CU: an eighth of the
 // CUs stays free for the shrink, which else starts when the first part ends
@@ -1407,7 +1408,7 @@ hipError_t adapter_of_type(const moe_adapter_shape &sh, const void *x_, const vo
         // 38.3 and 39.5
         return add(c4, c1, std::true_type{}, s.T > kFewRows ? 2 : 1, base, 0);
     float *parts = reinterpret_cast<float *>(ws + v_bytes(sh));
-    const ProjectArgs p{x, w, ids, order, b, scale, v, out, parts};
+    const ProjectArgs p{x, w, order, b, scale, v, out, parts};
     const int cus = device_cu_count();
     // 256 x 256 tiles from one a CU on: each value moved from the L2 enters twice
     // the products of 128 x 128 (4,096 x 4,096 x 4,096 130 against 151 us, 8,191 x

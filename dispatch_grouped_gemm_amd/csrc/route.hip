@@ -32,7 +32,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kLanes = 16; // of a token
-constexpr int kMaxK = 8;
 constexpr int kMaxPer = 64; // 16 lanes x 64: up to 1024 experts
 
 // Value of the lane N places on in the same row of 16.

@@ -141,3 +141,44 @@ def test_rows_without_an_adapter_are_the_base_to_the_bit(T, dt):
     out = project(rn(T, H), None, base, ids, rn(L, r, H), rn(L, N, r))
     bits = lambda t: t[ids < 0].view(torch.int16)
     assert torch.equal(bits(out), bits(base))
+
+
+@pytest.mark.parametrize("T,N", [(5, 72), (48, 1000), (300, 520), (1025, 264)])
+def test_base_in_place(T, N):
+    """out over base: a wavefront reads its next columns of base before it writes."""
+    say("base in place", T, N)
+    H, L, r = 512, 4, 40
+    g = torch.Generator().manual_seed(T)
+    rn = lambda *shape: torch.randn(*shape, generator=g).to(BF).to(DEV)
+    x, a, b, base = rn(T, H), rn(L, r, H), rn(L, N, r), rn(T, N)
+    ids = torch.randint(-1, L, (T,), generator=g).to(torch.int32).to(DEV)
+    want = project(x, None, base, ids, a, b)
+    s = moe.AdapterShape(T=T, H=H, N=N, L=L, rank=r)
+    moe.moe_adapter_project(s, x, None, ids, a, b, None, base, moe.alloc_adapter_workspace(s, DEV),
+                            base=base)
+    assert torch.equal(base, want)
+
+
+@pytest.mark.parametrize("weight", [True, False])
+@pytest.mark.parametrize("T,H,N", [(262000, 8192, 8),         # x ends just below 2^32 bytes
+                                   (20000, 128, 120000)])    # out and base past them
+def test_offsets_past_32_bits(T, H, N, weight):
+    """Whole numbers, so that every sum is exact; rows all over x and out."""
+    say("offsets", T, H, N, weight)
+    L, r = 3, 8
+    g = torch.Generator(device=DEV).manual_seed(T)
+    small = lambda *shape: torch.randint(-1, 2, shape, generator=g, device=DEV).to(BF)
+    x = torch.zeros(T, H, dtype=BF, device=DEV)
+    x[:, :32], x[:, -32:] = small(T, 32), small(T, 32)
+    w, base, a, b = small(N, H), None, small(L, r, H), small(L, N, r)
+    if not weight:
+        w, base = None, torch.empty(T, N, dtype=BF, device=DEV).random_(0, 9, generator=g)
+    ids = torch.randint(-1, L, (T,), generator=g, device=DEV).to(torch.int32)
+    out = project(x, w, base, ids, a, b)
+    at = torch.cat([torch.arange(0, T, T // 97), torch.tensor([T - 1])]).to(DEV)
+    xs, got = x[at].cpu().double(), out[at].cpu().double()
+    want = base[at].cpu().double() if w is None else xs @ w.cpu().double().t()
+    of = ids[at].cpu()
+    for l in range(L):
+        want[of == l] += (xs[of == l] @ a[l].cpu().double().t()) @ b[l].cpu().double().t()
+    assert torch.equal(got, want.to(BF).double())

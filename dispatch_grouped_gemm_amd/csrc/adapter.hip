@@ -1112,8 +1112,8 @@ project_large_kernel(AShape s, int tm, int tn, int whole, ProjectArgs p)
 }
 
 // Tiles of 128 x 128: with NS = 2 stages two workgroups a CU, with 4 one,
-// three steps ahead of memory, where there are no more tiles than CUs;
-// kParts: `splits` parts of H for fewer still, joined by the add launch.
+// three steps ahead of memory; kParts: `splits` parts of H, joined by the add
+// launch.  Which of them: at small_tiles below.
 template <int DT, int NS, bool kParts>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2)))
 project_small_kernel(AShape s, int tm, int tn, int splits, ProjectArgs p)
@@ -1243,21 +1243,40 @@ int few_splits(const moe_adapter_shape &s)
     return std::max(1, std::min({kFewGroups / tn, 6, s.H / 128}));
 }
 
-// Tiles of 128 x 128, and the parts of H that project_small_kernel makes of
-// few of them: two workgroups a CU, parts of at least four steps.  At 384 x
-// 7,168 x 7,168 (168 tiles) three parts take 86 us, one deep workgroup a CU 103;
-// at 512 rows (224 tiles) two parts' planes cost more than they give, and the
-// deep form takes 103, the two-stage form 129.
+// Tiles of 128 x 128 in one of three forms (us, whole calls, mixed or packed rows,
+// rank 32): parts of H, up to two workgroups a CU; whole, two workgroups a CU; or
+// whole, one deep workgroup a CU.
+//   rows, H, N (tiles)          parts  whole  deep
+//     300  1,024    520  (15)    20.4   23.0  27.7
+//   1,024  1,024  1,024  (64)    30.8   26.3  29.4
+//   1,024  2,048  1,024  (64)    35.3   36.4  40.3
+//     640  2,048  4,096 (160)    38.8   35.4  39.4
+//     640  4,096  4,096 (160)    48.4   55.5  61.1
+//     300  4,096  9,216 (216)    59.1   66.2  61.0
+//     640  4,480  4,096 (175)    53.7   55.7  61.1
+//   2,048  4,096  2,048 (256)    66.5   60.1  66.7
+//   2,048  7,168  2,048 (256)    89.9   94.7   100
+//     256  4,096 12,800 (200)    74.2   77.2  64.5
+//     256  7,168 12,800 (200)     107    128   100
+// What parts save grows with H, what their planes cost with the tiles: from 18 of
+// H a tile they win.  A weight that at most two tiles of rows share streams
+// best through deep rings, once its tiles fill two thirds of the CUs.
 long small_tiles(const moe_adapter_shape &s)
 {
     return (long)((s.T + 127) / 128) * ((s.N + 127) / 128);
 }
 
+bool small_deep(const moe_adapter_shape &s)
+{
+    return s.T <= 256 && s.H > 2048 && small_tiles(s) > 170 && small_tiles(s) <= 256;
+}
+
 int small_splits(const moe_adapter_shape &s)
 {
-    if (small_tiles(s) > 170)
+    const long n = small_tiles(s);
+    if (n > 256 || s.H < 18 * n || small_deep(s))
         return 1;
-    return (int)std::max(1l, std::min({512 / small_tiles(s), 8l, (long)s.H / 256}));
+    return (int)std::max(1l, std::min({512 / n, 8l, (long)s.H / 256}));
 }
 
 size_t parts_bytes(const moe_adapter_shape &s)
@@ -1427,10 +1446,10 @@ hipError_t adapter_of_type(const moe_adapter_shape &sh, const void *x_, const vo
         const int halves = 2 * left <= cus ? left : 0;
         project_large_kernel<DT>
             <<<tm * tn + halves, 512, 0, st>>>(s, tm, tn, tm * tn - halves, p);
-    } else if (sm * sn > cus) {
-        project_small_kernel<DT, 2, false><<<sm * sn, 256, 0, st>>>(s, sm, sn, 1, p);
-    } else {
+    } else if (small_deep(sh)) {
         project_small_kernel<DT, 4, false><<<sm * sn, 256, 0, st>>>(s, sm, sn, 1, p);
+    } else {
+        project_small_kernel<DT, 2, false><<<sm * sn, 256, 0, st>>>(s, sm, sn, 1, p);
     }
     return hipGetLastError();
 }

@@ -20,15 +20,17 @@ SIZES = [
     (40, 1024, 72, 5, 128),                        # few rows; given projections in any order,
     (41, 1024, 72, 5, 128),                        # and by adapter
     (64, 2048, 392, 30, 64),
+    (128, 4096, 2104, 9, 48),                      # few rows by 128 columns
     (4111, 2304, 264, 13, 128),                    # shrink by 32 x 64; tiles in parts of H
     (4111, 1152, 392, 300, 40),                    # shrink by 32 x 32, most blocks not full
     (8191, 768, 520, 5, 24),                       # the same; two workgroups a CU
     (8191, 1280, 264, 40, 64),                     # 32 x 64
     (9000, 640, 136, 21, 72),                      # 32 x 64, two walks of the order
-    (300, 2048, 520, 90, 136),                     # 16 x 16; parts
-    (700, 1152, 4352, 200, 256),                   # one deep workgroup a CU (204 tiles)
-    (520, 1664, 4480, 6, 72),                      # the same (175 tiles)
-    (1300, 1152, 4096, 30, 72),                    # two workgroups a CU (352 tiles)
+    (300, 2048, 520, 90, 136),                     # 16 x 16; eight parts
+    (520, 4224, 4480, 6, 72),                      # two parts of 175 tiles
+    (256, 2304, 11000, 60, 256),                   # one deep workgroup a CU (172 tiles)
+    (700, 1152, 4352, 200, 256),                   # two workgroups a CU (204 tiles)
+    (1300, 1152, 4096, 30, 72),                    # the same (352 tiles)
     (4111, 1152, 4504, 17, 72),                    # 256 x 256: 306 tiles, 50 as halves
     (4111, 896, 6104, 400, 16),                    # 408 tiles, none halved
 ]

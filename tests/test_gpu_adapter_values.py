@@ -9,10 +9,10 @@ from gpu_util import DEV, say
 pytestmark = pytest.mark.gpu
 BF, HF = torch.bfloat16, torch.float16
 
-# a size for each way through the projection on 256 CUs: 16, 32, 64 and 128 rows at most;
-# tiles in parts of H, one deep workgroup a CU, two, the largest tiles
-SIZES = [(1, 72), (16, 136), (40, 64), (64, 1000), (100, 264), (300, 520), (700, 4352), (1300, 4096),
-         (4111, 4104)]
+# rows, N and H for each way through the projection on 256 CUs: 16, 32, 64 and 128 rows
+# at most; tiles in parts of H, one deep workgroup a CU, two, the largest tiles
+SIZES = [(1, 72, 512), (16, 136, 512), (40, 64, 512), (64, 1000, 512), (100, 264, 512),
+         (300, 520, 512), (200, 11000, 2176), (1300, 4096, 512), (4111, 4104, 512)]
 
 
 def project(x, w, base, ids, a, b, scale=None):
@@ -26,13 +26,13 @@ def project(x, w, base, ids, a, b, scale=None):
 
 
 @pytest.mark.parametrize("dt", [BF, HF])
-@pytest.mark.parametrize("T,N", SIZES)
-def test_all_24_bits_of_v(T, N, dt):
+@pytest.mark.parametrize("T,N,H", SIZES)
+def test_all_24_bits_of_v(T, N, H, dt):
     """v0 = n, a whole number of 24 bits, and v1 = -n without its last 8: their sum, n mod 256,
     is left of them only if both products are exact.  Every sum is one of whole numbers
     below 2^24 (times a power of two that fits the type), so it is exact in float32."""
     say("24 bits", T, N, dt)
-    H, L, r = 512, 3, 16
+    L, r = 3, 16
     unit = 1.0 if dt is BF else 2.0 ** -12
     g = torch.Generator().manual_seed(T)
     n = torch.randint(1 << 23, 1 << 24, (T,), generator=g)
@@ -55,12 +55,12 @@ def test_all_24_bits_of_v(T, N, dt):
 
 
 @pytest.mark.parametrize("dt", [BF, HF])
-@pytest.mark.parametrize("T,N", SIZES)
-def test_small_values_beside_large_ones(T, N, dt):
+@pytest.mark.parametrize("T,N,H", SIZES)
+def test_small_values_beside_large_ones(T, N, H, dt):
     """A row of v holds 2^25, which B does not use, and k 2^-20, which it multiplies by 2^12:
     k 2^-8 (k of 8 bits) is exact in both types."""
     say("small beside large", T, N, dt)
-    H, L, r = 512, 2, 24
+    L, r = 2, 24
     g = torch.Generator().manual_seed(T)
     k = torch.randint(0, 256, (T,), generator=g)
     x = torch.zeros(T, H)
@@ -84,13 +84,13 @@ def same(got, want):
 
 @pytest.mark.parametrize("dt", [BF, HF])
 @pytest.mark.parametrize("r", [16, 72])
-@pytest.mark.parametrize("T,N", SIZES)
-def test_infinities_and_nan_as_the_definition_has_them(T, N, r, dt):
+@pytest.mark.parametrize("T,N,H", SIZES)
+def test_infinities_and_nan_as_the_definition_has_them(T, N, H, r, dt):
     """Whole numbers (every finite sum is exact, and below 2^8, so the outputs are too) with
     infinities and NaN in B, in A and in x: finite times infinite, infinite times
     infinite and 0 times infinite come out as in the definition, row by row."""
     say("infinities", T, N, r, dt)
-    H, L = 512, 5
+    L = 5
     inf, nan = float("inf"), float("nan")
     g = torch.Generator().manual_seed(T + r)
     whole = lambda *shape: torch.randint(-1, 2, shape, generator=g).float()

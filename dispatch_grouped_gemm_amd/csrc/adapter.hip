@@ -795,8 +795,8 @@ __device__ __forceinline__ void expand(const AShape &s, const float *__restrict_
 // A lane's sums of 16 NF columns from n0 of row t, rounded and stored in
 // pieces of 8 (N is a multiple of 8).  The stores leave the L2 first: with
 // ordinary ones the rows and weights that other workgroups read again leave
-// earlier (adding to 4,097 x 5,120 fp16 values 26.7 against 22.7 us, 8,191 x
-// 7,168 bf16 products 760 against 748).
+// earlier (whole calls: adding to 4,097 x 5,120 fp16 values 46 us, so 40; 8,191 x
+// 7,168 x 7,168 bf16 728, so 704).
 template <int DT, int NF>
 __device__ __forceinline__ void store_cols(const AShape &s, uint16_t *out, int t, int n0,
                                            const v4f *acc)
@@ -815,8 +815,8 @@ __device__ __forceinline__ void store_cols(const AShape &s, uint16_t *out, int t
 // The order of up to kFewRows rows, by one workgroup: a row's place is the
 // count of rows before it, by adapter and row, those without one last.  The
 // add then meets one or two adapters in 16 rows and reads B once: 128 rows at
-// 1,024 x 6,144 with 32 adapters of rank 64 take 25 us, in the caller's order 33;
-// at rank 16 both are alike.
+// 1,024 x 6,144 with 32 adapters of rank 64 take 31 us, in the caller's order 39,
+// of rank 16 18 and 20.
 __device__ __forceinline__ void order_few(const AShape &s, const int32_t *__restrict__ ids,
                                           Row *__restrict__ order, int32_t *key)
 {
@@ -1074,8 +1074,8 @@ __device__ __forceinline__ void project_tile(const AShape &s, const ProjectArgs 
     }
     static_assert(NF == 4 && MF % 4 == 0, "four blocks of rows at a time");
     // 64 of the rank at a time (whole lines of B) where one workgroup has the CU's
-    // registers (512 mixed rows of 64 adapters of rank 64 120 us, by 32 128), else
-    // 32, which fit beside the sums (8,191 rows 710, by 64 790)
+    // registers (512 x 7,168 x 7,168 with 64 adapters of rank 64 120 us, by 32 128),
+    // else 32, which fit beside the sums (8,191 rows 704, by 64 781)
     constexpr int kRank = NS == 4 ? 2 : 1;
 #pragma unroll
     for (int m = 0; m < MF; m += 4) {
@@ -1220,19 +1220,25 @@ add_kernel(AShape s, int blocks, int parts, const void *base, const int32_t *__r
 
 // Workgroups of few_kernel for the parts of x W^T, one a CU: an eighth of the
 // CUs stays free for the shrink, which else starts when the first part ends
-// (one row at 4,096 x 4,096 with an adapter of rank 64: 15 us, with 256 31;
-// 65 rows, rank 16: 21 and 28).
+// (one row at 4,096 x 4,096 with an adapter of rank 64: 18 us, with 256 35;
+// 65 rows, rank 16: 20 and 25).
 constexpr int kFewGroups = 224;
 
 // Columns of a workgroup of few_kernel.  Past 64 rows, 128 read x half as
-// often; 64 make fewer and larger parts of H, whose planes are written and read.
-// 128 win where 64 leave but two parts of a long H (128 rows, H = 7,168,
-// N = 5,120: 34 against 38 us, N = 10,240: 55 and 65), else 64 (H = 1,024,
-// N = 5,120: 18 against 23; H = 7,168, N = 2,304: 24 and 27).
+// often; 64 make more workgroups, so fewer and larger parts of H, whose planes
+// are written and read.  By 64 and by 128, us (32 adapters of rank 32):
+//   rows               72           100          128
+//   H 1,024  N 5,120                             18.4  22.7
+//   H 2,048  N 5,120   19.1  20.0   20.8  23.1   21.8  23.9
+//   H 4,096  N 1,024   16.8  18.6   17.0  19.2   17.8  20.3
+//            N 2,304   21.9  20.2   24.4  21.0   25.4  22.5
+//            N 4,608   22.6  23.6   27.9  23.8   26.1  27.2
+//   H 7,168  N 2,048   21.4  24.2                23.4  27.1
+//            N 2,304   27.2  25.1   30.0  25.8   30.1  27.3
+//            N 7,168   37.7  35.1   38.6  38.4   41.1  38.8
 int few_columns(const moe_adapter_shape &s)
 {
-    const int tn = (s.N + 63) / 64;
-    return s.T > 64 && s.H >= 4096 && 3 * tn > kFewGroups ? 128 : 64;
+    return s.T > 64 && s.H >= 4096 && s.N > 2048 ? 128 : 64;
 }
 
 // Parts of H of few_kernel: at most 6 (8 gain less than 1% in a short H and
@@ -1326,8 +1332,9 @@ hipError_t shrink_many(const AShape &s, const uint16_t *x, const int32_t *ids, c
     // as much of the rank per workgroup as there is (x is read once per
     // block of the rank), but a workgroup for every CU; x comes from memory
     // and gets the deeper ring (8,191 x 7,168 x 7,168 with rank 64, the whole call:
-    // by 64 717 us, by 32 732, by 16 769; 257 x 5,120 x 4,608 and 1,024 x 5,120 x
-    // 2,048, too few rows for every CU: by 64 54 and 58, by 16 and 32 48 and 54)
+    // by 64 704 us, by 32 710, by 16 733; 4,111 rows of rank 128 431, 437, 462;
+    // 257 x 5,120 x 4,608 and 1,024 x 5,120 x 2,048, too few rows for every CU: by
+    // 64 53 and 57, by 16 45 and 53)
     const int cus = device_cu_count(), t = up(s.T, 32);
     // blocks there may be (a workgroup takes several past 2^20)
     const auto blocks = [&](int rows) {
@@ -1423,16 +1430,16 @@ hipError_t adapter_of_type(const moe_adapter_shape &sh, const void *x_, const vo
         return e;
     if (!w)
         // two blocks of columns a wavefront read v once, where that leaves
-        // enough of them: 100 rows 18.7 us with two, 13.8 with one; 4,097 rows
-        // 38.3 and 39.5
+        // enough of them: 100 rows 18.5 us with two, 15.1 with one; 4,097 rows
+        // 40.3 and 43.0
         return add(c4, c1, std::true_type{}, s.T > kFewRows ? 2 : 1, base, 0);
     float *parts = reinterpret_cast<float *>(ws + v_bytes(sh));
     const ProjectArgs p{x, w, order, b, scale, v, out, parts};
     const int cus = device_cu_count();
     // 256 x 256 tiles from one a CU on: each value moved from the L2 enters twice
-    // the products of 128 x 128 (4,096 x 4,096 x 4,096 130 against 151 us, 8,191 x
-    // 7,168 x 7,168 714 against 811); the halves: 711 against 739 there, 231 against
-    // 283 at 4,352 x 5,120 x 5,120
+    // the products of 128 x 128 (4,096 x 4,096 x 4,096 141 against 167 us, 8,191 x
+    // 7,168 x 7,168 704 against 886); without the halves 768 there, and 278 where
+    // with them 251 at 4,352 x 5,120 x 5,120
     const int tm = up(s.T, 256), tn = up(s.N, 256), left = tm * tn % cus;
     const int sm = up(s.T, 128), sn = up(s.N, 128), splits = small_splits(sh);
     if (splits > 1) {

@@ -717,6 +717,8 @@ __device__ __forceinline__ bool expand_part(const AShape &s, const uint16_t *__r
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int q = 0; q < GB; ++q) {
+            if (q >= __builtin_amdgcn_readfirstlane(n))
+                break;
             constexpr int NB = DT == MOE_DT_F16 ? 2 : 1; // bf16 values of one of B
             uint4 bk[NF][KK][NB];
 #pragma unroll
@@ -734,7 +736,7 @@ __device__ __forceinline__ bool expand_part(const AShape &s, const uint16_t *__r
                 }
 #pragma unroll
             for (int m = 0; m < M; ++m) {
-                const bool take = row[m].id == g[q] && q < n;
+                const bool take = row[m].id == g[q];
                 if (M > 1 && !__any(take))
                     continue;
 #pragma unroll
@@ -1264,9 +1266,14 @@ int few_splits(const moe_adapter_shape &s)
 //   2,048  7,168  2,048 (256)    89.9   94.7   100
 //     256  4,096 12,800 (200)    74.2   77.2  64.5
 //     256  7,168 12,800 (200)     107    128   100
+//     512  5,120  6,144 (192)    60.4   68.0  71.2
+//     512  5,120  7,168 (224)    79.3   82.3  72.0
+//     512  7,168  7,168 (224)     101    119  96.7
+//   1,024  7,168  3,584 (224)    83.6   87.5  94.5
 // What parts save grows with H, what their planes cost with the tiles: from 18 of
-// H a tile they win.  A weight that at most two tiles of rows share streams
-// best through deep rings, once its tiles fill two thirds of the CUs.
+// H a tile they win.  A weight that few tiles of rows share streams best through
+// deep rings, once its tiles fill two thirds of the CUs (two tiles of rows) or
+// three quarters (four, in a long H).
 long small_tiles(const moe_adapter_shape &s)
 {
     return (long)((s.T + 127) / 128) * ((s.N + 127) / 128);
@@ -1274,7 +1281,9 @@ long small_tiles(const moe_adapter_shape &s)
 
 bool small_deep(const moe_adapter_shape &s)
 {
-    return s.T <= 256 && s.H > 2048 && small_tiles(s) > 170 && small_tiles(s) <= 256;
+    const long n = small_tiles(s);
+    return n <= 256 && ((s.T <= 256 && s.H > 2048 && n > 170) ||
+                        (s.T <= 512 && s.H > 4096 && n > 192));
 }
 
 int small_splits(const moe_adapter_shape &s)
@@ -1387,7 +1396,6 @@ hipError_t adapter_of_type(const moe_adapter_shape &sh, const void *x_, const vo
     const std::integral_constant<int, 1> c1;
     const std::integral_constant<int, 2> c2;
     const std::integral_constant<int, 4> c4;
-    const std::integral_constant<int, 8> c8;
     hipError_t e;
     if (few_rows) {
         float *parts = reinterpret_cast<float *>(ws + v_bytes(sh));
@@ -1415,8 +1423,9 @@ hipError_t adapter_of_type(const moe_adapter_shape &sh, const void *x_, const vo
             few(Stream<128, 128, 2, 2, 4, 5, 128>{}, FewStream8{});
         if ((e = hipGetLastError()) != hipSuccess)
             return e;
-        // few rows: many short wavefronts
-        return add(c2, c8, std::false_type{}, 1, parts, splits);
+        // few rows: many short wavefronts, four adapters' B in flight (128 fp16 rows
+        // of 7,168 x 7,168 with 64 adapters of rank 64 72 us, eight 79)
+        return add(c2, c4, std::false_type{}, 1, parts, splits);
     }
     if (!ordered) {
         shrink_few_kernel<DT>

@@ -28,7 +28,8 @@ SIZES = [
     (9000, 640, 136, 21, 72),                      # 32 x 64, two walks of the order
     (300, 2048, 520, 90, 136),                     # 16 x 16; eight parts
     (520, 4224, 4480, 6, 72),                      # two parts of 175 tiles
-    (256, 2304, 11000, 60, 256),                   # one deep workgroup a CU (172 tiles)
+    (400, 4224, 6152, 11, 40),                     # one deep workgroup a CU (196 tiles)
+    (256, 2304, 11000, 60, 256),                   # the same (172 tiles)
     (700, 1152, 4352, 200, 256),                   # two workgroups a CU (204 tiles)
     (1300, 1152, 4096, 30, 72),                    # the same (352 tiles)
     (4111, 1152, 4504, 17, 72),                    # 256 x 256: 306 tiles, 50 as halves

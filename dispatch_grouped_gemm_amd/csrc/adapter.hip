@@ -154,7 +154,8 @@ __device__ __forceinline__ int xcd_run(int b, int n)
 // a histogram (in LDS, or in the workspace past kOrderKeys adapters), its
 // scan, and a claim of a place per row.  A wavefront whose rows share an
 // adapter claims with one atomic.  Bound by its chain of loads and atomics:
-// 8,191 rows of 16 adapters 8.3 us, 4,097 of 96 5.8.
+// 8,191 rows of 16 adapters 10 us, 4,097 of 96 7; past 8,192 rows each claims
+// twice, 65,536 take 50 to 54.
 // ---------------------------------------------------------------------------
 constexpr int kOrderThreads = 1024, kOrderBatch = 8;
 
@@ -528,8 +529,8 @@ shrink_few_kernel(AShape s, const uint16_t *__restrict__ x, const int32_t *__res
     shrink_few<DT, FewStream>(s, x, ids, a, v, blockIdx.x, gridDim.x, lds);
 }
 
-// Shrink, many rows, ordered (8,191 rows of 7,168 bf16 values by rank 64: 31 us,
-// 130 MB read at 4.2 TB/s): workgroup (a block of up to BM places of one
+// Shrink, many rows, ordered (8,191 rows of 7,168 bf16 values by rank 64: 40 us,
+// 130 MB read at 3.2 TB/s): workgroup (a block of up to BM places of one
 // adapter, BN of the rank).
 template <int DT, int BM, int BN, int WM, int NX, int NR>
 __global__ void __launch_bounds__((Stream<BM, BN, WM, 1, NX, NR, 256, false>::kThreads))
@@ -843,8 +844,8 @@ __device__ __forceinline__ void order_few(const AShape &s, const int32_t *__rest
 // Splitting H gives every CU work without more copies of x than columns ask
 // for, and the adapters' chain of loads does not stand at the end of W's.
 // order is null for 16 rows, whose add is one block in any order.
-// Bound by reading W and A: 1 x 5,120 by 4,608 takes 10 us (4.7 TB/s), 128 x
-// 7,168 by 7,168 with 64 adapters of rank 32 31 us (145 MB, 4.7 TB/s); a step
+// Bound by reading W and A: 1 x 5,120 by 4,608 takes 12 us (4.0 TB/s), 128 x
+// 7,168 by 7,168 with 64 adapters of rank 32 33 us (145 MB, 4.5 TB/s); a step
 // of the 128-row tile multiplies in a fifth of that time.
 // ---------------------------------------------------------------------------
 template <int DT, typename S, typename F>
@@ -906,8 +907,8 @@ few_kernel(AShape s, int tn, int splits, const uint16_t *__restrict__ x,
 // the loads of the step after it, into the stage that all wavefronts have
 // just finished reading: one barrier a step, and a step's time for its loads.
 // Bound by the matrix instructions and what of the loads they do not cover: at
-// 8,191 x 7,168 x 7,168 bf16 they hold the matrix cores for two thirds of 700 us
-// (1.2 PFLOP/s with the adapters' term; 896 tiles are 3.5 rounds of 256 CUs).
+// 8,191 x 7,168 x 7,168 bf16 they hold the matrix cores for two thirds of 670 to
+// 727 us (1.2 PFLOP/s with the adapters' term; 896 tiles are 3.5 rounds of 256 CUs).
 // ---------------------------------------------------------------------------
 
 // Tile q of tm x tn: down 8 row tiles before the next column tile, so the
@@ -1133,7 +1134,8 @@ project_small_kernel(AShape s, int tm, int tn, int splits, ProjectArgs p)
 // ---------------------------------------------------------------------------
 // Add: out = base + the adapters' term, base a given projection, or (kParts)
 // the sum of `parts` float32 planes.  Bound by reading the base or the planes
-// and B, and writing out: 4,097 x 5,120 fp16 values 19 us (84 MB, 4.4 TB/s).  A
+// and B, and writing out: 4,097 x 5,120 fp16 values 26 us (84 MB, 3.2 TB/s; the
+// parts of v and of an fp16 B take the rest).  A
 // wavefront takes 16 places and `blocks` blocks of 16 NF columns: their v is
 // read once for all of them, up to a rank of 32 KK.
 // ---------------------------------------------------------------------------

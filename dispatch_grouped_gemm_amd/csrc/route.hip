@@ -19,11 +19,13 @@
 // then takes four lane rotations inside a row of the wavefront, and four
 // tokens share every instruction.
 //
-// Measured at 65,536 tokens of 384 experts, 6 chosen, the softmax over all:
-// bf16 20 us forward (50 MB read; instructions bound it: one expert of the six
-// takes 14) and 20 backward (100 MB read and written at 5.0 TB/s), float32 26
-// and 31 (6.4 TB/s); renormalized 17 and 10, 24 and 16.  Few tokens are bound by
-// launch latency: 128 take 3.7 us, 8,192 in float32 7.9 and 5.1.
+// Measured at 65,536 tokens of 384 experts, 6 chosen, the softmax over all, from
+// memory (four sets of inputs in turn): bf16 22 us forward (50 MB read;
+// instructions bound it) and 22 backward (100 MB read and written at 4.5 TB/s),
+// float32 32 and 33 (6.1 TB/s); renormalized 20 and 15, 33 and 18.  Of 512 experts
+// 23 and 18; of 1,024, 8 chosen, 42 and 31 (from 513 on a lane holds 64 logits).
+// Few tokens are bound by launch latency: 128 take 3.9 us, 8,192 in float32 7.8
+// and 5.1.
 #include "elem.hpp"
 
 namespace moe {
@@ -240,8 +242,9 @@ __device__ __forceinline__ void keep(uint32_t (&top)[3], uint32_t key)
 // maximum finds the winner and settles ties.  A lane keeps its three largest
 // keys that are still to be chosen (three instructions a key, once), so that
 // a round is one maximum over the 16 lanes; a lane that has given all three
-// looks through its keys again, below the last winner.  With a maximum over
-// every key in each round 6 of 384 bf16 experts took 25 us, float32 33.
+// looks through its keys again, below the last winner.  (65,536 tokens, inputs in
+// the cache: with a maximum over every key in each round 6 of 384 bf16 experts
+// took 25 us, so 20; float32 33 and 26.)
 template <int DT, int PER, bool kVec>
 __global__ void __launch_bounds__(kThreads)
 route_kernel(int T, int E, int K, bool renorm, const void *__restrict__ logits,
@@ -405,8 +408,8 @@ route_backward_kernel(int T, int E, int K, bool renorm, const void *logits,
     // the token's experts in LDS, zeroed, then written by the slots; slots of
     // the same expert all write their sum.  A wavefront's LDS operations run
     // in order, and no other touches its tokens.  (Finding each slot's register
-    // by comparisons took 23 us where this takes 10: 65,536 x 384 bf16,
-    // renormalized.)
+    // by comparisons took 23 us where this takes 10: 65,536 x 384 bf16 in the
+    // cache, renormalized.)
     __shared__ __align__(16) float room[kThreads / kLanes][kLanes * PER];
     float *mine = room[threadIdx.x / kLanes];
 #pragma unroll

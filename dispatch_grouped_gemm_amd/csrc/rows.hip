@@ -11,10 +11,10 @@
 // Sums are float32, k ascending, rounded once.
 //
 // Bound by memory, HBM bytes those of the formulas (within 2%).  8,192 tokens of
-// 7,168 bf16 values and 6 experts each: permute 132 us (822 MB, 6.2 TB/s), its
-// gradient 148 (5.6), unpermute 147 (5.6), its gradients 311 (1.53 GB, 4.9);
-// a large copy reaches 5.1, writing alone 6.8.  128 tokens take 2.4 to 3.5 us,
-// a launch.
+// 7,168 bf16 values and 6 experts each, from memory (three sets in turn): permute
+// 156 us (822 MB, 5.3 TB/s), its gradient 150 (5.5), unpermute 150 (5.5), its
+// gradients 314 (1.53 GB, 4.9); a large copy reaches 5.1.  128 tokens take 2.7 to
+// 3.4 us, a launch.
 #include "elem.hpp"
 
 namespace moe {
@@ -61,8 +61,8 @@ __device__ __forceinline__ Place place_of(int T, int pieces)
 // The stores leave the L2 first: what these kernels write is large and read
 // by another kernel, which would else find its own reads behind the lines
 // still to be written (permute and its gradient, one after the other at 8,192
-// tokens of 7,168 bf16 values and 6 experts each: 312 us, with ordinary
-// stores 362; unpermute and its gradients 465, and 485).
+// tokens of 7,168 bf16 values and 6 experts each: 304 us, with ordinary
+// stores 339; unpermute and its gradients 460, and 476).
 __device__ __forceinline__ void store_piece(void *base, size_t piece, const uint4 &q)
 {
     store_once(static_cast<uint4 *>(base) + piece, q);
@@ -151,8 +151,8 @@ unpermute_kernel(int T, int H, int K, long R, const void *__restrict__ rows,
 // A workgroup takes one token: its dout row read once, its expert rows read
 // for the weights' gradients (kDots) and their gradients written (kRows).  A
 // piece of every expert row is loaded before the first is used: loaded and used
-// in turn, 8,192 tokens of 2,560 bf16 values take 115 us instead of 93, the
-// weights' gradients alone 63 instead of 47.  A thread writes a piece of drows
+// in turn, 8,192 tokens of 2,560 bf16 values take 126 us instead of 114, the
+// weights' gradients alone 71 instead of 55.  A thread writes a piece of drows
 // after it has read the same piece of rows, and no other thread reads it: drows
 // may be rows itself.
 template <int DT, bool kRows, bool kDots, bool kWeights>

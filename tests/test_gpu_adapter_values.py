@@ -182,3 +182,27 @@ def test_offsets_past_32_bits(T, H, N, weight):
     for l in range(L):
         want[of == l] += (xs[of == l] @ a[l].cpu().double().t()) @ b[l].cpu().double().t()
     assert torch.equal(got, want.to(BF).double())
+
+
+@pytest.mark.parametrize("T,H,N", [(1, 2048, 1024), (100, 1024, 2048), (600, 1024, 1024)])
+def test_two_calls_at_once(T, H, N):
+    """Two streams, a workspace each, shared weights: the bits of one call after the other."""
+    say("two at once", T, H, N)
+    L, r = 6, 32
+    g = torch.Generator().manual_seed(T)
+    rn = lambda *shape: torch.randn(*shape, generator=g).to(BF).to(DEV)
+    w, a, b = rn(N, H), rn(L, r, H), rn(L, N, r)
+    s = moe.AdapterShape(T=T, H=H, N=N, L=L, rank=r)
+    calls = []
+    for _ in range(2):
+        ids = torch.randint(-1, L, (T,), generator=g).to(torch.int32).to(DEV)
+        calls.append((rn(T, H), ids, torch.empty(T, N, dtype=BF, device=DEV),
+                      moe.alloc_adapter_workspace(s, DEV), torch.cuda.Stream()))
+    want = [project(x, w, None, ids, a, b) for x, ids, _, _, _ in calls]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for x, ids, out, ws, st in calls:
+            moe.moe_adapter_project(s, x, w, ids, a, b, None, out, ws, stream=st)
+    torch.cuda.synchronize()
+    for (_, _, out, _, _), v in zip(calls, want):
+        assert torch.equal(out, v)

@@ -20,6 +20,10 @@ projection with low-rank adapters; gradients where a training step needs them):
     moe_route, moe_route_backward, moe_permute, moe_permute_backward,
     moe_unpermute, moe_unpermute_backward, moe_adapter_check,
     moe_adapter_workspace_size, moe_adapter_project
+beside the layer (the dense feed-forward block of a shared expert, the residual joint
+with the norms after and before a block; both with gradients):
+    moe_ffn_check, moe_ffn_workspace_size, moe_ffn_forward, moe_ffn_backward,
+    moe_norm_check, moe_norm_workspace_size, moe_norm_forward, moe_norm_backward
 """
 
 from __future__ import annotations
@@ -46,6 +50,9 @@ __all__ = [
     "moe_route", "moe_route_backward", "moe_permute", "moe_permute_backward",
     "moe_unpermute", "moe_unpermute_backward", "AdapterShape", "moe_adapter_check",
     "moe_adapter_workspace_size", "moe_adapter_project", "alloc_adapter_workspace",
+    "FfnShape", "moe_ffn_check", "moe_ffn_workspace_size", "alloc_ffn_workspace",
+    "moe_ffn_forward", "moe_ffn_backward", "NormShape", "moe_norm_check",
+    "moe_norm_workspace_size", "alloc_norm_workspace", "moe_norm_forward", "moe_norm_backward",
     "alloc_dispatch", "alloc_workspace", "COMPACT", "FIXED_SLOT", "Y_BF16", "Y_FP8", "Y_AUTO",
 ]
 
@@ -72,7 +79,10 @@ EXPORTED = ["moe_check_shape", "moe_row_capacity", "moe_dispatch_workspace_size"
             "moe_packed_scales_bytes", "moe_gemm1_swiglu_packed", "moe_gemm2_packed",
             "moe_route", "moe_route_backward", "moe_permute", "moe_permute_backward",
             "moe_unpermute", "moe_unpermute_backward", "moe_adapter_check",
-            "moe_adapter_workspace_size", "moe_adapter_project", "moe_strerror"]
+            "moe_adapter_workspace_size", "moe_adapter_project",
+            "moe_ffn_check", "moe_ffn_workspace_size", "moe_ffn_forward", "moe_ffn_backward",
+            "moe_norm_check", "moe_norm_workspace_size", "moe_norm_forward",
+            "moe_norm_backward", "moe_strerror"]
 
 
 class MoeError(RuntimeError):
@@ -103,6 +113,16 @@ class _CForwardArgs(ctypes.Structure):
 
 class _CAdapterShape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("T", "H", "N", "L", "rank")]
+
+
+class _CFfnShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "H", "I")] + [
+        (n, ctypes.c_float) for n in ("gate_limit", "up_limit")]
+
+
+class _CNormShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "H")] + [
+        (n, ctypes.c_float) for n in ("eps", "skip_scale", "block_scale")]
 
 
 class TileEntry(ctypes.Structure):
@@ -161,6 +181,32 @@ class AdapterShape(_Shape):
 
     def c(self) -> _CAdapterShape:
         return _CAdapterShape(self.T, self.H, self.N, self.L, self.rank)
+
+
+@dataclass(frozen=True)
+class FfnShape(_Shape):
+    """Sizes of moe_ffn_forward and moe_ffn_backward: T rows of H values, I inside."""
+    T: int
+    H: int
+    I: int
+    gate_limit: float = 10.0
+    up_limit: float = 10.0
+
+    def c(self) -> _CFfnShape:
+        return _CFfnShape(self.T, self.H, self.I, self.gate_limit, self.up_limit)
+
+
+@dataclass(frozen=True)
+class NormShape(_Shape):
+    """Sizes and factors of moe_norm_forward and moe_norm_backward: T rows of H values."""
+    T: int
+    H: int
+    eps: float = 1e-6
+    skip_scale: float = 1.0
+    block_scale: float = 1.0
+
+    def c(self) -> _CNormShape:
+        return _CNormShape(self.T, self.H, self.eps, self.skip_scale, self.block_scale)
 
 
 _lib = None
@@ -253,6 +299,21 @@ def lib() -> ctypes.CDLL:
             getattr(h, n).restype = ctypes.c_int
         h.moe_adapter_workspace_size.argtypes = [A]
         h.moe_adapter_workspace_size.restype = ctypes.c_size_t
+        F, N = ctypes.POINTER(_CFfnShape), ctypes.POINTER(_CNormShape)
+        size = ctypes.c_size_t
+        h.moe_ffn_check.argtypes = [F]
+        h.moe_ffn_workspace_size.argtypes = [F, i32]
+        h.moe_ffn_forward.argtypes = [F, i32, P, P, P, P, P, P, P, P, size, P]
+        h.moe_ffn_backward.argtypes = [F, i32, P, P, P, P, P, P, P, P, P, P, i32, i32, P, size, P]
+        h.moe_norm_check.argtypes = [N]
+        h.moe_norm_workspace_size.argtypes = [N]
+        h.moe_norm_forward.argtypes = [N, i32, P, P, P, P, P, P, P, P, P, P]
+        h.moe_norm_backward.argtypes = [N, i32, P, P, P, P, P, P, P, P, P, P, P, P, P, size, P]
+        for n in ("moe_ffn_check", "moe_ffn_forward", "moe_ffn_backward", "moe_norm_check",
+                  "moe_norm_forward", "moe_norm_backward"):
+            getattr(h, n).restype = ctypes.c_int
+        for n in ("moe_ffn_workspace_size", "moe_norm_workspace_size"):
+            getattr(h, n).restype = size
         h.moe_strerror.argtypes = [ctypes.c_int]
         h.moe_strerror.restype = ctypes.c_char_p
         _lib = h
@@ -972,3 +1033,136 @@ def moe_adapter_project(shape: AdapterShape, x, w, adapter_ids, a, b, scale, out
             None if scale is None else _at(scale, "scale", (L,), torch.float32, dev),
             _at(out, "out", (T, N), dt, dev),
             _ptr(workspace, "workspace", None, {torch.uint8}, dev), workspace.numel())
+
+
+# ---- the dense feed-forward block, the residual joint ------------------------------
+
+
+def _given(t, name: str, shape: tuple, dtype, device):
+    """_at, or NULL for None."""
+    return None if t is None else _at(t, name, shape, dtype, device)
+
+
+def _mx_pair(rows, scale, name: str, shape: tuple, device):
+    """MX FP8 rows: e4m3 codes [T, N] and exponent bytes [T, N/32]."""
+    return (_ptr(rows, name, shape, _fp8(), device),
+            _ptr(scale, name + "_scale", (shape[0], shape[1] // 32), _e8m0(name), device))
+
+
+def moe_ffn_check(shape: FfnShape) -> int:
+    return lib().moe_ffn_check(_ref(shape))
+
+
+def moe_ffn_workspace_size(shape: FfnShape, backward: bool = False) -> int:
+    return int(lib().moe_ffn_workspace_size(_ref(shape), 1 if backward else 0))
+
+
+def alloc_ffn_workspace(shape: FfnShape, device, backward: bool = False) -> torch.Tensor:
+    """A workspace of moe_ffn_forward, or (backward) of both calls."""
+    return torch.empty(max(moe_ffn_workspace_size(shape, backward), 256), dtype=torch.uint8,
+                       device=device)
+
+
+def moe_ffn_forward(shape: FfnShape, x, w13, w2, out, workspace, base=None, gate_up=None,
+                    gate_up_scale=None, stream=None):
+    """out = (silu(min(g, gate_limit)) clamp(u, up_limit)) W2^T + base, g | u = x W13^T:
+    x and out [T, H], w13 [2I, H] (gate rows, then up rows), w2 [H, I], bf16 or fp16;
+    base [T, H] or None, may be out.  gate_up keeps g | u [T, 2I] for moe_ffn_backward,
+    in x's type, or as MX FP8 codes with gate_up_scale [T, 2I/32]."""
+    code, dt, dev = _elem(x, "x", 1)
+    T, H, I = shape.T, shape.H, shape.I
+    if gate_up_scale is not None:
+        kept = _mx_pair(gate_up, gate_up_scale, "gate_up", (T, 2 * I), dev)
+    else:
+        kept = _given(gate_up, "gate_up", (T, 2 * I), dt, dev), None
+    _launch("moe_ffn_forward", dev, stream, _ref(shape), code, _at(x, "x", (T, H), dt, dev),
+            _at(w13, "w13", (2 * I, H), dt, dev), _at(w2, "w2", (H, I), dt, dev),
+            _given(base, "base", (T, H), dt, dev), *kept, _at(out, "out", (T, H), dt, dev),
+            _ptr(workspace, "workspace", None, {torch.uint8}, dev), workspace.numel())
+
+
+def moe_ffn_backward(shape: FfnShape, dout, x, w13, w2, gate_up, dx, dw13, dw2, workspace,
+                     gate_up_scale=None, x_scale=None, accumulate: bool = False, stream=None):
+    """moe_ffn_forward's gradients dx [T, H], dw13 [2I, H] and dw2 [H, I] (each may be
+    None) from dout [T, H] and the kept gate_up.  x may be MX FP8 codes with x_scale
+    [T, H/32] (and None without dw13).  dw13 and dw2 are of dout's type or float32;
+    accumulate adds to what they hold."""
+    code, dt, dev = _elem(dout, "dout", 1)
+    T, H, I = shape.T, shape.H, shape.I
+    if dx is None and dw13 is None and dw2 is None:
+        raise ValueError("moe_ffn_backward: give dx, dw13 or dw2")
+    dw_dt = next((t.dtype for t in (dw13, dw2) if isinstance(t, torch.Tensor)), dt)
+    if dw_dt not in (dt, torch.float32):
+        raise TypeError("dw13 and dw2 must be %s or float32" % dt)
+    if x_scale is not None:
+        rows = _mx_pair(x, x_scale, "x", (T, H), dev)
+    elif x is None and dw13 is not None:
+        raise ValueError("x is required")
+    else:
+        rows = _given(x, "x", (T, H), dt, dev), None
+    if gate_up_scale is not None:
+        kept = _mx_pair(gate_up, gate_up_scale, "gate_up", (T, 2 * I), dev)
+    else:
+        kept = _at(gate_up, "gate_up", (T, 2 * I), dt, dev), None
+    _launch("moe_ffn_backward", dev, stream, _ref(shape), code,
+            _at(dout, "dout", (T, H), dt, dev), *rows,
+            _at(w13, "w13", (2 * I, H), dt, dev) if w13 is not None or dx is not None else None,
+            _at(w2, "w2", (H, I), dt, dev), *kept, _given(dx, "dx", (T, H), dt, dev),
+            _given(dw13, "dw13", (2 * I, H), dw_dt, dev), _given(dw2, "dw2", (H, I), dw_dt, dev),
+            _ELEM[dw_dt], 1 if accumulate else 0,
+            _ptr(workspace, "workspace", None, {torch.uint8}, dev), workspace.numel())
+
+
+def moe_norm_check(shape: NormShape) -> int:
+    return lib().moe_norm_check(_ref(shape))
+
+
+def moe_norm_workspace_size(shape: NormShape) -> int:
+    return int(lib().moe_norm_workspace_size(_ref(shape)))
+
+
+def alloc_norm_workspace(shape: NormShape, device) -> torch.Tensor:
+    """A moe_norm_backward workspace for `shape`."""
+    return torch.empty(max(moe_norm_workspace_size(shape), 256), dtype=torch.uint8, device=device)
+
+
+def moe_norm_forward(shape: NormShape, x, w_pre, normed, y=None, w_post=None, gate=None, res=None,
+                     normed_fp8=None, normed_scale=None, stream=None):
+    """The residual joint: res = skip_scale x + block_scale sigmoid(gate[t]) z with z the
+    RMS norm of y by w_post (or y), and normed the RMS norm of res by w_pre; rows [T, H]
+    of one type, weights [H] of it, gate float32 [T].  y None: normed is the norm of x.
+    normed (and w_pre) may be None; normed_fp8 [T, H] and normed_scale [T, H/32] take
+    normed as MX FP8 rows.  res may be x or y itself."""
+    code, dt, dev = _elem(x, "x")
+    tok, w = (shape.T, shape.H), (shape.H,)
+    mx = (None, None)
+    if normed_fp8 is not None or normed_scale is not None:
+        mx = (_ptr(normed_fp8, "normed_fp8", tok, _fp8(), dev),
+              _ptr(normed_scale, "normed_scale", (shape.T, shape.H // 32), _e8m0(""), dev))
+    _launch("moe_norm_forward", dev, stream, _ref(shape), code, _at(x, "x", tok, dt, dev),
+            _given(y, "y", tok, dt, dev), _given(w_post, "w_post", w, dt, dev),
+            _given(gate, "gate", (shape.T,), torch.float32, dev),
+            _given(w_pre, "w_pre", w, dt, dev), _given(res, "res", tok, dt, dev),
+            _given(normed, "normed", tok, dt, dev), *mx)
+
+
+def moe_norm_backward(shape: NormShape, dnormed, res, w_pre, dx, dw_pre, workspace, dres=None,
+                      y=None, w_post=None, gate=None, dy=None, dw_post=None, dgate=None,
+                      stream=None):
+    """moe_norm_forward's gradients from dnormed (None, with res, w_pre and dw_pre: no norm
+    behind the joint) and dres (None: zero), with the stored res (y None: x): dx and dy
+    [T, H], dgate float32 [T], dw_pre and dw_post float32 [H], each may be None.  dx may
+    be dres, dnormed or res itself, dy may be y."""
+    t = dnormed if dnormed is not None else dres
+    code, dt, dev = _elem(t, "dnormed" if dnormed is not None else "dres")
+    tok, w, f32 = (shape.T, shape.H), (shape.H,), torch.float32
+    ws = (None, 0)
+    if workspace is not None:
+        ws = _ptr(workspace, "workspace", None, {torch.uint8}, dev), workspace.numel()
+    _launch("moe_norm_backward", dev, stream, _ref(shape), code,
+            _given(dnormed, "dnormed", tok, dt, dev), _given(dres, "dres", tok, dt, dev),
+            _given(res, "res", tok, dt, dev), _given(y, "y", tok, dt, dev),
+            _given(w_post, "w_post", w, dt, dev), _given(gate, "gate", (shape.T,), f32, dev),
+            _given(w_pre, "w_pre", w, dt, dev), _given(dx, "dx", tok, dt, dev),
+            _given(dy, "dy", tok, dt, dev), _given(dgate, "dgate", (shape.T,), f32, dev),
+            _given(dw_post, "dw_post", w, f32, dev), _given(dw_pre, "dw_pre", w, f32, dev), *ws)

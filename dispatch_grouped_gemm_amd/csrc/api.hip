@@ -759,6 +759,137 @@ int moe_adapter_project(const moe_adapter_shape *s, int32_t dtype, const void *x
                                                   out, ws, as_stream(stream)));
 }
 
+// ---- the dense feed-forward block, the residual joint -----------------------
+
+int moe_ffn_check(const moe_ffn_shape *s)
+{
+    if (!s || s->T < 0 || s->H <= 0 || s->I <= 0 || !(s->gate_limit > 0.0f) ||
+        !(s->up_limit > 0.0f))
+        return MOE_EINVAL;
+    if (s->T > (1 << 24) || s->H % 32 != 0 || s->H > (1 << 17) || s->I % 32 != 0 ||
+        s->I > (1 << 17))
+        return MOE_ENOTSUP;
+    return MOE_OK;
+}
+
+size_t moe_ffn_workspace_size(const moe_ffn_shape *s, int32_t backward)
+{
+    if (moe_ffn_check(s) != MOE_OK || s->T == 0)
+        return 0;
+    const size_t f = moe::ffn_forward_bytes(*s), b = backward ? moe::ffn_backward_bytes(*s) : 0;
+    return f > b ? f : b;
+}
+
+static bool ffn_type(int32_t dtype) { return dtype == MOE_DT_BF16 || dtype == MOE_DT_F16; }
+
+int moe_ffn_forward(const moe_ffn_shape *s, int32_t dtype, const void *x, const void *w13,
+                    const void *w2, const void *base, void *gate_up, uint8_t *gate_up_scale,
+                    void *out, void *ws, size_t ws_bytes, void *stream)
+{
+    int rc = moe_ffn_check(s);
+    if (rc != MOE_OK)
+        return rc;
+    if (!ffn_type(dtype))
+        return MOE_EINVAL;
+    if (s->T == 0)
+        return MOE_OK;
+    if (!x || !w13 || !w2 || !out || (gate_up_scale && !gate_up) ||
+        !all_aligned16(x, w13, w2, base, gate_up, out))
+        return MOE_EINVAL;
+    if (!ws || ws_bytes < moe::ffn_forward_bytes(*s) || ((uintptr_t)ws % kAlign) != 0)
+        return MOE_EWORKSPACE;
+    return hip_status(moe::launch_ffn_forward(*s, dtype, x, w13, w2, base, gate_up, gate_up_scale,
+                                              out, ws, as_stream(stream)));
+}
+
+int moe_ffn_backward(const moe_ffn_shape *s, int32_t dtype, const void *dout, const void *x,
+                     const uint8_t *x_scale, const void *w13, const void *w2,
+                     const void *gate_up, const uint8_t *gate_up_scale, void *dx, void *dw13,
+                     void *dw2, int32_t dw_dtype, int32_t accumulate, void *ws, size_t ws_bytes,
+                     void *stream)
+{
+    int rc = moe_ffn_check(s);
+    if (rc != MOE_OK)
+        return rc;
+    if (!ffn_type(dtype) || (dw_dtype != dtype && dw_dtype != MOE_DT_F32) ||
+        (!dx && !dw13 && !dw2) || !all_aligned16(dout, x, w13, w2, gate_up, dx, dw13, dw2))
+        return MOE_EINVAL;
+    if (s->T > 0) {
+        if (!dout || !w2 || !gate_up || (dw13 && !x) || (x_scale && !x) || (dx && !w13))
+            return MOE_EINVAL;
+        if (!ws || ws_bytes < moe::ffn_backward_bytes(*s) || ((uintptr_t)ws % kAlign) != 0)
+            return MOE_EWORKSPACE;
+    }
+    return hip_status(moe::launch_ffn_backward(*s, dtype, dout, x, x_scale, w13, w2, gate_up,
+                                               gate_up_scale, dx, dw13, dw2,
+                                               dw_dtype == MOE_DT_F32, accumulate != 0, ws,
+                                               as_stream(stream)));
+}
+
+int moe_norm_check(const moe_norm_shape *s)
+{
+    if (!s || s->T < 0 || s->H <= 0 || !(s->eps >= 0.0f) || !isfinite(s->skip_scale) ||
+        !isfinite(s->block_scale))
+        return MOE_EINVAL;
+    if (s->T > (1 << 24) || s->H % 32 != 0 || s->H > (1 << 14))
+        return MOE_ENOTSUP;
+    return MOE_OK;
+}
+
+size_t moe_norm_workspace_size(const moe_norm_shape *s)
+{
+    if (moe_norm_check(s) != MOE_OK || s->T == 0)
+        return 0;
+    return moe::norm_workspace_bytes(*s);
+}
+
+int moe_norm_forward(const moe_norm_shape *s, int32_t dtype, const void *x, const void *y,
+                     const void *w_post, const float *gate, const void *w_pre, void *res,
+                     void *normed, uint8_t *normed_fp8, uint8_t *normed_scale, void *stream)
+{
+    int rc = moe_norm_check(s);
+    if (rc != MOE_OK)
+        return rc;
+    if (!elem_type(dtype))
+        return MOE_EINVAL;
+    if (s->T == 0)
+        return MOE_OK;
+    const bool pre = normed || normed_fp8;
+    if (!x || (!y && (w_post || gate || res)) || (!res && !pre) || pre != (w_pre != nullptr) ||
+        (normed_fp8 != nullptr) != (normed_scale != nullptr) ||
+        !all_aligned16(x, y, w_post, w_pre, res, normed, normed_fp8))
+        return MOE_EINVAL;
+    return hip_status(moe::launch_norm_forward(*s, dtype, x, y, w_post, gate, w_pre, res, normed,
+                                               normed_fp8, normed_scale, as_stream(stream)));
+}
+
+int moe_norm_backward(const moe_norm_shape *s, int32_t dtype, const void *dnormed,
+                      const void *dres, const void *res, const void *y, const void *w_post,
+                      const float *gate, const void *w_pre, void *dx, void *dy, float *dgate,
+                      float *dw_post, float *dw_pre, void *ws, size_t ws_bytes, void *stream)
+{
+    int rc = moe_norm_check(s);
+    if (rc != MOE_OK)
+        return rc;
+    const bool planes = dw_post || dw_pre;
+    if (!elem_type(dtype) || (!dx && !dy && !dgate && !planes) ||
+        !all_aligned16(dnormed, dres, res, y, w_post, w_pre, dx, dy))
+        return MOE_EINVAL;
+    if (s->T > 0) {
+        const bool pre = dnormed != nullptr;
+        if ((!dnormed && !dres) || pre != (res != nullptr) || pre != (w_pre != nullptr) ||
+            (dw_pre && !pre) || (!y && (w_post || gate || dy || dgate)) || (dw_post && !w_post) ||
+            (dgate && !gate))
+            return MOE_EINVAL;
+        if (planes &&
+            (!ws || ws_bytes < moe::norm_workspace_bytes(*s) || ((uintptr_t)ws % kAlign) != 0))
+            return MOE_EWORKSPACE;
+    }
+    return hip_status(moe::launch_norm_backward(*s, dtype, dnormed, dres, res, y, w_post, gate,
+                                                w_pre, dx, dy, dgate, dw_post, dw_pre, ws,
+                                                as_stream(stream)));
+}
+
 const char *moe_strerror(int code)
 {
     switch (code) {
@@ -769,7 +900,9 @@ const char *moe_strerror(int code)
     case MOE_ENOTSUP:
         return "shape not supported (H and I multiples of 128, K <= 8, E_local <= 512, "
                "T*H and I*H below 2^32; router: E_total <= 1024; adapters: H a multiple of "
-               "128 up to 2^17, N of 8 up to 2^20, rank of 8 up to 256)";
+               "128 up to 2^17, N of 8 up to 2^20, rank of 8 up to 256; feed-forward block: H and "
+               "I multiples of 32 up to 2^17; norms: H a multiple of 32 up to 2^14; T up to "
+               "2^24 in both)";
     case MOE_EWORKSPACE:
         return "workspace missing, too small or not 256-byte aligned";
     case MOE_EHIP:

@@ -563,6 +563,29 @@ hipError_t launch_adapter_project(const moe_adapter_shape &s, int dtype, const v
                                   const void *a, const void *b, const float *scale, void *out,
                                   void *ws, hipStream_t st);
 
+// The dense feed-forward block and the residual joint with its norms
+// (arguments as the C ABI's; f32: the weights' gradients are float32).
+size_t ffn_forward_bytes(const moe_ffn_shape &s);
+size_t ffn_backward_bytes(const moe_ffn_shape &s);
+hipError_t launch_ffn_forward(const moe_ffn_shape &s, int dtype, const void *x, const void *w13,
+                              const void *w2, const void *base, void *gate_up,
+                              uint8_t *gate_up_scale, void *out, void *ws, hipStream_t st);
+hipError_t launch_ffn_backward(const moe_ffn_shape &s, int dtype, const void *dout, const void *x,
+                               const uint8_t *x_scale, const void *w13, const void *w2,
+                               const void *gate_up, const uint8_t *gate_up_scale, void *dx,
+                               void *dw13, void *dw2, bool f32, bool accumulate, void *ws,
+                               hipStream_t st);
+size_t norm_workspace_bytes(const moe_norm_shape &s);
+hipError_t launch_norm_forward(const moe_norm_shape &s, int dtype, const void *x, const void *y,
+                               const void *w_post, const float *gate, const void *w_pre,
+                               void *res, void *normed, uint8_t *codes, uint8_t *exps,
+                               hipStream_t st);
+hipError_t launch_norm_backward(const moe_norm_shape &s, int dtype, const void *dnormed,
+                                const void *dres, const void *res, const void *y,
+                                const void *w_post, const float *gate, const void *w_pre,
+                                void *dx, void *dy, float *dgate, float *dw_post, float *dw_pre,
+                                void *ws, hipStream_t st);
+
 int device_cu_count();
 
 } // namespace moe

@@ -1,0 +1,442 @@
+// The residual joint around a block, one pass over the rows:
+//   z   = y rho(y) w_post                 (w_post given, else y)
+//   res = skip x + scale logistic(gate_t) z     (y given, else x)
+//   normed = res rho(res) w_pre,  rho(v) = 1 / sqrt(mean v^2 + eps),
+// the second norm of res as it is stored (rounded to the type), so that the
+// backward pass, which has res, computes with the same values.  Sums are
+// float32.  normed may also, or only, be written as MX FP8 rows, the experts'
+// input, with the codes that moe_quant_mxfp8 makes of the rounded normed.
+//
+// Bound by HBM: a workgroup holds its row's 16-byte pieces in registers from
+// the one read to the write, so every array moves once.
+#include <algorithm>
+
+#include "elem.hpp"
+
+namespace moe {
+
+namespace {
+
+struct NShape {
+    int T, H;
+    float eps, skip, scale;
+};
+
+// Sum over the workgroup (whole wavefronts); every thread gets it.  `slot`
+// alternates between calls, so one barrier a sum is enough.
+template <int N>
+__device__ __forceinline__ void sum_all(float *v, float (*lds)[16][N], int slot)
+{
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1)
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            v[n] += __shfl_xor(v[n], d);
+    const int waves = blockDim.x >> 6;
+    if (waves == 1)
+        return;
+    if ((threadIdx.x & 63) == 0)
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            lds[slot][threadIdx.x >> 6][n] = v[n];
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+        v[n] = 0.0f;
+    for (int w = 0; w < waves; ++w)
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            v[n] += lds[slot][w][n];
+}
+
+__device__ __forceinline__ float rho_of(float squares, const NShape &s)
+{
+    return rsqrtf(squares / (float)s.H + s.eps);
+}
+
+__device__ __forceinline__ float gate_of(const float *gate, long t)
+{
+    return gate ? 1.0f / (1.0f + expf(-gate[t])) : 1.0f;
+}
+
+struct Forward {
+    const void *x, *y, *w_post, *w_pre;
+    const float *gate;
+    void *res, *normed;
+    uint8_t *codes, *exps;
+};
+
+// A row's pieces in thread order: piece p = i * threads + thread.
+template <int DT, int NP>
+__global__ void __launch_bounds__(1024) norm_forward_kernel(NShape s, Forward p)
+{
+    using E = Elem<DT>;
+    using V = typename E::type;
+    constexpr int kV = E::kVec;
+    __shared__ float lds[2][16][1];
+    const long t = blockIdx.x;
+    const int pieces = s.H / kV;
+    uint4 xq[NP], yq[NP], rq[NP];
+    const auto row = [&](const void *v) { return static_cast<const uint4 *>(v) + t * pieces; };
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        const int at = i * blockDim.x + threadIdx.x;
+        xq[i] = yq[i] = uint4{0, 0, 0, 0};
+        if (at < pieces) {
+            xq[i] = row(p.x)[at];
+            if (p.y)
+                yq[i] = row(p.y)[at];
+        }
+    }
+    if (p.y) {
+        float a = s.scale * gate_of(p.gate, t);
+        if (p.w_post) {
+            float sq[1] = {0.0f};
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                float f[kV];
+                E::unpack(yq[i], f);
+#pragma unroll
+                for (int k = 0; k < kV; ++k)
+                    sq[0] += f[k] * f[k];
+            }
+            sum_all<1>(sq, lds, 0);
+            a *= rho_of(sq[0], s);
+        }
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const int at = i * blockDim.x + threadIdx.x;
+            float x[kV], y[kV], w[kV];
+            E::unpack(xq[i], x);
+            E::unpack(yq[i], y);
+            if (p.w_post && at < pieces)
+                E::unpack(static_cast<const uint4 *>(p.w_post)[at], w);
+#pragma unroll
+            for (int k = 0; k < kV; ++k)
+                x[k] = s.skip * x[k] + a * (p.w_post ? y[k] * w[k] : y[k]);
+            xq[i] = E::pack(x);
+            if (p.res && at < pieces)
+                const_cast<uint4 *>(row(p.res))[at] = xq[i];
+            if (at >= pieces)
+                xq[i] = uint4{0, 0, 0, 0};
+        }
+    }
+    if (!p.normed && !p.codes)
+        return;
+    float sq[1] = {0.0f};
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        float f[kV];
+        E::unpack(xq[i], f);
+#pragma unroll
+        for (int k = 0; k < kV; ++k)
+            sq[0] += f[k] * f[k];
+    }
+    sum_all<1>(sq, lds, 1);
+    const float rho = rho_of(sq[0], s);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        const int at = i * blockDim.x + threadIdx.x;
+        float f[kV], w[kV];
+        E::unpack(xq[i], f);
+        if (at < pieces)
+            E::unpack(static_cast<const uint4 *>(p.w_pre)[at], w);
+#pragma unroll
+        for (int k = 0; k < kV; ++k)
+            f[k] = at < pieces ? f[k] * rho * w[k] : 0.0f;
+        rq[i] = E::pack(f);
+        if (p.normed && at < pieces)
+            const_cast<uint4 *>(row(p.normed))[at] = rq[i];
+        if (p.codes) {
+            E::unpack(rq[i], f); // the rounded values, as a quantiser of normed has them
+            float amax = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kV; ++k)
+                amax = fmaxf(amax, fabsf(f[k]));
+#pragma unroll
+            for (int d = 1; d < 32 / kV; d <<= 1)
+                amax = fmaxf(amax, __shfl_xor(amax, d));
+            if (at < pieces) {
+                const int e = mx8_block_exponent(amax);
+                uint32_t *o = reinterpret_cast<uint32_t *>(p.codes + t * s.H) + at * (kV / 4);
+#pragma unroll
+                for (int k = 0; k < kV / 4; ++k)
+                    o[k] = mx8_pack4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3], e, amax);
+                if (at % (32 / kV) == 0)
+                    p.exps[t * (s.H / 32) + at / (32 / kV)] = (uint8_t)(e + 127);
+            }
+        }
+    }
+}
+
+struct Backward {
+    const void *dnormed, *dres, *res, *y, *w_post, *w_pre;
+    const float *gate;
+    void *dx, *dy;
+    float *dgate, *part_pre, *part_post; // [groups][H]
+};
+
+// A workgroup takes every groups-th row and keeps its rows' sums of the
+// weights' gradients in registers; the planes are added in their order.
+template <int DT, int NP>
+__global__ void __launch_bounds__(1024) norm_backward_kernel(NShape s, Backward p)
+{
+    using E = Elem<DT>;
+    constexpr int kV = E::kVec;
+    __shared__ float l1[2][16][2], l2[2][16][2];
+    const int pieces = s.H / kV;
+    float sum_pre[NP][kV], sum_post[NP][kV];
+#pragma unroll
+    for (int i = 0; i < NP; ++i)
+#pragma unroll
+        for (int k = 0; k < kV; ++k)
+            sum_pre[i][k] = sum_post[i][k] = 0.0f;
+    int slot = 0;
+    for (long t = blockIdx.x; t < s.T; t += gridDim.x, slot ^= 1) {
+        const auto row = [&](const void *v) { return static_cast<const uint4 *>(v) + t * pieces; };
+        uint4 rq[NP], nq[NP], dq[NP], yq[NP];
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const int at = i * blockDim.x + threadIdx.x;
+            rq[i] = nq[i] = dq[i] = yq[i] = uint4{0, 0, 0, 0};
+            if (at < pieces) {
+                if (p.dnormed) {
+                    rq[i] = row(p.res)[at];
+                    nq[i] = row(p.dnormed)[at];
+                }
+                if (p.dres)
+                    dq[i] = row(p.dres)[at];
+                if (p.y)
+                    yq[i] = row(p.y)[at];
+            }
+        }
+        // mean res^2 and mean (dn w) res; mean y^2
+        float rho = 0.0f, back = 0.0f;
+        if (p.dnormed) {
+            float v[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                const int at = i * blockDim.x + threadIdx.x;
+                if (at >= pieces)
+                    continue;
+                float r[kV], d[kV], w[kV];
+                E::unpack(rq[i], r);
+                E::unpack(nq[i], d);
+                E::unpack(static_cast<const uint4 *>(p.w_pre)[at], w);
+#pragma unroll
+                for (int k = 0; k < kV; ++k) {
+                    v[0] += r[k] * r[k];
+                    v[1] += r[k] * d[k] * w[k];
+                }
+            }
+            sum_all<2>(v, l1, slot);
+            rho = rho_of(v[0], s);
+            back = rho * rho * rho * (v[1] / (float)s.H);
+        }
+        const float sig = gate_of(p.gate, t), a = s.scale * sig;
+        // dr, in place of dn; and the sums that y's gradient and the gate's need
+        float dr[NP][kV];
+        float v[2] = {0.0f, 0.0f}; // sum y^2, sum dr y w_post
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const int at = i * blockDim.x + threadIdx.x;
+            if (at >= pieces)
+                continue;
+            float r[kV], d[kV], w[kV];
+            E::unpack(dq[i], dr[i]);
+            if (p.dnormed) {
+                E::unpack(rq[i], r);
+                E::unpack(nq[i], d);
+                E::unpack(static_cast<const uint4 *>(p.w_pre)[at], w);
+#pragma unroll
+                for (int k = 0; k < kV; ++k) {
+                    dr[i][k] += rho * d[k] * w[k] - back * r[k];
+                    sum_pre[i][k] += d[k] * (r[k] * rho);
+                }
+            }
+            if (p.dx) {
+#pragma unroll
+                for (int k = 0; k < kV; ++k)
+                    r[k] = p.y ? s.skip * dr[i][k] : dr[i][k];
+                const_cast<uint4 *>(row(p.dx))[at] = E::pack(r);
+            }
+            if (p.y) {
+                E::unpack(yq[i], r);
+                if (p.w_post)
+                    E::unpack(static_cast<const uint4 *>(p.w_post)[at], w);
+#pragma unroll
+                for (int k = 0; k < kV; ++k) {
+                    v[0] += r[k] * r[k];
+                    v[1] += dr[i][k] * (p.w_post ? r[k] * w[k] : r[k]);
+                }
+            }
+        }
+        if (!p.y)
+            continue;
+        if (p.w_post || p.dgate)
+            sum_all<2>(v, l2, slot);
+        const float rho_y = p.w_post ? rho_of(v[0], s) : 1.0f;
+        if (p.dgate && threadIdx.x == 0)
+            p.dgate[t] = s.scale * sig * (1.0f - sig) * (rho_y * v[1]);
+        const float back_y = p.w_post ? a * rho_y * rho_y * rho_y * (v[1] / (float)s.H) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const int at = i * blockDim.x + threadIdx.x;
+            if (at >= pieces)
+                continue;
+            float y[kV], w[kV];
+            E::unpack(yq[i], y);
+            if (p.w_post) {
+                E::unpack(static_cast<const uint4 *>(p.w_post)[at], w);
+#pragma unroll
+                for (int k = 0; k < kV; ++k) {
+                    sum_post[i][k] += a * dr[i][k] * (y[k] * rho_y);
+                    y[k] = rho_y * a * dr[i][k] * w[k] - back_y * y[k];
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < kV; ++k)
+                    y[k] = a * dr[i][k];
+            }
+            if (p.dy)
+                const_cast<uint4 *>(row(p.dy))[at] = E::pack(y);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        const int at = i * blockDim.x + threadIdx.x;
+        if (at >= pieces)
+            continue;
+        const long o = (long)blockIdx.x * s.H + (long)at * kV;
+#pragma unroll
+        for (int k = 0; k < kV; k += 4) {
+            if (p.part_pre)
+                *reinterpret_cast<v4f *>(p.part_pre + o + k) =
+                    v4f{sum_pre[i][k], sum_pre[i][k + 1], sum_pre[i][k + 2], sum_pre[i][k + 3]};
+            if (p.part_post)
+                *reinterpret_cast<v4f *>(p.part_post + o + k) = v4f{
+                    sum_post[i][k], sum_post[i][k + 1], sum_post[i][k + 2], sum_post[i][k + 3]};
+        }
+    }
+}
+
+// out[h] = the sum of the groups' planes: 4 wavefronts of 64 columns take a
+// quarter of the planes each.
+__global__ void __launch_bounds__(256)
+norm_planes_kernel(int H, int groups, const float *part0, const float *part1, float *out0,
+                   float *out1)
+{
+    const float *part = blockIdx.y ? part1 : part0;
+    float *out = blockIdx.y ? out1 : out0;
+    if (!out)
+        return;
+    __shared__ float lds[4][64];
+    const int lane = threadIdx.x & 63, q = threadIdx.x >> 6, h = blockIdx.x * 64 + lane;
+    float sum = 0.0f;
+    if (h < H)
+        for (int g = groups * q / 4; g < groups * (q + 1) / 4; ++g)
+            sum += part[(long)g * H + h];
+    lds[q][lane] = sum;
+    __syncthreads();
+    if (q == 0 && h < H)
+        out[h] = (lds[0][lane] + lds[1][lane]) + (lds[2][lane] + lds[3][lane]);
+}
+
+// Threads and pieces a thread for a row of `pieces` (H up to 16,384: at most 4).
+struct Split {
+    int threads, np;
+};
+
+Split split_of(int pieces, int most)
+{
+    int np = 1;
+    while (np < most && (pieces + np - 1) / np > 256)
+        np *= 2;
+    while ((pieces + np - 1) / np > 1024)
+        np *= 2;
+    const int lanes = (pieces + np - 1) / np;
+    return Split{std::min(1024, (lanes + 63) / 64 * 64), np};
+}
+
+template <int DT>
+int pieces_of(const moe_norm_shape &s)
+{
+    return s.H / Elem<DT>::kVec;
+}
+
+NShape dev(const moe_norm_shape &s)
+{
+    return NShape{s.T, s.H, s.eps, s.skip_scale, s.block_scale};
+}
+
+int groups_of(const moe_norm_shape &s) { return std::min(s.T, 512); }
+
+size_t plane_bytes(const moe_norm_shape &s)
+{
+    return ((size_t)groups_of(s) * s.H * sizeof(float) + 255) / 256 * 256;
+}
+
+} // namespace
+
+size_t norm_workspace_bytes(const moe_norm_shape &s) { return 2 * plane_bytes(s); }
+
+hipError_t launch_norm_forward(const moe_norm_shape &sh, int dtype, const void *x, const void *y,
+                               const void *w_post, const float *gate, const void *w_pre,
+                               void *res, void *normed, uint8_t *codes, uint8_t *exps,
+                               hipStream_t st)
+{
+    const NShape s = dev(sh);
+    const Forward p{x, y, w_post, w_pre, gate, res, normed, codes, exps};
+    with_elem(dtype, [&](auto dt) {
+        constexpr int DT = decltype(dt)::value;
+        const Split c = split_of(pieces_of<DT>(sh), 4);
+        const auto go = [&](auto np) {
+            norm_forward_kernel<DT, decltype(np)::value><<<s.T, c.threads, 0, st>>>(s, p);
+        };
+        if (c.np == 1)
+            go(std::integral_constant<int, 1>{});
+        else if (c.np == 2)
+            go(std::integral_constant<int, 2>{});
+        else
+            go(std::integral_constant<int, 4>{});
+    });
+    return hipGetLastError();
+}
+
+hipError_t launch_norm_backward(const moe_norm_shape &sh, int dtype, const void *dnormed,
+                                const void *dres, const void *res, const void *y,
+                                const void *w_post, const float *gate, const void *w_pre,
+                                void *dx, void *dy, float *dgate, float *dw_post, float *dw_pre,
+                                void *ws, hipStream_t st)
+{
+    const NShape s = dev(sh);
+    const int groups = groups_of(sh);
+    float *pre = static_cast<float *>(ws);
+    float *post = pre ? pre + plane_bytes(sh) / sizeof(float) : nullptr;
+    const Backward p{dnormed, dres, res, y, w_post, w_pre, gate, dx, dy, dgate,
+                     dw_pre ? pre : nullptr, dw_post ? post : nullptr};
+    if (s.T > 0) {
+        with_elem(dtype, [&](auto dt) {
+            constexpr int DT = decltype(dt)::value;
+            const Split c = split_of(pieces_of<DT>(sh), 2);
+            const auto go = [&](auto np) {
+                norm_backward_kernel<DT, decltype(np)::value><<<groups, c.threads, 0, st>>>(s, p);
+            };
+            if (c.np == 1)
+                go(std::integral_constant<int, 1>{});
+            else if (c.np == 2)
+                go(std::integral_constant<int, 2>{});
+            else
+                go(std::integral_constant<int, 4>{});
+        });
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    if (dw_pre || dw_post) // of no rows: zeros
+        norm_planes_kernel<<<dim3((s.H + 63) / 64, 2), 256, 0, st>>>(s.H, groups, pre, post,
+                                                                    dw_pre, dw_post);
+    return hipGetLastError();
+}
+
+} // namespace moe

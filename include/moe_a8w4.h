@@ -568,6 +568,119 @@ int moe_adapter_project(const moe_adapter_shape *shape, int32_t dtype, const voi
                         const void *a, const void *b, const float *scale, void *out,
                         void *workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * The dense feed-forward block that every token takes beside its experts (a
+ * shared expert, or a dense layer), and its gradients.  dtype MOE_DT_BF16 or
+ * MOE_DT_F16 for every array without a type of its own; W13 and W2 are laid
+ * out as one expert's are: w13 [2I, H] (rows 0..I-1 gate, I..2I-1 up), w2 [H, I].
+ *
+ * moe_ffn_forward, x [T, H]:
+ *   g | u = x W13^T                          float32 sums
+ *   h = silu(min(g, gate_limit)) clamp(u, -up_limit, up_limit)   rounded once
+ *   out = h W2^T (+ base)                    float32 sums, rounded once
+ * base [T, H] (NULL: none) may be out itself, as the experts' output is.  For
+ * the backward pass it keeps g | u when gate_up is given: [T, 2I] in dtype
+ * (gate_up_scale NULL), or MX FP8 codes [T, 2I] with an exponent byte per 32
+ * columns in gate_up_scale [T, 2I/32] (the rule of moe_quant_mxfp8 on the
+ * float32 sums).  A NaN in g or u gives a NaN in h.
+ *
+ * moe_ffn_backward: from dout [T, H] and what was kept (the same two forms),
+ * each value taken as it was rounded,
+ *   dh = dout W2,  du = dh silu(g'),  dg = dh u' s (1 + g' (1 - s)),
+ * g' and u' the clamped values, s = 1 / (1 + exp(-g')), dg = 0 where g is above
+ * gate_limit and du = 0 where |u| is above up_limit; dg, du and h rounded once;
+ *   dx = (dg | du) W13,  dW13 = (dg | du)^T x,  dW2 = dout^T h.
+ * x is in dtype (x_scale NULL) or MX FP8: codes [T, H] and exponent bytes
+ * x_scale [T, H/32], as the experts take it; its values are rounded to dtype.
+ * dx [T, H], dw13 and dw2 (shaped as the weights) may each be NULL; x may be
+ * NULL without dw13, w13 without dx.  dw_dtype is dtype or MOE_DT_F32;
+ * accumulate != 0 adds to what dw13 and dw2 hold (float32 sum, rounded once).
+ * With T = 0 dw13 and dw2 become zeros (or stay, with accumulate).
+ *
+ * Sums have a fixed order: the same call gives the same bits.  Buffers do not
+ * overlap (but for base); x, weights, rows and gradients start on 16-byte
+ * boundaries, gate_up codes on 16 and exponent bytes anywhere.
+ * workspace: moe_ffn_workspace_size bytes of scratch (backward != 0: enough for
+ * both calls), 256-byte aligned; calls that overlap on one workspace race.
+ */
+typedef struct moe_ffn_shape {
+    int32_t T;        /* rows, at most 2^24 */
+    int32_t H;        /* hidden size, a multiple of 32, at most 2^17 */
+    int32_t I;        /* intermediate size, a multiple of 32, at most 2^17 */
+    float gate_limit; /* as in moe_shape, above 0 (INFINITY: no limit) */
+    float up_limit;
+} moe_ffn_shape;
+
+/* Check a shape; MOE_OK or the code a call with it would return. */
+int moe_ffn_check(const moe_ffn_shape *shape);
+
+/* Scratch bytes of moe_ffn_forward (backward 0) or of both calls; 0 for a
+ * refused shape or T = 0. */
+size_t moe_ffn_workspace_size(const moe_ffn_shape *shape, int32_t backward);
+
+int moe_ffn_forward(const moe_ffn_shape *shape, int32_t dtype, const void *x, const void *w13,
+                    const void *w2, const void *base, void *gate_up, uint8_t *gate_up_scale,
+                    void *out, void *workspace, size_t workspace_bytes, void *stream);
+
+int moe_ffn_backward(const moe_ffn_shape *shape, int32_t dtype, const void *dout, const void *x,
+                     const uint8_t *x_scale, const void *w13, const void *w2,
+                     const void *gate_up, const uint8_t *gate_up_scale, void *dx, void *dw13,
+                     void *dw2, int32_t dw_dtype, int32_t accumulate, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
+/*
+ * The residual joint around a block, with the norm after it and the norm
+ * before the next one, and its gradients.  dtype any of the three element
+ * types; rows [T, H]; rho(v) = 1 / sqrt(mean v^2 + eps), sums in float32.
+ *
+ * moe_norm_forward:
+ *   z = y rho(y) w_post             (w_post [H]; NULL: z = y)
+ *   res = skip_scale x + block_scale sigmoid(gate[t]) z    rounded once
+ *   normed = res rho(res) w_pre     of res as it is rounded; rounded once
+ * gate float [T] (NULL: factor 1).  y NULL: no block, normed is the norm of x,
+ * and res, w_post and gate are NULL too.  normed (with w_pre) may be NULL, or
+ * written as MX FP8 rows besides or instead: codes [T, H] and exponent bytes
+ * [T, H/32] (both or neither), the bytes moe_quant_mxfp8 makes of normed.  res
+ * may be NULL, or x or y itself; normed may be none of the inputs.
+ *
+ * moe_norm_backward: from dnormed (NULL: no norm before the next block; res,
+ * w_pre and dw_pre are then NULL) and dres (NULL: zero), one of them given, with
+ * the stored res (y NULL: x),
+ *   dr = dres + rho w_pre dnormed - res rho^3 mean(w_pre dnormed res)
+ *   dx = skip_scale dr  (y NULL: dr),  dw_pre[h] = sum_t dnormed res rho
+ *   dz = block_scale sigmoid(gate[t]) dr,  dw_post[h] = sum_t dz y rho(y)
+ *   dy = the gradient of y as dr is that of res (w_post NULL: dz)
+ *   dgate[t] = block_scale sigmoid'(gate[t]) <dr, z>
+ * dx, dy, dgate, dw_post and dw_pre may each be NULL, and are where what they
+ * belong to is; dgate, dw_post and dw_pre are float32.  dx may be dres, dnormed
+ * or res itself, dy may be y.  With T = 0 dw_pre and dw_post become zeros.  Sums
+ * have a fixed order.  workspace (for dw_pre or dw_post):
+ * moe_norm_workspace_size bytes, 256-byte aligned; calls that overlap on one race.
+ * Rows and weights start on 16-byte boundaries.
+ */
+typedef struct moe_norm_shape {
+    int32_t T;         /* rows, at most 2^24 */
+    int32_t H;         /* a multiple of 32, at most 2^14 */
+    float eps;         /* 0 or more */
+    float skip_scale;  /* factor of x */
+    float block_scale; /* factor of the block's z */
+} moe_norm_shape;
+
+int moe_norm_check(const moe_norm_shape *shape);
+
+/* Scratch bytes of moe_norm_backward; 0 for a refused shape or T = 0. */
+size_t moe_norm_workspace_size(const moe_norm_shape *shape);
+
+int moe_norm_forward(const moe_norm_shape *shape, int32_t dtype, const void *x, const void *y,
+                     const void *w_post, const float *gate, const void *w_pre, void *res,
+                     void *normed, uint8_t *normed_fp8, uint8_t *normed_scale, void *stream);
+
+int moe_norm_backward(const moe_norm_shape *shape, int32_t dtype, const void *dnormed,
+                      const void *dres, const void *res, const void *y, const void *w_post,
+                      const float *gate, const void *w_pre, void *dx, void *dy, float *dgate,
+                      float *dw_post, float *dw_pre, void *workspace, size_t workspace_bytes,
+                      void *stream);
+
 /* Static description of a return code. */
 const char *moe_strerror(int code);
 

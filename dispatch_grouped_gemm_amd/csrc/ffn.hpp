@@ -31,22 +31,15 @@ __device__ __forceinline__ float logistic(float g)
 
 // 8 neighbouring values of a 16-bit row, or of an MX FP8 one.
 template <int DT>
-__device__ __forceinline__ void load8(const uint16_t *p, float *f)
-{
-    Elem<DT>::unpack(*reinterpret_cast<const uint4 *>(p), f);
-}
-
-template <int DT>
 __device__ __forceinline__ void store8(uint16_t *p, const float *f)
 {
     *reinterpret_cast<uint4 *>(p) = Elem<DT>::pack(f);
 }
 
-__device__ __forceinline__ void load8_mx(const uint8_t *codes, uint8_t scale, float *f)
+__device__ __forceinline__ void from_mx(const uint2 &codes, uint32_t scale, float *f)
 {
-    const uint2 q = *reinterpret_cast<const uint2 *>(codes);
     const int e = (int)scale - 127;
-    const uint32_t w[2] = {q.x, q.y};
+    const uint32_t w[2] = {codes.x, codes.y};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], false);
@@ -76,6 +69,9 @@ __device__ __forceinline__ void store8_mx(uint8_t *codes, uint8_t *scale, const 
         *scale = (uint8_t)(e + 127);
 }
 
+// What a lane does with 8 neighbouring columns of a row once their sums are
+// complete.  Pre is what it reads for them, fetched for several rows ahead.
+
 // h = silu(min(g, gl)) clamp(u, ul) of 8 columns j .. j + 7 of row t, from the
 // float32 sums; D: lane distance of a block's four pieces.
 template <int DT, int D>
@@ -85,6 +81,8 @@ struct Activate {
     Kept kept;
     uint16_t *h;
 
+    struct Pre {};
+    __device__ __forceinline__ void fetch(long, int, Pre *) const {}
     __device__ __forceinline__ void operator()(long t, int j, const float *g, const float *u) const
     {
         if (kept.rows) {
@@ -121,19 +119,34 @@ struct ActivateBack {
     Kept kept;
     uint16_t *dgu, *h;
 
-    __device__ __forceinline__ void operator()(long t, int j, const float *dh) const
+    struct Pre {
+        uint4 g, u; // 16-bit rows; MX FP8: 8 codes in x and y, the exponent in z
+    };
+    __device__ __forceinline__ void fetch(long t, int j, Pre *p) const
     {
-        float g[8], u[8], v[8];
         const long at = t * 2 * I + j;
         if (kept.scale) {
             const uint8_t *c = static_cast<const uint8_t *>(kept.rows) + at;
             const uint8_t *s = kept.scale + at / 32;
-            load8_mx(c, *s, g);
-            load8_mx(c + I, s[I / 32], u);
+            const uint2 g = *reinterpret_cast<const uint2 *>(c);
+            const uint2 u = *reinterpret_cast<const uint2 *>(c + I);
+            p->g = uint4{g.x, g.y, s[0], 0};
+            p->u = uint4{u.x, u.y, s[I / 32], 0};
         } else {
             const uint16_t *r = static_cast<const uint16_t *>(kept.rows) + at;
-            load8<DT>(r, g);
-            load8<DT>(r + I, u);
+            p->g = *reinterpret_cast<const uint4 *>(r);
+            p->u = *reinterpret_cast<const uint4 *>(r + I);
+        }
+    }
+    __device__ __forceinline__ void operator()(long t, int j, const float *dh, const Pre &p) const
+    {
+        float g[8], u[8], v[8];
+        if (kept.scale) {
+            from_mx(uint2{p.g.x, p.g.y}, p.g.z, g);
+            from_mx(uint2{p.u.x, p.u.y}, p.u.z, u);
+        } else {
+            Elem<DT>::unpack(p.g, g);
+            Elem<DT>::unpack(p.u, u);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -145,6 +158,7 @@ struct ActivateBack {
             u[i] = fabsf(u[i]) > ul ? 0.0f : du;
         }
         // rounded once to the type: operands of the products that follow
+        const long at = t * 2 * I + j;
         store8<DT>(dgu + at, g);
         store8<DT>(dgu + at + I, u);
         if (h)
@@ -162,7 +176,15 @@ struct Put {
     float *out32;
     bool accumulate; // out32 += instead of =
 
-    __device__ __forceinline__ void operator()(long m, int n, const float *f) const
+    struct Pre {
+        uint4 base;
+    };
+    __device__ __forceinline__ void fetch(long m, int n, Pre *p) const
+    {
+        if (base)
+            p->base = *reinterpret_cast<const uint4 *>(base + m * ld + n);
+    }
+    __device__ __forceinline__ void operator()(long m, int n, const float *f, const Pre &p) const
     {
         const long at = m * ld + n;
         float v[8];
@@ -182,7 +204,7 @@ struct Put {
         }
         if (base) {
             float b[8];
-            load8<DT>(base + at, b);
+            Elem<DT>::unpack(p.base, b);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 v[i] += b[i];
@@ -192,110 +214,172 @@ struct Put {
 };
 
 // A product's sizes and operands: C [M, N] over K; tiles tm x tn, K in
-// `splits` parts.  kPairs: N is 2I rows of W13 and a tile's columns are half
-// gate, half up of the same I.
+// `splits` parts.
 struct Product {
     Operand a, b;
     long M, K;
-    int N, tm, tn, splits, whole;
-    float *parts; // [splits][M][N], null: the sums go to the functor
+    int N, tm, tn, splits;
+    float *parts; // [splits][M][N]: a part's sums, to be joined
 };
 
-template <typename T, bool kPairs, bool ADOWN, bool BDOWN, typename F>
-__device__ __forceinline__ void product_tile(const Product &p, const F &f, long m0, int in,
-                                             int part, uint8_t *lds)
+// The part's steps and the tile's sums.  kPairs: b's rows are W13's 2I and a
+// wavefront's columns half gate, half up of the same I.
+template <typename T, bool kPairs, bool ADOWN, bool BDOWN>
+__device__ __forceinline__ void tile_sums(T &tile, const Product &p, long m0, int n0, int part,
+                                          uint8_t *lds)
 {
-    const int n0 = in * (kPairs ? T::kBN / 2 : T::kBN);
     const int I = p.N / 2;
     const int steps = (int)((p.K + 63) / 64);
     const int first = (int)((long)steps * part / p.splits);
     const int end = (int)((long)steps * (part + 1) / p.splits);
-    T tile;
+    constexpr int W = 16 * T::NF; // columns of a wavefront
     tile.run(
         lds, p.a, [&](int i) { return min(m0 + i, p.M - 1); }, m0, p.M, p.b,
         [&](int i) -> long {
-            const int b = (i >> 4) & 3;
+            const int b = (i % W) >> 4;
             if (!kPairs)
-                return min(n0 + 64 * (i >> 6) + tile_column(b, i & 15), p.N - 1);
-            return (b >> 1) * (long)I + min(n0 + 32 * (i >> 6) + tile_column(b & 1, i & 15), I - 1);
+                return min(n0 + i / W * W + tile_column(b, i & 15), p.N - 1);
+            return (b >> 1) * (long)I +
+                   min(n0 + i / W * 32 + tile_column(b & 1, i & 15), I - 1);
         },
         n0, p.N, p.K, first, end - first);
+}
+
+// A lane's 8 columns of block pair h in a row block's sums.
+__device__ __forceinline__ void eight(const v4f *acc, int h, float *v)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i] = acc[2 * h][i];
+        v[4 + i] = acc[2 * h + 1][i];
+    }
+}
+
+// One tile of C, whole K, through the functor.
+template <typename T, bool kPairs, bool ADOWN, bool BDOWN, typename F>
+__device__ __forceinline__ void whole_tile(const Product &p, const F &f, long m0, int in,
+                                           uint8_t *lds)
+{
+    static_assert(!kPairs || T::NF == 4, "two blocks of gates, two of up");
+    const int n0 = in * (kPairs ? T::kBN / 2 : T::kBN);
+    T tile;
+    tile_sums<T, kPairs, ADOWN, BDOWN>(tile, p, m0, n0, 0, lds);
     const int lane = threadIdx.x & 63, wave = tile_wave();
     const int wm = wave / T::kWN, wn = wave % T::kWN;
-    const int q = 8 * (lane >> 4);
+    const long row0 = m0 + wm * T::MF * 16 + (lane & 15);
+    if constexpr (kPairs) {
+        const int n = n0 + 32 * wn + 8 * (lane >> 4);
+        if (n >= p.N / 2)
+            return;
 #pragma unroll
-    for (int m = 0; m < T::MF; ++m) {
-        const long row = m0 + (wm * T::MF + m) * 16 + (lane & 15);
-        if (row >= p.M)
-            continue;
-        float v[2][8];
+        for (int m = 0; m < T::MF; ++m) {
+            float g[8], u[8];
+            eight(tile.acc[m], 0, g);
+            eight(tile.acc[m], 1, u);
+            if (row0 + 16 * m < p.M)
+                f(row0 + 16 * m, n, g, u);
+        }
+    } else {
+        // what four row blocks need is fetched together: their loads would
+        // otherwise wait for the stores before them
+        constexpr int NH = T::NF / 2;
+        const int n = n0 + 16 * T::NF * wn + 8 * (lane >> 4);
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int g = 0; g < T::MF; g += T::GM) {
+            typename F::Pre pre[T::GM][NH];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[h][i] = tile.acc[m][2 * h][i];
-                v[h][4 + i] = tile.acc[m][2 * h + 1][i];
-            }
-        if (p.parts) {
-            float *o = p.parts + ((long)part * p.M + row) * p.N;
+            for (int m = 0; m < T::GM; ++m)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int n = kPairs ? n0 + 32 * wn + q : n0 + 64 * wn + 32 * h + q;
-                if (n < (kPairs ? I : p.N)) {
-                    v4f *d = reinterpret_cast<v4f *>(o + n + (kPairs ? h * I : 0));
-                    d[0] = tile.acc[m][2 * h];
-                    d[1] = tile.acc[m][2 * h + 1];
+                for (int h = 0; h < NH; ++h)
+                    if (n + 32 * h < p.N)
+                        f.fetch(min(row0 + 16 * (g + m), p.M - 1), n + 32 * h, &pre[m][h]);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int m = 0; m < T::GM; ++m)
+#pragma unroll
+                for (int h = 0; h < NH; ++h) {
+                    float v[8];
+                    eight(tile.acc[g + m], h, v);
+                    if (row0 + 16 * (g + m) < p.M && n + 32 * h < p.N)
+                        f(row0 + 16 * (g + m), n + 32 * h, v, pre[m][h]);
                 }
-            }
-        } else if constexpr (kPairs) {
-            const int n = n0 + 32 * wn + q;
-            if (n < I)
-                f(row, n, v[0], v[1]);
-        } else {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int n = n0 + 64 * wn + 32 * h + q;
-                if (n < p.N)
-                    f(row, n, v[h]);
-            }
         }
     }
+}
+
+// The tiles there are; measured with product_cost below.
+template <int DT, bool ADOWN, bool BDOWN>
+struct Tiles {
+    using Huge = Tile<DT, 256, 256, 2, 4, 2, ADOWN, BDOWN>;
+    using HugeHalf = Tile<DT, 128, 256, 2, 4, 2, ADOWN, BDOWN>;
+    using Tall = Tile<DT, 256, 128, 4, 2, 3, ADOWN, BDOWN>;
+    using Even = Tile<DT, 128, 128, 4, 2, 4, ADOWN, BDOWN>;
+    using Flat = Tile<DT, 64, 128, 4, 2, 4, ADOWN, BDOWN>;
+    using Small = Tile<DT, 64, 64, 4, 2, 4, ADOWN, BDOWN>;
+    using Few = Tile<DT, 32, 64, 2, 2, 6, ADOWN, BDOWN>;
+};
+
+template <typename T, bool kPairs, bool ADOWN, bool BDOWN, typename F>
+__global__ void __launch_bounds__(T::kThreads, 1) product_kernel(Product p, F f)
+{
+    __shared__ __align__(1024) uint8_t lds[T::kLds];
+    int im, in;
+    tile_place(tile_run(blockIdx.x, gridDim.x), p.tm, p.tn, &im, &in);
+    whole_tile<T, kPairs, ADOWN, BDOWN>(p, f, (long)im * T::kBM, in, lds);
 }
 
 // `whole` tiles of 256 x 256, then each tile left over as two of 128 rows.
 template <int DT, bool kPairs, bool ADOWN, bool BDOWN, typename F>
 __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2)))
-product_large_kernel(Product p, F f)
+product_huge_kernel(Product p, int whole, F f)
 {
-    using T = Tile<DT, 256, 256, 2, 4, 2, ADOWN, BDOWN>;
-    using H = Tile<DT, 128, 256, 2, 4, 2, ADOWN, BDOWN>;
+    using T = typename Tiles<DT, ADOWN, BDOWN>::Huge;
+    using H = typename Tiles<DT, ADOWN, BDOWN>::HugeHalf;
     __shared__ __align__(1024) uint8_t lds[T::kLds];
     const int b = blockIdx.x;
     int im, in;
-    if (b < p.whole) {
-        tile_place(tile_run(b, p.whole), p.tm, p.tn, &im, &in);
-        product_tile<T, kPairs, ADOWN, BDOWN>(p, f, im * 256l, in, 0, lds);
+    if (b < whole) {
+        tile_place(tile_run(b, whole), p.tm, p.tn, &im, &in);
+        whole_tile<T, kPairs, ADOWN, BDOWN>(p, f, im * 256l, in, lds);
         return;
     }
-    const int h = tile_run(b - p.whole, gridDim.x - p.whole);
-    tile_place(p.whole + (h >> 1), p.tm, p.tn, &im, &in);
+    const int h = tile_run(b - whole, gridDim.x - whole);
+    tile_place(whole + (h >> 1), p.tm, p.tn, &im, &in);
     const long m0 = im * 256l + 128 * (h & 1);
     if (m0 < p.M)
-        product_tile<H, kPairs, ADOWN, BDOWN>(p, f, m0, in, 0, lds);
+        whole_tile<H, kPairs, ADOWN, BDOWN>(p, f, m0, in, lds);
 }
 
-template <int DT, bool kPairs, bool ADOWN, bool BDOWN, typename F>
-__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2)))
-product_small_kernel(Product p, F f)
+// One of `splits` parts of K of a tile, as float32 sums in its plane.
+template <typename T, bool ADOWN, bool BDOWN>
+__global__ void __launch_bounds__(T::kThreads, 1) parts_kernel(Product p)
 {
-    using T = Tile<DT, 128, 128, 2, 2, 2, ADOWN, BDOWN>;
     __shared__ __align__(1024) uint8_t lds[T::kLds];
     const int tiles = p.tm * p.tn, q = tile_run(blockIdx.x, tiles * p.splits);
     const int part = q / tiles;
     int im, in;
     tile_place(q - part * tiles, p.tm, p.tn, &im, &in);
-    product_tile<T, kPairs, ADOWN, BDOWN>(p, f, im * 128l, in, part, lds);
+    T tile;
+    tile_sums<T, false, ADOWN, BDOWN>(tile, p, (long)im * T::kBM, in * T::kBN, part, lds);
+    const int lane = threadIdx.x & 63, wave = tile_wave();
+    const int wm = wave / T::kWN, wn = wave % T::kWN;
+    const int n = in * T::kBN + 16 * T::NF * wn + 8 * (lane >> 4);
+#pragma unroll
+    for (int m = 0; m < T::MF; ++m) {
+        const long row = (long)im * T::kBM + (wm * T::MF + m) * 16 + (lane & 15);
+        if (row >= p.M)
+            continue;
+        v4f *o = reinterpret_cast<v4f *>(p.parts + ((long)part * p.M + row) * p.N + n);
+#pragma unroll
+        for (int h = 0; h < T::NF / 2; ++h)
+            if (n + 32 * h < p.N) {
+                o[8 * h] = tile.acc[m][2 * h];
+                o[8 * h + 1] = tile.acc[m][2 * h + 1];
+            }
+    }
 }
+
+constexpr int kMostParts = 8;
 
 // The functor on the sum of the parts' planes, added in their order; four
 // neighbouring threads take a block of 32 columns.
@@ -308,16 +392,30 @@ __global__ void __launch_bounds__(256) join_kernel(Product p, F f)
     const int n = (int)(i - row * cols) * 8;
     if (row >= p.M)
         return;
+    typename F::Pre pre;
+    f.fetch(row, n, &pre);
     float v[2][8];
+    constexpr int S = kPairs ? 2 : 1;
+    v4f part[S][2][kMostParts];
 #pragma unroll
-    for (int h = 0; h < (kPairs ? 2 : 1); ++h) {
-        v4f lo = {0, 0, 0, 0}, hi = lo;
-        for (int s = 0; s < p.splits; ++s) {
-            const v4f *o = reinterpret_cast<const v4f *>(p.parts + (s * p.M + row) * p.N + n +
-                                                         h * (p.N / 2));
-            lo += o[0];
-            hi += o[1];
-        }
+    for (int s = 0; s < kMostParts; ++s)
+#pragma unroll
+        for (int h = 0; h < S; ++h)
+            if (s < p.splits) {
+                const v4f *o = reinterpret_cast<const v4f *>(p.parts + (s * p.M + row) * p.N + n +
+                                                             h * (p.N / 2));
+                part[h][0][s] = o[0];
+                part[h][1][s] = o[1];
+            }
+#pragma unroll
+    for (int h = 0; h < S; ++h) {
+        v4f lo = part[h][0][0], hi = part[h][1][0];
+#pragma unroll
+        for (int s = 1; s < kMostParts; ++s)
+            if (s < p.splits) {
+                lo += part[h][0][s];
+                hi += part[h][1][s];
+            }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             v[h][k] = lo[k];
@@ -327,62 +425,127 @@ __global__ void __launch_bounds__(256) join_kernel(Product p, F f)
     if constexpr (kPairs)
         f(row, n, v[0], v[1]);
     else
-        f(row, n, v[0]);
+        f(row, n, v[0], pre);
 }
-
-constexpr int kTileCus = 256; // workgroups that fill an MI355X; the workspace goes by it
 
 inline long tiles_up(long n, long by) { return (n + by - 1) / by; }
 
-// How a product of M x N over K is cut (kPairs: N the 2I rows of W13).
+constexpr int kTileCus = 256; // workgroups that fill an MI355X; the workspace goes by it
+
+// How a product of M x N over K is cut.
+enum TileKind { kHuge, kTall, kEven, kFlat, kSmall, kFew, kTileKinds };
+
 struct Cut {
-    bool large;
+    TileKind kind;
     int splits;
 };
 
-inline Cut product_cut(long M, long N, long K)
+inline void tile_sizes(TileKind k, int *bm, int *bn)
 {
-    const long n = tiles_up(M, 128) * tiles_up(N, 128);
-    const bool large = tiles_up(M, 256) * tiles_up(N, 256) >= kTileCus;
-    const long steps = tiles_up(K, 64);
-    int splits = 1;
-    if (!large && n <= 256)
-        splits = (int)std::max(1l, std::min({512 / n, 8l, steps / 8}));
-    return Cut{large, splits};
+    constexpr int m[] = {256, 256, 128, 64, 64, 32}, n[] = {256, 128, 128, 128, 64, 64};
+    *bm = m[k];
+    *bn = n[k];
 }
 
-inline size_t product_parts_bytes(long M, long N, long K)
+// Microseconds of a product: a round of one tile a CU takes its steps of 64 k
+// (us a step: measured alone on the CU) and what stands before and behind
+// them; parts cost their planes and a launch.
+inline float product_cost(TileKind kind, int splits, long M, long N, long K)
 {
-    const Cut c = product_cut(M, N, K);
+    constexpr float step[] = {1.30f, 0.74f, 0.43f, 0.31f, 0.20f, 0.17f};
+    int bm, bn;
+    tile_sizes(kind, &bm, &bn);
+    const long groups = tiles_up(M, bm) * tiles_up(N, bn) * splits;
+    const long steps = tiles_up(tiles_up(K, 64), splits);
+    float us = tiles_up(groups, kTileCus) * (steps * step[kind] + (kind <= kTall ? 5.0f : 2.0f));
+    // bytes of the operands once, at 4.8 TB/s
+    const float read = 2e-6f * (M * K + N * K) / 4.8f;
+    us = std::max(us, read + 2.0f);
+    if (splits > 1)
+        us += 2.5f + 4e-6f * 2 * splits * M * N / 6.0f;
+    return us;
+}
+
+// The cheapest cut.  Pairs need a tile's columns of both halves in a wavefront, which
+// the two smallest tiles lack, unless a join forms them.
+inline Cut product_cut(long M, long N, long K, bool pairs)
+{
+    Cut best{kHuge, 1};
+    float cost = product_cost(kHuge, 1, M, N, K);
+    for (int k = kTall; k < kTileKinds; ++k)
+        for (int s = 1; s <= kMostParts; ++s) {
+            if (s > 1 && (k < kEven || tiles_up(K, 64) < 4 * s || s * M * N > (1l << 25)))
+                continue;
+            if (s == 1 && pairs && k >= kSmall)
+                continue;
+            const float c = product_cost((TileKind)k, s, M, N, K);
+            if (c < cost) {
+                cost = c;
+                best = Cut{(TileKind)k, s};
+            }
+        }
+    return best;
+}
+
+inline size_t product_parts_bytes(long M, long N, long K, bool pairs)
+{
+    const Cut c = product_cut(M, N, K, pairs);
     return c.splits > 1 ? (size_t)c.splits * M * N * sizeof(float) : 0;
 }
 
-// join: the functor with the lane distance of the join kernel.
+// Launches a product; join: the functor with the lane distance of the join
+// kernel.
 template <int DT, bool kPairs, bool ADOWN, bool BDOWN, typename F, typename J>
 hipError_t launch_product(Product p, const F &f, const J &join, float *parts, hipStream_t st)
 {
-    const Cut c = product_cut(p.M, p.N, p.K);
+    using S = Tiles<DT, ADOWN, BDOWN>;
+    const Cut c = product_cut(p.M, p.N, p.K, kPairs);
+    int bm, bn;
+    tile_sizes(c.kind, &bm, &bn);
+    p.tm = (int)tiles_up(p.M, bm);
+    p.tn = (int)tiles_up(p.N, bn);
     p.splits = c.splits;
-    p.parts = c.splits > 1 ? parts : nullptr;
-    if (c.large) {
-        p.tm = (int)tiles_up(p.M, 256);
-        p.tn = (int)tiles_up(p.N, 256);
-        const int cus = kTileCus, left = (int)((long)p.tm * p.tn % cus);
-        const int halves = 2 * left <= cus ? left : 0;
-        p.whole = p.tm * p.tn - halves;
-        product_large_kernel<DT, kPairs, ADOWN, BDOWN>
-            <<<p.tm * p.tn + halves, 512, 0, st>>>(p, f);
+    p.parts = parts;
+    const int n = p.tm * p.tn;
+    const auto whole = [&](auto t) {
+        using T = decltype(t);
+        product_kernel<T, kPairs, ADOWN, BDOWN><<<n, T::kThreads, 0, st>>>(p, f);
+    };
+    const auto part = [&](auto t) {
+        using T = decltype(t);
+        parts_kernel<T, ADOWN, BDOWN><<<n * c.splits, T::kThreads, 0, st>>>(p);
+    };
+    if (c.splits > 1) {
+        if (c.kind == kEven)
+            part(typename S::Even{});
+        else if (c.kind == kFlat)
+            part(typename S::Flat{});
+        else if (c.kind == kSmall)
+            part(typename S::Small{});
+        else
+            part(typename S::Few{});
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+        const long threads = p.M * ((kPairs ? p.N / 2 : p.N) / 8);
+        join_kernel<kPairs><<<(unsigned)tiles_up(threads, 256), 256, 0, st>>>(p, join);
         return hipGetLastError();
     }
-    p.tm = (int)tiles_up(p.M, 128);
-    p.tn = (int)tiles_up(p.N, 128);
-    product_small_kernel<DT, kPairs, ADOWN, BDOWN>
-        <<<p.tm * p.tn * p.splits, 256, 0, st>>>(p, f);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !p.parts)
-        return e;
-    const long threads = p.M * ((kPairs ? p.N / 2 : p.N) / 8);
-    join_kernel<kPairs><<<(unsigned)tiles_up(threads, 256), 256, 0, st>>>(p, join);
+    if (c.kind == kHuge) {
+        const int left = n % kTileCus, halves = 2 * left <= kTileCus ? left : 0;
+        product_huge_kernel<DT, kPairs, ADOWN, BDOWN><<<n + halves, 512, 0, st>>>(p, n - halves, f);
+    } else if (c.kind == kTall) {
+        whole(typename S::Tall{});
+    } else if (c.kind == kEven) {
+        whole(typename S::Even{});
+    } else if (c.kind == kFlat) {
+        whole(typename S::Flat{});
+    } else if constexpr (!kPairs) {
+        if (c.kind == kSmall)
+            whole(typename S::Small{});
+        else
+            whole(typename S::Few{});
+    }
     return hipGetLastError();
 }
 

@@ -4,6 +4,8 @@
 //   dx = dg | du W13,  dW13 = (dg | du)^T x,  dW2 = dout^T h,
 // four products in MFMA tiles.  The first one's epilogue has the activation's
 // gradient and forms h again, so neither dh nor h of the forward pass is kept.
+// The other three need nothing of each other and are one launch, the longest
+// K first: the tiles of the next fill the CUs that the last of one leave idle.
 // Operands that these products need transposed are read from LDS transposed.
 // An x kept as MX FP8 becomes 16-bit rows in the workspace first.
 #include "ffn.hpp"
@@ -27,9 +29,7 @@ BackLayout back_layout(const moe_ffn_shape &s)
     l.h = l.dgu + align256(T * 2 * I * 2);
     l.x = l.h + align256(T * I * 2);
     l.parts = l.x + align256(T * H * 2);
-    l.bytes = l.parts + std::max({product_parts_bytes(T, I, H), product_parts_bytes(T, H, 2 * I),
-                                  product_parts_bytes(2 * I, H, T),
-                                  product_parts_bytes(H, I, T)});
+    l.bytes = l.parts + product_parts_bytes(T, I, H, false);
     return l;
 }
 
@@ -41,9 +41,83 @@ from_mx_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ sc
 {
     for (long i = blockIdx.x * 256l + threadIdx.x; i < pieces; i += gridDim.x * 256l) {
         float f[8];
-        load8_mx(codes + 8 * i, scale[i / 4], f);
+        from_mx(*reinterpret_cast<const uint2 *>(codes + 8 * i), scale[i / 4], f);
         store8<DT>(out + 8 * i, f);
     }
+}
+
+// Up to three products of one launch; job 0 may have A along its rows (dx),
+// the others have both operands down.  first: a job's first workgroup, each a
+// multiple of 8, so that a job's tiles keep their XCDs.
+template <int DT>
+struct Gradients {
+    Product p[3];
+    Put<DT> put[3];
+    int jobs, along; // along: job 0 is dx
+    int first[4];
+};
+
+template <int DT, typename TA, typename TD>
+__global__ void __launch_bounds__(TA::kThreads, 1) gradients_kernel(Gradients<DT> g)
+{
+    __shared__ __align__(1024) uint8_t lds[TA::kLds];
+    int j = 0;
+    while (j + 1 < g.jobs && (int)blockIdx.x >= g.first[j + 1])
+        ++j;
+    const Product &p = g.p[j];
+    const int b = blockIdx.x - g.first[j], n = p.tm * p.tn;
+    if (b >= n)
+        return;
+    int im, in;
+    tile_place(tile_run(b, n), p.tm, p.tn, &im, &in);
+    if (j < g.along)
+        whole_tile<TA, false, kAlong, kDown>(p, g.put[j], (long)im * TA::kBM, in, lds);
+    else
+        whole_tile<TD, false, kDown, kDown>(p, g.put[j], (long)im * TD::kBM, in, lds);
+}
+
+template <int DT>
+hipError_t launch_gradients(Gradients<DT> &g, hipStream_t st)
+{
+    if (g.jobs == 0)
+        return hipSuccess;
+    // all CUs share the tiles' time, and wait for half of the last tile
+    constexpr float step[] = {1.36f, 0.78f, 0.50f};
+    TileKind best = kHuge;
+    float cost = 0.0f;
+    for (int k = kHuge; k <= kEven; ++k) {
+        int bm, bn;
+        tile_sizes((TileKind)k, &bm, &bn);
+        float all = 0.0f, most = 0.0f;
+        for (int j = 0; j < g.jobs; ++j) {
+            const float one = tiles_up(g.p[j].K, 64) * step[k] + (k <= kTall ? 5.0f : 2.0f);
+            all += one * tiles_up(g.p[j].M, bm) * tiles_up(g.p[j].N, bn);
+            most = std::max(most, one);
+        }
+        const float c = std::max(all / kTileCus + 0.5f * most, most);
+        if (k == kHuge || c < cost) {
+            cost = c;
+            best = (TileKind)k;
+        }
+    }
+    int bm, bn, n = 0;
+    tile_sizes(best, &bm, &bn);
+    for (int j = 0; j < g.jobs; ++j) {
+        g.p[j].tm = (int)tiles_up(g.p[j].M, bm);
+        g.p[j].tn = (int)tiles_up(g.p[j].N, bn);
+        g.p[j].splits = 1;
+        g.first[j] = n;
+        n += (g.p[j].tm * g.p[j].tn + 7) / 8 * 8;
+    }
+    using A = Tiles<DT, kAlong, kDown>;
+    using D = Tiles<DT, kDown, kDown>;
+    if (best == kHuge)
+        gradients_kernel<DT, typename A::Huge, typename D::Huge><<<n, 512, 0, st>>>(g);
+    else if (best == kTall)
+        gradients_kernel<DT, typename A::Tall, typename D::Tall><<<n, 512, 0, st>>>(g);
+    else
+        gradients_kernel<DT, typename A::Even, typename D::Even><<<n, 512, 0, st>>>(g);
+    return hipGetLastError();
 }
 
 template <int DT>
@@ -56,11 +130,6 @@ hipError_t backward_of_type(const moe_ffn_shape &s, const uint16_t *dout, const 
     uint16_t *dgu = reinterpret_cast<uint16_t *>(ws + l.dgu);
     uint16_t *h = dw2 ? reinterpret_cast<uint16_t *>(ws + l.h) : nullptr;
     float *parts = reinterpret_cast<float *>(ws + l.parts);
-    const auto dw = [&](void *w, long ld) {
-        return Put<DT>{ld, accumulate && !f32 ? static_cast<const uint16_t *>(w) : nullptr,
-                       f32 ? nullptr : static_cast<uint16_t *>(w),
-                       f32 ? static_cast<float *>(w) : nullptr, accumulate};
-    };
     Product p{};
     p.a = Operand{dout, s.H};
     p.b = Operand{w2, s.I};
@@ -71,47 +140,34 @@ hipError_t backward_of_type(const moe_ffn_shape &s, const uint16_t *dout, const 
     hipError_t e = launch_product<DT, false, kAlong, kDown>(p, back, back, parts, st);
     if (e != hipSuccess)
         return e;
+    const uint16_t *x = static_cast<const uint16_t *>(x_);
+    if (dw13 && x_scale) {
+        uint16_t *to = reinterpret_cast<uint16_t *>(ws + l.x);
+        const long pieces = (long)s.T * s.H / 8;
+        from_mx_kernel<DT><<<(unsigned)std::min(tiles_up(pieces, 256), 4096l), 256, 0, st>>>(
+            static_cast<const uint8_t *>(x_), x_scale, pieces, to);
+        if ((e = hipGetLastError()) != hipSuccess)
+            return e;
+        x = to;
+    }
+    Gradients<DT> g{};
+    const auto job = [&](const Operand &a, const Operand &b, long M, int N, long K, void *out,
+                         bool wide) {
+        uint16_t *o = static_cast<uint16_t *>(out);
+        const bool add = accumulate && out != dx;
+        g.p[g.jobs] = Product{a, b, M, K, N, 0, 0, 1, nullptr};
+        g.put[g.jobs++] = Put<DT>{N, add && !wide ? o : nullptr, wide ? nullptr : o,
+                                  wide ? static_cast<float *>(out) : nullptr, add};
+    };
     if (dx) {
-        p.a = Operand{dgu, 2l * s.I};
-        p.b = Operand{w13, s.H};
-        p.M = s.T;
-        p.N = s.H;
-        p.K = 2l * s.I;
-        const Put<DT> put{s.H, nullptr, dx, nullptr, false};
-        if ((e = launch_product<DT, false, kAlong, kDown>(p, put, put, parts, st)) != hipSuccess)
-            return e;
+        g.along = 1;
+        job(Operand{dgu, 2l * s.I}, Operand{w13, s.H}, s.T, s.H, 2l * s.I, dx, false);
     }
-    if (dw13) {
-        const uint16_t *x = static_cast<const uint16_t *>(x_);
-        if (x_scale) {
-            uint16_t *to = reinterpret_cast<uint16_t *>(ws + l.x);
-            const long pieces = (long)s.T * s.H / 8;
-            from_mx_kernel<DT><<<(unsigned)std::min(tiles_up(pieces, 256), 4096l), 256, 0, st>>>(
-                static_cast<const uint8_t *>(x_), x_scale, pieces, to);
-            if ((e = hipGetLastError()) != hipSuccess)
-                return e;
-            x = to;
-        }
-        p.a = Operand{dgu, 2l * s.I};
-        p.b = Operand{x, s.H};
-        p.M = 2l * s.I;
-        p.N = s.H;
-        p.K = s.T;
-        const Put<DT> put = dw(dw13, s.H);
-        if ((e = launch_product<DT, false, kDown, kDown>(p, put, put, parts, st)) != hipSuccess)
-            return e;
-    }
-    if (dw2) {
-        p.a = Operand{dout, s.H};
-        p.b = Operand{h, s.I};
-        p.M = s.H;
-        p.N = s.I;
-        p.K = s.T;
-        const Put<DT> put = dw(dw2, s.I);
-        if ((e = launch_product<DT, false, kDown, kDown>(p, put, put, parts, st)) != hipSuccess)
-            return e;
-    }
-    return hipSuccess;
+    if (dw13)
+        job(Operand{dgu, 2l * s.I}, Operand{x, s.H}, 2l * s.I, s.H, s.T, dw13, f32);
+    if (dw2)
+        job(Operand{dout, s.H}, Operand{h, s.I}, s.H, s.I, s.T, dw2, f32);
+    return launch_gradients<DT>(g, st);
 }
 
 // The weights' gradients of no rows.

@@ -43,8 +43,8 @@ hipError_t forward_of_type(const moe_ffn_shape &s, const uint16_t *x, const uint
 
 size_t ffn_forward_bytes(const moe_ffn_shape &s)
 {
-    return h_bytes(s) + std::max(product_parts_bytes(s.T, 2 * s.I, s.H),
-                                 product_parts_bytes(s.T, s.H, s.I));
+    return h_bytes(s) + std::max(product_parts_bytes(s.T, 2 * s.I, s.H, true),
+                                 product_parts_bytes(s.T, s.H, s.I, false));
 }
 
 hipError_t launch_ffn_forward(const moe_ffn_shape &s, int dtype, const void *x, const void *w13,

@@ -97,12 +97,15 @@ struct Side {
     static constexpr int kPitch = DOWN ? 2 * ROWS : 128; // LDS bytes of a row
     static constexpr int kPieces = kPitch / 16;
     static constexpr int kRows = 1024 / kPitch; // LDS rows of a load
+    static_assert(kPieces >= 8, "the turns stay inside a row");
 
     // what the 16-byte piece c of LDS row i is moved by
     static __device__ __forceinline__ int turn(int i)
     {
         if (!DOWN)
             return (i >> 1) & 7;
+        if (kPieces == 8) // two rows fill the banks
+            return PERM ? 4 * ((i >> 1) & 1) : 2 * (((i >> 1) & 1) | ((i >> 2) & 2));
         return PERM ? 4 * (i & 3) : 2 * ((i & 3) | ((i >> 1) & 4));
     }
     // LDS row and piece of this lane in load u
@@ -144,7 +147,8 @@ struct Tile {
     static constexpr int kStage = SA::kBytes + SB::kBytes, kLds = NS * kStage;
     // loads per wavefront and step, A's first
     static constexpr int UA = SA::kLoads / NW, UB = SB::kLoads / NW, U = UA + UB;
-    static_assert(MF % 4 == 0 && NF == 4, "blocks in groups of four");
+    static constexpr int GM = MF < 4 ? MF : 4; // row blocks of a phase
+    static_assert(MF % GM == 0 && NF % 2 == 0 && NF <= 4, "whole groups and pairs of blocks");
     static_assert(UA * NW == SA::kLoads && UB * NW == SB::kLoads, "whole loads");
 
     v4f acc[MF][NF];
@@ -279,14 +283,14 @@ struct Tile {
 #pragma unroll
             for (int f = 0; f < NF; ++f)
                 acc[m][f] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-        // The phases of a step: half k of its 64 values, a group of 4 of the
+        // The phases of a step: half k of its 64 values, a group of GM of the
         // wavefront's row blocks.  Phase p multiplies the operands in sets p mod 2
         // (A) and k (B) and reads those of phase p + 1 into the other sets.
-        constexpr int G = MF / 4, P = 2 * G;
+        constexpr int G = MF / GM, P = 2 * G;
         static_assert(P % 2 == 0, "the next step starts with A's set 0");
-        uint4 ao[2][4], bo[2][NF];
+        uint4 ao[2][GM], bo[2][NF];
         const auto read_a = [&](int q, int ph, int buf) {
-            ao[ph & 1][q] = read<SA, ADOWN>(lds + buf * kStage, aoff, (ph % G) * 4 + q, ph / G);
+            ao[ph & 1][q] = read<SA, ADOWN>(lds + buf * kStage, aoff, (ph % G) * GM + q, ph / G);
         };
         const auto read_b = [&](int f, int half, int buf) {
             bo[half][f] = read<SB, BDOWN>(lds + buf * kStage + SA::kBytes, boff, f, half);
@@ -303,17 +307,19 @@ struct Tile {
                     raw_barrier();
                 }
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
+                for (int q = 0; q < GM; ++q) {
                     read_a(q, np, nbuf);
                     if (np % G == 0)
-                        read_b(q, np / G, nbuf);
+#pragma unroll
+                        for (int f = q * NF / GM; f < (q + 1) * NF / GM; ++f)
+                            read_b(f, np / G, nbuf);
                     if (end)
 #pragma unroll
-                        for (int u = q * U / 4; u < (q + 1) * U / 4; ++u)
+                        for (int u = q * U / GM; u < (q + 1) * U / GM; ++u)
                             load(u, min(s + NS, last), buf);
 #pragma unroll
                     for (int f = 0; f < NF; ++f) {
-                        v4f &c = acc[(ph % G) * 4 + q][f];
+                        v4f &c = acc[(ph % G) * GM + q][f];
                         c = mfma16<DT>(bo[ph / G][f], ao[ph & 1][q], c);
                     }
                     __builtin_amdgcn_sched_barrier(0);
@@ -329,7 +335,7 @@ struct Tile {
             raw_barrier();
         }
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+        for (int q = 0; q < GM; ++q)
             read_a(q, 0, 0);
 #pragma unroll
         for (int f = 0; f < NF; ++f)

@@ -29,11 +29,19 @@ __device__ __forceinline__ float logistic(float g)
     return __builtin_amdgcn_rcpf(1.0f + __expf(-g));
 }
 
-// 8 neighbouring values of a 16-bit row, or of an MX FP8 one.
+// 8 (or 4) neighbouring values of a 16-bit row, or of an MX FP8 one.
 template <int DT>
 __device__ __forceinline__ void store8(uint16_t *p, const float *f)
 {
     *reinterpret_cast<uint4 *>(p) = Elem<DT>::pack(f);
+}
+
+template <int DT>
+__device__ __forceinline__ void store4(uint16_t *p, const v4f &v)
+{
+    const float f[8] = {v[0], v[1], v[2], v[3], 0.0f, 0.0f, 0.0f, 0.0f};
+    const uint4 q = Elem<DT>::pack(f);
+    *reinterpret_cast<uint2 *>(p) = uint2{q.x, q.y};
 }
 
 __device__ __forceinline__ void from_mx(const uint2 &codes, uint32_t scale, float *f)
@@ -100,12 +108,26 @@ struct Activate {
         }
         float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float gc = not_above(g[i], gl);
-            v[i] = gc * logistic(gc) * between(u[i], ul);
-        }
+        for (int i = 0; i < 8; ++i)
+            v[i] = one(g[i], u[i]);
         // h is rounded once to the type: the second product's operand
         store8<DT>(h + t * I + j, v);
+    }
+    __device__ __forceinline__ float one(float g, float u) const
+    {
+        const float gc = not_above(g, gl);
+        return gc * logistic(gc) * between(u, ul);
+    }
+    // four columns; kept in the elements' type or not at all
+    __device__ __forceinline__ void four(long t, int j, const v4f &g, const v4f &u) const
+    {
+        if (kept.rows) {
+            uint16_t *r = static_cast<uint16_t *>(kept.rows) + t * 2 * I + j;
+            store4<DT>(r, g);
+            store4<DT>(r + I, u);
+        }
+        store4<DT>(h + t * I + j,
+                   v4f{one(g[0], u[0]), one(g[1], u[1]), one(g[2], u[2]), one(g[3], u[3])});
     }
 };
 
@@ -211,6 +233,16 @@ struct Put {
         }
         store_once(out + at, Elem<DT>::pack(v));
     }
+    // four columns of a 16-bit row
+    __device__ __forceinline__ void four(long m, int n, v4f v) const
+    {
+        const long at = m * ld + n;
+        if (base)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] += Elem<DT>::load(base + at + i);
+        store4<DT>(out + at, v);
+    }
 };
 
 // A product's sizes and operands: C [M, N] over K; tiles tm x tn, K in
@@ -307,14 +339,17 @@ __device__ __forceinline__ void whole_tile(const Product &p, const F &f, long m0
     }
 }
 
-// The tiles there are; measured with product_cost below.
+// The tiles there are; what each costs: product_cost below.  Where B's k lies
+// down its rows, its transpose reads run at half the rate of A's: wavefronts
+// then share B's columns among two rows of them, not four (4,096 x 2,304 over
+// 5,120 by 128 x 128: 107 us, so 124).
 template <int DT, bool ADOWN, bool BDOWN>
 struct Tiles {
+    static constexpr int WM = BDOWN ? 2 : 4, WN = 8 / WM;
     using Huge = Tile<DT, 256, 256, 2, 4, 2, ADOWN, BDOWN>;
-    using HugeHalf = Tile<DT, 128, 256, 2, 4, 2, ADOWN, BDOWN>;
-    using Tall = Tile<DT, 256, 128, 4, 2, 3, ADOWN, BDOWN>;
-    using Even = Tile<DT, 128, 128, 4, 2, 4, ADOWN, BDOWN>;
-    using Flat = Tile<DT, 64, 128, 4, 2, 4, ADOWN, BDOWN>;
+    using Wide = Tile<DT, 128, 256, 2, 4, 3, ADOWN, BDOWN>;
+    using Even = Tile<DT, 128, 128, WM, WN, 4, ADOWN, BDOWN>;
+    using Flat = Tile<DT, 64, 128, WM, WN, 4, ADOWN, BDOWN>;
     using Small = Tile<DT, 64, 64, 4, 2, 4, ADOWN, BDOWN>;
     using Few = Tile<DT, 32, 64, 2, 2, 6, ADOWN, BDOWN>;
 };
@@ -328,26 +363,27 @@ __global__ void __launch_bounds__(T::kThreads, 1) product_kernel(Product p, F f)
     whole_tile<T, kPairs, ADOWN, BDOWN>(p, f, (long)im * T::kBM, in, lds);
 }
 
-// `whole` tiles of 256 x 256, then each tile left over as two of 128 rows.
-template <int DT, bool kPairs, bool ADOWN, bool BDOWN, typename F>
-__global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2)))
-product_huge_kernel(Product p, int whole, F f)
+// `whole` tiles of 256 x 256, and those left over, which would leave CUs idle
+// for a tile's time, as kCut smaller tiles TL each.
+template <typename T, typename TL, bool kPairs, bool ADOWN, bool BDOWN, typename F>
+__global__ void __launch_bounds__(T::kThreads, 1) product_rest_kernel(Product p, int whole, F f)
 {
-    using T = typename Tiles<DT, ADOWN, BDOWN>::Huge;
-    using H = typename Tiles<DT, ADOWN, BDOWN>::HugeHalf;
-    __shared__ __align__(1024) uint8_t lds[T::kLds];
+    constexpr int kMost = TL::kLds > T::kLds ? TL::kLds : T::kLds;
+    constexpr int kDownward = T::kBM / TL::kBM, kCut = kDownward * (T::kBN / TL::kBN);
+    __shared__ __align__(1024) uint8_t lds[kMost];
     const int b = blockIdx.x;
     int im, in;
     if (b < whole) {
         tile_place(tile_run(b, whole), p.tm, p.tn, &im, &in);
-        whole_tile<T, kPairs, ADOWN, BDOWN>(p, f, im * 256l, in, lds);
+        whole_tile<T, kPairs, ADOWN, BDOWN>(p, f, (long)im * T::kBM, in, lds);
         return;
     }
-    const int h = tile_run(b - whole, gridDim.x - whole);
-    tile_place(whole + (h >> 1), p.tm, p.tn, &im, &in);
-    const long m0 = im * 256l + 128 * (h & 1);
-    if (m0 < p.M)
-        whole_tile<H, kPairs, ADOWN, BDOWN>(p, f, m0, in, lds);
+    const int h = tile_run(b - whole, gridDim.x - whole), part = h % kCut;
+    tile_place(whole + h / kCut, p.tm, p.tn, &im, &in);
+    const long m0 = (long)im * T::kBM + part % kDownward * TL::kBM;
+    in = in * (T::kBN / TL::kBN) + part / kDownward;
+    if (m0 < p.M && in * (kPairs ? TL::kBN / 2 : TL::kBN) < (kPairs ? p.N / 2 : p.N))
+        whole_tile<TL, kPairs, ADOWN, BDOWN>(p, f, m0, in, lds);
 }
 
 // One of `splits` parts of K of a tile, as float32 sums in its plane.
@@ -433,7 +469,7 @@ inline long tiles_up(long n, long by) { return (n + by - 1) / by; }
 constexpr int kTileCus = 256; // workgroups that fill an MI355X; the workspace goes by it
 
 // How a product of M x N over K is cut.
-enum TileKind { kHuge, kTall, kEven, kFlat, kSmall, kFew, kTileKinds };
+enum TileKind { kHuge, kWide, kEven, kFlat, kSmall, kFew, kTileKinds };
 
 struct Cut {
     TileKind kind;
@@ -442,27 +478,57 @@ struct Cut {
 
 inline void tile_sizes(TileKind k, int *bm, int *bn)
 {
-    constexpr int m[] = {256, 256, 128, 64, 64, 32}, n[] = {256, 128, 128, 128, 64, 64};
+    constexpr int m[] = {256, 128, 128, 64, 64, 32}, n[] = {256, 256, 128, 128, 64, 64};
     *bm = m[k];
     *bn = n[k];
 }
 
-// Microseconds of a product: a round of one tile a CU takes its steps of 64 k
-// (us a step: measured alone on the CU) and what stands before and behind
-// them; parts cost their planes and a launch.
+// How many smaller tiles the 256 x 256 ones of the last round become each, 0
+// where there is no round before it or it keeps more than half the CUs busy.
+inline int huge_rest(long tiles)
+{
+    const long left = tiles % kTileCus;
+    return tiles < kTileCus || left == 0 || 2 * left > kTileCus ? 0
+           : 4 * left > kTileCus                               ? 2
+                                                               : 4;
+}
+
+// Microseconds of a product.  A CU takes its tiles one after the other: a round
+// costs its steps of 64 k and what stands before and behind them.  The steps of
+// the largest tiles are bound by the matrix instructions, at clocks that fall as
+// more of the CUs are busy (full: the share that is); those of
+// the others by what a CU draws from the L2, about 30 bytes a clock.  The second
+// operand comes from memory at 4.5 TB/s at best.  Parts cost their planes and a
+// launch.  Measured (us, in a row of calls, by the tiles in their order):
+//   8,192 x 4,096 pairs over 7,168    355  409       524
+//   4,096 x 4,608 pairs over 5,120    212  214       241
+//   8,192 x 7,168 over 2,048          199  208       248
+//   4,096 x 5,120 over 2,304          103   93        97
+//   4,096 x 2,304 over 5,120 (down)   133  135       146
+//   1,021 x 2,816 over 2,304           48   26  25    35   30   43
+//   1,021 x 2,304 over 1,408           32   18  17    20   20   25
+//     128 x 7,168 over 2,048                    23    18   13   17
+//      90 x 1,344 over 544                      11     9  6.5  5.8
 inline float product_cost(TileKind kind, int splits, long M, long N, long K)
 {
-    constexpr float step[] = {1.30f, 0.74f, 0.43f, 0.31f, 0.20f, 0.17f};
+    constexpr float step[] = {0.85f, 0.52f, 0.45f, 0.36f, 0.26f, 0.21f};
+    constexpr float more[] = {0.60f, 0.31f, 0.09f, 0.0f, 0.0f, 0.0f}; // where all are busy
+    constexpr float once[] = {7.0f, 5.0f, 3.0f, 2.8f, 2.6f, 2.6f};
     int bm, bn;
     tile_sizes(kind, &bm, &bn);
-    const long groups = tiles_up(M, bm) * tiles_up(N, bn) * splits;
+    long groups = tiles_up(M, bm) * tiles_up(N, bn) * splits;
     const long steps = tiles_up(tiles_up(K, 64), splits);
-    float us = tiles_up(groups, kTileCus) * (steps * step[kind] + (kind <= kTall ? 5.0f : 2.0f));
-    // bytes of the operands once, at 4.8 TB/s
-    const float read = 2e-6f * (M * K + N * K) / 4.8f;
-    us = std::max(us, read + 2.0f);
+    float us = 0.0f;
+    if (kind == kHuge && huge_rest(groups)) {
+        const TileKind k = huge_rest(groups) == 2 ? kWide : kEven;
+        us = steps * (step[k] + 0.8f * more[k]) + once[k];
+        groups -= groups % kTileCus;
+    }
+    const float rounds = (float)tiles_up(groups, kTileCus), full = groups / (rounds * kTileCus);
+    us += rounds * (steps * (step[kind] + full * more[kind]) + once[kind]);
+    us = std::max(us, 2e-6f * N * K / 4.5f + 2.0f);
     if (splits > 1)
-        us += 2.5f + 4e-6f * 2 * splits * M * N / 6.0f;
+        us += 3.0f + 4e-6f * 2 * splits * M * N / 5.0f;
     return us;
 }
 
@@ -472,7 +538,7 @@ inline Cut product_cut(long M, long N, long K, bool pairs)
 {
     Cut best{kHuge, 1};
     float cost = product_cost(kHuge, 1, M, N, K);
-    for (int k = kTall; k < kTileKinds; ++k)
+    for (int k = kWide; k < kTileKinds; ++k)
         for (int s = 1; s <= kMostParts; ++s) {
             if (s > 1 && (k < kEven || tiles_up(K, 64) < 4 * s || s * M * N > (1l << 25)))
                 continue;
@@ -531,11 +597,20 @@ hipError_t launch_product(Product p, const F &f, const J &join, float *parts, hi
         join_kernel<kPairs><<<(unsigned)tiles_up(threads, 256), 256, 0, st>>>(p, join);
         return hipGetLastError();
     }
-    if (c.kind == kHuge) {
-        const int left = n % kTileCus, halves = 2 * left <= kTileCus ? left : 0;
-        product_huge_kernel<DT, kPairs, ADOWN, BDOWN><<<n + halves, 512, 0, st>>>(p, n - halves, f);
-    } else if (c.kind == kTall) {
-        whole(typename S::Tall{});
+    const auto rest = [&](auto t) {
+        using L = decltype(t);
+        const int left = n % kTileCus;
+        product_rest_kernel<typename S::Huge, L, kPairs, ADOWN, BDOWN>
+            <<<n - left + huge_rest(n) * left, 512, 0, st>>>(p, n - left, f);
+    };
+    if (c.kind == kHuge && huge_rest(n) == 2) {
+        rest(typename S::Wide{});
+    } else if (c.kind == kHuge && huge_rest(n) == 4) {
+        rest(typename S::Even{});
+    } else if (c.kind == kHuge) {
+        whole(typename S::Huge{});
+    } else if (c.kind == kWide) {
+        whole(typename S::Wide{});
     } else if (c.kind == kEven) {
         whole(typename S::Even{});
     } else if (c.kind == kFlat) {

@@ -57,10 +57,12 @@ struct Gradients {
     int first[4];
 };
 
-template <int DT, typename TA, typename TD>
+// The last job's tiles are TL.
+template <int DT, typename TA, typename TD, typename TL>
 __global__ void __launch_bounds__(TA::kThreads, 1) gradients_kernel(Gradients<DT> g)
 {
-    __shared__ __align__(1024) uint8_t lds[TA::kLds];
+    constexpr int kMost = TL::kLds > TA::kLds ? TL::kLds : TA::kLds;
+    __shared__ __align__(1024) uint8_t lds[kMost];
     int j = 0;
     while (j + 1 < g.jobs && (int)blockIdx.x >= g.first[j + 1])
         ++j;
@@ -72,8 +74,10 @@ __global__ void __launch_bounds__(TA::kThreads, 1) gradients_kernel(Gradients<DT
     tile_place(tile_run(b, n), p.tm, p.tn, &im, &in);
     if (j < g.along)
         whole_tile<TA, false, kAlong, kDown>(p, g.put[j], (long)im * TA::kBM, in, lds);
-    else
+    else if (j + 1 < g.jobs)
         whole_tile<TD, false, kDown, kDown>(p, g.put[j], (long)im * TD::kBM, in, lds);
+    else
+        whole_tile<TL, false, kDown, kDown>(p, g.put[j], (long)im * TL::kBM, in, lds);
 }
 
 template <int DT>
@@ -81,28 +85,35 @@ hipError_t launch_gradients(Gradients<DT> &g, hipStream_t st)
 {
     if (g.jobs == 0)
         return hipSuccess;
-    // all CUs share the tiles' time, and wait for half of the last tile
-    constexpr float step[] = {1.36f, 0.78f, 0.50f};
-    TileKind best = kHuge;
+    // all CUs share the tiles' time, and wait for half of the last tile: that is
+    // a smaller one where the others are the largest (4,096 x 5,120 by 2,304: , by
+    // 256 x 256 throughout )
+    constexpr float step[] = {1.42f, 0.81f, 0.53f}, once[] = {7.0f, 5.0f, 3.0f};
+    const auto kind_of = [&](int kind, int j) {
+        return kind == kHuge && j + 1 == g.jobs && j >= g.along ? kWide : (TileKind)kind;
+    };
+    int best = kHuge;
     float cost = 0.0f;
     for (int k = kHuge; k <= kEven; ++k) {
         int bm, bn;
-        tile_sizes((TileKind)k, &bm, &bn);
-        float all = 0.0f, most = 0.0f;
+        float all = 0.0f, last = 0.0f, most = 0.0f;
         for (int j = 0; j < g.jobs; ++j) {
-            const float one = tiles_up(g.p[j].K, 64) * step[k] + (k <= kTall ? 5.0f : 2.0f);
-            all += one * tiles_up(g.p[j].M, bm) * tiles_up(g.p[j].N, bn);
-            most = std::max(most, one);
+            const TileKind q = kind_of(k, j);
+            tile_sizes(q, &bm, &bn);
+            last = tiles_up(g.p[j].K, 64) * step[q] + once[q];
+            most = std::max(most, last);
+            all += last * tiles_up(g.p[j].M, bm) * tiles_up(g.p[j].N, bn);
         }
-        const float c = std::max(all / kTileCus + 0.5f * most, most);
+        const float c = std::max(all / kTileCus + 0.5f * last, most);
         if (k == kHuge || c < cost) {
             cost = c;
-            best = (TileKind)k;
+            best = k;
         }
     }
-    int bm, bn, n = 0;
-    tile_sizes(best, &bm, &bn);
+    int n = 0;
     for (int j = 0; j < g.jobs; ++j) {
+        int bm, bn;
+        tile_sizes(kind_of(best, j), &bm, &bn);
         g.p[j].tm = (int)tiles_up(g.p[j].M, bm);
         g.p[j].tn = (int)tiles_up(g.p[j].N, bn);
         g.p[j].splits = 1;
@@ -112,11 +123,14 @@ hipError_t launch_gradients(Gradients<DT> &g, hipStream_t st)
     using A = Tiles<DT, kAlong, kDown>;
     using D = Tiles<DT, kDown, kDown>;
     if (best == kHuge)
-        gradients_kernel<DT, typename A::Huge, typename D::Huge><<<n, 512, 0, st>>>(g);
-    else if (best == kTall)
-        gradients_kernel<DT, typename A::Tall, typename D::Tall><<<n, 512, 0, st>>>(g);
+        gradients_kernel<DT, typename A::Huge, typename D::Huge, typename D::Wide>
+            <<<n, 512, 0, st>>>(g);
+    else if (best == kWide)
+        gradients_kernel<DT, typename A::Wide, typename D::Wide, typename D::Wide>
+            <<<n, 512, 0, st>>>(g);
     else
-        gradients_kernel<DT, typename A::Even, typename D::Even><<<n, 512, 0, st>>>(g);
+        gradients_kernel<DT, typename A::Even, typename D::Even, typename D::Even>
+            <<<n, 512, 0, st>>>(g);
     return hipGetLastError();
 }
 

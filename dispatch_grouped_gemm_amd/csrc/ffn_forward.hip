@@ -13,6 +13,215 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 size_t h_bytes(const moe_ffn_shape &s) { return align256((size_t)s.T * s.I * 2); }
 
+// ---------------------------------------------------------------------------
+// Few rows (up to 32): 16 MB rows by 32 rows of a weight, bound by reading the
+// weight once.  Eight wavefronts: two take 16 weight rows each, four a quarter
+// of every step's 256 k, so a CU has a whole tile's K without parts of it in
+// memory, and the activation is done where the sums meet, in LDS.  A step is
+// 512 neighbouring bytes of every row; NS stages keep 72 KB or more in flight.
+// The first product takes 16 gate rows and the 16 up rows of the same I.
+// ---------------------------------------------------------------------------
+template <int MB, int NB>
+struct FewRows {
+    static constexpr int kStepK = 256, kRow = 2 * kStepK; // bytes of a row's step
+    static constexpr int kX = 16 * MB * kRow, kW = 32 * NB * kRow, kStage = kX + kW;
+    static constexpr int NS = NB == 2 ? 3 : MB == 1 ? 5 : 4, kLds = NS * kStage;
+    static constexpr int UX = kX / 1024 / 8, UW = kW / 1024 / 8, U = UX + UW;
+    static_assert(UX * 8192 == kX && UW * 8192 == kW, "whole loads");
+};
+
+struct FewProduct {
+    const uint16_t *x, *w;
+    int T, K;
+};
+
+// The sums of weight rows w_row(0 .. 32 NB - 1), in LDS: few_sum(b, m) is then a
+// lane's rows 16 m + lane mod 16 by columns 4 (lane div 16) .. + 3 of block b of 16.
+template <int DT, int MB, int NB, typename R>
+__device__ __forceinline__ void few_sums(const FewProduct &p, R w_row, uint8_t *lds)
+{
+    using F = FewRows<MB, NB>;
+    const int lane = threadIdx.x & 63, wave = tile_wave();
+    const int slice = wave & 3, block = (wave >> 2) * NB;
+    const uint32_t l0 = lds_addr(lds);
+    // a load: two rows' steps, pieces stored at piece ^ (row mod 16), so that the
+    // 16 rows that an operand read touches lie in different banks
+    const uint8_t *base[F::U];
+    uint32_t row[F::U];
+    int k8[F::U];
+#pragma unroll
+    for (int u = 0; u < F::U; ++u) {
+        const int q = u < F::UX ? wave * F::UX + u : wave * F::UW + u - F::UX;
+        const int i = 2 * q + (lane >> 5);
+        k8[u] = ((lane & 31) ^ (i & 15)) * 8;
+        const auto of = [&](int r) { return u < F::UX ? (long)min(r, p.T - 1) : w_row(r); };
+        base[u] = uniform_ptr(reinterpret_cast<const uint8_t *>((u < F::UX ? p.x : p.w) +
+                                                                of(2 * q) * p.K));
+        row[u] = (uint32_t)((of(i) - of(2 * q)) * p.K * 2);
+    }
+    const int steps = (p.K + F::kStepK - 1) / F::kStepK;
+    const auto load = [&](int step, int buf) {
+        step = min(step, steps - 1);
+#pragma unroll
+        for (int u = 0; u < F::U; ++u) {
+            // past a row's end its last piece, which no product takes
+            const uint32_t v = row[u] + 2 * min(step * F::kStepK + k8[u], p.K - 8);
+            if (u < F::UX)
+                g2lds<16>(base[u], v, l0 + buf * F::kStage + (wave * F::UX + u) * 1024);
+            else
+                g2lds<16, true>(base[u], v, l0 + buf * F::kStage + F::kX +
+                                                (wave * F::UW + u - F::UX) * 1024);
+        }
+    };
+    const int i = lane & 15;
+    const auto read = [&](const uint8_t *rows, int half) {
+        return *reinterpret_cast<const uint4 *>(
+            rows + i * F::kRow + ((8 * slice + 4 * half + (lane >> 4)) ^ i) * 16);
+    };
+    v4f acc[NB][MB];
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int m = 0; m < MB; ++m)
+            acc[n][m] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int s = 0; s < F::NS - 1; ++s)
+        load(s, s);
+    int buf = 0;
+    for (int s = 0; s < steps; ++s) {
+        // the step has landed; the one before it is done with everywhere, and its
+        // stage takes the next load
+        tile_wait<(F::NS - 2) * F::U>();
+        raw_barrier();
+        const uint8_t *st = lds + buf * F::kStage;
+        uint4 wq[2][NB], xq[2][MB];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+                wq[h][n] = read(st + F::kX + (block + n) * 16 * F::kRow, h);
+#pragma unroll
+            for (int m = 0; m < MB; ++m)
+                xq[h][m] = read(st + m * 16 * F::kRow, h);
+        }
+        load(s + F::NS - 1, buf == 0 ? F::NS - 1 : buf - 1);
+        buf = buf + 1 == F::NS ? 0 : buf + 1;
+        // (K is a multiple of 32: a half's k are all there or none)
+        const int k = s * F::kStepK + 64 * slice;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (k + 32 * h < p.K)
+#pragma unroll
+                for (int n = 0; n < NB; ++n)
+#pragma unroll
+                    for (int m = 0; m < MB; ++m)
+                        acc[n][m] = mfma16<DT>(wq[h][n], xq[h][m], acc[n][m]);
+    }
+    tile_wait<0>();
+    raw_barrier();
+    v4f *part = reinterpret_cast<v4f *>(lds); // [block][m][slice][lane]
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int m = 0; m < MB; ++m)
+            part[(((block + n) * MB + m) * 4 + slice) * 64 + lane] = acc[n][m];
+    __syncthreads();
+}
+
+template <int MB>
+__device__ __forceinline__ v4f few_sum(const uint8_t *lds, int b, int m)
+{
+    const v4f *q = reinterpret_cast<const v4f *>(lds) + (b * MB + m) * 256 + (threadIdx.x & 63);
+    return ((q[0] + q[64]) + q[128]) + q[192];
+}
+
+template <int DT, int MB>
+__global__ void __launch_bounds__(512) few_gate_up_kernel(FewProduct p, Activate<DT, 16> f)
+{
+    __shared__ __align__(1024) uint8_t lds[FewRows<MB, 1>::kLds];
+    const int j0 = tile_run(blockIdx.x, gridDim.x) * 16, lane = threadIdx.x & 63;
+    few_sums<DT, MB, 1>(p, [&](int i) { return (long)(i >> 4) * f.I + j0 + (i & 15); }, lds);
+    const int wave = tile_wave();
+    const long t = 16 * wave + (lane & 15);
+    if (wave < MB && t < p.T)
+        f.four(t, j0 + 4 * (lane >> 4), few_sum<MB>(lds, 0, wave), few_sum<MB>(lds, 1, wave));
+}
+
+// The same sums by 32 columns, whose MX FP8 blocks are then whole: a wavefront
+// has a row's block in the four lanes 16 apart.
+template <int DT, int MB>
+__global__ void __launch_bounds__(512) few_gate_up_mx_kernel(FewProduct p, Activate<DT, 16> f)
+{
+    __shared__ __align__(1024) uint8_t lds[FewRows<MB, 2>::kLds];
+    const int j0 = tile_run(blockIdx.x, gridDim.x) * 32, lane = threadIdx.x & 63;
+    few_sums<DT, MB, 2>(p, [&](int i) { return (long)(i >> 5) * f.I + j0 + (i & 31); }, lds);
+    const int wave = tile_wave();
+    const long t = 16 * wave + (lane & 15);
+    if (wave >= MB || t >= p.T)
+        return;
+    // 8 neighbouring columns a lane: those of two lanes of the sums
+    float v[2][8];
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int c = lane >> 4, b = 2 * n + (c >> 1), from = 2 * (c & 1) + i;
+            const v4f *q = reinterpret_cast<const v4f *>(lds) + (b * MB + wave) * 256 +
+                           16 * from + (lane & 15);
+            const v4f s = ((q[0] + q[64]) + q[128]) + q[192];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                v[n][4 * i + k] = s[k];
+        }
+    f(t, j0 + 8 * (lane >> 4), v[0], v[1]);
+}
+
+template <int DT, int MB>
+__global__ void __launch_bounds__(512) few_out_kernel(FewProduct p, Put<DT> f)
+{
+    __shared__ __align__(1024) uint8_t lds[FewRows<MB, 1>::kLds];
+    const int n0 = tile_run(blockIdx.x, gridDim.x) * 32, lane = threadIdx.x & 63;
+    few_sums<DT, MB, 1>(p, [&](int i) { return (long)(n0 + i); }, lds);
+    const int wave = tile_wave(), m = wave % MB, b = wave / MB;
+    const long t = 16 * m + (lane & 15);
+    if (b < 2 && t < p.T)
+        f.four(t, n0 + 16 * b + 4 * (lane >> 4), few_sum<MB>(lds, b, m));
+}
+
+// Whether few rows by 32 of N weight rows a workgroup beat the tiles: each draws
+// its part of the weight at some 48 KB a us, so they need to be many (14 x 1,216
+// gate and up rows over 6,304, 38 workgroups: 11 us, by tiles with K in parts 8;
+// 4,608 rows over 5,120 12 and 15).
+bool few_pay(const moe_ffn_shape &s, long N, long K, bool pairs)
+{
+    if (s.T > 32)
+        return false;
+    const float memory = 2e-6f * N * K / 4.5f;
+    const float us = std::max(tiles_up(N / 32, kTileCus) * 64e-3f * K / 48.0f, memory) + 2.5f;
+    const Cut c = product_cut(s.T, N, K, pairs);
+    return us <= product_cost(c.kind, c.splits, s.T, N, K);
+}
+
+template <int DT, int MB>
+hipError_t few_gate_up(const moe_ffn_shape &s, const uint16_t *x, const uint16_t *w13,
+                       const Activate<DT, 16> &act, hipStream_t st)
+{
+    const FewProduct p{x, w13, s.T, s.H};
+    if (act.kept.scale)
+        few_gate_up_mx_kernel<DT, MB><<<s.I / 32, 512, 0, st>>>(p, act);
+    else
+        few_gate_up_kernel<DT, MB><<<s.I / 16, 512, 0, st>>>(p, act);
+    return hipGetLastError();
+}
+
+template <int DT, int MB>
+hipError_t few_out(const moe_ffn_shape &s, const uint16_t *h, const uint16_t *w2,
+                   const Put<DT> &put, hipStream_t st)
+{
+    few_out_kernel<DT, MB><<<s.H / 32, 512, 0, st>>>(FewProduct{h, w2, s.T, s.I}, put);
+    return hipGetLastError();
+}
+
 template <int DT>
 hipError_t forward_of_type(const moe_ffn_shape &s, const uint16_t *x, const uint16_t *w13,
                            const uint16_t *w2, const uint16_t *base, const Kept &kept,
@@ -20,22 +229,30 @@ hipError_t forward_of_type(const moe_ffn_shape &s, const uint16_t *x, const uint
 {
     uint16_t *h = reinterpret_cast<uint16_t *>(ws);
     float *parts = reinterpret_cast<float *>(ws + h_bytes(s));
+    const Activate<DT, 16> act{s.I, s.gate_limit, s.up_limit, kept, h};
+    const Put<DT> put{s.H, base, out, nullptr, false};
     Product p{};
-    p.a = Operand{x, s.H};
-    p.b = Operand{w13, s.H};
     p.M = s.T;
-    p.N = 2 * s.I;
-    p.K = s.H;
-    hipError_t e = launch_product<DT, true, kAlong, kAlong>(
-        p, Activate<DT, 16>{s.I, s.gate_limit, s.up_limit, kept, h},
-        Activate<DT, 1>{s.I, s.gate_limit, s.up_limit, kept, h}, parts, st);
+    hipError_t e;
+    if (few_pay(s, 2l * s.I, s.H, true)) {
+        e = s.T <= 16 ? few_gate_up<DT, 1>(s, x, w13, act, st)
+                      : few_gate_up<DT, 2>(s, x, w13, act, st);
+    } else {
+        p.a = Operand{x, s.H};
+        p.b = Operand{w13, s.H};
+        p.N = 2 * s.I;
+        p.K = s.H;
+        e = launch_product<DT, true, kAlong, kAlong>(
+            p, act, Activate<DT, 1>{s.I, s.gate_limit, s.up_limit, kept, h}, parts, st);
+    }
     if (e != hipSuccess)
         return e;
+    if (few_pay(s, s.H, s.I, false))
+        return s.T <= 16 ? few_out<DT, 1>(s, h, w2, put, st) : few_out<DT, 2>(s, h, w2, put, st);
     p.a = Operand{h, s.I};
     p.b = Operand{w2, s.I};
     p.N = s.H;
     p.K = s.I;
-    const Put<DT> put{s.H, base, out, nullptr, false};
     return launch_product<DT, false, kAlong, kAlong>(p, put, put, parts, st);
 }
 

@@ -320,9 +320,9 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(NShape s, Backward 
     }
 }
 
-// out[h] = the sum of the groups' planes: 4 wavefronts of 64 columns take a
-// quarter of the planes each.
-__global__ void __launch_bounds__(256)
+// out[h] = the sum of the groups' planes: 64 columns a workgroup, 16 wavefronts
+// with a part of the planes each, their loads in flight together.
+__global__ void __launch_bounds__(1024)
 norm_planes_kernel(int H, int groups, const float *part0, const float *part1, float *out0,
                    float *out1)
 {
@@ -330,16 +330,31 @@ norm_planes_kernel(int H, int groups, const float *part0, const float *part1, fl
     float *out = blockIdx.y ? out1 : out0;
     if (!out)
         return;
-    __shared__ float lds[4][64];
+    __shared__ float lds[16][64];
     const int lane = threadIdx.x & 63, q = threadIdx.x >> 6, h = blockIdx.x * 64 + lane;
     float sum = 0.0f;
-    if (h < H)
-        for (int g = groups * q / 4; g < groups * (q + 1) / 4; ++g)
+    if (h < H) {
+        const int end = groups * (q + 1) / 16;
+        int g = groups * q / 16;
+        for (; g + 8 <= end; g += 8) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = part[(long)(g + i) * H + h];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                sum += v[i];
+        }
+        for (; g < end; ++g)
             sum += part[(long)g * H + h];
+    }
     lds[q][lane] = sum;
     __syncthreads();
-    if (q == 0 && h < H)
-        out[h] = (lds[0][lane] + lds[1][lane]) + (lds[2][lane] + lds[3][lane]);
+    if (q == 0 && h < H) {
+        for (int w = 1; w < 16; ++w)
+            sum += lds[w][lane];
+        out[h] = sum;
+    }
 }
 
 // Threads and pieces a thread for a row of `pieces` (H up to 16,384: at most 4).
@@ -434,7 +449,7 @@ hipError_t launch_norm_backward(const moe_norm_shape &sh, int dtype, const void 
             return e;
     }
     if (dw_pre || dw_post) // of no rows: zeros
-        norm_planes_kernel<<<dim3((s.H + 63) / 64, 2), 256, 0, st>>>(s.H, groups, pre, post,
+        norm_planes_kernel<<<dim3((s.H + 63) / 64, 2), 1024, 0, st>>>(s.H, groups, pre, post,
                                                                     dw_pre, dw_post);
     return hipGetLastError();
 }

@@ -865,6 +865,17 @@ def moe_forward_persistent(shape: MoeShape, x_fp8, x_scale, topk_ids, topk_w, w1
 _ELEM = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
+def _address(t, shape, dtype, index) -> int:
+    """The first call loads the built checks and puts them in this function's place."""
+    global _address
+    if not os.path.exists(os.path.join(_HERE, "_checks.so")):
+        raise RuntimeError(
+            "_checks.so is not built; run `python -m dispatch_grouped_gemm_amd._build`")
+    from ._checks import address
+    _address = address
+    return address(t, shape, dtype, index)
+
+
 def _elem(t: torch.Tensor, name: str, most: int = 2):
     """The element code, dtype and device that a call's other tensors share."""
     if not isinstance(t, torch.Tensor):
@@ -879,11 +890,20 @@ def _elem(t: torch.Tensor, name: str, most: int = 2):
 
 
 def _at(t, name: str, shape: tuple, dtype, device) -> int:
-    """_ptr for one dtype; these calls are short enough for its time to count."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device
-            and t.shape == shape and t.is_contiguous()):
-        return t.data_ptr()
-    return _ptr(t, name, shape, {dtype}, device)
+    """_ptr for one dtype; these calls are short enough for its time to count, so the
+    comparisons are made in C++ (csrc/checks.cpp)."""
+    p = _address(t, shape, dtype, device.index)
+    return p if p >= 0 else _ptr(t, name, shape, {dtype}, device)
+
+
+def _space(workspace, device):
+    """Pointer and bytes of a workspace."""
+    if isinstance(workspace, torch.Tensor):
+        n = workspace.numel()
+        p = _address(workspace, (n,), torch.uint8, device.index)
+        if p >= 0:
+            return p, n
+    return _ptr(workspace, "workspace", None, {torch.uint8}, device), workspace.numel()
 
 
 def _kept(shape, name: str, make):
@@ -900,7 +920,10 @@ def _kept(shape, name: str, make):
 
 
 def _ref(shape):
-    return _kept(shape, "c_ref", lambda s: ctypes.byref(s.c()))
+    try:
+        return shape._calls["c_ref"]
+    except (AttributeError, KeyError):
+        return _kept(shape, "c_ref", lambda s: ctypes.byref(s.c()))
 
 
 def _row_sizes(shape: MoeShape):
@@ -1032,7 +1055,7 @@ def moe_adapter_project(shape: AdapterShape, x, w, adapter_ids, a, b, scale, out
             _at(a, "a", (L, r, H), dt, dev), _at(b, "b", (L, N, r), dt, dev),
             None if scale is None else _at(scale, "scale", (L,), torch.float32, dev),
             _at(out, "out", (T, N), dt, dev),
-            _ptr(workspace, "workspace", None, {torch.uint8}, dev), workspace.numel())
+            *_space(workspace, dev))
 
 
 # ---- the dense feed-forward block, the residual joint ------------------------------
@@ -1040,7 +1063,10 @@ def moe_adapter_project(shape: AdapterShape, x, w, adapter_ids, a, b, scale, out
 
 def _given(t, name: str, shape: tuple, dtype, device):
     """_at, or NULL for None."""
-    return None if t is None else _at(t, name, shape, dtype, device)
+    if t is None:
+        return None
+    p = _address(t, shape, dtype, device.index)
+    return p if p >= 0 else _ptr(t, name, shape, {dtype}, device)
 
 
 def _mx_pair(rows, scale, name: str, shape: tuple, device):
@@ -1078,7 +1104,7 @@ def moe_ffn_forward(shape: FfnShape, x, w13, w2, out, workspace, base=None, gate
     _launch("moe_ffn_forward", dev, stream, _ref(shape), code, _at(x, "x", (T, H), dt, dev),
             _at(w13, "w13", (2 * I, H), dt, dev), _at(w2, "w2", (H, I), dt, dev),
             _given(base, "base", (T, H), dt, dev), *kept, _at(out, "out", (T, H), dt, dev),
-            _ptr(workspace, "workspace", None, {torch.uint8}, dev), workspace.numel())
+            *_space(workspace, dev))
 
 
 def moe_ffn_backward(shape: FfnShape, dout, x, w13, w2, gate_up, dx, dw13, dw2, workspace,
@@ -1110,7 +1136,7 @@ def moe_ffn_backward(shape: FfnShape, dout, x, w13, w2, gate_up, dx, dw13, dw2, 
             _at(w2, "w2", (H, I), dt, dev), *kept, _given(dx, "dx", (T, H), dt, dev),
             _given(dw13, "dw13", (2 * I, H), dw_dt, dev), _given(dw2, "dw2", (H, I), dw_dt, dev),
             _ELEM[dw_dt], 1 if accumulate else 0,
-            _ptr(workspace, "workspace", None, {torch.uint8}, dev), workspace.numel())
+            *_space(workspace, dev))
 
 
 def moe_norm_check(shape: NormShape) -> int:
@@ -1156,9 +1182,7 @@ def moe_norm_backward(shape: NormShape, dnormed, res, w_pre, dx, dw_pre, workspa
     t = dnormed if dnormed is not None else dres
     code, dt, dev = _elem(t, "dnormed" if dnormed is not None else "dres")
     tok, w, f32 = (shape.T, shape.H), (shape.H,), torch.float32
-    ws = (None, 0)
-    if workspace is not None:
-        ws = _ptr(workspace, "workspace", None, {torch.uint8}, dev), workspace.numel()
+    ws = (None, 0) if workspace is None else _space(workspace, dev)
     _launch("moe_norm_backward", dev, stream, _ref(shape), code,
             _given(dnormed, "dnormed", tok, dt, dev), _given(dres, "dres", tok, dt, dev),
             _given(res, "res", tok, dt, dev), _given(y, "y", tok, dt, dev),

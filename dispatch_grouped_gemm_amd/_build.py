@@ -1,4 +1,5 @@
-"""Ahead-of-time build of libmoe_a8w4.so for gfx950 with hipcc."""
+"""Ahead-of-time build of libmoe_a8w4.so for gfx950 with hipcc, and of the binding's tensor
+checks with the host compiler."""
 
 from __future__ import annotations
 
@@ -13,6 +14,8 @@ BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["api.hip", "dispatch.hip", "quant.hip", "gemm_skinny.hip", "gemm_tiled.hip",
            "gemm_stream.hip", "combine.hip", "route.hip", "rows.hip", "adapter.hip",
            "ffn_forward.hip", "ffn_backward.hip", "norm.hip"]
+CHECKS = os.path.join(HERE, "_checks.so")
+CXX = os.environ.get("CXX", "g++")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall",
@@ -22,13 +25,31 @@ FLAGS = [
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(CHECKS):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CHECKS))
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
     deps.append(os.path.join(HERE, "..", "include", "moe_a8w4.h"))
     deps.append(os.path.abspath(__file__))
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _build_checks() -> None:
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    tmp = CHECKS + ".tmp%d" % os.getpid()
+    dirs = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"]]
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+           *["-isystem" + d for d in dirs], os.path.join(CSRC, "checks.cpp"), "-o", tmp,
+           "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("%s failed for checks.cpp:\n%s%s" % (CXX, r.stdout, r.stderr))
+    os.replace(tmp, CHECKS)
 
 
 def build(force: bool = True, verbose: bool = False) -> str:
@@ -48,7 +69,9 @@ def build(force: bool = True, verbose: bool = False) -> str:
         return obj
 
     with ThreadPoolExecutor(max_workers=min(8, len(SOURCES))) as ex:
+        checks = ex.submit(_build_checks)
         objs = list(ex.map(compile_one, SOURCES))
+        checks.result()
     tmp = LIB + ".tmp%d" % os.getpid()
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)

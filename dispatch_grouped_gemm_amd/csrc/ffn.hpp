@@ -528,7 +528,7 @@ inline float product_cost(TileKind kind, int splits, long M, long N, long K)
     us += rounds * (steps * (step[kind] + full * more[kind]) + once[kind]);
     us = std::max(us, 2e-6f * N * K / 4.5f + 2.0f);
     if (splits > 1)
-        us += 3.0f + 4e-6f * 2 * splits * M * N / 5.0f;
+        us += 4.0f + 4e-6f * 2 * splits * M * N / 5.0f;
     return us;
 }
 

@@ -4,8 +4,8 @@
 //   dx = dg | du W13,  dW13 = (dg | du)^T x,  dW2 = dout^T h,
 // four products in MFMA tiles.  The first one's epilogue has the activation's
 // gradient and forms h again, so neither dh nor h of the forward pass is kept.
-// The other three need nothing of each other and are one launch, the longest
-// K first: the tiles of the next fill the CUs that the last of one leave idle.
+// The other three need nothing of each other and are one launch: the tiles of
+// the next fill the CUs that the last of one leave idle.
 // Operands that these products need transposed are read from LDS transposed.
 // An x kept as MX FP8 becomes 16-bit rows in the workspace first.
 #include "ffn.hpp"
@@ -86,8 +86,9 @@ hipError_t launch_gradients(Gradients<DT> &g, hipStream_t st)
     if (g.jobs == 0)
         return hipSuccess;
     // all CUs share the tiles' time, and wait for half of the last tile: that is
-    // a smaller one where the others are the largest (4,096 x 5,120 by 2,304: , by
-    // 256 x 256 throughout )
+    // a smaller one where the others are the largest (8,192 x 7,168 by 2,048: 926
+    // us, by 256 x 256 throughout 955; with dx, the larger job, last and so in
+    // smaller tiles 974)
     constexpr float step[] = {1.42f, 0.81f, 0.53f}, once[] = {7.0f, 5.0f, 3.0f};
     const auto kind_of = [&](int kind, int j) {
         return kind == kHuge && j + 1 == g.jobs && j >= g.along ? kWide : (TileKind)kind;

@@ -14,7 +14,7 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 size_t h_bytes(const moe_ffn_shape &s) { return align256((size_t)s.T * s.I * 2); }
 
 // ---------------------------------------------------------------------------
-// Few rows (up to 32): 16 MB rows by 32 rows of a weight, bound by reading the
+// Few rows (up to 64): 16 MB rows by 32 rows of a weight, bound by reading the
 // weight once.  Eight wavefronts: two take 16 weight rows each, four a quarter
 // of every step's 256 k, so a CU has a whole tile's K without parts of it in
 // memory, and the activation is done where the sums meet, in LDS.  A step is
@@ -25,7 +25,8 @@ template <int MB, int NB>
 struct FewRows {
     static constexpr int kStepK = 256, kRow = 2 * kStepK; // bytes of a row's step
     static constexpr int kX = 16 * MB * kRow, kW = 32 * NB * kRow, kStage = kX + kW;
-    static constexpr int NS = NB == 2 ? 3 : MB == 1 ? 5 : 4, kLds = NS * kStage;
+    static constexpr int NS = MB == 4 ? (NB == 2 ? 2 : 3) : NB == 2 ? 3 : MB == 1 ? 5 : 4;
+    static constexpr int kLds = NS * kStage;
     static constexpr int UX = kX / 1024 / 8, UW = kW / 1024 / 8, U = UX + UW;
     static_assert(UX * 8192 == kX && UW * 8192 == kW, "whole loads");
 };
@@ -184,41 +185,37 @@ __global__ void __launch_bounds__(512) few_out_kernel(FewProduct p, Put<DT> f)
     few_sums<DT, MB, 1>(p, [&](int i) { return (long)(n0 + i); }, lds);
     const int wave = tile_wave(), m = wave % MB, b = wave / MB;
     const long t = 16 * m + (lane & 15);
-    if (b < 2 && t < p.T)
+    if (b < 2 && t < p.T) // (eight wavefronts: 2 MB at most)
         f.four(t, n0 + 16 * b + 4 * (lane >> 4), few_sum<MB>(lds, b, m));
 }
 
 // Whether few rows by 32 of N weight rows a workgroup beat the tiles: each draws
-// its part of the weight at some 48 KB a us, so they need to be many (14 x 1,216
-// gate and up rows over 6,304, 38 workgroups: 11 us, by tiles with K in parts 8;
-// 4,608 rows over 5,120 12 and 15).
+// its rows of x and of the weight at some 72 KB a us, so they need to be many and
+// the rows few (14 x 1,216 gate and up rows over 6,304, 38 workgroups: 11 us, by
+// tiles with K in parts 8; 4,608 rows over 5,120 12 and 15).
+int few_blocks(int T) { return T <= 16 ? 1 : T <= 32 ? 2 : 4; }
+
 bool few_pay(const moe_ffn_shape &s, long N, long K, bool pairs)
 {
-    if (s.T > 32)
+    if (s.T > 64)
         return false;
-    const float memory = 2e-6f * N * K / 4.5f;
-    const float us = std::max(tiles_up(N / 32, kTileCus) * 64e-3f * K / 48.0f, memory) + 2.5f;
+    const float memory = 2e-6f * N * K / 4.5f, drawn = 2e-3f * (16 * few_blocks(s.T) + 32) * K;
+    const float us = std::max(tiles_up(N / 32, kTileCus) * drawn / 72.0f, memory) + 2.5f;
     const Cut c = product_cut(s.T, N, K, pairs);
     return us <= product_cost(c.kind, c.splits, s.T, N, K);
 }
 
-template <int DT, int MB>
-hipError_t few_gate_up(const moe_ffn_shape &s, const uint16_t *x, const uint16_t *w13,
-                       const Activate<DT, 16> &act, hipStream_t st)
+// f with the 16-row blocks of T as a constant.
+template <typename F>
+hipError_t with_blocks(int T, F f)
 {
-    const FewProduct p{x, w13, s.T, s.H};
-    if (act.kept.scale)
-        few_gate_up_mx_kernel<DT, MB><<<s.I / 32, 512, 0, st>>>(p, act);
+    const int n = few_blocks(T);
+    if (n == 1)
+        f(std::integral_constant<int, 1>{});
+    else if (n == 2)
+        f(std::integral_constant<int, 2>{});
     else
-        few_gate_up_kernel<DT, MB><<<s.I / 16, 512, 0, st>>>(p, act);
-    return hipGetLastError();
-}
-
-template <int DT, int MB>
-hipError_t few_out(const moe_ffn_shape &s, const uint16_t *h, const uint16_t *w2,
-                   const Put<DT> &put, hipStream_t st)
-{
-    few_out_kernel<DT, MB><<<s.H / 32, 512, 0, st>>>(FewProduct{h, w2, s.T, s.I}, put);
+        f(std::integral_constant<int, 4>{});
     return hipGetLastError();
 }
 
@@ -235,8 +232,14 @@ hipError_t forward_of_type(const moe_ffn_shape &s, const uint16_t *x, const uint
     p.M = s.T;
     hipError_t e;
     if (few_pay(s, 2l * s.I, s.H, true)) {
-        e = s.T <= 16 ? few_gate_up<DT, 1>(s, x, w13, act, st)
-                      : few_gate_up<DT, 2>(s, x, w13, act, st);
+        const FewProduct q{x, w13, s.T, s.H};
+        e = with_blocks(s.T, [&](auto mb) {
+            constexpr int MB = decltype(mb)::value;
+            if (kept.scale)
+                few_gate_up_mx_kernel<DT, MB><<<s.I / 32, 512, 0, st>>>(q, act);
+            else
+                few_gate_up_kernel<DT, MB><<<s.I / 16, 512, 0, st>>>(q, act);
+        });
     } else {
         p.a = Operand{x, s.H};
         p.b = Operand{w13, s.H};
@@ -248,7 +251,10 @@ hipError_t forward_of_type(const moe_ffn_shape &s, const uint16_t *x, const uint
     if (e != hipSuccess)
         return e;
     if (few_pay(s, s.H, s.I, false))
-        return s.T <= 16 ? few_out<DT, 1>(s, h, w2, put, st) : few_out<DT, 2>(s, h, w2, put, st);
+        return with_blocks(s.T, [&](auto mb) {
+            few_out_kernel<DT, decltype(mb)::value>
+                <<<s.H / 32, 512, 0, st>>>(FewProduct{h, w2, s.T, s.I}, put);
+        });
     p.a = Operand{h, s.I};
     p.b = Operand{w2, s.I};
     p.N = s.H;

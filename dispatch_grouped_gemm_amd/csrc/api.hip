@@ -796,10 +796,12 @@ int moe_ffn_forward(const moe_ffn_shape *s, int32_t dtype, const void *x, const 
     if (!x || !w13 || !w2 || !out || (gate_up_scale && !gate_up) ||
         !all_aligned16(x, w13, w2, base, gate_up, out))
         return MOE_EINVAL;
-    if (!ws || ws_bytes < moe::ffn_forward_bytes(*s) || ((uintptr_t)ws % kAlign) != 0)
+    if (!ws || ((uintptr_t)ws % kAlign) != 0)
         return MOE_EWORKSPACE;
-    return hip_status(moe::launch_ffn_forward(*s, dtype, x, w13, w2, base, gate_up, gate_up_scale,
-                                              out, ws, as_stream(stream)));
+    bool fits;
+    rc = hip_status(moe::launch_ffn_forward(*s, dtype, x, w13, w2, base, gate_up, gate_up_scale,
+                                            out, ws, ws_bytes, &fits, as_stream(stream)));
+    return fits ? rc : MOE_EWORKSPACE;
 }
 
 int moe_ffn_backward(const moe_ffn_shape *s, int32_t dtype, const void *dout, const void *x,
@@ -817,13 +819,15 @@ int moe_ffn_backward(const moe_ffn_shape *s, int32_t dtype, const void *dout, co
     if (s->T > 0) {
         if (!dout || !w2 || !gate_up || (dw13 && !x) || (x_scale && !x) || (dx && !w13))
             return MOE_EINVAL;
-        if (!ws || ws_bytes < moe::ffn_backward_bytes(*s) || ((uintptr_t)ws % kAlign) != 0)
+        if (!ws || ((uintptr_t)ws % kAlign) != 0)
             return MOE_EWORKSPACE;
     }
-    return hip_status(moe::launch_ffn_backward(*s, dtype, dout, x, x_scale, w13, w2, gate_up,
-                                               gate_up_scale, dx, dw13, dw2,
-                                               dw_dtype == MOE_DT_F32, accumulate != 0, ws,
-                                               as_stream(stream)));
+    bool fits;
+    rc = hip_status(moe::launch_ffn_backward(*s, dtype, dout, x, x_scale, w13, w2, gate_up,
+                                             gate_up_scale, dx, dw13, dw2,
+                                             dw_dtype == MOE_DT_F32, accumulate != 0, ws, ws_bytes,
+                                             &fits, as_stream(stream)));
+    return fits ? rc : MOE_EWORKSPACE;
 }
 
 int moe_norm_check(const moe_norm_shape *s)
@@ -831,7 +835,8 @@ int moe_norm_check(const moe_norm_shape *s)
     if (!s || s->T < 0 || s->H <= 0 || !(s->eps >= 0.0f) || !isfinite(s->skip_scale) ||
         !isfinite(s->block_scale))
         return MOE_EINVAL;
-    if (s->T > (1 << 24) || s->H % 32 != 0 || s->H > (1 << 14))
+    // (one workgroup of up to 1,024 threads a row, 2^32 threads a launch)
+    if (s->T > (1 << 21) || s->H % 32 != 0 || s->H > (1 << 14))
         return MOE_ENOTSUP;
     return MOE_OK;
 }
@@ -902,7 +907,7 @@ const char *moe_strerror(int code)
                "T*H and I*H below 2^32; router: E_total <= 1024; adapters: H a multiple of "
                "128 up to 2^17, N of 8 up to 2^20, rank of 8 up to 256; feed-forward block: H and "
                "I multiples of 32 up to 2^17; norms: H a multiple of 32 up to 2^14; T up to "
-               "2^24 in both)";
+               "2^24 and 2^21)";
     case MOE_EWORKSPACE:
         return "workspace missing, too small or not 256-byte aligned";
     case MOE_EHIP:

@@ -60,19 +60,41 @@ __device__ __forceinline__ void from_mx(const uint2 &codes, uint32_t scale, floa
 }
 
 // 8 of a block of 32 values as MX FP8; the block's other values are in the
-// lanes D, 2 D and 3 D further (xor).
+// lanes D, 2 D and 3 D further (xor).  An infinity or NaN becomes the code of a
+// NaN and has no part in the block's exponent, so it is not lost between the passes.
 template <int D>
 __device__ __forceinline__ void store8_mx(uint8_t *codes, uint8_t *scale, const float *f, bool first)
 {
-    float amax = 0.0f;
+    const auto block = [](float v) {
+        v = fmaxf(v, __shfl_xor(v, D));
+        return fmaxf(v, __shfl_xor(v, 2 * D));
+    };
+    float amax = 0.0f, sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        amax = fmaxf(amax, fabsf(f[i]));
+        sum += f[i] - f[i]; // 0, or NaN
+    }
+    uint32_t lost[2] = {0, 0};
+    float v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        amax = fmaxf(amax, fabsf(f[i]));
-    amax = fmaxf(amax, __shfl_xor(amax, D));
-    amax = fmaxf(amax, __shfl_xor(amax, 2 * D));
+        v[i] = f[i];
+    if (__any(sum != 0.0f)) {
+        amax = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const bool there = fabsf(f[i]) < INFINITY;
+            v[i] = there ? f[i] : 0.0f;
+            amax = fmaxf(amax, fabsf(v[i]));
+            lost[i / 4] |= there ? 0u : 0x7fu << 8 * (i % 4);
+        }
+    }
+    amax = block(amax);
     const int e = mx8_block_exponent(amax);
-    *reinterpret_cast<uint2 *>(codes) = uint2{mx8_pack4(f[0], f[1], f[2], f[3], e, amax),
-                                              mx8_pack4(f[4], f[5], f[6], f[7], e, amax)};
+    *reinterpret_cast<uint2 *>(codes) =
+        uint2{mx8_pack4(v[0], v[1], v[2], v[3], e, amax) | lost[0],
+              mx8_pack4(v[4], v[5], v[6], v[7], e, amax) | lost[1]};
     if (first)
         *scale = (uint8_t)(e + 127);
 }
@@ -474,13 +496,20 @@ enum TileKind { kHuge, kWide, kEven, kFlat, kSmall, kFew, kTileKinds };
 struct Cut {
     TileKind kind;
     int splits;
+    float us; // what that is expected to take
 };
 
-inline void tile_sizes(TileKind k, int *bm, int *bn)
+// Tiles of a kind down and across (all sizes are powers of two, so the costs of a
+// call are shifts and a few products: 0.1 us a product).
+constexpr int kTileRows[] = {8, 7, 7, 6, 6, 5}, kTileCols[] = {8, 8, 7, 7, 6, 6}; // log2
+
+inline long tiles_down(TileKind k, long M)
 {
-    constexpr int m[] = {256, 128, 128, 64, 64, 32}, n[] = {256, 256, 128, 128, 64, 64};
-    *bm = m[k];
-    *bn = n[k];
+    return (M + (1l << kTileRows[k]) - 1) >> kTileRows[k];
+}
+inline long tiles_across(TileKind k, long N)
+{
+    return (N + (1l << kTileCols[k]) - 1) >> kTileCols[k];
 }
 
 // How many smaller tiles the 256 x 256 ones of the last round become each, 0
@@ -514,21 +543,21 @@ inline float product_cost(TileKind kind, int splits, long M, long N, long K)
     constexpr float step[] = {0.85f, 0.52f, 0.45f, 0.36f, 0.26f, 0.21f};
     constexpr float more[] = {0.60f, 0.31f, 0.09f, 0.0f, 0.0f, 0.0f}; // where all are busy
     constexpr float once[] = {7.0f, 5.0f, 3.0f, 2.8f, 2.6f, 2.6f};
-    int bm, bn;
-    tile_sizes(kind, &bm, &bn);
-    long groups = tiles_up(M, bm) * tiles_up(N, bn) * splits;
-    const long steps = tiles_up(tiles_up(K, 64), splits);
+    long groups = tiles_down(kind, M) * tiles_across(kind, N) * splits;
+    const int all = (int)((K + 63) >> 6), steps = splits == 1 ? all : (all + splits - 1) / splits;
     float us = 0.0f;
     if (kind == kHuge && huge_rest(groups)) {
         const TileKind k = huge_rest(groups) == 2 ? kWide : kEven;
         us = steps * (step[k] + 0.8f * more[k]) + once[k];
         groups -= groups % kTileCus;
     }
-    const float rounds = (float)tiles_up(groups, kTileCus), full = groups / (rounds * kTileCus);
-    us += rounds * (steps * (step[kind] + full * more[kind]) + once[kind]);
-    us = std::max(us, 2e-6f * N * K / 4.5f + 2.0f);
+    // rounds times the share of CUs that are busy in them is groups / kTileCus
+    const float rounds = (float)((groups + kTileCus - 1) / kTileCus);
+    us += rounds * (steps * step[kind] + once[kind]) +
+          groups * (1.0f / kTileCus) * steps * more[kind];
+    us = std::max(us, (2e-6f / 4.5f) * N * K + 2.0f);
     if (splits > 1)
-        us += 4.0f + 4e-6f * 2 * splits * M * N / 5.0f;
+        us += 4.0f + (8e-6f / 5.0f) * splits * M * N;
     return us;
 }
 
@@ -536,40 +565,35 @@ inline float product_cost(TileKind kind, int splits, long M, long N, long K)
 // the two smallest tiles lack, unless a join forms them.
 inline Cut product_cut(long M, long N, long K, bool pairs)
 {
-    Cut best{kHuge, 1};
-    float cost = product_cost(kHuge, 1, M, N, K);
-    for (int k = kWide; k < kTileKinds; ++k)
-        for (int s = 1; s <= kMostParts; ++s) {
-            if (s > 1 && (k < kEven || tiles_up(K, 64) < 4 * s || s * M * N > (1l << 25)))
-                continue;
-            if (s == 1 && pairs && k >= kSmall)
-                continue;
+    Cut best{kHuge, 1, product_cost(kHuge, 1, M, N, K)};
+    const int steps = (int)((K + 63) >> 6);
+    for (int k = kWide; k < kTileKinds; ++k) {
+        const int most = k < kEven ? 1 : std::min(kMostParts, steps / 4);
+        for (int s = pairs && k >= kSmall ? 2 : 1; s <= std::max(1, most); ++s) {
+            if (s > 1 && s * M * N > (1l << 25))
+                break;
             const float c = product_cost((TileKind)k, s, M, N, K);
-            if (c < cost) {
-                cost = c;
-                best = Cut{(TileKind)k, s};
-            }
+            if (c < best.us)
+                best = Cut{(TileKind)k, s, c};
         }
+    }
     return best;
 }
 
-inline size_t product_parts_bytes(long M, long N, long K, bool pairs)
+inline size_t product_parts_bytes(const Cut &c, long M, long N)
 {
-    const Cut c = product_cut(M, N, K, pairs);
     return c.splits > 1 ? (size_t)c.splits * M * N * sizeof(float) : 0;
 }
 
 // Launches a product; join: the functor with the lane distance of the join
 // kernel.
 template <int DT, bool kPairs, bool ADOWN, bool BDOWN, typename F, typename J>
-hipError_t launch_product(Product p, const F &f, const J &join, float *parts, hipStream_t st)
+hipError_t launch_product(Product p, const Cut &c, const F &f, const J &join, float *parts,
+                          hipStream_t st)
 {
     using S = Tiles<DT, ADOWN, BDOWN>;
-    const Cut c = product_cut(p.M, p.N, p.K, kPairs);
-    int bm, bn;
-    tile_sizes(c.kind, &bm, &bn);
-    p.tm = (int)tiles_up(p.M, bm);
-    p.tn = (int)tiles_up(p.N, bn);
+    p.tm = (int)tiles_down(c.kind, p.M);
+    p.tn = (int)tiles_across(c.kind, p.N);
     p.splits = c.splits;
     p.parts = parts;
     const int n = p.tm * p.tn;

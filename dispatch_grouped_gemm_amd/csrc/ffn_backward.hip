@@ -16,20 +16,23 @@ namespace {
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
-// dgu [T, 2I], h [T, I], x [T, H] (MX FP8 only) and the parts
-struct BackLayout {
+// How a backward call is cut, and its workspace: dgu [T, 2I], h [T, I], x [T, H]
+// (MX FP8 only) and the parts of dh.
+struct BackwardPlan {
+    Cut dh;
     size_t dgu, h, x, parts, bytes;
 };
 
-BackLayout back_layout(const moe_ffn_shape &s)
+BackwardPlan plan_of(const moe_ffn_shape &s)
 {
-    BackLayout l{};
+    BackwardPlan l{};
     const size_t T = s.T, H = s.H, I = s.I;
+    l.dh = product_cut(s.T, s.I, s.H, false);
     l.dgu = 0;
     l.h = l.dgu + align256(T * 2 * I * 2);
     l.x = l.h + align256(T * I * 2);
     l.parts = l.x + align256(T * H * 2);
-    l.bytes = l.parts + product_parts_bytes(T, I, H, false);
+    l.bytes = l.parts + product_parts_bytes(l.dh, s.T, s.I);
     return l;
 }
 
@@ -96,14 +99,12 @@ hipError_t launch_gradients(Gradients<DT> &g, hipStream_t st)
     int best = kHuge;
     float cost = 0.0f;
     for (int k = kHuge; k <= kEven; ++k) {
-        int bm, bn;
         float all = 0.0f, last = 0.0f, most = 0.0f;
         for (int j = 0; j < g.jobs; ++j) {
             const TileKind q = kind_of(k, j);
-            tile_sizes(q, &bm, &bn);
-            last = tiles_up(g.p[j].K, 64) * step[q] + once[q];
+            last = ((g.p[j].K + 63) >> 6) * step[q] + once[q];
             most = std::max(most, last);
-            all += last * tiles_up(g.p[j].M, bm) * tiles_up(g.p[j].N, bn);
+            all += last * tiles_down(q, g.p[j].M) * tiles_across(q, g.p[j].N);
         }
         const float c = std::max(all / kTileCus + 0.5f * last, most);
         if (k == kHuge || c < cost) {
@@ -113,10 +114,8 @@ hipError_t launch_gradients(Gradients<DT> &g, hipStream_t st)
     }
     int n = 0;
     for (int j = 0; j < g.jobs; ++j) {
-        int bm, bn;
-        tile_sizes(kind_of(best, j), &bm, &bn);
-        g.p[j].tm = (int)tiles_up(g.p[j].M, bm);
-        g.p[j].tn = (int)tiles_up(g.p[j].N, bn);
+        g.p[j].tm = (int)tiles_down(kind_of(best, j), g.p[j].M);
+        g.p[j].tn = (int)tiles_across(kind_of(best, j), g.p[j].N);
         g.p[j].splits = 1;
         g.first[j] = n;
         n += (g.p[j].tm * g.p[j].tn + 7) / 8 * 8;
@@ -136,12 +135,12 @@ hipError_t launch_gradients(Gradients<DT> &g, hipStream_t st)
 }
 
 template <int DT>
-hipError_t backward_of_type(const moe_ffn_shape &s, const uint16_t *dout, const void *x_,
-                            const uint8_t *x_scale, const uint16_t *w13, const uint16_t *w2,
+hipError_t backward_of_type(const moe_ffn_shape &s, const BackwardPlan &l, const uint16_t *dout,
+                            const void *x_, const uint8_t *x_scale, const uint16_t *w13,
+                            const uint16_t *w2,
                             const Kept &kept, uint16_t *dx, void *dw13, void *dw2, bool f32,
                             bool accumulate, uint8_t *ws, hipStream_t st)
 {
-    const BackLayout l = back_layout(s);
     uint16_t *dgu = reinterpret_cast<uint16_t *>(ws + l.dgu);
     uint16_t *h = dw2 ? reinterpret_cast<uint16_t *>(ws + l.h) : nullptr;
     float *parts = reinterpret_cast<float *>(ws + l.parts);
@@ -152,7 +151,7 @@ hipError_t backward_of_type(const moe_ffn_shape &s, const uint16_t *dout, const 
     p.N = s.I;
     p.K = s.H;
     const ActivateBack<DT> back{s.I, s.gate_limit, s.up_limit, kept, dgu, h};
-    hipError_t e = launch_product<DT, false, kAlong, kDown>(p, back, back, parts, st);
+    hipError_t e = launch_product<DT, false, kAlong, kDown>(p, l.dh, back, back, parts, st);
     if (e != hipSuccess)
         return e;
     const uint16_t *x = static_cast<const uint16_t *>(x_);
@@ -202,14 +201,15 @@ hipError_t zero(void *p, size_t bytes, hipStream_t st)
 
 } // namespace
 
-size_t ffn_backward_bytes(const moe_ffn_shape &s) { return back_layout(s).bytes; }
+size_t ffn_backward_bytes(const moe_ffn_shape &s) { return plan_of(s).bytes; }
 
 hipError_t launch_ffn_backward(const moe_ffn_shape &s, int dtype, const void *dout, const void *x,
                                const uint8_t *x_scale, const void *w13, const void *w2,
                                const void *gate_up, const uint8_t *gate_up_scale, void *dx,
                                void *dw13, void *dw2, bool f32, bool accumulate, void *ws,
-                               hipStream_t st)
+                               size_t ws_bytes, bool *fits, hipStream_t st)
 {
+    *fits = true;
     const auto u16 = [](const void *p) { return static_cast<const uint16_t *>(p); };
     const Kept kept{const_cast<void *>(gate_up), const_cast<uint8_t *>(gate_up_scale)};
     if (s.T == 0) {
@@ -221,12 +221,16 @@ hipError_t launch_ffn_backward(const moe_ffn_shape &s, int dtype, const void *do
             e = zero(dw2, one, st);
         return e;
     }
+    const BackwardPlan plan = plan_of(s);
+    *fits = ws_bytes >= plan.bytes;
+    if (!*fits)
+        return hipSuccess;
     uint16_t *d = static_cast<uint16_t *>(dx);
     uint8_t *w = static_cast<uint8_t *>(ws);
     if (dtype == MOE_DT_BF16)
-        return backward_of_type<MOE_DT_BF16>(s, u16(dout), x, x_scale, u16(w13), u16(w2), kept, d,
+        return backward_of_type<MOE_DT_BF16>(s, plan, u16(dout), x, x_scale, u16(w13), u16(w2), kept, d,
                                              dw13, dw2, f32, accumulate, w, st);
-    return backward_of_type<MOE_DT_F16>(s, u16(dout), x, x_scale, u16(w13), u16(w2), kept, d,
+    return backward_of_type<MOE_DT_F16>(s, plan, u16(dout), x, x_scale, u16(w13), u16(w2), kept, d,
                                         dw13, dw2, f32, accumulate, w, st);
 }
 

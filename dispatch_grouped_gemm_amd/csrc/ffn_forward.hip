@@ -195,14 +195,30 @@ __global__ void __launch_bounds__(512) few_out_kernel(FewProduct p, Put<DT> f)
 // tiles with K in parts 8; 4,608 rows over 5,120 12 and 15).
 int few_blocks(int T) { return T <= 16 ? 1 : T <= 32 ? 2 : 4; }
 
-bool few_pay(const moe_ffn_shape &s, long N, long K, bool pairs)
+// How a forward call is cut.
+struct ForwardPlan {
+    bool few_gate_up, few_out;
+    Cut gate_up, out;
+    size_t bytes;
+};
+
+ForwardPlan plan_of(const moe_ffn_shape &s)
 {
-    if (s.T > 64)
-        return false;
-    const float memory = 2e-6f * N * K / 4.5f, drawn = 2e-3f * (16 * few_blocks(s.T) + 32) * K;
-    const float us = std::max(tiles_up(N / 32, kTileCus) * drawn / 72.0f, memory) + 2.5f;
-    const Cut c = product_cut(s.T, N, K, pairs);
-    return us <= product_cost(c.kind, c.splits, s.T, N, K);
+    ForwardPlan p{};
+    const auto few = [&](long N, long K, const Cut &c) {
+        const float memory = (2e-6f / 4.5f) * N * K;
+        const float drawn = (2e-3f / 72.0f) * (16 * few_blocks(s.T) + 32) * K;
+        const long rounds = (N / 32 + kTileCus - 1) / kTileCus;
+        return s.T <= 64 && std::max(rounds * drawn, memory) + 2.5f <= c.us;
+    };
+    p.gate_up = product_cut(s.T, 2l * s.I, s.H, true);
+    p.out = product_cut(s.T, s.H, s.I, false);
+    p.few_gate_up = few(2l * s.I, s.H, p.gate_up);
+    p.few_out = few(s.H, s.I, p.out);
+    p.bytes = h_bytes(s) +
+              std::max(p.few_gate_up ? 0 : product_parts_bytes(p.gate_up, s.T, 2l * s.I),
+                       p.few_out ? 0 : product_parts_bytes(p.out, s.T, s.H));
+    return p;
 }
 
 // f with the 16-row blocks of T as a constant.
@@ -220,9 +236,9 @@ hipError_t with_blocks(int T, F f)
 }
 
 template <int DT>
-hipError_t forward_of_type(const moe_ffn_shape &s, const uint16_t *x, const uint16_t *w13,
-                           const uint16_t *w2, const uint16_t *base, const Kept &kept,
-                           uint16_t *out, uint8_t *ws, hipStream_t st)
+hipError_t forward_of_type(const moe_ffn_shape &s, const ForwardPlan &plan, const uint16_t *x,
+                           const uint16_t *w13, const uint16_t *w2, const uint16_t *base,
+                           const Kept &kept, uint16_t *out, uint8_t *ws, hipStream_t st)
 {
     uint16_t *h = reinterpret_cast<uint16_t *>(ws);
     float *parts = reinterpret_cast<float *>(ws + h_bytes(s));
@@ -231,7 +247,7 @@ hipError_t forward_of_type(const moe_ffn_shape &s, const uint16_t *x, const uint
     Product p{};
     p.M = s.T;
     hipError_t e;
-    if (few_pay(s, 2l * s.I, s.H, true)) {
+    if (plan.few_gate_up) {
         const FewProduct q{x, w13, s.T, s.H};
         e = with_blocks(s.T, [&](auto mb) {
             constexpr int MB = decltype(mb)::value;
@@ -246,11 +262,12 @@ hipError_t forward_of_type(const moe_ffn_shape &s, const uint16_t *x, const uint
         p.N = 2 * s.I;
         p.K = s.H;
         e = launch_product<DT, true, kAlong, kAlong>(
-            p, act, Activate<DT, 1>{s.I, s.gate_limit, s.up_limit, kept, h}, parts, st);
+            p, plan.gate_up, act, Activate<DT, 1>{s.I, s.gate_limit, s.up_limit, kept, h}, parts,
+            st);
     }
     if (e != hipSuccess)
         return e;
-    if (few_pay(s, s.H, s.I, false))
+    if (plan.few_out)
         return with_blocks(s.T, [&](auto mb) {
             few_out_kernel<DT, decltype(mb)::value>
                 <<<s.H / 32, 512, 0, st>>>(FewProduct{h, w2, s.T, s.I}, put);
@@ -259,29 +276,31 @@ hipError_t forward_of_type(const moe_ffn_shape &s, const uint16_t *x, const uint
     p.b = Operand{w2, s.I};
     p.N = s.H;
     p.K = s.I;
-    return launch_product<DT, false, kAlong, kAlong>(p, put, put, parts, st);
+    return launch_product<DT, false, kAlong, kAlong>(p, plan.out, put, put, parts, st);
 }
 
 } // namespace
 
-size_t ffn_forward_bytes(const moe_ffn_shape &s)
-{
-    return h_bytes(s) + std::max(product_parts_bytes(s.T, 2 * s.I, s.H, true),
-                                 product_parts_bytes(s.T, s.H, s.I, false));
-}
+size_t ffn_forward_bytes(const moe_ffn_shape &s) { return plan_of(s).bytes; }
 
 hipError_t launch_ffn_forward(const moe_ffn_shape &s, int dtype, const void *x, const void *w13,
                               const void *w2, const void *base, void *gate_up,
-                              uint8_t *gate_up_scale, void *out, void *ws, hipStream_t st)
+                              uint8_t *gate_up_scale, void *out, void *ws, size_t ws_bytes,
+                              bool *fits, hipStream_t st)
 {
+    const ForwardPlan plan = plan_of(s);
+    *fits = ws_bytes >= plan.bytes;
+    if (!*fits)
+        return hipSuccess;
     const auto u16 = [](const void *p) { return static_cast<const uint16_t *>(p); };
     const Kept kept{gate_up, gate_up_scale};
     uint16_t *o = static_cast<uint16_t *>(out);
     uint8_t *w = static_cast<uint8_t *>(ws);
     if (dtype == MOE_DT_BF16)
-        return forward_of_type<MOE_DT_BF16>(s, u16(x), u16(w13), u16(w2), u16(base), kept, o, w,
-                                            st);
-    return forward_of_type<MOE_DT_F16>(s, u16(x), u16(w13), u16(w2), u16(base), kept, o, w, st);
+        return forward_of_type<MOE_DT_BF16>(s, plan, u16(x), u16(w13), u16(w2), u16(base), kept, o,
+                                            w, st);
+    return forward_of_type<MOE_DT_F16>(s, plan, u16(x), u16(w13), u16(w2), u16(base), kept, o, w,
+                                       st);
 }
 
 } // namespace moe

@@ -564,17 +564,19 @@ hipError_t launch_adapter_project(const moe_adapter_shape &s, int dtype, const v
                                   void *ws, hipStream_t st);
 
 // The dense feed-forward block and the residual joint with its norms
-// (arguments as the C ABI's; f32: the weights' gradients are float32).
+// (arguments as the C ABI's; f32: the weights' gradients are float32; *fits
+// is false, and nothing launched, where the workspace is too small).
 size_t ffn_forward_bytes(const moe_ffn_shape &s);
 size_t ffn_backward_bytes(const moe_ffn_shape &s);
 hipError_t launch_ffn_forward(const moe_ffn_shape &s, int dtype, const void *x, const void *w13,
                               const void *w2, const void *base, void *gate_up,
-                              uint8_t *gate_up_scale, void *out, void *ws, hipStream_t st);
+                              uint8_t *gate_up_scale, void *out, void *ws, size_t ws_bytes,
+                              bool *fits, hipStream_t st);
 hipError_t launch_ffn_backward(const moe_ffn_shape &s, int dtype, const void *dout, const void *x,
                                const uint8_t *x_scale, const void *w13, const void *w2,
                                const void *gate_up, const uint8_t *gate_up_scale, void *dx,
                                void *dw13, void *dw2, bool f32, bool accumulate, void *ws,
-                               hipStream_t st);
+                               size_t ws_bytes, bool *fits, hipStream_t st);
 size_t norm_workspace_bytes(const moe_norm_shape &s);
 hipError_t launch_norm_forward(const moe_norm_shape &s, int dtype, const void *x, const void *y,
                                const void *w_post, const float *gate, const void *w_pre,

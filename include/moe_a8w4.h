@@ -582,7 +582,8 @@ int moe_adapter_project(const moe_adapter_shape *shape, int32_t dtype, const voi
  * the backward pass it keeps g | u when gate_up is given: [T, 2I] in dtype
  * (gate_up_scale NULL), or MX FP8 codes [T, 2I] with an exponent byte per 32
  * columns in gate_up_scale [T, 2I/32] (the rule of moe_quant_mxfp8 on the
- * float32 sums).  A NaN in g or u gives a NaN in h.
+ * float32 sums; an infinity or NaN becomes a NaN code).  A NaN in g or u gives
+ * a NaN in h.
  *
  * moe_ffn_backward: from dout [T, H] and what was kept (the same two forms),
  * each value taken as it was rounded,
@@ -659,7 +660,7 @@ int moe_ffn_backward(const moe_ffn_shape *shape, int32_t dtype, const void *dout
  * Rows and weights start on 16-byte boundaries.
  */
 typedef struct moe_norm_shape {
-    int32_t T;         /* rows, at most 2^24 */
+    int32_t T;         /* rows, at most 2^21 */
     int32_t H;         /* a multiple of 32, at most 2^14 */
     float eps;         /* 0 or more */
     float skip_scale;  /* factor of x */

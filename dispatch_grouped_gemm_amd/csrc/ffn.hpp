@@ -372,7 +372,9 @@ template <int DT, bool ADOWN, bool BDOWN>
 struct Tiles {
     static constexpr int WM = BDOWN ? 2 : 4, WN = 8 / WM;
     using Huge = Tile<DT, 256, 256, 2, 4, 2, ADOWN, BDOWN>;
+    using Tall = Tile<DT, 192, 256, 2, 4, 2, ADOWN, BDOWN>; // this and Slim: k along A's rows
     using Wide = Tile<DT, 128, 256, 2, 4, 3, ADOWN, BDOWN>;
+    using Slim = Tile<DT, 192, 128, WM, WN, 4, ADOWN, BDOWN>;
     using Even = Tile<DT, 128, 128, WM, WN, 4, ADOWN, BDOWN>;
     using Flat = Tile<DT, 64, 128, WM, WN, 4, ADOWN, BDOWN>;
     using Small = Tile<DT, 64, 64, 4, 2, 4, ADOWN, BDOWN>;
@@ -500,7 +502,7 @@ inline long tiles_up(long n, long by) { return (n + by - 1) / by; }
 constexpr int kTileCus = 256; // workgroups that fill an MI355X; the workspace goes by it
 
 // How a product of M x N over K is cut.
-enum TileKind { kHuge, kWide, kEven, kFlat, kSmall, kFew, kTileKinds };
+enum TileKind { kHuge, kWide, kEven, kFlat, kSmall, kFew, kTall, kSlim, kTileKinds };
 
 struct Cut {
     TileKind kind;
@@ -508,12 +510,14 @@ struct Cut {
     float us; // what that is expected to take
 };
 
-// Tiles of a kind down and across (all sizes are powers of two, so the costs of a
-// call are shifts and a few products: 0.1 us a product).
-constexpr int kTileRows[] = {8, 7, 7, 6, 6, 5}, kTileCols[] = {8, 8, 7, 7, 6, 6}; // log2
+// Tiles of a kind down and across: shifts, or a division by a constant.
+constexpr int kTileRows[] = {8, 7, 7, 6, 6, 5, 0, 0}; // log2; the last two have 192
+constexpr int kTileCols[] = {8, 8, 7, 7, 6, 6, 8, 7}; // log2
 
 inline long tiles_down(TileKind k, long M)
 {
+    if (k == kTall || k == kSlim)
+        return (M + 191) / 192;
     return (M + (1l << kTileRows[k]) - 1) >> kTileRows[k];
 }
 inline long tiles_across(TileKind k, long N)
@@ -534,24 +538,27 @@ inline int huge_rest(long tiles)
 // Microseconds of a product.  A CU takes its tiles one after the other: a round
 // costs its steps of 64 k and what stands before and behind them.  The steps of
 // the largest tiles are bound by the matrix instructions, at clocks that fall as
-// more of the CUs are busy (full: the share that is); those of
-// the others by what a CU draws from the L2, about 30 bytes a clock.  The second
-// operand comes from memory at 4.5 TB/s at best.  Parts cost their planes and a
-// launch.  Measured (us, in a row of calls, by the tiles in their order):
-//   8,192 x 4,096 pairs over 7,168    355  409       524
-//   4,096 x 4,608 pairs over 5,120    212  214       241
-//   8,192 x 7,168 over 2,048          199  208       248
-//   4,096 x 5,120 over 2,304          103   93        97
-//   4,096 x 2,304 over 5,120 (down)   133  135       146
-//   1,021 x 2,816 over 2,304           48   26  25    35   30   43
-//   1,021 x 2,304 over 1,408           32   18  17    20   20   25
+// more of the CUs are busy; those of the others by what a CU draws from the L2,
+// about 30 bytes a clock.  The second operand comes from memory at 4.5 TB/s at
+// best.  Parts cost their planes and a launch.  Measured (us, in a row of calls, by
+// the kinds in their order; the sums over 51 products of 200 to 8,192 rows of three
+// blocks are within 0.1% of those of the fastest tiles):
+//   8,192 x 4,096 pairs over 7,168    344  391  524  666            371  444
+//   4,096 x 4,608 pairs over 5,120    151  183  193  234            167  195
+//   8,192 x 7,168 over 2,048          196  224  286  353            204  240
+//   4,096 x 5,120 over 2,304           79   92   96  126             83  100
+//   4,096 x 2,304 over 5,120 (down)   123  135  125  140             97  122
+//   2,048 x 5,120 over 2,304           48   57   54   65             43   49
+//   1,021 x 4,608 pairs over 5,120     92   53   71   77             75   49
+//   1,021 x 2,816 pairs over 2,304     47   27   19   25             37   23
+//   1,021 x 2,304 over 1,408           31   18   12   17   20   25   24   16
 //     128 x 7,168 over 2,048                    23    18   13   17
 //      90 x 1,344 over 544                      11     9  6.5  5.8
 inline float product_cost(TileKind kind, int splits, long M, long N, long K)
 {
-    constexpr float step[] = {0.85f, 0.52f, 0.45f, 0.36f, 0.26f, 0.21f};
-    constexpr float more[] = {0.60f, 0.31f, 0.09f, 0.0f, 0.0f, 0.0f}; // where all are busy
-    constexpr float once[] = {7.0f, 5.0f, 3.0f, 2.8f, 2.6f, 2.6f};
+    constexpr float step[] = {0.85f, 0.52f, 0.45f, 0.36f, 0.26f, 0.21f, 0.67f, 0.5f};
+    constexpr float more[] = {0.60f, 0.31f, 0.09f, 0.0f, 0.0f, 0.0f, 0.45f, 0.2f}; // all busy
+    constexpr float once[] = {7.0f, 5.0f, 3.0f, 2.8f, 2.6f, 2.6f, 6.0f, 4.0f};
     long groups = tiles_down(kind, M) * tiles_across(kind, N) * splits;
     const int all = (int)((K + 63) >> 6), steps = splits == 1 ? all : (all + splits - 1) / splits;
     float us = 0.0f;
@@ -577,8 +584,8 @@ inline Cut product_cut(long M, long N, long K, bool pairs)
     Cut best{kHuge, 1, product_cost(kHuge, 1, M, N, K)};
     const int steps = (int)((K + 63) >> 6);
     for (int k = kWide; k < kTileKinds; ++k) {
-        const int most = k < kEven ? 1 : std::min(kMostParts, steps / 4);
-        for (int s = pairs && k >= kSmall ? 2 : 1; s <= std::max(1, most); ++s) {
+        const int most = k < kEven || k >= kTall ? 1 : std::min(kMostParts, steps / 4);
+        for (int s = pairs && (k == kSmall || k == kFew) ? 2 : 1; s <= std::max(1, most); ++s) {
             if (s > 1 && s * M * N > (1l << 25))
                 break;
             const float c = product_cost((TileKind)k, s, M, N, K);
@@ -643,6 +650,10 @@ hipError_t launch_product(Product p, const Cut &c, const F &f, const J &join, fl
         rest(typename S::Even{});
     } else if (c.kind == kHuge) {
         whole(typename S::Huge{});
+    } else if (c.kind == kTall) {
+        whole(typename S::Tall{});
+    } else if (c.kind == kSlim) {
+        whole(typename S::Slim{});
     } else if (c.kind == kWide) {
         whole(typename S::Wide{});
     } else if (c.kind == kEven) {

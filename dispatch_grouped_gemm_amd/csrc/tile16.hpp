@@ -117,7 +117,7 @@ struct Side {
     static __device__ __forceinline__ int lane() { return threadIdx.x & 63; }
 
     // byte offset of this lane's part of the 16 rows (kDown: columns) of block
-    // f from row0, k 0 .. 31 of the stage; k 32 .. 63 lie at `half`
+    // f from row0, k 0 .. 31 of the stage (the others: Tile::read)
     static __device__ __forceinline__ int at(int row0, int f, int second)
     {
         const int l = lane() & 15, g = lane() >> 4;
@@ -147,7 +147,7 @@ struct Tile {
     static constexpr int kStage = SA::kBytes + SB::kBytes, kLds = NS * kStage;
     // loads per wavefront and step, A's first
     static constexpr int UA = SA::kLoads / NW, UB = SB::kLoads / NW, U = UA + UB;
-    static constexpr int GM = MF < 4 ? MF : 4; // row blocks of a phase
+    static constexpr int GM = MF % 4 == 0 ? 4 : MF % 3 == 0 ? 3 : MF; // row blocks of a phase
     static_assert(MF % GM == 0 && NF % 2 == 0 && NF <= 4, "whole groups and pairs of blocks");
     static_assert(UA * NW == SA::kLoads && UB * NW == SB::kLoads, "whole loads");
 

@@ -4,7 +4,10 @@
 //   normed = res rho(res) w_pre,  rho(v) = 1 / sqrt(mean v^2 + eps),
 // the second norm of res as it is stored (rounded to the type), so that the
 // backward pass, which has res, computes with the same values.  Sums are
-// float32.  normed may also, or only, be written as MX FP8 rows, the experts'
+// float32.  The norm's gradient, with hat = v rho and g = w d,
+//   rho (g - hat mean(g hat)),
+// keeps every factor as near 1 as hat is: rho^3 leaves float32's range at rows of
+// 1e-13 and of 1e14, rho alone and the gradient do not.  normed may also, or only, be written as MX FP8 rows, the experts'
 // input, with the codes that moe_quant_mxfp8 makes of the rounded normed.
 //
 // Bound by HBM: a workgroup holds its row's 16-byte pieces in registers from
@@ -225,8 +228,8 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(NShape s, Backward 
                     yq[i] = row(p.y)[at];
             }
         }
-        // mean res^2 and mean (dn w) res; mean y^2
-        float rho = 0.0f, back = 0.0f;
+        // mean res^2 and mean (dn w) hat; mean y^2
+        float rho = 0.0f, mean = 0.0f;
         if (p.dnormed) {
             float v[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -246,7 +249,7 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(NShape s, Backward 
             }
             sum_all<2>(v, l1, slot, wave0, waves);
             rho = rho_of(v[0], s);
-            back = rho * rho * rho * (v[1] / (float)s.H);
+            mean = rho * (v[1] / (float)s.H);
         }
         const float sig = p.gate ? logistic_of(p.gate[t]) : 1.0f, a = s.scale * sig;
         // dr, in place of dn; and the sums that y's gradient and the gate's need
@@ -265,8 +268,9 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(NShape s, Backward 
                 E::unpack(static_cast<const uint4 *>(p.w_pre)[at], w);
 #pragma unroll
                 for (int k = 0; k < kV; ++k) {
-                    dr[i][k] += rho * d[k] * w[k] - back * r[k];
-                    sum_pre[i][k] += d[k] * (r[k] * rho);
+                    const float hat = r[k] * rho;
+                    dr[i][k] += rho * (d[k] * w[k] - hat * mean);
+                    sum_pre[i][k] += d[k] * hat;
                 }
             }
             if (p.dx) {
@@ -293,7 +297,7 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(NShape s, Backward 
         const float rho_y = p.w_post ? rho_of(v[0], s) : 1.0f;
         if (p.dgate && tid == 0 && there)
             p.dgate[t] = s.scale * sig * (1.0f - sig) * (rho_y * v[1]);
-        const float back_y = p.w_post ? a * rho_y * rho_y * rho_y * (v[1] / (float)s.H) : 0.0f;
+        const float mean_y = a * (rho_y * (v[1] / (float)s.H));
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             const int at = i * threads + tid;
@@ -305,8 +309,9 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(NShape s, Backward 
                 E::unpack(static_cast<const uint4 *>(p.w_post)[at], w);
 #pragma unroll
                 for (int k = 0; k < kV; ++k) {
-                    sum_post[i][k] += a * dr[i][k] * (y[k] * rho_y);
-                    y[k] = rho_y * a * dr[i][k] * w[k] - back_y * y[k];
+                    const float hat = y[k] * rho_y, dz = a * dr[i][k];
+                    sum_post[i][k] += dz * hat;
+                    y[k] = rho_y * (dz * w[k] - hat * mean_y);
                 }
             } else {
 #pragma unroll

@@ -1,0 +1,56 @@
+"""The residual joint's gradients at the ends of what its header allows: rows far from 1, eps 0
+and next to it."""
+
+import pytest
+import torch
+
+import dispatch_grouped_gemm_amd as moe
+import ffn_ref
+import test_gpu_norm as base
+from ops_ref import assert_close
+
+pytestmark = pytest.mark.gpu
+
+BF, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+DEV = "cuda"
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("size,eps", [(1e-14, 0.0), (1e-13, 0.0), (1e-13, 1e-30), (1e10, 1e-6),
+                                      (1e14, 1e-6), (1e15, 0.0), (1e16, 1e-6)])
+@pytest.mark.parametrize("T,H", [(5, 96), (3, 7168), (1100, 160)])
+def test_rows_far_from_one(T, H, size, eps, dt):
+    """rho(v) ^ 3 leaves float32's range long before rho and the gradients do."""
+    c = base._case(T, H, dt, T + H)
+    c["x"], c["y"] = c["x"] * size, c["y"] * size
+    s = moe.NormShape(T=T, H=H, eps=eps, skip_scale=0.75, block_scale=0.4)
+    o = dict(dx=torch.empty_like(c["x"]), dw_pre=torch.empty(H, device=DEV),
+             dy=torch.empty_like(c["x"]), dw_post=torch.empty(H, device=DEV),
+             dgate=torch.empty(T, device=DEV))
+    kw = dict(y=c["y"], w_post=c["w_post"], gate=c["gate"])
+    # (without dres, beside which the gradient of large rows is nothing)
+    moe.moe_norm_backward(s, c["dnormed"], c["x"], c["w_pre"], o["dx"], o["dw_pre"],
+                          moe.alloc_norm_workspace(s, DEV), dy=o["dy"], dw_post=o["dw_post"],
+                          dgate=o["dgate"], **kw)
+    r = ffn_ref.norm_backward(c["dnormed"], None, c["x"], c["w_pre"], eps, 0.75, 0.4, **kw)
+    for k, (v, b) in r.items():
+        # dy of large rows goes by dr, which is as small as they are large, over their size
+        # again: below the normal numbers of bf16 and float32 each is off by steps of 2^-133
+        # and 2^-149, and a flushed one by 2^-126
+        assert_close(o[k], v, b + (2.0 ** -125 if k == "dy" else 0.0), k)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_zero_rows_with_a_small_eps(dt):
+    """rho of a row of zeros is 1 / sqrt(eps): its gradients are rho times what comes in."""
+    T, H, eps = 4, 512, 1e-28
+    c = base._case(T, H, dt, 31)
+    c["x"][1], c["y"][2] = 0, 0
+    s = moe.NormShape(T=T, H=H, eps=eps, block_scale=0.5)
+    dx, dy = torch.empty_like(c["x"]), torch.empty_like(c["x"])
+    kw = dict(y=c["y"], w_post=c["w_post"], gate=c["gate"])
+    moe.moe_norm_backward(s, c["dnormed"], c["x"], c["w_pre"], dx, None, None, dres=c["dres"],
+                          dy=dy, **kw)
+    r = ffn_ref.norm_backward(c["dnormed"], c["dres"], c["x"], c["w_pre"], eps, 1.0, 0.5, **kw)
+    assert_close(dx, *r["dx"], "dx")
+    assert_close(dy, *r["dy"], "dy")

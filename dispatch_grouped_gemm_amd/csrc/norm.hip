@@ -296,7 +296,8 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(NShape s, Backward 
             sum_all<2>(v, l2, slot, wave0, waves);
         const float rho_y = p.w_post ? rho_of(v[0], s) : 1.0f;
         if (p.dgate && tid == 0 && there)
-            p.dgate[t] = s.scale * sig * (1.0f - sig) * (rho_y * v[1]);
+            // logistic(-gate), not 1 - sig, which has no bits left for a gate above 17
+            p.dgate[t] = s.scale * sig * logistic_of(-p.gate[t]) * (rho_y * v[1]);
         const float mean_y = a * (rho_y * (v[1] / (float)s.H));
 #pragma unroll
         for (int i = 0; i < NP; ++i) {

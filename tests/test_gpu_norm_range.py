@@ -54,3 +54,22 @@ def test_zero_rows_with_a_small_eps(dt):
     r = ffn_ref.norm_backward(c["dnormed"], c["dres"], c["x"], c["w_pre"], eps, 1.0, 0.5, **kw)
     assert_close(dx, *r["dx"], "dx")
     assert_close(dy, *r["dy"], "dy")
+
+
+def test_gradients_of_open_and_shut_gates():
+    """sigmoid'(gate) = s(gate) s(-gate): both factors keep their bits however far the gate is
+    open; 1 - s(gate) has none of them left from 17 on."""
+    T, H = 12, 512
+    c = base._case(T, H, F32, 17)
+    c["gate"] = torch.tensor([-80.0, -30, -20, -17, -10, 0, 10, 15, 17, 20, 30, 80], device=DEV)
+    s = moe.NormShape(T=T, H=H, block_scale=0.5)
+    dg = torch.empty(T, device=DEV)
+    kw = dict(y=c["y"], w_post=c["w_post"], gate=c["gate"])
+    moe.moe_norm_backward(s, None, None, None, None, None, None, dres=c["dres"], dgate=dg, **kw)
+    g, y, dr = c["gate"].double(), c["y"].double(), c["dres"].double()
+    z = y * ffn_ref.rms(y, 1e-6) * c["w_post"].double()
+    k = 0.5 / ((1 + torch.exp(g)) * (1 + torch.exp(-g)))
+    # exp within 2 steps of 2^-23, the sum, the quotient: 6 of 2^-24 a factor, three products;
+    # the sums as in every row's dot product
+    m = (dr * z).abs().sum(1)
+    assert_close(dg, k * (dr * z).sum(1), k * 2.0 ** -24 * (20 + 2 * (H + 40)) * m, "dgate")

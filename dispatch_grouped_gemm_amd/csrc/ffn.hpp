@@ -80,16 +80,8 @@ __device__ __forceinline__ void store8_mx(uint8_t *codes, uint8_t *scale, const 
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         v[i] = f[i];
-    if (__any(sum != 0.0f)) {
-        amax = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const bool there = fabsf(f[i]) < INFINITY;
-            v[i] = there ? f[i] : 0.0f;
-            amax = fmaxf(amax, fabsf(v[i]));
-            lost[i / 4] |= there ? 0u : 0x7fu << 8 * (i % 4);
-        }
-    }
+    if (__any(sum != 0.0f))
+        amax = mx8_finite<8>(f, v, lost);
     amax = block(amax);
     const int e = mx8_block_exponent(amax);
     *reinterpret_cast<uint2 *>(codes) =

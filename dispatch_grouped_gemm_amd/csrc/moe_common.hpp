@@ -182,6 +182,24 @@ __device__ __forceinline__ uint32_t mx8_pack4(float a, float b, float c, float d
     return (uint32_t)r;
 }
 
+// The finite ones of N values (0 in the place of others) and their largest
+// magnitude; `lost` has the code of a NaN in each other's byte, to be set in
+// what mx8_pack4 makes of v: an infinity or NaN stays one in a row that a model
+// reads on, and has no part in its block's exponent.
+template <int N>
+__device__ __forceinline__ float mx8_finite(const float *f, float *v, uint32_t *lost)
+{
+    float amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const bool there = fabsf(f[i]) < INFINITY;
+        v[i] = there ? f[i] : 0.0f;
+        amax = fmaxf(amax, fabsf(v[i]));
+        lost[i / 4] = (i % 4 ? lost[i / 4] : 0u) | (there ? 0u : 0x7fu << 8 * (i % 4));
+    }
+    return amax;
+}
+
 // ---------------------------------------------------------------------------
 // BF16 activation rows to MX FP8 (the 1x32 rule of the requant above): the
 // step in front of the layer ("MegaMoEV2: fuse dispatch, GEMM1, GEMM2 and

@@ -4,11 +4,13 @@
 //   normed = res rho(res) w_pre,  rho(v) = 1 / sqrt(mean v^2 + eps),
 // the second norm of res as it is stored (rounded to the type), so that the
 // backward pass, which has res, computes with the same values.  Sums are
-// float32.  The norm's gradient, with hat = v rho and g = w d,
+// float32.  normed may also, or only, be written as MX FP8 rows, the experts'
+// input, with the codes that moe_quant_mxfp8 makes of the rounded normed, and
+// those of NaN where it is not finite.  The norm's gradient, with hat = v rho
+// and g = w d,
 //   rho (g - hat mean(g hat)),
-// keeps every factor as near 1 as hat is: rho^3 leaves float32's range at rows of
-// 1e-13 and of 1e14, rho alone and the gradient do not.  normed may also, or only, be written as MX FP8 rows, the experts'
-// input, with the codes that moe_quant_mxfp8 makes of the rounded normed.
+// keeps every factor as near 1 as hat is: rho^3 leaves float32's range at rows
+// of 1e-13 and of 1e14, rho alone and the gradient do not.
 //
 // Bound by HBM: a workgroup holds its row's 16-byte pieces in registers from
 // the one read to the write, so every array moves once (8,192 x 7,168 bf16, all
@@ -157,10 +159,9 @@ __global__ void __launch_bounds__(1024) norm_forward_kernel(NShape s, Forward p)
             const_cast<uint4 *>(row(p.normed))[at] = rq[i];
         if (p.codes) {
             E::unpack(rq[i], f); // the rounded values, as a quantiser of normed has them
-            float amax = 0.0f;
-#pragma unroll
-            for (int k = 0; k < kV; ++k)
-                amax = fmaxf(amax, fabsf(f[k]));
+            float v[kV];
+            uint32_t lost[kV / 4];
+            float amax = mx8_finite<kV>(f, v, lost);
 #pragma unroll
             for (int d = 1; d < 32 / kV; d <<= 1)
                 amax = fmaxf(amax, __shfl_xor(amax, d));
@@ -169,7 +170,8 @@ __global__ void __launch_bounds__(1024) norm_forward_kernel(NShape s, Forward p)
                 uint32_t *o = reinterpret_cast<uint32_t *>(p.codes + t * s.H) + at * (kV / 4);
 #pragma unroll
                 for (int k = 0; k < kV / 4; ++k)
-                    o[k] = mx8_pack4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3], e, amax);
+                    o[k] = mx8_pack4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3], e, amax) |
+                           lost[k];
                 if (at % (32 / kV) == 0)
                     p.exps[t * (s.H / 32) + at / (32 / kV)] = (uint8_t)(e + 127);
             }

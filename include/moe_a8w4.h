@@ -644,8 +644,9 @@ int moe_ffn_backward(const moe_ffn_shape *shape, int32_t dtype, const void *dout
  * gate float [T] (NULL: factor 1).  y NULL: no block, normed is the norm of x,
  * and res, w_post and gate are NULL too.  normed (with w_pre) may be NULL, or
  * written as MX FP8 rows besides or instead: codes [T, H] and exponent bytes
- * [T, H/32] (both or neither), the bytes moe_quant_mxfp8 makes of normed.  res
- * may be NULL, or x or y itself; normed may be none of the inputs.
+ * [T, H/32] (both or neither), the bytes moe_quant_mxfp8 makes of normed; an
+ * infinity or NaN of normed becomes a NaN code and has no part in its block's
+ * exponent.  res may be NULL, or x or y itself; normed may be none of the inputs.
  *
  * moe_norm_backward: from dnormed (NULL: no norm before the next block; res,
  * w_pre and dw_pre are then NULL) and dres (NULL: zero), one of them given, with

@@ -73,3 +73,30 @@ def test_gradients_of_open_and_shut_gates():
     # the sums as in every row's dot product
     m = (dr * z).abs().sum(1)
     assert_close(dg, k * (dr * z).sum(1), k * 2.0 ** -24 * (20 + 2 * (H + 40)) * m, "dgate")
+
+
+@pytest.mark.parametrize("dt", [BF, F16, F32])
+@pytest.mark.parametrize("T,H", [(6, 512), (7, 7168), (6, 96)])
+def test_mx_rows_keep_what_is_not_finite(T, H, dt):
+    """An infinity or NaN of normed is a NaN code and has no part in its block's exponent."""
+    c = base._case(T, H, dt, T + H)
+    s = moe.NormShape(T=T, H=H)
+    c["x"][1, 5], c["x"][2, 40] = float("nan"), float("inf")
+    w = c["w_pre"]
+    w[33], w[64] = float("inf"), float("nan")     # whole columns of every row
+    normed = torch.empty_like(c["x"])
+    codes = torch.empty(T, H, dtype=torch.uint8, device=DEV)
+    exps = torch.empty(T, H // 32, dtype=torch.uint8, device=DEV)
+    moe.moe_norm_forward(s, c["x"], w, normed, normed_fp8=codes, normed_scale=exps)
+    there = normed.isfinite()
+    assert not there[1].any() and not there[:, [33, 64]].any() and there[0].sum() == H - 2
+    want, we = ffn_ref.mx_rows(torch.where(there, normed, 0.0))
+    got, lost = codes.cpu(), ~there.cpu()
+    assert ((got[lost] & 0x7f) == 0x7f).all()
+    assert torch.equal(exps.cpu(), we)
+    zero = (want & 0x7f) == 0
+    want = torch.where(zero, 0, want)
+    assert torch.equal(torch.where(zero, got & 0x7f, got)[~lost], want[~lost])
+    alone, ae = torch.empty_like(codes), torch.empty_like(exps)
+    moe.moe_norm_forward(s, c["x"], w, None, normed_fp8=alone, normed_scale=ae)
+    assert torch.equal(alone, codes) and torch.equal(ae, exps)

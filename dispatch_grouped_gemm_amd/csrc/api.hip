@@ -814,10 +814,11 @@ int moe_ffn_backward(const moe_ffn_shape *s, int32_t dtype, const void *dout, co
     if (rc != MOE_OK)
         return rc;
     if (!ffn_type(dtype) || (dw_dtype != dtype && dw_dtype != MOE_DT_F32) ||
-        (!dx && !dw13 && !dw2) || !all_aligned16(dout, x, w13, w2, gate_up, dx, dw13, dw2))
+        !all_aligned16(dout, x, w13, w2, gate_up, dx, dw13, dw2))
         return MOE_EINVAL;
-    if (s->T > 0) {
-        if (!dout || !w2 || !gate_up || (dw13 && !x) || (x_scale && !x) || (dx && !w13))
+    if (s->T > 0) { // (rows of no rows may be NULL, as an empty tensor's pointer is)
+        if ((!dx && !dw13 && !dw2) || !dout || !w2 || !gate_up || (dw13 && !x) ||
+            (x_scale && !x) || (dx && !w13))
             return MOE_EINVAL;
         if (!ws || ((uintptr_t)ws % kAlign) != 0)
             return MOE_EWORKSPACE;
@@ -877,18 +878,19 @@ int moe_norm_backward(const moe_norm_shape *s, int32_t dtype, const void *dnorme
     if (rc != MOE_OK)
         return rc;
     const bool planes = dw_post || dw_pre;
-    if (!elem_type(dtype) || (!dx && !dy && !dgate && !planes) ||
-        !all_aligned16(dnormed, dres, res, y, w_post, w_pre, dx, dy))
+    if (!elem_type(dtype) || !all_aligned16(dnormed, dres, res, y, w_post, w_pre, dx, dy))
         return MOE_EINVAL;
-    if (s->T > 0) {
+    if (s->T > 0) { // (rows of no rows may be NULL, as an empty tensor's pointer is)
         const bool pre = dnormed != nullptr;
-        if ((!dnormed && !dres) || pre != (res != nullptr) || pre != (w_pre != nullptr) ||
-            (dw_pre && !pre) || (!y && (w_post || gate || dy || dgate)) || (dw_post && !w_post) ||
-            (dgate && !gate))
+        if ((!dx && !dy && !dgate && !planes) || (!dnormed && !dres) ||
+            pre != (res != nullptr) || pre != (w_pre != nullptr) || (dw_pre && !pre) ||
+            (!y && (w_post || gate || dy || dgate)) || (dw_post && !w_post) || (dgate && !gate))
             return MOE_EINVAL;
         if (planes &&
             (!ws || ws_bytes < moe::norm_workspace_bytes(*s) || ((uintptr_t)ws % kAlign) != 0))
             return MOE_EWORKSPACE;
+    } else if (!planes) {
+        return MOE_OK;
     }
     return hip_status(moe::launch_norm_backward(*s, dtype, dnormed, dres, res, y, w_post, gate,
                                                 w_pre, dx, dy, dgate, dw_post, dw_pre, ws,

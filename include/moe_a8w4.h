@@ -596,7 +596,7 @@ int moe_adapter_project(const moe_adapter_shape *shape, int32_t dtype, const voi
  * dx [T, H], dw13 and dw2 (shaped as the weights) may each be NULL; x may be
  * NULL without dw13, w13 without dx.  dw_dtype is dtype or MOE_DT_F32;
  * accumulate != 0 adds to what dw13 and dw2 hold (float32 sum, rounded once).
- * With T = 0 dw13 and dw2 become zeros (or stay, with accumulate).
+ * With T = 0 dw13 and dw2, where given, become zeros (or stay, with accumulate).
  *
  * Sums have a fixed order: the same call gives the same bits.  Buffers do not
  * overlap (but for base); x, weights, rows and gradients start on 16-byte
@@ -658,8 +658,8 @@ int moe_ffn_backward(const moe_ffn_shape *shape, int32_t dtype, const void *dout
  *   dgate[t] = block_scale sigmoid'(gate[t]) <dr, z>
  * dx, dy, dgate, dw_post and dw_pre may each be NULL, and are where what they
  * belong to is; dgate, dw_post and dw_pre are float32.  dx may be dres, dnormed
- * or res itself, dy may be y.  With T = 0 dw_pre and dw_post become zeros.  Sums
- * have a fixed order.  workspace (for dw_pre or dw_post):
+ * or res itself, dy may be y.  With T = 0 dw_pre and dw_post, where given,
+ * become zeros.  Sums have a fixed order.  workspace (for dw_pre or dw_post):
  * moe_norm_workspace_size bytes, 256-byte aligned; calls that overlap on one race.
  * Rows and weights start on 16-byte boundaries.
  */

@@ -1,0 +1,32 @@
+"""What the feed-forward block and the residual joint accept without a GPU's work: calls of no
+rows."""
+
+import pytest
+
+import dispatch_grouped_gemm_amd as moe
+from dispatch_grouped_gemm_amd import _build
+from test_ffn_refusals import FAKE, f_shape, n_shape
+
+
+@pytest.fixture(scope="module")
+def lib():
+    _build.build(force=False)
+    return moe.lib()
+
+
+def test_no_rows_and_frozen_weights(lib):
+    """The gradients of no rows, none of the weights' asked for: an empty tensor's pointer is
+    NULL, and that is not a call without outputs."""
+    none = [None] * 16
+    assert lib.moe_ffn_backward(f_shape(T=0), 0, *none[:10], 0, 0, None, 0, None) == 0
+    # ... with the weights at hand and kept rows in 8 bits
+    assert lib.moe_ffn_backward(f_shape(T=0), 0, None, None, None, FAKE, FAKE, None, None, None,
+                                None, None, 0, 1, FAKE, 1 << 20, None) == 0
+    assert lib.moe_norm_backward(n_shape(T=0), 0, *none[:13], 0, None) == 0
+    assert lib.moe_norm_backward(n_shape(T=0), 0, None, None, None, None, FAKE, None, FAKE,
+                                 *none[:6], 0, None) == 0
+    # of some rows it is one
+    assert lib.moe_ffn_backward(f_shape(), 0, *([FAKE] * 7), None, None, None, 0, 0, FAKE,
+                                1 << 30, None) == -1
+    assert lib.moe_norm_backward(n_shape(), 0, *([FAKE] * 7), *none[:5], FAKE, 1 << 30,
+                                 None) == -1

@@ -1084,7 +1084,8 @@ def moe_ffn_workspace_size(shape: FfnShape, backward: bool = False) -> int:
 
 
 def alloc_ffn_workspace(shape: FfnShape, device, backward: bool = False) -> torch.Tensor:
-    """A workspace of moe_ffn_forward, or (backward) of both calls."""
+    """A workspace of moe_ffn_forward, or (backward) of both calls, for shape.T rows or
+    any fewer."""
     return torch.empty(max(moe_ffn_workspace_size(shape, backward), 256), dtype=torch.uint8,
                        device=device)
 

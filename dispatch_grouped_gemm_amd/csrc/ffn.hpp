@@ -569,23 +569,84 @@ inline float product_cost(TileKind kind, int splits, long M, long N, long K)
     return us;
 }
 
-// The cheapest cut.  Pairs need a tile's columns of both halves in a wavefront, which
-// the two smallest tiles lack, unless a join forms them.
+// The numbers of parts that tiles of a kind may go in.  Pairs need a tile's columns of
+// both halves in a wavefront, which the two smallest tiles lack, unless a join forms them.
+constexpr long kMostPlanes = 1l << 25; // float32 sums in all parts
+
+inline int fewest_parts(int kind, bool pairs)
+{
+    return pairs && (kind == kSmall || kind == kFew) ? 2 : 1;
+}
+inline int most_parts(int kind, long K)
+{
+    return kind < kEven || kind >= kTall
+               ? 1
+               : std::max(1, std::min(kMostParts, (int)((K + 63) >> 6) / 4));
+}
+
+// The cheapest cut.
 inline Cut product_cut(long M, long N, long K, bool pairs)
 {
     Cut best{kHuge, 1, product_cost(kHuge, 1, M, N, K)};
-    const int steps = (int)((K + 63) >> 6);
-    for (int k = kWide; k < kTileKinds; ++k) {
-        const int most = k < kEven || k >= kTall ? 1 : std::min(kMostParts, steps / 4);
-        for (int s = pairs && (k == kSmall || k == kFew) ? 2 : 1; s <= std::max(1, most); ++s) {
-            if (s > 1 && s * M * N > (1l << 25))
+    for (int k = kWide; k < kTileKinds; ++k)
+        for (int s = fewest_parts(k, pairs); s <= most_parts(k, K); ++s) {
+            if (s > 1 && s * M * N > kMostPlanes)
                 break;
             const float c = product_cost((TileKind)k, s, M, N, K);
             if (c < best.us)
                 best = Cut{(TileKind)k, s, c};
         }
-    }
     return best;
+}
+
+// No fewer than the parts that product_cut chooses for any of the M to M + 31 rows that
+// have the same tiles (M - 1 a multiple of 32): what a cut costs then rises with the
+// rows by its planes, so that more parts beat fewer for some of them only where they do for
+// M itself, but for the rounding of the costs.
+inline int parts_from(long M, long N, long K, bool pairs)
+{
+    int most = 1;
+    float best = 0.0f;
+    for (int s = 1; s <= kMostParts; ++s) {
+        float us = INFINITY;
+        for (int k = kHuge; k < kTileKinds; ++k)
+            if (s >= fewest_parts(k, pairs) && s <= most_parts(k, K))
+                us = std::min(us, product_cost((TileKind)k, s, M, N, K));
+        if (s == 1 || us <= best * 1.0001f)
+            most = s;
+        best = s == 1 ? us : std::min(best, us);
+    }
+    return most;
+}
+
+// A product's sizes beside its rows.
+struct ProductSides {
+    long N, K;
+    bool pairs;
+};
+
+// The most bytes that a call of 1 to T rows needs: parts come and go with the rows, so
+// the call of most rows is not the one that needs most.  need(M): those of M rows.
+template <int P, typename F>
+size_t most_bytes(long T, const ProductSides (&sides)[P], F need)
+{
+    size_t most = need(T);
+    long end = 0; // (two parts of more rows would be past kMostPlanes)
+    for (const ProductSides &p : sides)
+        end = std::max(end, kMostPlanes / 2 / p.N);
+    end = std::min(end, T);
+    for (long lo = 1; lo <= end; lo += 32) {
+        const long hi = std::min(lo + 31, end);
+        // with as many parts for all of them the last rows need most; up to 64 rows the
+        // kernels of few rows may take a product's place
+        bool alike = lo > 64;
+        for (const ProductSides &p : sides)
+            alike = alike && parts_from(lo, p.N, p.K, p.pairs) ==
+                                 product_cut(hi, p.N, p.K, p.pairs).splits;
+        for (long M = alike ? hi : lo; M <= hi; ++M)
+            most = std::max(most, need(M));
+    }
+    return most;
 }
 
 inline size_t product_parts_bytes(const Cut &c, long M, long N)

@@ -269,7 +269,14 @@ hipError_t zero(void *p, size_t bytes, hipStream_t st)
 
 } // namespace
 
-size_t ffn_backward_bytes(const moe_ffn_shape &s) { return plan_of(s).bytes; }
+size_t ffn_backward_bytes(const moe_ffn_shape &s)
+{
+    const ProductSides sides[] = {{s.I, s.H, false}};
+    return most_bytes(s.T, sides, [q = s](long M) mutable {
+        q.T = (int32_t)M;
+        return plan_of(q).bytes;
+    });
+}
 
 hipError_t launch_ffn_backward(const moe_ffn_shape &s, int dtype, const void *dout, const void *x,
                                const uint8_t *x_scale, const void *w13, const void *w2,

@@ -282,7 +282,14 @@ hipError_t forward_of_type(const moe_ffn_shape &s, const ForwardPlan &plan, cons
 
 } // namespace
 
-size_t ffn_forward_bytes(const moe_ffn_shape &s) { return plan_of(s).bytes; }
+size_t ffn_forward_bytes(const moe_ffn_shape &s)
+{
+    const ProductSides sides[] = {{2l * s.I, s.H, true}, {s.H, s.I, false}};
+    return most_bytes(s.T, sides, [q = s](long M) mutable {
+        q.T = (int32_t)M;
+        return plan_of(q).bytes;
+    });
+}
 
 hipError_t launch_ffn_forward(const moe_ffn_shape &s, int dtype, const void *x, const void *w13,
                               const void *w2, const void *base, void *gate_up,

@@ -583,7 +583,8 @@ hipError_t launch_adapter_project(const moe_adapter_shape &s, int dtype, const v
 
 // The dense feed-forward block and the residual joint with its norms
 // (arguments as the C ABI's; f32: the weights' gradients are float32; *fits
-// is false, and nothing launched, where the workspace is too small).
+// is false, and nothing launched, where the workspace is too small; the bytes are
+// those that calls of up to T rows need).
 size_t ffn_forward_bytes(const moe_ffn_shape &s);
 size_t ffn_backward_bytes(const moe_ffn_shape &s);
 hipError_t launch_ffn_forward(const moe_ffn_shape &s, int dtype, const void *x, const void *w13,

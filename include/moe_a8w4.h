@@ -602,7 +602,9 @@ int moe_adapter_project(const moe_adapter_shape *shape, int32_t dtype, const voi
  * overlap (but for base); x, weights, rows and gradients start on 16-byte
  * boundaries, gate_up codes on 16 and exponent bytes anywhere.
  * workspace: moe_ffn_workspace_size bytes of scratch (backward != 0: enough for
- * both calls), 256-byte aligned; calls that overlap on one workspace race.
+ * both calls), 256-byte aligned; one for T rows also serves calls of fewer, and
+ * calls that overlap on one race.  MOE_EWORKSPACE where it is less than the call
+ * itself needs.
  */
 typedef struct moe_ffn_shape {
     int32_t T;        /* rows, at most 2^24 */
@@ -615,8 +617,8 @@ typedef struct moe_ffn_shape {
 /* Check a shape; MOE_OK or the code a call with it would return. */
 int moe_ffn_check(const moe_ffn_shape *shape);
 
-/* Scratch bytes of moe_ffn_forward (backward 0) or of both calls; 0 for a
- * refused shape or T = 0. */
+/* Scratch bytes of moe_ffn_forward (backward 0) or of both calls, for T rows and
+ * any fewer; 0 for a refused shape or T = 0. */
 size_t moe_ffn_workspace_size(const moe_ffn_shape *shape, int32_t backward);
 
 int moe_ffn_forward(const moe_ffn_shape *shape, int32_t dtype, const void *x, const void *w13,

@@ -1,5 +1,5 @@
-"""What the feed-forward block and the residual joint accept without a GPU's work: calls of no
-rows."""
+"""What the feed-forward block and the residual joint accept, without a GPU's work: calls of no
+rows, and one workspace for many sizes."""
 
 import pytest
 
@@ -30,3 +30,17 @@ def test_no_rows_and_frozen_weights(lib):
                                 1 << 30, None) == -1
     assert lib.moe_norm_backward(n_shape(), 0, *([FAKE] * 7), *none[:5], FAKE, 1 << 30,
                                  None) == -1
+
+
+@pytest.mark.parametrize("H,I", [(5120, 2304), (2304, 1408), (7168, 18432), (7168, 2048),
+                                 (96, 64), (2304, 96), (1632, 352), (32, 32), (64, 131072)])
+def test_a_workspace_serves_fewer_rows(lib, H, I):
+    """Parts of K come and go with the rows; the workspace of many rows has room for all of
+    them (a server keeps the one of its largest batch)."""
+    rows = sorted({*range(1, 700), *range(700, 3000, 31), 4096, 8191, 65536, 1 << 20})
+    for backward in (False, True):
+        before = 0
+        for T in rows:
+            n = moe.moe_ffn_workspace_size(moe.FfnShape(T=T, H=H, I=I), backward)
+            assert n >= before, (T, backward)
+            before = n

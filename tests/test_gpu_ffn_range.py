@@ -23,3 +23,30 @@ def test_no_rows_and_frozen_weights():
     moe.moe_norm_backward(n, e, e, w, e, None, None)
     moe.moe_norm_backward(n, None, None, None, None, None, None, dres=e, y=e, w_post=w, gate=none,
                           dy=e, dgate=none)
+
+
+def test_a_workspace_serves_fewer_rows():
+    """One workspace for the largest batch, calls of fewer rows that go in parts of K: the bits
+    that a workspace of their own gives."""
+    H, I, most = 2304, 1408, 1200
+    g = torch.Generator(device=DEV)
+    g.manual_seed(41)
+    n = lambda *s: torch.randn(*s, generator=g, device=DEV)  # noqa: E731
+    x, dout = n(most, H).to(BF), n(most, H).to(BF)
+    w13, w2 = (n(2 * I, H) * H ** -0.5).to(BF), (n(H, I) * I ** -0.5).to(BF)
+    large = moe.alloc_ffn_workspace(moe.FfnShape(T=most, H=H, I=I), DEV, backward=True)
+    only = moe.alloc_ffn_workspace(moe.FfnShape(T=most, H=H, I=I), DEV)
+    for T in (most, 256, 192, 128, 65, 64, 20):
+        s = moe.FfnShape(T=T, H=H, I=I)
+        own = moe.alloc_ffn_workspace(s, DEV, backward=True)
+        results = []
+        for ws in (own, large, only):
+            out, kept = torch.empty(T, H, dtype=BF, device=DEV), torch.empty(T, 2 * I, dtype=BF,
+                                                                             device=DEV)
+            moe.moe_ffn_forward(s, x[:T], w13, w2, out, ws, gate_up=kept)
+            grads = [torch.empty_like(t) for t in (out, w13, w2)]
+            if ws is not only:
+                moe.moe_ffn_backward(s, dout[:T], x[:T], w13, w2, kept, *grads, ws)
+            results.append([out, kept] + (grads if ws is not only else []))
+        for r in results[1:]:
+            assert all(torch.equal(a, b) for a, b in zip(results[0], r)), T

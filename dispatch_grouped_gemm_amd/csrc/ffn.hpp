@@ -44,10 +44,12 @@ __device__ __forceinline__ void store4(uint16_t *p, const v4f &v)
     *reinterpret_cast<uint2 *>(p) = uint2{q.x, q.y};
 }
 
+// (an exponent byte of 255 is NaN: the codes of NaN then, whatever the exponent)
 __device__ __forceinline__ void from_mx(const uint2 &codes, uint32_t scale, float *f)
 {
     const int e = (int)scale - 127;
-    const uint32_t w[2] = {codes.x, codes.y};
+    const uint32_t nan = scale == 255 ? 0x7f7f7f7fu : 0u;
+    const uint32_t w[2] = {codes.x | nan, codes.y | nan};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], false);

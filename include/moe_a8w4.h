@@ -593,6 +593,7 @@ int moe_adapter_project(const moe_adapter_shape *shape, int32_t dtype, const voi
  *   dx = (dg | du) W13,  dW13 = (dg | du)^T x,  dW2 = dout^T h.
  * x is in dtype (x_scale NULL) or MX FP8: codes [T, H] and exponent bytes
  * x_scale [T, H/32], as the experts take it; its values are rounded to dtype.
+ * (An exponent byte of 255, in either, is 32 NaN.)
  * dx [T, H], dw13 and dw2 (shaped as the weights) may each be NULL; x may be
  * NULL without dw13, w13 without dx.  dw_dtype is dtype or MOE_DT_F32;
  * accumulate != 0 adds to what dw13 and dw2 hold (float32 sum, rounded once).

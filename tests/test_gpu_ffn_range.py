@@ -50,3 +50,37 @@ def test_a_workspace_serves_fewer_rows():
             results.append([out, kept] + (grads if ws is not only else []))
         for r in results[1:]:
             assert all(torch.equal(a, b) for a, b in zip(results[0], r)), T
+
+
+@pytest.mark.parametrize("T", [40, 300])
+@pytest.mark.parametrize("dt", [BF, F16])
+def test_an_exponent_byte_of_255_is_nan(T, dt):
+    """E8M0 255 stands for NaN, as in the experts' products: the whole block of 32 values, in
+    x as the experts take it and in what was kept."""
+    H, I, row = 96, 64, T // 2
+    g = torch.Generator(device=DEV)
+    g.manual_seed(T)
+    n = lambda *s: torch.randn(*s, generator=g, device=DEV).to(dt)  # noqa: E731
+    dout, w13, w2 = n(T, H), n(2 * I, H), n(H, I)
+    s = moe.FfnShape(T=T, H=H, I=I)
+    ws = moe.alloc_ffn_workspace(s, DEV, backward=True)
+    # codes of 0 and of 1 and -1 in turn, of exponent 0
+    code = torch.tensor([0x00, 0x38, 0xb8], dtype=torch.uint8, device=DEV)
+    x = code[torch.arange(T * H, device=DEV).reshape(T, H) % 3]
+    kept = code[torch.arange(T * 2 * I, device=DEV).reshape(T, 2 * I) % 3]
+    xs = torch.full((T, H // 32), 127, dtype=torch.uint8, device=DEV)
+    ks = torch.full((T, 2 * I // 32), 127, dtype=torch.uint8, device=DEV)
+    xs[row, 1], ks[3, 2] = 255, 255                     # columns 32 .. 63; u of 0 .. 31
+    dx, dw13, dw2 = torch.empty_like(dout), torch.empty_like(w13), torch.empty_like(w2)
+    moe.moe_ffn_backward(s, dout, x, w13, w2, kept, dx, dw13, dw2, ws, gate_up_scale=ks,
+                         x_scale=xs)
+    nan = torch.zeros(T, H, dtype=torch.bool, device=DEV)
+    nan[3] = True                                       # dg of a NaN u
+    assert torch.equal(dx.isnan(), nan) and dx[~nan].isfinite().all()
+    nan = torch.zeros(2 * I, H, dtype=torch.bool, device=DEV)
+    nan[:, 32:64] = True
+    nan[:32] = True                                     # its dg (du has no u in it)
+    assert torch.equal(dw13.isnan(), nan) and dw13[~nan].isfinite().all()
+    nan = torch.zeros(H, I, dtype=torch.bool, device=DEV)
+    nan[:, :32] = True                                  # its h
+    assert torch.equal(dw2.isnan(), nan) and dw2[~nan].isfinite().all()

@@ -24,8 +24,27 @@ FLAGS = [
 ]
 
 
+def _checks_mark() -> bytes:
+    """What _checks.so holds of the torch and the Python that it was built for."""
+    import sys
+
+    import torch
+    return b"tensor checks for torch %s, %s\0" % (torch.__version__.encode(),
+                                                  sys.implementation.cache_tag.encode())
+
+
+def checks_current() -> bool:
+    """Whether _checks.so is there and is this torch's and this Python's (it reads their
+    structures, so it is not loaded to find out)."""
+    try:
+        with open(CHECKS, "rb") as f:
+            return _checks_mark() in f.read()
+    except OSError:
+        return False
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(CHECKS):
+    if not os.path.exists(LIB) or not checks_current():
         return True
     t = min(os.path.getmtime(LIB), os.path.getmtime(CHECKS))
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
@@ -44,6 +63,7 @@ def _build_checks() -> None:
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
            "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+           '-DCHECKS_MARK="%s"' % _checks_mark()[:-1].decode(),
            *["-isystem" + d for d in dirs], os.path.join(CSRC, "checks.cpp"), "-o", tmp,
            "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -8,6 +8,10 @@
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+// The torch and the Python that this was built for; the binding looks for it in
+// the file before it loads it (for others it compares through Python).
+extern "C" __attribute__((used)) const char moe_checks_mark[] = CHECKS_MARK;
+
 namespace {
 
 bool as_wanted(PyObject *tensor, PyObject *shape, PyObject *dtype, PyObject *index, void **p)

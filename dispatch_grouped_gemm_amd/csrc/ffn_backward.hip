@@ -105,91 +105,15 @@ __global__ void __launch_bounds__(512, 1) gradients_kernel(Gradients<DT> g)
     }
 }
 
-// When the last of up to three jobs of n[j] workgroups that take d[j] each, in
-// their order, is through on 32 CUs: an XCD's, which gets every eighth one.
-float finish(const int *n, const float *d, int jobs)
-{
-    struct {
-        float t; // CUs that are free from then on
-        int cus;
-    } level[4] = {{0.0f, 32}};
-    int levels = 1;
-    float end = 0.0f;
-    for (int j = 0; j < jobs; ++j)
-        for (int left = n[j]; left > 0;) {
-            int i = 0;
-            for (int k = 1; k < levels; ++k)
-                if (level[k].t < level[i].t)
-                    i = k;
-            const float t = level[i].t + d[j];
-            end = std::max(end, t);
-            if (left >= level[i].cus) {
-                left -= level[i].cus;
-                level[i].t = t;
-            } else { // the job's last: once a job
-                level[i].cus -= left;
-                level[levels++] = {t, left};
-                left = 0;
-            }
-        }
-    return end;
-}
-
-// The tiles of each job: those whose schedule ends first, the smallest of such, by
-// what a tile takes with all CUs busy (steps of 64 k, and once).  Measured, all 45 choices at 17
-// sizes (us; one kind for all jobs but a last 128 x 256 beside 256 x 256, and as
-// chosen; in the mean 1.2% behind the fastest, one kind 11%):
-//      64 rows, 5,120 by 2,304    41   32 (dx 64 x 128, 256 x 256, 128 x 256)
-//     700 rows, 5,120 by 2,304    94   81 (128 x 256, 256 x 256, 128 x 256)
-//   1,500 rows, 2,304 by 1,408    57   50 (192 x 256, then 128 x 256)
-//   2,048 rows, 5,120 by 2,304   196  189 (192 x 256, then 256 x 256)
-//   8,192 rows, 1,024 by   512    74   59 (256 x 256, then 128 x 128)
-//   8,192 rows, 7,168 by 2,048   923  923 (256 x 256, the last 128 x 256)
-template <int DT>
-void choose_tiles(Gradients<DT> &g)
-{
-    constexpr TileKind kinds[] = {kHuge, kTall, kWide, kEven, kFlat};
-    constexpr float step[] = {1.22f, 0.99f, 0.74f, 0.43f, 0.32f};
-    constexpr float once[2][5] = {{9.1f, 0.0f, 4.6f, 4.0f, 0.0f}, {7.9f, 2.8f, 4.0f, 3.7f, 0.8f}};
-    const auto can = [&](int j, int q) {
-        return j < g.jobs ? j < g.along || (kinds[q] != kTall && kinds[q] != kFlat) : q == 0;
-    };
-    int n[3][5] = {};
-    float d[3][5] = {}, best = 0.0f;
-    for (int j = 0; j < g.jobs; ++j)
-        for (int q = 0; q < 5; ++q) {
-            const long tiles = tiles_down(kinds[q], g.p[j].M) * tiles_across(kinds[q], g.p[j].N);
-            n[j][q] = (int)((tiles + 7) / 8);
-            d[j][q] = ((g.p[j].K + 63) >> 6) * step[q] + once[j < g.along][q];
-        }
-    // long calls: what the schedule's end costs is small beside the largest tiles' rate
-    const bool rounds = n[0][0] + n[1][0] + n[2][0] > 32 * 32;
-    for (int a = 0; a < 5; ++a)
-        for (int b = 0; b < 5; ++b)
-            for (int c = 0; c < 5; ++c) {
-                if (!can(0, a) || !can(1, b) || !can(2, c))
-                    continue;
-                const int q[3] = {a, b, c}, ns[3] = {n[0][a], n[1][b], n[2][c]};
-                const float ds[3] = {d[0][a], d[1][b], d[2][c]};
-                if (best > 0.0f && (rounds || ns[0] * ds[0] + ns[1] * ds[1] + ns[2] * ds[2] >= 32 * best))
-                    continue;
-                const float us = rounds ? 1.0f : finish(ns, ds, g.jobs);
-                if (best == 0.0f || us <= best) {
-                    best = us;
-                    for (int j = 0; j < g.jobs; ++j)
-                        g.kind[j] = kinds[q[j]];
-                }
-            }
-    if (rounds && g.along < g.jobs)
-        g.kind[g.jobs - 1] = kWide;
-}
-
 template <int DT>
 hipError_t launch_gradients(Gradients<DT> &g, hipStream_t st)
 {
     if (g.jobs == 0)
         return hipSuccess;
-    choose_tiles(g);
+    Sides sides[3];
+    for (int j = 0; j < g.jobs; ++j)
+        sides[j] = {g.p[j].M, g.p[j].N, g.p[j].K};
+    choose_tiles(sides, g.jobs, g.along, g.kind);
     int n = 0;
     for (int j = 0; j < g.jobs; ++j) {
         g.p[j].tm = (int)tiles_down(g.kind[j], g.p[j].M);

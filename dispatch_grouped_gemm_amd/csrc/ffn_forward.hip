@@ -190,12 +190,6 @@ __global__ void __launch_bounds__(512) few_out_kernel(FewProduct p, Put<DT> f)
         f.four(t, n0 + 16 * b + 4 * (lane >> 4), few_sum<MB>(lds, b, m));
 }
 
-// Whether few rows by 32 of N weight rows a workgroup beat the tiles: each draws
-// its rows of x and of the weight at some 72 KB a us, so they need to be many and
-// the rows few (14 x 1,216 gate and up rows over 6,304, 38 workgroups: 11 us, by
-// tiles with K in parts 8; 4,608 rows over 5,120 12 and 15).
-int few_blocks(int T) { return T <= 16 ? 1 : T <= 32 ? 2 : 4; }
-
 // How a forward call is cut.
 struct ForwardPlan {
     bool few_gate_up, few_out;
@@ -206,16 +200,10 @@ struct ForwardPlan {
 ForwardPlan plan_of(const moe_ffn_shape &s)
 {
     ForwardPlan p{};
-    const auto few = [&](long N, long K, const Cut &c) {
-        const float memory = (2e-6f / 4.5f) * N * K;
-        const float drawn = (2e-3f / 72.0f) * (16 * few_blocks(s.T) + 32) * K;
-        const long rounds = (N / 32 + kTileCus - 1) / kTileCus;
-        return s.T <= 64 && std::max(rounds * drawn, memory) + 2.5f <= c.us;
-    };
     p.gate_up = product_cut(s.T, 2l * s.I, s.H, true);
     p.out = product_cut(s.T, s.H, s.I, false);
-    p.few_gate_up = few(2l * s.I, s.H, p.gate_up);
-    p.few_out = few(s.H, s.I, p.out);
+    p.few_gate_up = few_rows_pay(s.T, 2l * s.I, s.H, p.gate_up);
+    p.few_out = few_rows_pay(s.T, s.H, s.I, p.out);
     p.bytes = h_bytes(s) +
               std::max(p.few_gate_up ? 0 : product_parts_bytes(p.gate_up, s.T, 2l * s.I),
                        p.few_out ? 0 : product_parts_bytes(p.out, s.T, s.H));

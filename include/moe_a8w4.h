@@ -637,8 +637,8 @@ int moe_ffn_backward(const moe_ffn_shape *shape, int32_t dtype, const void *dout
  * before the next one, and its gradients.  dtype any of the three element
  * types; rows [T, H]; rho(v) = 1 / sqrt(mean v^2 + eps), sums in float32.
  * Those sums bound the rows: their root mean square is at most 2^56 and, where
- * eps is no larger than its square, at least 2^-60 (a row of zeros needs an eps
- * above 0).
+ * eps is no larger than its square, at least 2^-60 (a row of zeros: an eps of
+ * 2^-120 or more).
  *
  * moe_norm_forward:
  *   z = y rho(y) w_post             (w_post [H]; NULL: z = y)

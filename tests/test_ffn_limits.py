@@ -1,11 +1,11 @@
 """What the feed-forward block and the residual joint accept, without a GPU's work: calls of no
-rows, and one workspace for many sizes."""
+rows, one workspace for many sizes, and the largest sizes there are."""
 
 import pytest
 
 import dispatch_grouped_gemm_amd as moe
 from dispatch_grouped_gemm_amd import _build
-from test_ffn_refusals import FAKE, f_shape, n_shape
+from test_ffn_refusals import FAKE, FF, NO, f_shape, n_shape
 
 
 @pytest.fixture(scope="module")
@@ -44,3 +44,13 @@ def test_a_workspace_serves_fewer_rows(lib, H, I):
             n = moe.moe_ffn_workspace_size(moe.FfnShape(T=T, H=H, I=I), backward)
             assert n >= before, (T, backward)
             before = n
+
+
+def test_the_largest_sizes(lib):
+    for kw, code in [(dict(T=1 << 21), 0), (dict(T=(1 << 21) + 1), -2), (dict(H=1 << 14), 0),
+                     (dict(H=(1 << 14) + 32), -2)]:
+        assert moe.moe_norm_check(moe.NormShape(**{**NO, **kw})) == code, kw
+    for kw, code in [(dict(T=1 << 24), 0), (dict(T=(1 << 24) + 1), -2), (dict(H=1 << 17), 0),
+                     (dict(H=(1 << 17) + 32), -2), (dict(I=1 << 17), 0),
+                     (dict(I=(1 << 17) + 32), -2)]:
+        assert moe.moe_ffn_check(moe.FfnShape(**{**FF, **kw})) == code, kw

@@ -1,4 +1,4 @@
-"""The residual joint's gradients at the ends of what its header allows: rows far from 1, eps 0
+"""The residual joint and its gradients at the ends of what its header allows: rows far from 1, eps 0
 and next to it."""
 
 import pytest
@@ -38,6 +38,21 @@ def test_rows_far_from_one(T, H, size, eps, dt):
         # again: below the normal numbers of bf16 and float32 each is off by steps of 2^-133
         # and 2^-149, and a flushed one by 2^-126
         assert_close(o[k], v, b + (2.0 ** -125 if k == "dy" else 0.0), k)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("size,eps", [(1e-14, 0.0), (1e-13, 1e-30), (1e10, 1e-6), (1e16, 1e-6)])
+@pytest.mark.parametrize("T,H", [(5, 96), (3, 7168)])
+def test_the_joint_of_rows_far_from_one(T, H, size, eps, dt):
+    c = base._case(T, H, dt, T * H)
+    c["x"], c["y"] = c["x"] * size, c["y"] * size
+    s = moe.NormShape(T=T, H=H, eps=eps, skip_scale=0.75, block_scale=0.4 * size)
+    res, normed = torch.empty_like(c["x"]), torch.empty_like(c["x"])
+    kw = dict(y=c["y"], w_post=c["w_post"], gate=c["gate"])
+    moe.moe_norm_forward(s, c["x"], c["w_pre"], normed, res=res, **kw)
+    assert_close(res, *ffn_ref.norm_forward(c["x"], None, eps, 0.75, s.c().block_scale, **kw),
+                 "res")
+    assert_close(normed, *ffn_ref.norm_of(res, c["w_pre"], eps), "normed")
 
 
 @pytest.mark.parametrize("dt", [BF, F32])

@@ -383,28 +383,25 @@ __global__ void __launch_bounds__(T::kThreads, 1) product_kernel(Product p, F f)
     whole_tile<T, kPairs, ADOWN, BDOWN>(p, f, (long)im * T::kBM, in, lds);
 }
 
-// `whole` tiles of 256 x 256, and those left over, which would leave CUs idle
-// for a tile's time, as kCut smaller tiles TL each.  `early` of the small ones
-// (a multiple of 8) come first: the CUs that take them are then out of step with
-// the others, and their epilogues do not all ask for the memory at once (8,191 x
-// 7,168 over 2,048 262 -> 255 us with a base, 205 -> 201 without; quarters gain
-// nothing).
+// `whole` tiles of 256 x 256, and behind them those left over, which would leave CUs
+// idle for a tile's time, as kCut smaller tiles TL each.  (Some of the small ones first,
+// so that the CUs' epilogues are out of step: 8,191 x 7,168 over 2,048 then reads 828 MB
+// past the L2s, not 525, since tiles that share rows no longer ask for them together,
+// and takes as long.)
 template <typename T, typename TL, bool kPairs, bool ADOWN, bool BDOWN, typename F>
-__global__ void __launch_bounds__(T::kThreads, 1)
-product_rest_kernel(Product p, int whole, int early, F f)
+__global__ void __launch_bounds__(T::kThreads, 1) product_rest_kernel(Product p, int whole, F f)
 {
     constexpr int kMost = TL::kLds > T::kLds ? TL::kLds : T::kLds;
     constexpr int kDownward = T::kBM / TL::kBM, kCut = kDownward * (T::kBN / TL::kBN);
     __shared__ __align__(1024) uint8_t lds[kMost];
-    const int b = blockIdx.x - early;
+    const int b = blockIdx.x;
     int im, in;
-    if (b >= 0 && b < whole) {
+    if (b < whole) {
         tile_place(tile_run(b, whole), p.tm, p.tn, &im, &in);
         whole_tile<T, kPairs, ADOWN, BDOWN>(p, f, (long)im * T::kBM, in, lds);
         return;
     }
-    const int q = b < 0 ? (int)blockIdx.x : b - whole + early;
-    const int h = tile_run(q, gridDim.x - whole), part = h % kCut;
+    const int h = tile_run(b - whole, gridDim.x - whole), part = h % kCut;
     tile_place(whole + h / kCut, p.tm, p.tn, &im, &in);
     const long m0 = (long)im * T::kBM + part % kDownward * TL::kBM;
     in = in * (T::kBN / TL::kBN) + part / kDownward;
@@ -528,8 +525,7 @@ hipError_t launch_product(Product p, const Cut &c, const F &f, const J &join, fl
         using L = decltype(t);
         const int left = n % kTileCus, small = huge_rest(n) * left;
         product_rest_kernel<typename S::Huge, L, kPairs, ADOWN, BDOWN>
-            <<<n - left + small, 512, 0, st>>>(p, n - left,
-                                               huge_rest(n) == 2 ? small / 16 * 8 : 0, f);
+            <<<n - left + small, 512, 0, st>>>(p, n - left, f);
     };
     if (c.kind == kHuge && huge_rest(n) == 2) {
         rest(typename S::Wide{});

@@ -358,9 +358,10 @@ __device__ __forceinline__ void whole_tile(const Product &p, const F &f, long m0
 }
 
 // The tiles there are; what each costs: product_cost (ffn_plan.hpp).  Where B's k lies
-// down its rows, its transpose reads run at half the rate of A's: wavefronts
-// then share B's columns among two rows of them, not four (4,096 x 2,304 over
-// 5,120 by 128 x 128: 107 us, so 124).
+// down its rows, its transpose reads run at half the rate of A's: wavefronts then share
+// B's columns among two rows of them, not four (dh, two rows and four, us: 1,021 x 1,408
+// over 2,304 by 64 x 128 16.5 and 18.2, by 128 x 128 22.2 and 23.4; 4,096 x 2,304 over
+// 5,120 by 128 x 128 152 and 156, by 192 x 128 127 and 122).
 template <int DT, bool ADOWN, bool BDOWN>
 struct Tiles {
     static constexpr int WM = BDOWN ? 2 : 4, WN = 8 / WM;

@@ -61,7 +61,8 @@ inline int huge_rest(long tiles)
 //   4,096 x 4,608 pairs over 5,120    151  183  193  234            167  195
 //   8,192 x 7,168 over 2,048          196  224  286  353            204  240
 //   4,096 x 5,120 over 2,304           79   92   96  126             83  100
-//   4,096 x 2,304 over 5,120 (down)   123  135  125  140             97  122
+//   4,096 x 2,304 over 5,120 (down)    99  118  108  131             84  106
+//         the same with dh's epilogue  145  143  155  185            123  130
 //   2,048 x 5,120 over 2,304           48   57   54   65             43   49
 //   1,021 x 4,608 pairs over 5,120     92   53   71   77             75   49
 //   1,021 x 2,816 pairs over 2,304     47   27   19   25             37   23
